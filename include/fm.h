@@ -58,6 +58,7 @@ extern "C" {
 #define FM_F32 0
 #define FM_I16 1
 #define FM_F16 2
+#define FM_BF16 3 /* operators below only (layer norm, attention, scores)    */
 
 /* normalized: STFT normalisation folded into the window (flashmel/filters.py
  * make_window): none, divide by sqrt(sum of the squared window), or divide
@@ -338,6 +339,137 @@ int fm_plan_mel_blocks(const fm_plan* plan, int32_t* blocks, int32_t* wave_beg,
  */
 int fm_plan_mel_quads(const fm_plan* plan, int32_t* headers, int32_t* share_beg,
                       float* weights, int32_t* n_quads, int64_t* n_weights);
+
+/* ---- operators of the models on top of the mel front end ------------------
+ *
+ * Element types are FM_F32, FM_F16 and FM_BF16; sums, statistics and
+ * reductions are float32, results are rounded once to the element type.
+ * Every call only enqueues on `stream`, allocates nothing and is
+ * deterministic.  Workspaces are device memory of the caller, 16-byte
+ * aligned, of at least the size that the _workspace function returns
+ * (negative: FM_E_*; 0: NULL is accepted), free again when the call's work
+ * on the stream is done.
+ */
+
+/*
+ * fm_layer_norm_forward -- y = (x - mean) / sqrt(var + eps) * weight + bias
+ * over the last axis, var the mean squared deviation.
+ *   x [rows, width], x_stride elements from row to row, elements of a row
+ *   contiguous; y [rows, width] contiguous, same type; weight, bias [width]
+ *   of type param_dtype (dtype or FM_F32), both NULL or bias NULL allowed;
+ *   mean, rstd [rows] float32, each may be NULL (the backward needs them).
+ *   0 <= rows < 2^31, 1 <= width <= 2^20, eps >= 0.
+ */
+int fm_layer_norm_forward(const void* x, int64_t x_stride, const void* weight, const void* bias,
+                          void* y, float* mean, float* rstd, int64_t rows, int64_t width,
+                          double eps, int dtype, int param_dtype, void* stream);
+
+/* Bytes of fm_layer_norm_backward's workspace. */
+int64_t fm_layer_norm_backward_workspace(int64_t rows, int64_t width, int dtype);
+
+/*
+ * fm_layer_norm_backward -- gradients of sum(dy * y).  dy, x as above; dx
+ * [rows, width] contiguous; dw, db [width] of type param_dtype: dw NULL
+ * leaves both out (workspace unused), db may be NULL by itself.  weight NULL:
+ * the forward had none.
+ */
+int fm_layer_norm_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                           const void* weight, const float* mean, const float* rstd, void* dx,
+                           void* dw, void* db, void* workspace, int64_t rows, int64_t width,
+                           int dtype, int param_dtype, void* stream);
+
+/* Bytes of fm_token_logprobs's workspace. */
+int64_t fm_token_logprobs_workspace(int64_t rows, int64_t vocab, int top, int dtype);
+
+/*
+ * fm_token_logprobs -- per row of logits x [rows, vocab] (x_stride elements
+ * from row to row): lp [rows] = x[token] - lse, the entropy of softmax(x),
+ * lse = log sum exp(x), and the `top` largest entries (0 <= top <= 64, <=
+ * vocab) in descending order, ties to the lower index: top_ids [rows, top]
+ * int64 and top_lp [rows, top].  tokens [rows]: int64 (token_bits 64) or int32
+ * (32); a negative token asks for nothing (lp 0), one >= vocab gives NaN.
+ * -inf entries have probability 0; a row of only -inf has lp = lse = -inf
+ * and entropy 0.  A NaN or +inf entry makes its row's results NaN.  lp, ent,
+ * lse may be NULL.  vocab < 2^31 - 65536, rows * (row segments) < 2^31.
+ */
+int fm_token_logprobs(const void* x, int64_t x_stride, const void* tokens, int token_bits,
+                      float* lp, float* ent, float* lse, int64_t* top_ids, float* top_lp,
+                      void* workspace, int64_t rows, int64_t vocab, int top, int dtype,
+                      void* stream);
+
+/*
+ * fm_token_logprobs_backward -- dx [rows, vocab] contiguous, the gradient of
+ * sum(g_lp * lp) + sum(g_ent * ent) + sum(g_top * top_lp) with respect to x;
+ * any of g_lp, g_ent, g_top (float32) may be NULL; lse and ent from the
+ * forward call, top_ids too where g_top is given.  Rows without a valid token
+ * take no g_lp; rows of only -inf have a zero gradient.
+ */
+int fm_token_logprobs_backward(const void* x, int64_t x_stride, const void* tokens,
+                               int token_bits, const float* lse, const float* ent,
+                               const float* g_lp, const float* g_ent, const int64_t* top_ids,
+                               const float* g_top, void* dx, int64_t rows, int64_t vocab, int top,
+                               int dtype, void* stream);
+
+/*
+ * fm_attention_args -- attention with a learned relative position bias:
+ *
+ *   s[i, j] = scale * q[i].k[j] + table[bucket_map[far + clamp(j - pos(i), -far, far)]][head]
+ *   o[i] = sum_j softmax_j(s[i, j]) v[j],  pos(i) = query_offset[entry] + i
+ *
+ * over the keys j < key_lengths[entry], and j <= pos(i) if causal.  A query
+ * without any key gives o = 0, lse = -inf and zero gradients; keys and values
+ * at or past key_lengths are not read (NaN there does no harm).
+ *   dtype        of q, k, v, o and their gradients;
+ *   q, o [batch, heads, q_len, head_dim], k, v [batch, kv_heads, k_len,
+ *                head_dim]: strides in elements of (entry, head, time), >= 0,
+ *                the last axis contiguous; heads a multiple of kv_heads, query
+ *                head h reads key head h / (heads / kv_heads); head_dim <= 128;
+ *   table        [num_buckets, heads] contiguous, table_dtype (dtype or
+ *                FM_F32), num_buckets <= 1024;
+ *   bucket_map   [2 far + 1] int32, the bucket of each distance key - query
+ *                from -far to far (<= 1024), farther ones taken at the ends; a
+ *                distance with an entry outside [0, num_buckets) has no bias;
+ *   key_lengths  [batch] int32 (clamped to [0, k_len]) or NULL: k_len;
+ *   query_offset [batch] int32 or NULL: query_offset_value for every entry;
+ *   o_rest       NULL, or (16-bit types; strides as o) what rounding o left:
+ *                with it the backward has o in twice the bits, which the sums
+ *                of the table's gradient profit from;
+ *   lse          [batch, heads, q_len] float32, NULL allowed in the forward;
+ * backward: grad_o in; grad_q, grad_k, grad_v out (every element written);
+ *                grad_table out, [num_buckets, heads] of table_dtype, or NULL.
+ */
+typedef struct fm_attention_args {
+  int dtype, table_dtype, causal, far, num_buckets, reserved;
+  int64_t batch, heads, kv_heads, q_len, k_len, head_dim, query_offset_value;
+  double scale;
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* table;
+  const int32_t* bucket_map;
+  const int32_t* key_lengths;
+  const int32_t* query_offset;
+  void* o;
+  void* o_rest;
+  float* lse;
+  const void* grad_o;
+  void* grad_q;
+  void* grad_k;
+  void* grad_v;
+  void* grad_table;
+  int64_t q_stride[3], k_stride[3], v_stride[3], o_stride[3];
+  int64_t grad_o_stride[3], grad_q_stride[3], grad_k_stride[3], grad_v_stride[3];
+} fm_attention_args;
+
+/* Bytes of the workspace of fm_attention_forward (backward 0) or _backward
+ * (1); pointers and strides are not looked at. */
+int64_t fm_attention_workspace(const fm_attention_args* args, int backward);
+
+/* o (and o_rest, lse if not NULL). */
+int fm_attention_forward(const fm_attention_args* args, void* workspace, void* stream);
+
+/* Gradients of sum(grad_o * o); o, o_rest and lse as the forward wrote them. */
+int fm_attention_backward(const fm_attention_args* args, void* workspace, void* stream);
 
 #ifdef __cplusplus
 }

@@ -25,6 +25,7 @@ FM_NORM = {None: 0, "slaney": 1}
 FM_F32 = 0
 FM_I16 = 1
 FM_F16 = 2
+FM_BF16 = 3
 FM_FWD_SPLIT = 0
 FM_FWD_PAIRED = 1
 FM_FWD_LARGE = 2
@@ -58,6 +59,23 @@ class Args(ctypes.Structure):
                                               "normalized", "out_dtype")])
 
 
+class AttentionArgs(ctypes.Structure):
+    """fm_attention_args of include/fm.h (its stride arrays field by field, so
+    that one positional call fills it)."""
+    _fields_ = ([(n, ctypes.c_int) for n in ("dtype", "table_dtype", "causal", "far",
+                                              "num_buckets", "reserved")] +
+                [(n, ctypes.c_int64) for n in ("batch", "heads", "kv_heads", "q_len", "k_len",
+                                                "head_dim", "query_offset_value")] +
+                [("scale", ctypes.c_double)] +
+                [(n, ctypes.c_void_p) for n in ("q", "k", "v", "table", "bucket_map",
+                                                 "key_lengths", "query_offset", "o", "o_rest",
+                                                 "lse", "grad_o", "grad_q", "grad_k", "grad_v",
+                                                 "grad_table")] +
+                [(f"{t}_stride_{axis}", ctypes.c_int64)
+                 for t in ("q", "k", "v", "o", "grad_o", "grad_q", "grad_k", "grad_v")
+                 for axis in ("entry", "head", "time")])
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
@@ -86,6 +104,15 @@ def _load() -> ctypes.CDLL:
         "fm_plan_tables": (I, [P, P, P, P, P, P, P, P]),
         "fm_plan_mel_blocks": (I, [P, P, P, P, P, P]),
         "fm_plan_mel_quads": (I, [P, P, P, P, P, P]),
+        "fm_layer_norm_forward": (I, [P, I64, P, P, P, P, P, I64, I64, D, I, I, P]),
+        "fm_layer_norm_backward_workspace": (I64, [I64, I64, I]),
+        "fm_layer_norm_backward": (I, [P, I64, P, I64, P, P, P, P, P, P, P, I64, I64, I, I, P]),
+        "fm_attention_workspace": (I64, [ctypes.POINTER(AttentionArgs), I]),
+        "fm_attention_forward": (I, [ctypes.POINTER(AttentionArgs), P, P]),
+        "fm_attention_backward": (I, [ctypes.POINTER(AttentionArgs), P, P]),
+        "fm_token_logprobs_workspace": (I64, [I64, I64, I, I]),
+        "fm_token_logprobs": (I, [P, I64, P, I, P, P, P, P, P, P, I64, I64, I, I, P]),
+        "fm_token_logprobs_backward": (I, [P, I64, P, I, P, P, P, P, P, P, P, I64, I64, I, I, P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)

@@ -1,0 +1,93 @@
+"""What the operators' torch-facing callers share: element types, the rows of
+a strided tensor, the launch on a tensor's device and torch's current stream."""
+from __future__ import annotations
+
+import torch
+
+from . import _native as N
+
+DTYPES = {torch.float32: N.FM_F32, torch.float16: N.FM_F16, torch.bfloat16: N.FM_BF16}
+
+
+def dtype_code(x: torch.Tensor, name: str) -> int:
+    """The library's code of x's element type; x must be a GPU tensor."""
+    if not isinstance(x, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor, got {type(x).__name__}")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be on a GPU, got {x.device}")
+    code = DTYPES.get(x.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {x.dtype}")
+    return code
+
+
+def rows_of(x: torch.Tensor, name: str):
+    """(rows, width, elements between rows) of x's last axis."""
+    if x.dim() < 1:
+        raise ValueError(f"{name} must have at least one axis")
+    width = x.shape[-1]
+    if width == 0:
+        raise ValueError(f"{name} must have a last axis of at least one element")
+    n = x.numel()
+    if x.is_contiguous():
+        return n // width, width, width
+    if n == 0:
+        return 0, width, width
+    if width > 1 and x.stride(-1) != 1:
+        raise ValueError(f"{name}'s last axis must be contiguous")
+    stride, rows = None, 1
+    for size, st in zip(reversed(x.shape[:-1]), reversed(x.stride()[:-1])):
+        if size == 1:
+            continue
+        if stride is None:
+            stride = st
+        elif st != stride * rows:
+            raise ValueError(f"{name}'s leading axes must lie at one stride (make it contiguous)")
+        rows *= size
+    return rows, width, width if stride is None else stride
+
+
+def same_device(x: torch.Tensor, **others) -> None:
+    for name, t in others.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a tensor, got {type(t).__name__}")
+        if t.device != x.device:
+            raise ValueError(f"{name} must be on {x.device}, got {t.device}")
+
+
+def contiguous_f32(t, shape, name: str) -> None:
+    """Checks a float32 statistics or gradient tensor (None passes)."""
+    if t is None:
+        return
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be float32, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}")
+
+
+def call(x: torch.Tensor, fn, *args) -> None:
+    """fn(*args, stream) on x's device, on torch's current stream there."""
+    dev = x.device
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st < 0:
+        N.check(st)
+
+
+def workspace(x: torch.Tensor, nbytes: int):
+    """Scratch memory from torch's allocator (None for 0 bytes); it may be
+    freed as soon as the call is enqueued, since the allocator hands it out
+    again in stream order."""
+    if nbytes < 0:
+        N.check(nbytes)
+    return torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
+
+
+def ptr(t):
+    return None if t is None else t.data_ptr()

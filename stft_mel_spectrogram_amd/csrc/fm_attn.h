@@ -1,0 +1,258 @@
+// Attention with a learned relative position bias by buckets: what its
+// kernels share (matrix fragments, tiles in LDS, the bias window).
+//
+//   s_ij = scale q_i.k_j + table[map[clamp(j - pos_i, -far, far)]][head]
+//   p_ij = exp(s_ij - lse_i) over the keys that query i sees,  o_i = sum p_ij v_j
+//   dv_j = sum p_ij do_i,  dp_ij = do_i.v_j,  ds_ij = p_ij (dp_ij - delta_i),
+//   delta_i = do_i.o_i,  dq_i = scale sum ds_ij k_j,  dk_j = scale sum ds_ij q_i,
+//   dtable[b][head] = sum of ds_ij over the pairs of bucket b
+//
+// Matrix products run on 32x32x16 MFMAs (float32: eight 32x32x2 ones, which
+// take the same fragments).  Lane l = 32 h + n of a fragment holds row (or
+// column) n and the 8 contraction indices of half h.  A result's lane holds
+// column n and rows 8 (r / 4) + 4 h + r % 4 for its 16 registers r.
+//
+// Probabilities never pass through LDS: their product with the next operand
+// contracts over the result's rows, in whatever order, as long as the other
+// operand is read in that order too.  Registers 8 c .. 8 c + 7 of a lane are
+// its 8 contraction indices of step c: rows 16 c + 4 h + 0..3 and 16 c + 8 + 4 h
+// + 0..3.  The other operand comes out of a row-major LDS tile column by
+// column in exactly these rows, with the transposing LDS read for 16-bit types.
+#pragma once
+
+#include "fm_op.h"
+
+namespace fm {
+
+typedef float acc16 __attribute__((ext_vector_type(16)));
+typedef float acc4 __attribute__((ext_vector_type(4)));
+typedef short short4v __attribute__((ext_vector_type(4)));
+
+template <class T>
+struct FragOf {
+  typedef T type __attribute__((ext_vector_type(8)));
+};
+template <class T>
+using Frag = typename FragOf<T>::type;
+
+__device__ __forceinline__ acc16 mma32(Frag<bf16_t> a, Frag<bf16_t> b, acc16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ acc16 mma32(Frag<f16_t> a, Frag<f16_t> b, acc16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ acc16 mma32(Frag<float> a, Frag<float> b, acc16 c) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
+  return c;
+}
+// 16x16x32 (float32: eight 16x16x4): lane 16 g + n holds row n and the 8
+// contraction indices of quarter g; a result's lane column n, rows 4 g + r.
+__device__ __forceinline__ acc4 mma16(Frag<bf16_t> a, Frag<bf16_t> b, acc4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ acc4 mma16(Frag<f16_t> a, Frag<f16_t> b, acc4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ acc4 mma16(Frag<float> a, Frag<float> b, acc4 c) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+  return c;
+}
+
+// Eight contiguous elements of a row in memory, of which `have` exist.
+template <class T>
+__device__ __forceinline__ Frag<T> load_frag(const T* p, int have) {
+  Frag<T> f;
+  if (have >= 8) {
+    __builtin_memcpy(&f, p, sizeof(f));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = e < have ? p[e] : (T)0.f;
+  }
+  return f;
+}
+
+// Row-major LDS tile: 16 bytes of padding per row spread the rows over the
+// banks.
+template <class T, int DP>
+struct Tile {
+  static constexpr int ld = DP + 16 / (int)sizeof(T);
+  static constexpr int chunks = DP * (int)sizeof(T) / 16;  // 16-byte groups per row
+};
+
+// Fragment of row n (a lane's own), contraction indices 16 s + 8 h ..: one
+// 16-byte read (two for float32).
+template <class T, int DP>
+__device__ __forceinline__ Frag<T> tile_rows(const T* tile, int row, int s, int h) {
+  return *(const Frag<T>*)(tile + row * Tile<T, DP>::ld + 16 * s + 8 * h);
+}
+
+// Fragment of column d0 + l % 32, contraction over rows r0 + 4 h + 0..3 and
+// r0 + 8 + 4 h + 0..3.
+__device__ __forceinline__ short4v lds_read_tr(const void* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) short4v*)p);
+}
+template <class T, int DP>
+__device__ __forceinline__ Frag<T> tile_cols(const T* tile, int r0, int d0, int lane) {
+  constexpr int ld = Tile<T, DP>::ld;
+  Frag<T> f;
+  if constexpr (sizeof(T) == 2) {
+    // a group of 16 lanes reads 4 rows of 16 columns, 8 bytes each, and gets
+    // them transposed: lane i the 4 rows of column i
+    const int g = lane >> 4, i = lane & 15;
+    const T* p = tile + (r0 + 4 * (g >> 1) + (i >> 2)) * ld + d0 + 16 * (g & 1) + 4 * (i & 3);
+    const short4v lo = lds_read_tr(p), hi = lds_read_tr(p + 8 * ld);
+    typedef short short8v __attribute__((ext_vector_type(8)));
+    const short8v both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    f = __builtin_bit_cast(Frag<T>, both);
+  } else {
+    const T* p = tile + (r0 + 4 * (lane >> 5)) * ld + d0 + (lane & 31);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[e] = p[e * ld];
+      f[4 + e] = p[(8 + e) * ld];
+    }
+  }
+  return f;
+}
+
+// Registers 8 c .. 8 c + 7 of a result as the fragment of contraction step c.
+template <class T>
+__device__ __forceinline__ Frag<T> acc_frag(const acc16& a, int c) {
+  typedef float f8 __attribute__((ext_vector_type(8)));
+  f8 v;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = a[8 * c + e];
+  return __builtin_convertvector(v, Frag<T>);
+}
+
+// A tile of ROWS rows on its way from memory to LDS: 16-byte groups held by
+// NT threads.  Rows from `valid` on and columns from `dim` on become zero;
+// nothing past them is read.
+template <class T, int DP, int ROWS, int NT>
+struct TileLoad {
+  static constexpr int ch = Tile<T, DP>::chunks;
+  static constexpr int n = (ROWS * ch + NT - 1) / NT;
+  static constexpr int ve = Vec16<T>::n;
+  Vec16<T> v[n];
+  __device__ __forceinline__ void load(const T* base, int64_t stride, int valid, int dim, int tid) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const int c = i * NT + tid, row = c / ch, col = (c - row * ch) * ve;
+      const int have = row < valid && row < ROWS ? dim - col : 0;
+      v[i] = load16_part(base + row * stride + col, have, (T)0.f);
+    }
+  }
+  __device__ __forceinline__ void store(T* tile, int tid) const {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const int c = i * NT + tid, row = c / ch, col = (c - row * ch) * ve;
+      if (ROWS * ch % NT == 0 || row < ROWS)
+        *(Vec16<T>*)__builtin_assume_aligned(tile + row * Tile<T, DP>::ld + col, 16) = v[i];
+    }
+  }
+};
+
+// Bias by distance, as the accumulators' start: table value / scale, so that
+// one multiplication scales both.  The window covers every distance of a
+// 32x32 tile that reaches inside +-far (kBiasPad more on either side); tiles
+// beyond take an end value.
+template <class T>
+__device__ __forceinline__ float bias_of(const AttnArgs& a, int head, int d) {
+  const int i = d < -a.far ? 0 : d > a.far ? 2 * a.far : d + a.far;
+  const int b = a.map[i];
+  if (b < 0 || b >= a.num_buckets) return 0.f;  // a distance without a bucket
+  const int64_t at = (int64_t)b * a.heads + head;
+  return a.table32 ? ((const float*)a.table)[at] : (float)((const T*)a.table)[at];
+}
+
+__device__ __forceinline__ int clamp_int(int v, int lo, int hi) {
+  return v < lo ? lo : v > hi ? hi : v;
+}
+__device__ __forceinline__ int key_count(const AttnArgs& a, int b) {
+  return a.key_lengths ? clamp_int(a.key_lengths[b], 0, a.k_len) : a.k_len;
+}
+__device__ __forceinline__ int position_of_first(const AttnArgs& a, int b) {
+  const int o = a.query_offset ? a.query_offset[b] : a.query_offset_value;
+  return clamp_int(o, -(1 << 30), 1 << 30);
+}
+
+// Start of a 32x32 tile whose rows are keys and whose columns are queries:
+// dist = first key - first query's position.  Rows 8 (r / 4) + 4 h + r % 4,
+// column n: distance dist + row - n.
+__device__ __forceinline__ acc16 bias_start_keys(const float* bias, int far, int dist, float lo,
+                                                 float hi, int h, int n) {
+  acc16 acc;
+  if (dist + 31 <= -far || dist - 31 >= far) {
+    const float c = dist < 0 ? lo : hi;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[r] = c;
+  } else {
+    const float* p = bias + dist + far + kBiasPad + 4 * h - n;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[r] = p[8 * (r / 4) + r % 4];
+  }
+  return acc;
+}
+// The same with queries as rows and keys as columns: distance dist + n - row.
+__device__ __forceinline__ acc16 bias_start_queries(const float* bias, int far, int dist, float lo,
+                                                    float hi, int h, int n) {
+  acc16 acc;
+  if (dist + 31 <= -far || dist - 31 >= far) {
+    const float c = dist < 0 ? lo : hi;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[r] = c;
+  } else {
+    const float* p = bias + dist + far + kBiasPad - 4 * h + n;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[r] = p[-(8 * (r / 4) + r % 4)];
+  }
+  return acc;
+}
+
+template <class T>
+__device__ __forceinline__ void fill_bias(const AttnArgs& a, int head, float* bias, int tid, int nt) {
+  const float inv = 1.f / a.scale;
+  for (int i = tid; i < bias_window(a.far); i += nt)
+    bias[i] = bias_of<T>(a, head, i - a.far - kBiasPad) * inv;
+}
+
+// Which (entry, head) and block a workgroup takes.  Workgroups go round the 8
+// XCDs one by one; where the heads divide among them, an XCD keeps whole
+// heads (neighbouring ones, which share keys), so that their keys and values
+// stay in its L2.
+struct Place {
+  int unit, block;
+  bool none;
+};
+__device__ __forceinline__ Place place_of(int units, int blocks, int id) {
+  if (units % 8 == 0 || units >= 64) {
+    const int per = (units + 7) / 8;
+    const int x = id & 7, t = id >> 3;
+    const int u = x * per + t / blocks;
+    return {u, t % blocks, u >= units || t / blocks >= per};
+  }
+  return {id / blocks, id % blocks, id / blocks >= units};
+}
+inline unsigned place_grid(int64_t units, int64_t blocks) {
+  return (unsigned)((units % 8 == 0 || units >= 64) ? (units + 7) / 8 * 8 * blocks : units * blocks);
+}
+
+// Stores 4 consecutive elements of a result column's rows.
+template <class T>
+__device__ __forceinline__ void store4(T* p, float a, float b, float c, float d, int have) {
+  typedef T t4 __attribute__((ext_vector_type(4)));
+  typedef float f4 __attribute__((ext_vector_type(4)));
+  const f4 v = {a, b, c, d};
+  const t4 r = __builtin_convertvector(v, t4);
+  if (have >= 4) {
+    __builtin_memcpy(p, &r, sizeof(r));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+      if (e < have) p[e] = r[e];
+  }
+}
+
+}  // namespace fm

@@ -1,0 +1,447 @@
+// Attention forward: the kernel for many queries (a wave's 32 queries in its
+// registers, key tiles in LDS shared by 4 waves), the one for single tokens
+// (the waves divide the keys), and the join of key ranges.
+#pragma once
+
+#include "fm_attn.h"
+
+namespace fm {
+
+constexpr int kAttnThreads = 256;
+// Keys per LDS tile: two 32-key steps for 16-bit types, one for float32,
+// whose tile of 64 x 128 would leave room for one workgroup per CU.
+template <class T>
+constexpr int attn_keys() { return sizeof(T) == 2 ? 64 : 32; }
+
+template <class T, int DP>
+constexpr size_t attn_forward_lds(int far) {
+  return 4 * attn_keys<T>() * Tile<T, DP>::ld * sizeof(T) + bias_window(far) * sizeof(float);
+}
+
+// The transposed scores s' = K q' have queries as columns, so that a lane
+// keeps one query's running maximum and sum, and the probabilities are the
+// next product's right operand as they stand: o' = V' p'.
+template <class T, int DP, bool SPLIT>
+__global__ __launch_bounds__(kAttnThreads) void attn_forward_kernel(const AttnArgs a) {
+  constexpr int BK = attn_keys<T>(), NS = BK / 32, LD = Tile<T, DP>::ld, KS = DP / 16, DT = DP / 32;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  T* kt = (T*)smem;              // [2][BK][LD]
+  T* vt = kt + 2 * BK * LD;      // [2][BK][LD]
+  float* bias = (float*)(vt + 2 * BK * LD);
+
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 31, h = lane >> 5;
+  const int blocks = (a.q_len + kAttnQueries - 1) / kAttnQueries;
+  const Place at = place_of(a.batch * a.heads, blocks, blockIdx.x);
+  if (at.none) return;
+  const int b = at.unit / a.heads, head = at.unit % a.heads, kvh = head / (a.heads / a.kv_heads);
+  // the last queries see the most keys when causal: they start first
+  const int qb = a.causal ? blocks - 1 - at.block : at.block;
+  const int q0 = qb * kAttnQueries + wave * 32;
+  const int i = q0 + n;
+  const int len = key_count(a, b), first = position_of_first(a, b);
+  const int q_end = min((qb + 1) * kAttnQueries, a.q_len);  // of the workgroup
+  int k_beg = 0, k_end = a.causal ? clamp_int(first + q_end, 0, len) : len;
+  if constexpr (SPLIT) {
+    const int per = ((len + a.splits - 1) / a.splits + BK - 1) / BK * BK;
+    k_beg = min((int)blockIdx.y * per, k_end);
+    k_end = min(k_beg + per, k_end);
+  }
+
+  const T* kp = (const T*)a.k + b * a.ks[0] + kvh * a.ks[1];
+  const T* vp = (const T*)a.v + b * a.vs[0] + kvh * a.vs[1];
+  TileLoad<T, DP, BK, kAttnThreads> kl, vl;
+  kl.load(kp + k_beg * a.ks[2], a.ks[2], k_end - k_beg, a.dim, tid);
+  vl.load(vp + k_beg * a.vs[2], a.vs[2], k_end - k_beg, a.dim, tid);
+  Frag<T> qf[KS];
+  const T* qp = (const T*)a.q + b * a.qs[0] + head * a.qs[1] + i * a.qs[2];
+#pragma unroll
+  for (int s = 0; s < KS; ++s)
+    qf[s] = load_frag(qp + 16 * s + 8 * h, i < a.q_len ? a.dim - 16 * s - 8 * h : 0);
+  fill_bias<T>(a, head, bias, tid, kAttnThreads);
+  const float lo = bias_of<T>(a, head, -a.far) / a.scale, hi = bias_of<T>(a, head, a.far) / a.scale;
+  kl.store(kt, tid);
+  vl.store(vt, tid);
+  __syncthreads();
+
+  acc16 o[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) o[d][r] = 0.f;
+  float m = -INFINITY, l = 0.f;
+  const float c = a.scale * kLog2e;
+  const float grow = 8.f / c;  // a maximum raised by less than 2^8 leaves m as it is
+  const int mine = a.causal ? min(len, first + i + 1) : len;   // keys this lane's query sees
+  const int least = a.causal ? min(len, first + q0 + 1) : len; // of the wave's first query
+  const int wave_end = a.causal ? min(k_end, first + q0 + 32) : k_end;
+  const bool idle = q0 >= a.q_len;
+
+  int buf = 0;
+  for (int j0 = k_beg; j0 < k_end; j0 += BK, buf ^= 1) {
+    const bool more = j0 + BK < k_end;
+    if (more) {
+      kl.load(kp + (int64_t)(j0 + BK) * a.ks[2], a.ks[2], k_end - j0 - BK, a.dim, tid);
+      vl.load(vp + (int64_t)(j0 + BK) * a.vs[2], a.vs[2], k_end - j0 - BK, a.dim, tid);
+    }
+    if (!idle && j0 < wave_end) {
+      const T* ktb = kt + buf * BK * LD;
+      const T* vtb = vt + buf * BK * LD;
+      acc16 s[NS];
+#pragma unroll
+      for (int u = 0; u < NS; ++u) {
+        s[u] = bias_start_keys(bias, a.far, j0 + 32 * u - first - q0, lo, hi, h, n);
+#pragma unroll
+        for (int x = 0; x < KS; ++x) s[u] = mma32(tile_rows<T, DP>(ktb, 32 * u + n, x, h), qf[x], s[u]);
+        if (j0 + 32 * u + 32 > least) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            s[u][r] = j0 + 32 * u + 8 * (r / 4) + 4 * h + r % 4 < mine ? s[u][r] : -INFINITY;
+        }
+      }
+      float mx = s[0][0];
+#pragma unroll
+      for (int u = 0; u < NS; ++u)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[u][r]);
+      mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+      const bool raise = mx > m + grow || (m == -INFINITY && mx > m);
+      if (__any(raise)) {
+        const float m2 = raise ? mx : m;
+        // nothing seen yet: o and l are 0
+        const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - m2) * c);
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) o[d][r] *= f;
+        l *= f;
+        m = m2;
+      }
+      const float mc = m == -INFINITY ? 0.f : m * c;
+      float sum = 0.f;
+#pragma unroll
+      for (int u = 0; u < NS; ++u)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          s[u][r] = __builtin_amdgcn_exp2f(fmaf(s[u][r], c, -mc));
+          sum += s[u][r];
+        }
+      l += sum;
+#pragma unroll
+      for (int u = 0; u < NS; ++u)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          // rounded to the element type for the product: half a step of each
+          // probability, as the result's own rounding; the sum l is not
+          const Frag<T> p = acc_frag<T>(s[u], x);
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+            o[d] = mma32(tile_cols<T, DP>(vtb, 32 * u + 16 * x, 32 * d, lane), p, o[d]);
+        }
+    }
+    if (more) {
+      kl.store(kt + (buf ^ 1) * BK * LD, tid);
+      vl.store(vt + (buf ^ 1) * BK * LD, tid);
+    }
+    __syncthreads();
+  }
+
+  l += __shfl_xor(l, 32, 64);
+  if (i >= a.q_len) return;
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  const int64_t row = (int64_t)(b * a.heads + head) * a.q_len + i;
+  const float lse = l != l ? l : m == -INFINITY ? -INFINITY : fmaf(m, a.scale, logf(l));
+  if constexpr (SPLIT) {
+    const int64_t rows = (int64_t)a.batch * a.heads * a.q_len;
+    if (h == 0) a.part_lse[blockIdx.y * rows + row] = lse;
+    float* po = a.part_o + (blockIdx.y * rows + row) * a.dim;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int at_d = 32 * d + 8 * y + 4 * h;
+        if (at_d < a.dim)
+          store4(po + at_d, o[d][4 * y] * inv, o[d][4 * y + 1] * inv, o[d][4 * y + 2] * inv,
+                 o[d][4 * y + 3] * inv, a.dim - at_d);
+      }
+  } else {
+    if (a.lse && h == 0) a.lse[row] = lse;
+    const int64_t off = b * a.os[0] + head * a.os[1] + i * a.os[2];
+    T* op = (T*)a.o + off;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int at_d = 32 * d + 8 * y + 4 * h;
+        if (at_d < a.dim) {
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = o[d][4 * y + e] * inv;
+          store4(op + at_d, v[0], v[1], v[2], v[3], a.dim - at_d);
+          if (a.o_rest)
+            store4((T*)a.o_rest + off + at_d, v[0] - (float)(T)v[0], v[1] - (float)(T)v[1],
+                   v[2] - (float)(T)v[2], v[3] - (float)(T)v[3], a.dim - at_d);
+        }
+      }
+  }
+}
+
+// Few query rows per key head (rows = heads of the group x queries, at most
+// 16): one 16-column fragment holds them all; the 4 waves take 32 keys each
+// in turn, straight from memory, and join at the end.  Memory bound: keys are
+// the left operand as they lie in memory, values pass through a wave's own
+// LDS tile to be read by columns.
+constexpr int kTokenKeys = 32;
+template <class T, int DP>
+constexpr size_t attn_token_lds() {
+  constexpr size_t tiles = 4 * kTokenKeys * Tile<T, DP>::ld * sizeof(T);
+  constexpr size_t join = 4 * 16 * (DP + 2) * sizeof(float);
+  return tiles > join ? tiles : join;
+}
+
+template <class T, int DP, bool SPLIT>
+__global__ __launch_bounds__(kAttnThreads) void attn_token_kernel(const AttnArgs a) {
+  constexpr int LD = Tile<T, DP>::ld, KS = DP / 32, DT = DP / 16;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 15, g = lane >> 4;
+  T* vt = (T*)smem + wave * kTokenKeys * LD;
+  const int group = a.heads / a.kv_heads, rows = group * a.q_len;
+  const int b = blockIdx.x / a.kv_heads, kvh = blockIdx.x % a.kv_heads;
+  const int head = kvh * group + n / a.q_len, i = n % a.q_len;
+  const bool real = n < rows;
+  const int len = key_count(a, b), first = position_of_first(a, b);
+  int k_beg = 0, k_end = a.causal ? clamp_int(first + a.q_len, 0, len) : len;
+  if constexpr (SPLIT) {
+    const int per = ((k_end + a.splits - 1) / a.splits + 127) / 128 * 128;
+    k_beg = min((int)blockIdx.y * per, k_end);
+    k_end = min(k_beg + per, k_end);
+  }
+  const T* kp = (const T*)a.k + b * a.ks[0] + kvh * a.ks[1];
+  const T* vp = (const T*)a.v + b * a.vs[0] + kvh * a.vs[1];
+
+  Frag<T> qf[KS];
+  const T* qp = (const T*)a.q + b * a.qs[0] + (real ? head : 0) * a.qs[1] + i * a.qs[2];
+#pragma unroll
+  for (int s = 0; s < KS; ++s) qf[s] = load_frag(qp + 32 * s + 8 * g, real ? a.dim - 32 * s - 8 * g : 0);
+  const float lo = real ? bias_of<T>(a, head, -a.far) / a.scale : 0.f;
+  const float hi = real ? bias_of<T>(a, head, a.far) / a.scale : 0.f;
+  const int pos = first + i;
+  const int mine = real ? (a.causal ? min(len, pos + 1) : len) : 0;
+  const int least = a.causal ? min(len, first + 1) : len;
+  const float c = a.scale * kLog2e;
+
+  acc4 o[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d) o[d] = acc4{0.f, 0.f, 0.f, 0.f};
+  float m = -INFINITY, l = 0.f;
+
+  Frag<T> kf[2][KS];
+  TileLoad<T, DP, kTokenKeys, 64> vl;
+  const auto fetch = [&](int j) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int key = j + 16 * u + n;
+      const T* p = kp + (int64_t)key * a.ks[2] + 8 * g;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) kf[u][s] = load_frag(p + 32 * s, key < k_end ? a.dim - 32 * s - 8 * g : 0);
+    }
+    vl.load(vp + (int64_t)j * a.vs[2], a.vs[2], k_end - j, a.dim, lane);
+  };
+  int j0 = k_beg + wave * kTokenKeys;
+  if (j0 < k_end) fetch(j0);
+  for (; j0 < k_end; j0 += 4 * kTokenKeys) {
+    // the wave's own tile: its reads of the last round are done
+    vl.store(vt, lane);
+    acc4 s[2];
+    const int dist = j0 - first;  // of key j0 to the first query
+    const bool left = dist + kTokenKeys - 1 <= -a.far, right = dist - (a.q_len - 1) >= a.far;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (left || right) {
+        const float v = left ? lo : hi;
+        s[u] = acc4{v, v, v, v};
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          s[u][r] = real ? bias_of<T>(a, head, j0 + 16 * u + 4 * g + r - pos) / a.scale : 0.f;
+      }
+#pragma unroll
+      for (int x = 0; x < KS; ++x) s[u] = mma16(kf[u][x], qf[x], s[u]);
+    }
+    const int j = j0;
+    if (j0 + 4 * kTokenKeys < k_end) fetch(j0 + 4 * kTokenKeys);
+    if (j + kTokenKeys > least || rows < 16) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[u][r] = j + 16 * u + 4 * g + r < mine ? s[u][r] : -INFINITY;
+    }
+    float mx = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                     fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+    mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+    if (__any(mx > m)) {
+      const float m2 = fmaxf(m, mx);
+      const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - m2) * c);
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[d] *= f;
+      l *= f;
+      m = m2;
+    }
+    const float mc = m == -INFINITY ? 0.f : m * c;
+    Frag<T> p;
+    {
+      typedef float f8 __attribute__((ext_vector_type(8)));
+      f8 e;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          e[4 * u + r] = __builtin_amdgcn_exp2f(fmaf(s[u][r], c, -mc));
+          l += e[4 * u + r];
+        }
+      p = __builtin_convertvector(e, Frag<T>);
+    }
+    // contraction over rows 4 g + 0..3 and 16 + 4 g + 0..3 of the tile
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+      Frag<T> vf;
+      if constexpr (sizeof(T) == 2) {
+        const T* q = vt + (4 * g + (n >> 2)) * LD + 16 * d + 4 * (n & 3);
+        const short4v x = lds_read_tr(q), y = lds_read_tr(q + 16 * LD);
+        typedef short short8v __attribute__((ext_vector_type(8)));
+        const short8v both = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+        vf = __builtin_bit_cast(Frag<T>, both);
+      } else {
+        const T* q = vt + 4 * g * LD + 16 * d + n;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          vf[e] = q[e * LD];
+          vf[4 + e] = q[(16 + e) * LD];
+        }
+      }
+      o[d] = mma16(vf, p, o[d]);
+    }
+  }
+  l += __shfl_xor(l, 16, 64);
+  l += __shfl_xor(l, 32, 64);
+
+  // the waves' shares: o[row][d], m and l per row
+  __syncthreads();
+  float* join = (float*)smem;
+  constexpr int JL = DP + 2;
+  float* jw = join + (wave * 16 + n) * JL;
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) jw[16 * d + 4 * g + r] = o[d][r];
+  if (g == 0) {
+    jw[DP] = m;
+    jw[DP + 1] = l;
+  }
+  __syncthreads();
+  for (int t = tid; t < rows * DP; t += kAttnThreads) {
+    const int r = t / DP, d = t - r * DP;
+    if (d >= a.dim) continue;
+    float mm = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) mm = fmaxf(mm, join[(w * 16 + r) * JL + DP]);
+    float sum = 0.f, val = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float* p = join + (w * 16 + r) * JL;
+      const float f = p[DP] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((p[DP] - mm) * c);
+      // a NaN sum has to survive a maximum that never was one
+      sum += p[DP + 1] != p[DP + 1] ? p[DP + 1] : f * p[DP + 1];
+      val = fmaf(f, p[d], val);
+    }
+    const float out = sum == 0.f ? 0.f : val / sum;
+    const float lse = sum != sum ? sum : mm == -INFINITY ? -INFINITY : fmaf(mm, a.scale, logf(sum));
+    const int hd = kvh * group + r / a.q_len, qi = r % a.q_len;
+    const int64_t row = (int64_t)(b * a.heads + hd) * a.q_len + qi;
+    if constexpr (SPLIT) {
+      const int64_t all = (int64_t)a.batch * a.heads * a.q_len;
+      a.part_o[(blockIdx.y * all + row) * a.dim + d] = out;
+      if (d == 0) a.part_lse[blockIdx.y * all + row] = lse;
+    } else {
+      const int64_t off = b * a.os[0] + hd * a.os[1] + qi * a.os[2] + d;
+      ((T*)a.o)[off] = (T)out;
+      if (a.o_rest) ((T*)a.o_rest)[off] = (T)(out - (float)(T)out);
+      if (a.lse && d == 0) a.lse[row] = lse;
+    }
+  }
+}
+
+// Joins the key ranges of a row: one wave per row.
+template <class T>
+__global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(const AttnArgs a) {
+  const int64_t rows = (int64_t)a.batch * a.heads * a.q_len;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (row >= rows) return;
+  float mm = -INFINITY;
+  bool bad = false;
+  for (int s = lane; s < a.splits; s += 64) {
+    const float v = a.part_lse[s * rows + row];
+    mm = fmaxf(mm, v);
+    bad |= v != v;
+  }
+  mm = lanes_max<64>(mm);
+  if (__any(bad)) mm = NAN;
+  const float ms = mm == -INFINITY ? 0.f : mm;
+  float sum = 0.f, v0 = 0.f, v1 = 0.f;
+  for (int s = 0; s < a.splits; ++s) {
+    const float f = __builtin_amdgcn_exp2f((a.part_lse[s * rows + row] - ms) * kLog2e);
+    const float* p = a.part_o + (s * rows + row) * a.dim;
+    sum += f;
+    if (lane < a.dim) v0 = fmaf(f, p[lane], v0);
+    if (lane + 64 < a.dim) v1 = fmaf(f, p[lane + 64], v1);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int i = (int)(row % a.q_len);
+  const int64_t bh = row / a.q_len;
+  const int64_t off = bh / a.heads * a.os[0] + bh % a.heads * a.os[1] + i * a.os[2];
+  v0 *= inv;
+  v1 *= inv;
+  if (lane < a.dim) {
+    ((T*)a.o)[off + lane] = (T)v0;
+    if (a.o_rest) ((T*)a.o_rest)[off + lane] = (T)(v0 - (float)(T)v0);
+  }
+  if (lane + 64 < a.dim) {
+    ((T*)a.o)[off + lane + 64] = (T)v1;
+    if (a.o_rest) ((T*)a.o_rest)[off + lane + 64] = (T)(v1 - (float)(T)v1);
+  }
+  if (a.lse && lane == 0) a.lse[row] = mm == -INFINITY ? mm : ms + logf(sum);
+}
+
+template <class T, int DP>
+int attn_forward_dim(const AttnArgs& a, void* stream) {
+  if (attn_token_kernel(a)) {
+    static const int opted = lds_opt_in(attn_token_kernel<T, DP, false>, attn_token_lds<T, DP>()) |
+                             lds_opt_in(attn_token_kernel<T, DP, true>, attn_token_lds<T, DP>());
+    if (opted != FM_OK) return set_error(FM_E_HIP, "attention: LDS size refused");
+    return launch("attention of single tokens",
+                  a.splits > 1 ? attn_token_kernel<T, DP, true> : attn_token_kernel<T, DP, false>,
+                  dim3((unsigned)(a.batch * a.kv_heads), (unsigned)a.splits), dim3(kAttnThreads),
+                  attn_token_lds<T, DP>(), stream, a);
+  }
+  static const int opted =
+      lds_opt_in(attn_forward_kernel<T, DP, false>, attn_forward_lds<T, DP>(kAttnMaxFar)) |
+      lds_opt_in(attn_forward_kernel<T, DP, true>, attn_forward_lds<T, DP>(kAttnMaxFar));
+  if (opted != FM_OK) return set_error(FM_E_HIP, "attention: LDS size refused");
+  return launch("attention",
+                a.splits > 1 ? attn_forward_kernel<T, DP, true> : attn_forward_kernel<T, DP, false>,
+                dim3(place_grid((int64_t)a.batch * a.heads, attn_query_blocks(a)), (unsigned)a.splits),
+                dim3(kAttnThreads), attn_forward_lds<T, DP>(a.far), stream, a);
+}
+
+template <class T>
+int attn_forward_t(const AttnArgs& a, void* stream) {
+  const int st = a.dim <= 64   ? attn_forward_dim<T, 64>(a, stream)
+                 : a.dim <= 96 ? attn_forward_dim<T, 96>(a, stream)
+                               : attn_forward_dim<T, 128>(a, stream);
+  if (st != FM_OK || a.splits == 1) return st;
+  return launch("attention (join)", attn_join_kernel<T>, dim3((unsigned)((attn_rows(a) + 3) / 4)),
+                dim3(kAttnThreads), 0, stream, a);
+}
+
+}  // namespace fm

@@ -1,0 +1,422 @@
+// Layer norm over the last axis, forward and backward.
+//
+//   u = (x - mean(x)) * rstd,  rstd = 1 / sqrt(var(x) + eps),  y = u * w + b
+//   g = dy * w,  dx = rstd * (g - mean(g) - u * mean(g u))
+//   dw = sum over rows of dy * u,  db = sum over rows of dy
+//
+// The variance is the mean square of the centred row (two sweeps over the
+// row's registers, no difference of large sums); all sums are in float32.
+//
+// One row is held in registers by LPR lanes, VPL groups of 16 bytes each, so
+// x (and dy) are read from memory once per pass; a wave takes 64 / LPR rows
+// where LPR < 64.  Memory bound: the backward adds dw and db up in registers
+// over a workgroup's rows, writes one partial row per workgroup and a second
+// launch adds the partials in a fixed order.
+#pragma once
+
+#include "fm_op.h"
+
+namespace fm {
+
+// Sum over the LPR lanes that hold a row: within a wave by lane exchange, over
+// several waves through LDS (`red`, one slot set per call site).
+template <int LPR>
+__device__ __forceinline__ float2 row_sum2(float2 v, float2* red) {
+  constexpr int L = LPR < 64 ? LPR : 64;
+#pragma unroll
+  for (int m = L / 2; m >= 1; m >>= 1) {
+    v.x += __shfl_xor(v.x, m, 64);
+    v.y += __shfl_xor(v.y, m, 64);
+  }
+  if constexpr (LPR > 64) {
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) red[wave] = v;
+    __syncthreads();
+    v = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < LPR / 64; ++w) {
+      v.x += red[w].x;
+      v.y += red[w].y;
+    }
+    __syncthreads();
+  }
+  return v;
+}
+
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v, float2* red) {
+  return row_sum2<LPR>(make_float2(v, 0.f), red).x;
+}
+
+template <class T, class W, int LPR, int VPL>
+__global__ __launch_bounds__(kNormThreads) void norm_forward_kernel(
+    const T* __restrict__ x, int64_t x_stride, const W* __restrict__ w, const W* __restrict__ b,
+    T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int width,
+    float eps) {
+  constexpr int VE = Vec16<T>::n;
+  constexpr int NT = kNormThreads;
+  __shared__ float2 red[LPR > 64 ? LPR / 64 : 1];
+  const int lane = threadIdx.x % LPR;
+  const int64_t row = (int64_t)blockIdx.x * (NT / LPR) + threadIdx.x / LPR;
+  // rows past the end (whole lane groups; never in kernels with barriers,
+  // where a workgroup is one row) run on an empty width
+  const int have_all = row < rows ? width : 0;
+  const T* xr = x + row * x_stride;
+  Vec16<T> raw[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int c = (i * LPR + lane) * VE;
+    raw[i] = load16_part(xr + c, have_all - c, (T)0.f);
+  }
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+#pragma unroll
+    for (int e = 0; e < VE; ++e) s += (float)raw[i].v[e];
+  // divided, not multiplied by 1 / n: a constant row has exactly that mean
+  const float n = (float)width;
+  const float mu = row_sum<LPR>(s, red) / n;
+  float q = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int c = (i * LPR + lane) * VE;
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const float d = c + e < width ? (float)raw[i].v[e] - mu : 0.f;
+      q = fmaf(d, d, q);
+    }
+  }
+  const float rs = 1.f / sqrtf(row_sum<LPR>(q, red) / n + eps);
+  if (row >= rows) return;
+  if (lane == 0) {
+    if (mean) mean[row] = mu;
+    if (rstd) rstd[row] = rs;
+  }
+  T* yr = y + row * width;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int c = (i * LPR + lane) * VE;
+    const int have = width - c;
+    if (have <= 0) break;
+    Vec16<T> out;
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const int ce = e < have ? c + e : c;
+      float u = ((float)raw[i].v[e] - mu) * rs;
+      if (w) u = fmaf(u, (float)w[ce], b ? (float)b[ce] : 0.f);
+      out.v[e] = (T)u;
+    }
+    store16_part(yr + c, out, have);
+  }
+}
+
+// grid-stride over rows; PARTS: also add up dw and db (part: one row of
+// [dw | db], 2 * width floats, per workgroup).
+template <class T, class W, int LPR, int VPL, bool PARTS>
+__global__ __launch_bounds__(kNormThreads) void norm_backward_kernel(
+    const T* __restrict__ dy, int64_t dy_stride, const T* __restrict__ x, int64_t x_stride,
+    const W* __restrict__ w, const float* __restrict__ mean, const float* __restrict__ rstd,
+    T* __restrict__ dx, float* __restrict__ part, int64_t rows, int width) {
+  constexpr int VE = Vec16<T>::n;
+  constexpr int NT = kNormThreads;
+  constexpr int RPB = NT / LPR;
+  __shared__ float2 red[LPR > 64 ? LPR / 64 : 1];
+  const int lane = threadIdx.x % LPR;
+  const int sub = threadIdx.x / LPR;
+  const float inv_n = 1.f / (float)width;
+  float aw[PARTS ? VPL * VE : 1], ab[PARTS ? VPL * VE : 1];
+  if constexpr (PARTS) {
+#pragma unroll
+    for (int i = 0; i < VPL * VE; ++i) aw[i] = ab[i] = 0.f;
+  }
+  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < rows; r0 += (int64_t)gridDim.x * RPB) {
+    const int64_t row = r0 + sub;
+    const int have_all = row < rows ? width : 0;
+    const T* xr = x + row * x_stride;
+    const T* gr = dy + row * dy_stride;
+    Vec16<T> xv[VPL], gv[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int c = (i * LPR + lane) * VE;
+      xv[i] = load16_part(xr + c, have_all - c, (T)0.f);
+      gv[i] = load16_part(gr + c, have_all - c, (T)0.f);
+    }
+    const float mu = row < rows ? mean[row] : 0.f;
+    const float rs = row < rows ? rstd[row] : 0.f;
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int c = (i * LPR + lane) * VE;
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        const bool in = c + e < have_all;
+        const float d = (float)gv[i].v[e];
+        const float u = in ? ((float)xv[i].v[e] - mu) * rs : 0.f;
+        const float g = (w && in) ? d * (float)w[c + e] : d;
+        s.x += g;
+        s.y = fmaf(g, u, s.y);
+        if constexpr (PARTS) {
+          aw[i * VE + e] = fmaf(d, u, aw[i * VE + e]);
+          ab[i * VE + e] += d;
+        }
+      }
+    }
+    s = row_sum2<LPR>(s, red);
+    const float m1 = s.x * inv_n, m2 = s.y * inv_n;
+    T* dr = dx + row * width;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int c = (i * LPR + lane) * VE;
+      const int have = have_all - c;
+      if (have > 0) {
+        Vec16<T> out;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          const int ce = e < have ? c + e : c;
+          const float d = (float)gv[i].v[e];
+          const float u = ((float)xv[i].v[e] - mu) * rs;
+          const float g = w ? d * (float)w[ce] : d;
+          out.v[e] = (T)(rs * (g - m1 - u * m2));
+        }
+        store16_part(dr + c, out, have);
+      }
+    }
+  }
+  if constexpr (PARTS) {
+    // lanes of the same columns: RPB groups of LPR lanes
+    if constexpr (RPB > 1) {
+      __shared__ float col[RPB > 1 ? NT * VE : 1];
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          __syncthreads();
+#pragma unroll
+          for (int e = 0; e < VE; ++e)
+            col[threadIdx.x * VE + e] = k ? ab[i * VE + e] : aw[i * VE + e];
+          __syncthreads();
+          for (int t = threadIdx.x; t < LPR * VE; t += NT) {
+            float s = 0.f;
+#pragma unroll
+            for (int r = 0; r < RPB; ++r) s += col[r * LPR * VE + t];
+            const int c = i * LPR * VE + t;
+            if (c < width) part[((int64_t)blockIdx.x * 2 + k) * width + c] = s;
+          }
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          const int c = (i * LPR + lane) * VE + e;
+          if (c < width) {
+            part[((int64_t)blockIdx.x * 2 + 0) * width + c] = aw[i * VE + e];
+            part[((int64_t)blockIdx.x * 2 + 1) * width + c] = ab[i * VE + e];
+          }
+        }
+    }
+  }
+}
+
+// Rows too wide for the registers: one workgroup of 1024 lanes per row, the
+// row read once from memory and twice more from the cache.
+constexpr int kNormWide = 1024;
+
+template <class T, class W>
+__global__ __launch_bounds__(kNormWide) void norm_forward_wide_kernel(
+    const T* __restrict__ x, int64_t x_stride, const W* __restrict__ w, const W* __restrict__ b,
+    T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int width,
+    float eps) {
+  constexpr int VE = Vec16<T>::n;
+  __shared__ float2 red[kNormWide / 64];
+  const int64_t row = blockIdx.x;
+  const T* xr = x + row * x_stride;
+  T* yr = y + row * width;
+  const float n = (float)width;
+  float s = 0.f;
+#pragma unroll 1
+  for (int c = threadIdx.x * VE; c < width; c += kNormWide * VE) {
+    const Vec16<T> v = load16_part(xr + c, width - c, (T)0.f);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) s += (float)v.v[e];
+  }
+  const float mu = row_sum<kNormWide>(s, red) / n;
+  float q = 0.f;
+#pragma unroll 1
+  for (int c = threadIdx.x * VE; c < width; c += kNormWide * VE) {
+    const Vec16<T> v = load16_part(xr + c, width - c, (T)0.f);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const float d = c + e < width ? (float)v.v[e] - mu : 0.f;
+      q = fmaf(d, d, q);
+    }
+  }
+  const float rs = 1.f / sqrtf(row_sum<kNormWide>(q, red) / n + eps);
+  if (threadIdx.x == 0) {
+    if (mean) mean[row] = mu;
+    if (rstd) rstd[row] = rs;
+  }
+#pragma unroll 1
+  for (int c = threadIdx.x * VE; c < width; c += kNormWide * VE) {
+    Vec16<T> v = load16_part(xr + c, width - c, (T)0.f);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const int ce = c + e < width ? c + e : c;
+      float u = ((float)v.v[e] - mu) * rs;
+      if (w) u = fmaf(u, (float)w[ce], b ? (float)b[ce] : 0.f);
+      v.v[e] = (T)u;
+    }
+    store16_part(yr + c, v, width - c);
+  }
+}
+
+template <class T, class W>
+__global__ __launch_bounds__(kNormWide) void norm_backward_wide_kernel(
+    const T* __restrict__ dy, int64_t dy_stride, const T* __restrict__ x, int64_t x_stride,
+    const W* __restrict__ w, const float* __restrict__ mean, const float* __restrict__ rstd,
+    T* __restrict__ dx, int64_t rows, int width) {
+  constexpr int VE = Vec16<T>::n;
+  __shared__ float2 red[kNormWide / 64];
+  const int64_t row = blockIdx.x;
+  const T* xr = x + row * x_stride;
+  const T* gr = dy + row * dy_stride;
+  T* dr = dx + row * width;
+  const float inv_n = 1.f / (float)width, mu = mean[row], rs = rstd[row];
+  float2 s = make_float2(0.f, 0.f);
+#pragma unroll 1
+  for (int c = threadIdx.x * VE; c < width; c += kNormWide * VE) {
+    const Vec16<T> xv = load16_part(xr + c, width - c, (T)0.f);
+    const Vec16<T> gv = load16_part(gr + c, width - c, (T)0.f);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      if (c + e < width) {
+        const float g = (float)gv.v[e] * (w ? (float)w[c + e] : 1.f);
+        s.x += g;
+        s.y = fmaf(g, ((float)xv.v[e] - mu) * rs, s.y);
+      }
+    }
+  }
+  s = row_sum2<kNormWide>(s, red);
+  const float m1 = s.x * inv_n, m2 = s.y * inv_n;
+#pragma unroll 1
+  for (int c = threadIdx.x * VE; c < width; c += kNormWide * VE) {
+    const Vec16<T> xv = load16_part(xr + c, width - c, (T)0.f);
+    Vec16<T> gv = load16_part(gr + c, width - c, (T)0.f);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const int ce = c + e < width ? c + e : c;
+      const float g = (float)gv.v[e] * (w ? (float)w[ce] : 1.f);
+      gv.v[e] = (T)(rs * (g - m1 - ((float)xv.v[e] - mu) * rs * m2));
+    }
+    store16_part(dr + c, gv, width - c);
+  }
+}
+
+// Column sums of dy * u and dy for widths whose accumulators do not fit the
+// registers beside the row: one thread per column, a block of rows per
+// workgroup, the same partial layout.
+template <class T>
+__global__ __launch_bounds__(kNormThreads) void norm_columns_kernel(
+    const T* __restrict__ dy, int64_t dy_stride, const T* __restrict__ x, int64_t x_stride,
+    const float* __restrict__ mean, const float* __restrict__ rstd, float* __restrict__ part,
+    int64_t rows, int width) {
+  const int c = blockIdx.x * kNormThreads + threadIdx.x;
+  if (c >= width) return;
+  float aw = 0.f, ab = 0.f;
+  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+    const float d = (float)dy[r * dy_stride + c];
+    aw = fmaf(d, ((float)x[r * x_stride + c] - mean[r]) * rstd[r], aw);
+    ab += d;
+  }
+  part[((int64_t)blockIdx.y * 2 + 0) * width + c] = aw;
+  part[((int64_t)blockIdx.y * 2 + 1) * width + c] = ab;
+}
+
+// Adds the workgroups' partial rows: 64 columns of [dw | db] per workgroup,
+// 16 lanes sets of every 16th partial, then over the sets.
+template <class W>
+__global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* __restrict__ part,
+                                                           int parts, W* __restrict__ dw,
+                                                           W* __restrict__ db, int width) {
+  __shared__ float red[16][64];
+  const int lane = threadIdx.x & 63, set = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  const bool in = c < 2 * (int64_t)width;
+  float s = 0.f;
+  if (in)
+    for (int p = set; p < parts; p += 16) s += part[(int64_t)p * 2 * width + c];
+  red[set][lane] = s;
+  __syncthreads();
+  if (set == 0 && in) {
+    float t = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) t += red[k][lane];
+    if (c < width)
+      dw[c] = (W)t;
+    else if (db)
+      db[c - width] = (W)t;
+  }
+}
+
+template <class T, class W>
+int norm_forward_t(const NormForward& a) {
+  const NormShape s = norm_shape(a.width, Vec16<T>::n);
+#define FM_NORM_FWD(L, V)                                                                  \
+  if (s.lpr == L && s.vpl == V) {                                                          \
+    constexpr int nt = kNormThreads;                                \
+    const int64_t blocks = (a.rows + nt / L - 1) / (nt / L);                               \
+    return launch("layer norm forward", norm_forward_kernel<T, W, L, V>,                   \
+                  dim3((unsigned)blocks), dim3(nt), 0, a.stream, (const T*)a.x, a.x_stride, \
+                  (const W*)a.weight, (const W*)a.bias, (T*)a.y, a.mean, a.rstd, a.rows,   \
+                  a.width, a.eps);                                                         \
+  }
+  FM_NORM_SHAPES(FM_NORM_FWD)
+#undef FM_NORM_FWD
+  return launch("layer norm forward", norm_forward_wide_kernel<T, W>, dim3((unsigned)a.rows),
+                dim3(kNormWide), 0, a.stream, (const T*)a.x, a.x_stride, (const W*)a.weight,
+                (const W*)a.bias, (T*)a.y, a.mean, a.rstd, a.rows, a.width, a.eps);
+}
+
+template <class T, class W>
+int norm_backward_t(const NormBackward& a) {
+  constexpr int VE = Vec16<T>::n;
+  const NormShape s = norm_shape(a.width, VE);
+  const int parts = norm_parts(a.rows, a.width, VE);
+  const bool want = a.dw != nullptr;
+  float* part = (float*)a.workspace;
+  if (a.rows > 0) {
+    int st = FM_OK;
+    if (s.vpl == 0)
+      st = launch("layer norm backward", norm_backward_wide_kernel<T, W>, dim3((unsigned)a.rows),
+                  dim3(kNormWide), 0, a.stream, (const T*)a.dy, a.dy_stride, (const T*)a.x,
+                  a.x_stride, (const W*)a.weight, a.mean, a.rstd, (T*)a.dx, a.rows, a.width);
+#define FM_NORM_BWD(L, V)                                                                       \
+  if (s.lpr == L && s.vpl == V) {                                                               \
+    constexpr int nt = kNormThreads;                                     \
+    constexpr bool in = V * VE <= 32;                                               \
+    const int64_t need = (a.rows + nt / L - 1) / (nt / L);                                      \
+    const bool sums = in && want;                                                               \
+    st = launch("layer norm backward",                                                          \
+                sums ? norm_backward_kernel<T, W, L, V, in> : norm_backward_kernel<T, W, L, V, false>, \
+                dim3(sums ? (unsigned)parts : (unsigned)(need < 65536 ? need : 65536)), dim3(nt), 0, \
+                a.stream, (const T*)a.dy, a.dy_stride, (const T*)a.x, a.x_stride,               \
+                (const W*)a.weight, a.mean, a.rstd, (T*)a.dx, part, a.rows, a.width);           \
+  }
+    FM_NORM_SHAPES(FM_NORM_BWD)
+#undef FM_NORM_BWD
+    if (st != FM_OK) return st;
+    if (want && !norm_parts_inline(s, VE)) {
+      st = launch("layer norm backward columns", norm_columns_kernel<T>,
+                  dim3((a.width + kNormThreads - 1) / kNormThreads, parts), dim3(kNormThreads), 0,
+                  a.stream, (const T*)a.dy, a.dy_stride, (const T*)a.x, a.x_stride, a.mean, a.rstd,
+                  part, a.rows, a.width);
+      if (st != FM_OK) return st;
+    }
+  }
+  if (!want) return FM_OK;
+  const int64_t cols = 2 * (int64_t)a.width;
+  return launch("layer norm backward sums", norm_reduce_kernel<W>, dim3((unsigned)((cols + 63) / 64)),
+                dim3(1024), 0, a.stream, part, a.rows > 0 ? parts : 0, (W*)a.dw, (W*)a.db, a.width);
+}
+
+}  // namespace fm

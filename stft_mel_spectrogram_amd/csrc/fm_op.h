@@ -1,0 +1,115 @@
+// Device helpers shared by the speech-model operators (layer norm, relative
+// attention, token log probabilities): element types, 16-byte vectors from
+// any element alignment, wave reductions.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <string>
+#include <tuple>
+#include <utility>
+
+#include "fm_ops.h"
+
+namespace fm {
+
+// Launches `kernel` on `stream`; FM_OK or FM_E_HIP with a message.
+template <class... P, std::size_t... I>
+int launch_packed(const char* what, void (*kernel)(P...), dim3 grid, dim3 block, size_t lds,
+                  void* stream, std::tuple<P...>& args, std::index_sequence<I...>) {
+  void* ptrs[] = {const_cast<void*>(static_cast<const void*>(&std::get<I>(args)))...};
+  const hipError_t e =
+      hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, ptrs, lds,
+                      static_cast<hipStream_t>(stream));
+  if (e == hipSuccess) return FM_OK;
+  return set_error(FM_E_HIP, std::string(what) + ": " + hipGetErrorString(e));
+}
+
+template <class... P, class... A>
+int launch(const char* what, void (*kernel)(P...), dim3 grid, dim3 block, size_t lds, void* stream,
+           const A&... a) {
+  std::tuple<P...> args{static_cast<P>(a)...};
+  return launch_packed(what, kernel, grid, block, lds, stream, args,
+                       std::index_sequence_for<P...>{});
+}
+
+typedef __bf16 bf16_t;
+typedef _Float16 f16_t;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Lets a kernel use `bytes` of dynamic LDS (over 64 KiB needs this).
+template <class K>
+int lds_opt_in(K kernel, size_t bytes) {
+  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                             hipFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(bytes)) == hipSuccess
+             ? FM_OK
+             : FM_E_HIP;
+}
+
+// A 16-byte group of elements.  Loads and stores take any element-aligned
+// address: gfx950 runs with unaligned global access on, so one dwordx4
+// access serves rows of odd widths too.
+template <class T>
+struct Vec16 {
+  static constexpr int n = 16 / sizeof(T);
+  T v[n];
+};
+
+template <class T>
+__device__ __forceinline__ Vec16<T> load16(const T* p) {
+  Vec16<T> r;
+  __builtin_memcpy(&r, p, 16);
+  return r;
+}
+
+template <class T>
+__device__ __forceinline__ void store16(T* p, const Vec16<T>& r) {
+  __builtin_memcpy(p, &r, 16);
+}
+
+// The first `have` elements of a group at p (none if have <= 0), the rest
+// `fill`.
+template <class T>
+__device__ __forceinline__ Vec16<T> load16_part(const T* p, int have, T fill) {
+  Vec16<T> r;
+  if (have >= Vec16<T>::n) {
+    r = load16(p);
+  } else {
+#pragma unroll
+    for (int e = 0; e < Vec16<T>::n; ++e) r.v[e] = e < have ? p[e] : fill;
+  }
+  return r;
+}
+
+template <class T>
+__device__ __forceinline__ void store16_part(T* p, const Vec16<T>& r, int have) {
+  if (have >= Vec16<T>::n) {
+    store16(p, r);
+  } else {
+#pragma unroll
+    for (int e = 0; e < Vec16<T>::n; ++e)
+      if (e < have) p[e] = r.v[e];
+  }
+}
+
+// Sum over aligned groups of LANES lanes of a wave (every lane gets it); the
+// order of the additions is fixed.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int m = LANES / 2; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
+  return v;
+}
+
+template <int LANES>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+  for (int m = LANES / 2; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor(v, m, 64));
+  return v;
+}
+
+}  // namespace fm

@@ -1,0 +1,251 @@
+// Internal declarations of the speech-model operators: the arguments that
+// the C ABI (fm_ops.cpp) has checked, and the launches per element type
+// (fm_op_*.hip).  No HIP types, so that host-only builds can include it.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include "fm_internal.h"
+
+namespace fm {
+
+struct NormForward {
+  const void* x;
+  int64_t x_stride;  // elements between rows
+  const void* weight;
+  const void* bias;
+  void* y;
+  float* mean;
+  float* rstd;
+  int64_t rows;
+  int width;
+  float eps;
+  void* stream;
+};
+
+struct NormBackward {
+  const void* dy;
+  int64_t dy_stride;
+  const void* x;
+  int64_t x_stride;
+  const void* weight;
+  const float* mean;
+  const float* rstd;
+  void* dx;
+  void* dw;
+  void* db;
+  void* workspace;
+  int64_t rows;
+  int width;
+  void* stream;
+};
+
+constexpr int kNormMaxWidth = 1 << 20;
+constexpr int kNormThreads = 256;
+
+// Lane layout of a width: lanes per row and 16-byte groups per lane.  Rows of
+// more than 2048 groups do not stay in registers: {1024, 0}, sweeps that read
+// the row again from the cache.
+struct NormShape {
+  int lpr, vpl;
+};
+inline NormShape norm_shape(int width, int ve) {
+  const int nvec = (width + ve - 1) / ve;
+  if (nvec <= 16) return {16, 1};
+  if (nvec <= 32) return {16, 2};
+  if (nvec <= 64) return {64, 1};
+  if (nvec <= 128) return {64, 2};
+  if (nvec <= 256) return {64, 4};
+  if (nvec <= 512) return {256, 2};
+  if (nvec <= 1024) return {256, 4};
+  if (nvec <= 2048) return {256, 8};
+  return {1024, 0};
+}
+#define FM_NORM_SHAPES(X) \
+  X(16, 1) X(16, 2) X(64, 1) X(64, 2) X(64, 4) X(256, 2) X(256, 4) X(256, 8)
+
+// Whether the backward adds dw and db up beside the row (else in a launch of
+// its own): 2 * vpl * ve accumulators per lane.
+inline bool norm_parts_inline(NormShape s, int ve) { return s.vpl > 0 && s.vpl * ve <= 32; }
+
+// Partial rows (workgroups of the backward): enough to fill the chip several
+// times over, few enough that their sum stays small.
+inline int norm_parts(int64_t rows, int width, int ve) {
+  const NormShape s = norm_shape(width, ve);
+  const int rpb = s.lpr > kNormThreads ? 1 : kNormThreads / s.lpr;
+  const int64_t need = (rows + rpb - 1) / rpb;
+  const int64_t most = norm_parts_inline(s, ve) ? 1024 : 64;
+  return (int)(need < most ? need : most);
+}
+
+
+// One translation unit per element type; w32: float32 parameters.
+int norm_forward_f32(const NormForward& a);
+int norm_forward_f16(const NormForward& a, bool w32);
+int norm_forward_bf16(const NormForward& a, bool w32);
+int norm_backward_f32(const NormBackward& a);
+int norm_backward_f16(const NormBackward& a, bool w32);
+int norm_backward_bf16(const NormBackward& a, bool w32);
+
+struct ScoreForward {
+  const void* x;
+  int64_t x_stride;
+  const void* tokens;
+  int tok64;
+  float* lp;
+  float* ent;
+  float* lse;
+  int64_t* top_ids;
+  float* top_lp;
+  void* workspace;
+  int64_t rows;
+  int vocab;
+  int top;
+  void* stream;
+};
+
+struct ScoreBackward {
+  const void* x;
+  int64_t x_stride;
+  const void* tokens;
+  int tok64;
+  const float* lse;
+  const float* ent;
+  const float* g_lp;
+  const float* g_ent;
+  const int64_t* top_ids;
+  const float* g_top;
+  void* dx;
+  int64_t rows;
+  int vocab;
+  int top;
+  void* stream;
+};
+
+constexpr int kScoreMaxTop = 64;  // one kept entry per lane of a wave
+
+// Work split of a call: waves per workgroup and row segments.  A row that one
+// wave holds in its registers takes one wave; longer rows take four, and are
+// cut into segments while the rows alone give fewer than 1024 workgroups.
+struct ScoreSplit {
+  int waves, segs, seg_len;
+};
+inline ScoreSplit score_split(int64_t rows, int vocab, int ve) {
+  const int wave_chunk = 64 * ve * 4;
+  if (vocab <= wave_chunk) return {1, 1, vocab};
+  const int chunk = 4 * wave_chunk;
+  const int chunks = (vocab + chunk - 1) / chunk;
+  int64_t segs = rows > 0 ? (1024 + rows - 1) / rows : 1;
+  if (segs > chunks) segs = chunks;
+  if (segs < 1) segs = 1;
+  const int per = (chunks + (int)segs - 1) / (int)segs;
+  return {4, (chunks + per - 1) / per, per * chunk};
+}
+inline int64_t score_part_bytes(int64_t rows, int segs) {
+  return (rows * segs * 3 * (int64_t)sizeof(float) + 15) / 16 * 16;
+}
+inline int64_t score_workspace(int64_t rows, int vocab, int top, int ve) {
+  const ScoreSplit p = score_split(rows, vocab, ve);
+  return p.segs == 1 ? 0 : score_part_bytes(rows, p.segs) + rows * p.segs * (int64_t)top * 8;
+}
+
+// Attention with a relative position bias; strides in elements (entry, head,
+// time), the last axis contiguous.  Also the kernels' argument.
+struct AttnArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* table;         // [num_buckets, heads]
+  const int32_t* map;        // [2 far + 1]
+  const int32_t* key_lengths;   // [batch] or NULL
+  const int32_t* query_offset;  // [batch] or NULL: query_offset_value
+  int query_offset_value;
+  int far, num_buckets, table32, causal;
+  int batch, heads, kv_heads, q_len, k_len, dim;
+  float scale;
+  int64_t qs[3], ks[3], vs[3], os[3];
+  void* o;
+  void* o_rest;  // what rounding o to 16 bits left, or NULL
+  float* lse;    // [batch, heads, q_len] or NULL
+  // backward
+  const void* d_o;
+  int64_t dos[3], dqs[3], dks[3], dvs[3];
+  void* dq;
+  void* dk;
+  void* dv;
+  void* d_table;
+  float* delta;       // [batch, heads, q_len]
+  float* amax;        // [batch, heads, q_len], float16 only
+  float* table_part;  // [batch * heads * query blocks, distances of the window]
+  float* table_dist;  // [heads, distances of the window]
+  // forward over key ranges
+  float* part_o;    // [splits, batch, heads, q_len, dim]
+  float* part_lse;  // [splits, batch, heads, q_len]
+  int splits;
+};
+
+constexpr int kAttnMaxDim = 128;
+constexpr int kAttnMaxFar = 1024;
+constexpr int kAttnMaxBuckets = 1024;
+constexpr int kAttnQueries = 128;   // queries of a workgroup
+constexpr int kAttnTokenRows = 16;  // query rows of the single-token kernel
+
+// Query rows that share a key head: a few of them take the single-token
+// kernel, whose waves divide the keys instead of the queries.
+inline bool attn_token_kernel(const AttnArgs& a) {
+  return (int64_t)a.q_len * (a.heads / a.kv_heads) <= kAttnTokenRows;
+}
+// Key ranges a forward call is cut into while its workgroups alone do not
+// fill the chip (256 compute units): four workgroups per unit for the
+// single-token kernel, two for the other; at least 256 keys (512) each.
+inline int attn_splits(const AttnArgs& a) {
+  const bool token = attn_token_kernel(a);
+  const int64_t wgs = token ? (int64_t)a.batch * a.kv_heads
+                            : (int64_t)a.batch * a.heads * ((a.q_len + kAttnQueries - 1) / kAttnQueries);
+  if (wgs == 0) return 1;
+  int64_t s = (token ? 1024 : 512) / wgs;
+  const int64_t most = (a.k_len + (token ? 255 : 511)) / (token ? 256 : 512);
+  if (s > most) s = most;
+  return s < 1 ? 1 : (int)s;
+}
+inline int64_t attn_round16(int64_t n) { return (n + 15) / 16 * 16; }
+inline int64_t attn_rows(const AttnArgs& a) { return (int64_t)a.batch * a.heads * a.q_len; }
+inline int attn_query_blocks(const AttnArgs& a) {
+  return (a.q_len + kAttnQueries - 1) / kAttnQueries;
+}
+inline int64_t attn_forward_workspace(const AttnArgs& a) {
+  const int s = attn_splits(a);
+  return s == 1 ? 0 : attn_round16(4 * s * attn_rows(a) * a.dim) + 4 * s * attn_rows(a);
+}
+// Distances of the bias window: +-(far + 63), see fm_attn.h.
+constexpr int kBiasPad = 63;
+constexpr int bias_window(int far) { return 2 * (far + kBiasPad) + 1; }
+struct AttnBackwardSpace {
+  int64_t amax, part, dist, total;  // byte offsets; delta at 0
+};
+inline AttnBackwardSpace attn_backward_space(const AttnArgs& a, bool f16) {
+  const int64_t rows = attn_round16(4 * attn_rows(a));
+  AttnBackwardSpace s;
+  s.amax = rows;
+  s.part = rows * (f16 ? 2 : 1);
+  s.dist = s.part + attn_round16(4 * (int64_t)a.batch * a.heads * attn_query_blocks(a) * bias_window(a.far));
+  s.total = s.dist + attn_round16(4 * (int64_t)a.heads * bias_window(a.far));
+  return s;
+}
+
+int attn_forward_f32(const AttnArgs& a, void* stream);
+int attn_forward_f16(const AttnArgs& a, void* stream);
+int attn_forward_bf16(const AttnArgs& a, void* stream);
+int attn_backward_f32(const AttnArgs& a, void* stream);
+int attn_backward_f16(const AttnArgs& a, void* stream);
+int attn_backward_bf16(const AttnArgs& a, void* stream);
+
+int score_forward_f32(const ScoreForward& a);
+int score_forward_f16(const ScoreForward& a);
+int score_forward_bf16(const ScoreForward& a);
+int score_backward_f32(const ScoreBackward& a);
+int score_backward_f16(const ScoreBackward& a);
+int score_backward_bf16(const ScoreBackward& a);
+
+}  // namespace fm

@@ -1,0 +1,363 @@
+// Log probabilities of given tokens with entropy and top alternatives, and
+// the logits' gradient.
+//
+//   lse = log sum exp(x),  lp_t = x_t - lse,  H = lse - sum p x = log s - t / s
+//   with s = sum exp(x - m), t = sum exp(x - m) (x - m), m = max x
+//   dx_j = sum of g over the named tokens equal to j - p_j (sum of all g)
+//          - g_H p_j (lp_j + H)
+//
+// One pass over the logits: every lane keeps a running maximum with the two
+// sums in float32 and rescales them when a register chunk raises it; the
+// lanes' triples are joined in a fixed order.  Entries of -inf have p = 0 and
+// add nothing to the entropy; NaN anywhere in a row makes its results NaN.
+// A row of -inf only has lp = -inf, H = 0 and a zero gradient.
+//
+// Top alternatives: a wave keeps its best `top` entries as 64-bit keys
+// (value in an ordered integer, then the complement of the index, so that
+// ties go to the lower index), one per lane in descending order; a chunk's
+// entries are taken in descending order while they beat the last one kept.
+//
+// Memory bound.  Few rows with a long vocabulary are cut into segments, one
+// workgroup each, whose partial results a second launch joins.
+#pragma once
+
+#include "fm_op.h"
+
+namespace fm {
+
+constexpr int kScoreVecs = 4;  // 16-byte groups a lane holds at a time
+
+typedef unsigned long long key_t;
+
+__device__ __forceinline__ key_t score_key(float x, int idx) {
+  uint32_t b = __float_as_uint(x);
+  if (x == 0.f) b = 0;  // -0 ranks as 0
+  b = (b >> 31) ? ~b : (b | 0x80000000u);
+  return ((key_t)b << 32) | (uint32_t)~(uint32_t)idx;
+}
+__device__ __forceinline__ float key_value(key_t k) {
+  const uint32_t b = (uint32_t)(k >> 32);
+  return __uint_as_float((b >> 31) ? (b & 0x7fffffffu) : ~b);
+}
+__device__ __forceinline__ int key_index(key_t k) { return (int)~(uint32_t)k; }
+
+__device__ __forceinline__ key_t wave_max_key(key_t k) {
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) {
+    const key_t o = __shfl_xor(k, m, 64);
+    k = o > k ? o : k;
+  }
+  return k;
+}
+
+// Inserts `k` (the same in every lane) into the wave's descending list.
+__device__ __forceinline__ void list_insert(key_t& list, key_t k, int lane) {
+  const key_t up = __shfl_up(list, 1, 64);
+  const bool below = list < k;
+  const bool above_too = lane > 0 && up < k;
+  list = below ? (above_too ? up : k) : list;
+}
+
+// (m, s, t) of two disjoint sets of entries.
+struct ScoreSum {
+  float m, s, t;
+};
+__device__ __forceinline__ ScoreSum score_join(ScoreSum a, ScoreSum b) {
+  const float m = fmaxf(a.m, b.m);
+  if (m == -INFINITY) return {m, a.s + b.s, a.t + b.t};
+  // a set of -inf only has s = t = 0.  Past -200 the factor is 0, and so must
+  // its product with the distance be, however far the maxima are apart.
+  const float da = a.m == -INFINITY ? 0.f : fmaxf(a.m - m, -200.f);
+  const float db = b.m == -INFINITY ? 0.f : fmaxf(b.m - m, -200.f);
+  const float ra = __builtin_amdgcn_exp2f(da * kLog2e), rb = __builtin_amdgcn_exp2f(db * kLog2e);
+  return {m, a.s * ra + b.s * rb, (a.t + a.s * da) * ra + (b.t + b.s * db) * rb};
+}
+
+struct ScoreOut {
+  float* lp;
+  float* ent;
+  float* lse;
+  int64_t* top_ids;
+  float* top_lp;
+};
+
+// Writes a row's results; one wave, `list` its descending keys.
+template <class T>
+__device__ __forceinline__ void score_finish(const ScoreSum& r, const T* xr, int64_t row, int vocab,
+                                             const void* tokens, int tok64, key_t list, int top,
+                                             const ScoreOut& o, int lane) {
+  const float lse = r.m == -INFINITY ? (r.s == 0.f ? -INFINITY : NAN) : r.m + logf(r.s);
+  if (lane == 0) {
+    const int64_t t = tok64 ? ((const int64_t*)tokens)[row] : ((const int32_t*)tokens)[row];
+    float lp;
+    if (t < 0)
+      lp = 0.f;  // no token asked for
+    else if (t >= vocab)
+      lp = NAN;
+    else if (lse == -INFINITY)
+      lp = -INFINITY;
+    else
+      lp = ((float)xr[t] - r.m) - logf(r.s);
+    if (o.lp) o.lp[row] = lp;
+    if (o.ent) o.ent[row] = lse == -INFINITY ? 0.f : logf(r.s) - r.t / r.s;
+    if (o.lse) o.lse[row] = lse;
+  }
+  if (lane < top) {
+    const float v = key_value(list);
+    o.top_ids[row * top + lane] = key_index(list);
+    o.top_lp[row * top + lane] = v == -INFINITY && lse == -INFINITY ? -INFINITY : (v - r.m) - logf(r.s);
+  }
+}
+
+// WAVES waves per row segment; WAVES == 1: four rows per workgroup.  With
+// several segments, `part` gets (m, s, t) and the keys of each.
+template <class T, int WAVES, bool TOP>
+__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void score_forward_kernel(
+    const T* __restrict__ x, int64_t x_stride, const void* __restrict__ tokens, int tok64,
+    ScoreOut out, float* __restrict__ part, key_t* __restrict__ part_keys, int64_t rows, int vocab,
+    int top, int seg_len, int segs) {
+  constexpr int VE = Vec16<T>::n;
+  constexpr int NT = WAVES * 64;
+  constexpr int CH = NT * VE * kScoreVecs;
+  const int lane = threadIdx.x & 63;
+  const int wave = WAVES == 1 ? 0 : threadIdx.x >> 6;
+  const int tid = WAVES == 1 ? lane : threadIdx.x;
+  const int64_t unit = WAVES == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  const int64_t row = unit / segs;
+  const int seg = (int)(unit - row * segs);
+  if (WAVES == 1 && row >= rows) return;  // whole waves, no barriers there
+  const T* xr = x + row * x_stride;
+  const int beg = seg * seg_len;
+  const int end = beg + seg_len < vocab ? beg + seg_len : vocab;
+
+  ScoreSum acc = {-INFINITY, 0.f, 0.f};
+  key_t list = 0;
+  for (int c0 = beg; c0 < end; c0 += CH) {
+    Vec16<T> v[kScoreVecs];
+#pragma unroll
+    for (int i = 0; i < kScoreVecs; ++i) {
+      const int c = c0 + (i * NT + tid) * VE;
+      v[i] = load16_part(xr + c, end - c, (T)-INFINITY);
+    }
+    float cm = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kScoreVecs; ++i)
+#pragma unroll
+      for (int e = 0; e < VE; ++e) cm = fmaxf(cm, (float)v[i].v[e]);
+    const float m = fmaxf(acc.m, cm);
+    const float ms = m == -INFINITY ? 0.f : m;
+    const float d0 = acc.m == -INFINITY ? 0.f : fmaxf(acc.m - ms, -200.f);
+    const float r0 = __builtin_amdgcn_exp2f(d0 * kLog2e);
+    float s = 0.f, t = 0.f;
+#pragma unroll
+    for (int i = 0; i < kScoreVecs; ++i)
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        const float d = (float)v[i].v[e] - ms;
+        const float p = __builtin_amdgcn_exp2f(d * kLog2e);
+        s += p;
+        // p is 0 long before -200, where the product with -inf would be NaN
+        t = fmaf(p, fmaxf(d, -200.f), t);
+      }
+    acc.t = (acc.t + acc.s * d0) * r0 + t;
+    acc.s = acc.s * r0 + s;
+    acc.m = m;
+    if constexpr (TOP) {
+      // descending over the chunk: `last` is what has been taken so far
+      key_t last = ~(key_t)0;
+      while (true) {
+        key_t best = 0;
+#pragma unroll
+        for (int i = 0; i < kScoreVecs; ++i)
+#pragma unroll
+          for (int e = 0; e < VE; ++e) {
+            const int c = c0 + (i * NT + tid) * VE + e;
+            const key_t k = c < end ? score_key((float)v[i].v[e], c) : 0;
+            if (k < last && k > best) best = k;
+          }
+        best = wave_max_key(best);
+        const key_t worst = __shfl(list, top - 1, 64);
+        if (best <= worst) break;
+        list_insert(list, best, lane);
+        last = best;
+      }
+    }
+  }
+#pragma unroll
+  for (int mk = 32; mk >= 1; mk >>= 1) {
+    const ScoreSum o = {__shfl_xor(acc.m, mk, 64), __shfl_xor(acc.s, mk, 64),
+                        __shfl_xor(acc.t, mk, 64)};
+    acc = score_join(acc, o);
+  }
+  if constexpr (WAVES > 1) {
+    __shared__ ScoreSum sums[WAVES];
+    __shared__ key_t keys[TOP ? WAVES * 64 : 1];
+    if (lane == 0) sums[wave] = acc;
+    if constexpr (TOP) keys[wave * 64 + lane] = lane < top ? list : 0;
+    __syncthreads();
+    if (wave != 0) return;
+    acc = sums[0];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) acc = score_join(acc, sums[w]);
+    if constexpr (TOP) {
+      for (int w = 1; w < WAVES; ++w)
+        for (int i = 0; i < top; ++i) {
+          const key_t k = keys[w * 64 + i];
+          if (k <= __shfl(list, top - 1, 64)) break;
+          list_insert(list, k, lane);
+        }
+    }
+  }
+  if (segs == 1) {
+    score_finish(acc, xr, row, vocab, tokens, tok64, list, TOP ? top : 0, out, lane);
+  } else {
+    if (lane == 0) {
+      part[unit * 3 + 0] = acc.m;
+      part[unit * 3 + 1] = acc.s;
+      part[unit * 3 + 2] = acc.t;
+    }
+    if (TOP && lane < top) part_keys[unit * top + lane] = list;
+  }
+}
+
+// One wave per row: joins the segments in order.
+template <class T>
+__global__ __launch_bounds__(64) void score_join_kernel(
+    const T* __restrict__ x, int64_t x_stride, const void* __restrict__ tokens, int tok64,
+    ScoreOut out, const float* __restrict__ part, const key_t* __restrict__ part_keys, int vocab,
+    int top, int segs) {
+  const int lane = threadIdx.x;
+  const int64_t row = blockIdx.x;
+  ScoreSum acc = {-INFINITY, 0.f, 0.f};
+  for (int s = lane; s < segs; s += 64) {
+    const float* p = part + (row * segs + s) * 3;
+    acc = score_join(acc, ScoreSum{p[0], p[1], p[2]});
+  }
+#pragma unroll
+  for (int mk = 32; mk >= 1; mk >>= 1) {
+    const ScoreSum o = {__shfl_xor(acc.m, mk, 64), __shfl_xor(acc.s, mk, 64),
+                        __shfl_xor(acc.t, mk, 64)};
+    acc = score_join(acc, o);
+  }
+  key_t list = 0;
+  if (top > 0) {
+    const int64_t n = (int64_t)segs * top;
+    const key_t* keys = part_keys + row * n;
+    for (int64_t i0 = 0; i0 < n; i0 += 64) {
+      key_t mine = i0 + lane < n ? keys[i0 + lane] : 0;
+      while (true) {
+        const key_t best = wave_max_key(mine);
+        if (best <= __shfl(list, top - 1, 64)) break;
+        list_insert(list, best, lane);
+        if (mine == best) mine = 0;
+      }
+    }
+  }
+  score_finish(acc, x + row * x_stride, row, vocab, tokens, tok64, list, top, out, lane);
+}
+
+// dx of one row segment; see the formula above.
+template <class T, int WAVES>
+__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void score_backward_kernel(
+    const T* __restrict__ x, int64_t x_stride, const void* __restrict__ tokens, int tok64,
+    const float* __restrict__ lse_, const float* __restrict__ ent, const float* __restrict__ g_lp,
+    const float* __restrict__ g_ent, const int64_t* __restrict__ top_ids,
+    const float* __restrict__ g_top, T* __restrict__ dx, int64_t rows, int vocab, int top,
+    int seg_len, int segs) {
+  constexpr int VE = Vec16<T>::n;
+  constexpr int NT = WAVES * 64;
+  const int tid = WAVES == 1 ? threadIdx.x & 63 : threadIdx.x;
+  const int64_t unit = WAVES == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  const int64_t row = unit / segs;
+  const int seg = (int)(unit - row * segs);
+  if (WAVES == 1 && row >= rows) return;
+  const T* xr = x + row * x_stride;
+  T* dr = dx + row * vocab;
+  const int beg = seg * seg_len;
+  const int end = beg + seg_len < vocab ? beg + seg_len : vocab;
+  const float lse = lse_[row];
+  const bool empty = lse == -INFINITY;
+  const float ls = empty ? 0.f : lse;
+  int64_t tok = tok64 ? ((const int64_t*)tokens)[row] : ((const int32_t*)tokens)[row];
+  if (tok >= vocab) tok = -1;
+  const float g = g_lp && tok >= 0 && !empty ? g_lp[row] : 0.f;
+  float all = g;
+  if (g_top && !empty)
+    for (int i = 0; i < top; ++i) all += g_top[row * top + i];
+  const float ge = g_ent && !empty ? g_ent[row] : 0.f;
+  const float h = ge != 0.f ? ent[row] : 0.f;
+  const auto dense = [&](float xv) {
+    const float l = xv - ls;
+    const float p = exp2f(l * kLog2e);  // with the subnormal ones, which a gradient may lift
+    return -p * fmaf(ge, fmaxf(l, -200.f) + h, all);
+  };
+  for (int c0 = beg; c0 < end; c0 += NT * VE * kScoreVecs) {
+    Vec16<T> v[kScoreVecs];
+#pragma unroll
+    for (int i = 0; i < kScoreVecs; ++i) {
+      const int c = c0 + (i * NT + tid) * VE;
+      v[i] = load16_part(xr + c, end - c, (T)0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < kScoreVecs; ++i) {
+      const int c = c0 + (i * NT + tid) * VE;
+#pragma unroll
+      for (int e = 0; e < VE; ++e) v[i].v[e] = (T)dense((float)v[i].v[e]);
+      store16_part(dr + c, v[i], end - c);
+    }
+  }
+  // The named tokens' entries, written again by the lane that wrote them
+  // above (one thread's stores to one address stay in order), from the
+  // unrounded sum.
+  const auto named = [&](int64_t j) {
+    if (j < beg || j >= end || (int)(((j - beg) / VE) % NT) != tid) return;
+    float d = dense((float)xr[j]);
+    if (tok == j) d += g;
+    if (g_top)
+      for (int i = 0; i < top; ++i)
+        if (top_ids[row * top + i] == j) d += g_top[row * top + i];
+    dr[j] = (T)d;
+  };
+  if (empty) return;
+  if (tok >= 0) named(tok);
+  if (g_top)
+    for (int i = 0; i < top; ++i) named(top_ids[row * top + i]);
+}
+
+template <class T>
+int score_forward_t(const ScoreForward& a) {
+  const ScoreSplit p = score_split(a.rows, a.vocab, Vec16<T>::n);
+  ScoreOut out = {a.lp, a.ent, a.lse, a.top_ids, a.top_lp};
+  float* part = (float*)a.workspace;
+  key_t* keys = (key_t*)((char*)a.workspace + score_part_bytes(a.rows, p.segs));
+  const int64_t units = a.rows * p.segs;
+  const auto go = [&](auto kernel) {
+    const int64_t blocks = p.waves == 1 ? (units + 3) / 4 : units;
+    return launch("token log probabilities", kernel, dim3((unsigned)blocks),
+                  dim3(p.waves == 1 ? 256 : 256), 0, a.stream, (const T*)a.x, a.x_stride, a.tokens,
+                  a.tok64, out, part, keys, a.rows, a.vocab, a.top, p.seg_len, p.segs);
+  };
+  int st;
+  if (p.waves == 1)
+    st = a.top ? go(score_forward_kernel<T, 1, true>) : go(score_forward_kernel<T, 1, false>);
+  else
+    st = a.top ? go(score_forward_kernel<T, 4, true>) : go(score_forward_kernel<T, 4, false>);
+  if (st != FM_OK || p.segs == 1) return st;
+  return launch("token log probabilities (join)", score_join_kernel<T>, dim3((unsigned)a.rows),
+                dim3(64), 0, a.stream, (const T*)a.x, a.x_stride, a.tokens, a.tok64, out, part, keys,
+                a.vocab, a.top, p.segs);
+}
+
+template <class T>
+int score_backward_t(const ScoreBackward& a) {
+  const ScoreSplit p = score_split(a.rows, a.vocab, Vec16<T>::n);
+  const int64_t units = a.rows * p.segs;
+  const int64_t blocks = p.waves == 1 ? (units + 3) / 4 : units;
+  return launch("token log probabilities backward",
+                p.waves == 1 ? score_backward_kernel<T, 1> : score_backward_kernel<T, 4>,
+                dim3((unsigned)blocks), dim3(256), 0, a.stream, (const T*)a.x, a.x_stride, a.tokens,
+                a.tok64, a.lse, a.ent, a.g_lp, a.g_ent, a.top_ids, a.g_top, (T*)a.dx, a.rows,
+                a.vocab, a.top, p.seg_len, p.segs);
+}
+
+}  // namespace fm

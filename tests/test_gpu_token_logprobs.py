@@ -1,0 +1,289 @@
+"""Token log probabilities, entropy, top alternatives and the logits' gradient
+against a plain float64 implementation on the same inputs.
+
+Tolerances: an exponential's relative error is that of its argument's rounding
+(2^-24 times the argument in base 2) and one step; sums add 2^-24 per addition
+of the longest chain.  With D the largest distance of a counted entry from the
+row's maximum, E = 2^-23 (D + 64 + entries per lane) bounds the relative error
+of the row's sums.
+"""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def reference(x, tok, top, g_lp=None, g_ent=None, g_top=None):
+    """Rows without any finite entry are not passed here."""
+    x = x.double()
+    lse = torch.logsumexp(x, -1)
+    lp = x - lse[..., None]
+    p = lp.exp()
+    plp = torch.where(p > 0, p * lp, torch.zeros_like(p))
+    ent = -plp.sum(-1)
+    valid = tok >= 0
+    at = torch.where(valid, lp.gather(-1, tok.clamp(min=0)[..., None])[..., 0], torch.zeros_like(ent))
+    ids = torch.sort(x, dim=-1, descending=True, stable=True).indices[..., :top]
+    tops = lp.gather(-1, ids)
+    dx = torch.zeros_like(x)
+    if g_lp is not None:
+        g = torch.where(valid, g_lp.double(), torch.zeros_like(ent))
+        dx -= g[..., None] * p
+        dx.scatter_add_(-1, tok.clamp(min=0)[..., None], g[..., None])
+    if g_ent is not None:
+        dx -= g_ent.double()[..., None] * torch.where(p > 0, p * (lp + ent[..., None]), torch.zeros_like(p))
+    if g_top is not None:
+        dx -= g_top.double().sum(-1, keepdim=True) * p
+        dx.scatter_add_(-1, ids, g_top.double())
+    return at, ent, ids, tops, lse, dx, p, lp
+
+
+def row_error(x, lp):
+    xd = x.double()
+    m = xd.amax(-1, keepdim=True)
+    d = torch.where(lp > -200, m - xd, torch.zeros_like(xd)).amax(-1)
+    return 2.0 ** -23 * (d + 64 + x.shape[-1] / 256)
+
+
+def close(name, got, ref, tol):
+    fin = torch.isfinite(ref)
+    assert torch.equal(torch.isfinite(got), fin), name
+    assert torch.equal(got.double()[~fin], ref[~fin]), name
+    worst = ((got.double() - ref).abs() / tol)[fin].max().item() if fin.any() else 0.0
+    print(f"[{name}] worst error / tolerance {worst:.3g}")
+    assert worst <= 1.0, (name, worst)
+
+
+def run_case(x, tok, top, seed=0):
+    from stft_mel_spectrogram_amd import (token_logprobs, token_logprobs_backward,
+                                          token_logprobs_forward)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    lead = x.shape[:-1]
+    g_lp, g_ent = (torch.randn(lead, generator=g, device="cuda") for _ in range(2))
+    g_top = torch.randn((*lead, top), generator=g, device="cuda") if top else None
+    r, lse = token_logprobs_forward(x, tok, top)
+    at, ent, ids, tops, rlse, dx, p, lp = reference(x, tok.long(), top, g_lp, g_ent, g_top)
+    e = row_error(x, lp)
+    mean_d = (p * torch.where(p > 0, lp, torch.zeros_like(lp)).abs()).sum(-1) + x.double().amax(-1).sub(rlse).abs()
+    close("logprobs", r.logprobs, at, e + 2.0 ** -22 * at.abs().nan_to_num(posinf=0))
+    close("entropy", r.entropy, ent, e * (2 + 2 * mean_d))
+    close("lse", lse, rlse, e + 2.0 ** -22 * (rlse.abs() + x.double().amax(-1).abs()))
+    if top:
+        assert torch.equal(r.top_ids, ids)
+        close("top", r.top_logprobs, tops, (e[..., None] + 2.0 ** -22 * tops.abs()).nan_to_num(posinf=1))
+    else:
+        assert r.top_ids is None and r.top_logprobs is None
+    got = token_logprobs_backward(x, tok, lse, r.entropy, g_lp, g_ent, r.top_ids, g_top)
+    size = g_lp.double().abs() + (g_top.double().abs().sum(-1) if top else 0)
+    lpa = torch.where(p > 0, lp.abs(), torch.zeros_like(lp))
+    scale = p * (size[..., None] + g_ent.double().abs()[..., None] * (lpa + ent[..., None] + 1))
+    named = torch.zeros_like(p).scatter_add_(-1, tok.long().clamp(min=0)[..., None], g_lp.double().abs()[..., None])
+    if top:
+        named.scatter_add_(-1, ids, g_top.double().abs())
+    fi = torch.finfo(x.dtype)
+    # the exponential's argument x - lse carries the roundings of both
+    rel = 4 * e[..., None] + 2.0 ** -22 * (lpa + rlse.abs()[..., None])
+    tol = fi.eps / 2 * dx.abs() + fi.smallest_normal * fi.eps / 2 + rel * scale + 2.0 ** -22 * named + 1e-37
+    close("dx", got, dx, tol)
+    same = token_logprobs(x, tok, top)
+    for a, b in zip(same, r):
+        assert a is None and b is None or torch.equal(a, b)
+    return r, lse, got
+
+
+def inputs(rows, vocab, dtype, seed, std=2.5):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    x = (torch.randn(rows, vocab, generator=g, device="cuda") * std).to(dtype)
+    return x, torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+
+
+# one entry; a wave's registers and their borders; several chunks and segments
+VOCABS = [1, 2, 29, 129, 1023, 1024, 1025, 2048, 2049, 4097, 8192, 8193, 20011, 50001]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("vocab", VOCABS)
+def test_vocabularies(vocab, dtype):
+    for rows, top in ((5, min(5, vocab)), (3, 0)):
+        x, tok = inputs(rows, vocab, DT[dtype], vocab)
+        run_case(x, tok, top)
+
+
+@pytest.mark.parametrize("top", [1, 2, 20, 63, 64])
+@pytest.mark.parametrize("vocab", [70, 3000, 40003])
+def test_top_counts(vocab, top):
+    x, tok = inputs(4, vocab, torch.bfloat16, top)
+    run_case(x, tok, top)
+
+
+@pytest.mark.parametrize("rows", [0, 1, 7, 1500])
+def test_row_counts(rows):
+    from stft_mel_spectrogram_amd import token_logprobs
+    x, tok = inputs(rows, 9001, torch.bfloat16, rows)
+    if rows == 0:
+        r = token_logprobs(x, tok, 3)
+        assert r.logprobs.shape == (0,) and r.top_ids.shape == (0, 3)
+        return
+    run_case(x, tok, 3)
+
+
+def test_ties_go_to_the_lower_index():
+    for vocab in (64, 5000, 30000):
+        x = torch.zeros(3, vocab, device="cuda", dtype=torch.float16)
+        x[1, ::2] = -0.0  # ranks with +0
+        x[2, vocab // 2:] = 1.0
+        tok = torch.tensor([0, 1, vocab - 1], device="cuda")
+        r, _, _ = run_case(x, tok, 10)
+        assert r.top_ids[0].tolist() == list(range(10))
+        assert r.top_ids[1].tolist() == list(range(10))
+        assert r.top_ids[2].tolist() == list(range(vocab // 2, vocab // 2 + 10))
+
+
+@pytest.mark.parametrize("vocab", [40, 6000, 50001])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_masked_entries(vocab, dtype):
+    x, tok = inputs(6, vocab, DT[dtype], 4)
+    x[:, 1::3] = -math.inf
+    tok[0] = 1  # a masked token: log probability -inf
+    x[1] = -math.inf
+    x[1, vocab - 1] = 0.25  # a single entry left
+    tok[1] = vocab - 1
+    low = torch.finfo(DT[dtype]).min
+    x[2, 5:] = low  # the type's lowest value as a mask
+    tok[2] = 3
+    run_case(x, tok, 5)
+
+
+def test_rows_with_nothing_left():
+    from stft_mel_spectrogram_amd import token_logprobs_backward, token_logprobs_forward
+    for vocab in (33, 30001):
+        x, tok = inputs(3, vocab, torch.bfloat16, 6)
+        x[1] = -math.inf
+        r, lse = token_logprobs_forward(x, tok, 4)
+        assert r.logprobs[1].item() == -math.inf and lse[1].item() == -math.inf
+        assert r.entropy[1].item() == 0
+        assert r.top_ids[1].tolist() == [0, 1, 2, 3]
+        assert (r.top_logprobs[1] == -math.inf).all()
+        one = torch.ones(3, device="cuda")
+        dx = token_logprobs_backward(x, tok, lse, r.entropy, one, one, r.top_ids,
+                                     torch.ones(3, 4, device="cuda"))
+        assert (dx[1] == 0).all()
+        keep = [0, 2]
+        dk = token_logprobs_backward(x[keep].contiguous(), tok[keep], lse[keep], r.entropy[keep], one[:2],
+                                     one[:2], r.top_ids[keep], torch.ones(2, 4, device="cuda"))
+        assert torch.equal(dx[keep], dk)
+
+
+def test_tokens_not_asked_for_or_out_of_range():
+    from stft_mel_spectrogram_amd import token_logprobs_backward, token_logprobs_forward
+    x, tok = inputs(4, 7000, torch.float32, 7)
+    tok[0], tok[1] = -100, 7000
+    r, lse = token_logprobs_forward(x, tok, 0)
+    assert r.logprobs[0].item() == 0 and r.logprobs[1].isnan()
+    dx = token_logprobs_backward(x, tok, lse, r.entropy, torch.ones(4, device="cuda"))
+    assert (dx[:2] == 0).all() and dx[2, tok[2]] > 0
+    i32 = tok.to(torch.int32)
+    r2, _ = token_logprobs_forward(x, i32, 0)
+    assert torch.equal(r2.logprobs[2:], r.logprobs[2:]) and r2.logprobs[0].item() == 0
+    ok = [2, 3]
+    run_case(x[ok].contiguous(), tok[ok], 2)
+
+
+def test_nan_and_infinity_stay_in_their_rows():
+    from stft_mel_spectrogram_amd import token_logprobs_backward, token_logprobs_forward
+    for vocab in (100, 30000):
+        x, tok = inputs(4, vocab, torch.float32, 8)
+        clean, _ = token_logprobs_forward(x, tok)
+        x[1, 50], x[2, vocab - 1] = math.nan, math.inf
+        r, lse = token_logprobs_forward(x, tok)
+        assert r.logprobs[1:3].isnan().all() and r.entropy[1:3].isnan().all()
+        assert torch.equal(r.logprobs[[0, 3]], clean.logprobs[[0, 3]])
+        dx = token_logprobs_backward(x, tok, lse, r.entropy, torch.ones(4, device="cuda"))
+        assert dx[1:3].isnan().any(-1).all() and torch.isfinite(dx[[0, 3]]).all()
+
+
+def test_peaked_and_wide_rows():
+    x, tok = inputs(6, 12000, torch.float32, 9, std=30.0)
+    x[0, 77] = 400.0
+    run_case(x, tok, 8)
+
+
+def test_strided_rows_and_leading_axes():
+    x, tok = inputs(12, 5000, torch.bfloat16, 10)
+    run_case(x[:, 11:4000], tok % 3989, 5)
+    x3 = x.view(3, 4, 5000)[:, :, 1:]
+    run_case(x3, (tok % 4999).view(3, 4), 5)
+
+
+def test_autograd():
+    from stft_mel_spectrogram_amd import token_logprobs
+    x, tok = inputs(5, 3001, torch.float32, 11)
+    r, lse, _ = run_case(x, tok, 4)
+    leaf = x.clone().requires_grad_(True)
+    out = token_logprobs(leaf, tok, 4)
+    g = [torch.randn_like(t) for t in (out.logprobs, out.entropy, out.top_logprobs)]
+    sum((a * b).sum() for a, b in zip((out.logprobs, out.entropy, out.top_logprobs), g)).backward()
+    dx = reference(x, tok, 4, *g)[5]
+    assert (leaf.grad.double() - dx).abs().max().item() <= 1e-5
+    leaf2 = x.clone().requires_grad_(True)
+    token_logprobs(leaf2, tok).logprobs.sum().backward()
+    assert (leaf2.grad.double() - reference(x, tok, 0, torch.ones(5, device="cuda"))[5]).abs().max() <= 1e-5
+
+
+def test_gradient_against_differences():
+    from stft_mel_spectrogram_amd import token_logprobs_backward, token_logprobs_forward
+    x, tok = inputs(2, 50, torch.float32, 12)
+    g_lp, g_ent = torch.tensor([0.7, -1.3], device="cuda"), torch.tensor([0.4, 0.9], device="cuda")
+    r, lse = token_logprobs_forward(x, tok)
+    dx = token_logprobs_backward(x, tok, lse, r.entropy, g_lp, g_ent)
+
+    def value(xd):
+        at, ent = reference(xd, tok, 0)[:2]
+        return (at * g_lp.double() + ent * g_ent.double()).sum().item()
+
+    h = 1e-5
+    for i, j in ((0, 0), (0, int(tok[0])), (1, 49), (1, int(tok[1]))):
+        d = torch.zeros(2, 50, dtype=torch.float64, device="cuda")
+        d[i, j] = h
+        num = (value(x.double() + d) - value(x.double() - d)) / (2 * h)
+        assert abs(num - dx[i, j].item()) <= 1e-6 + 2.0 ** -17
+
+
+def test_another_stream_and_graph_replays():
+    from stft_mel_spectrogram_amd import token_logprobs_backward, token_logprobs_forward
+    x, tok = inputs(6, 20000, torch.bfloat16, 13)
+    g = torch.ones(6, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        r, lse = token_logprobs_forward(x, tok, 5)
+        token_logprobs_backward(x, tok, lse, r.entropy, g, g)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    sx = x.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gr, gl = token_logprobs_forward(sx, tok, 5)
+        gdx = token_logprobs_backward(sx, tok, gl, gr.entropy, g, g)
+    for seed in range(3):
+        nx, _ = inputs(6, 20000, torch.bfloat16, 30 + seed)
+        sx.copy_(nx)
+        graph.replay()
+        torch.cuda.synchronize()
+        er, el = token_logprobs_forward(nx, tok, 5)
+        edx = token_logprobs_backward(nx, tok, el, er.entropy, g, g)
+        torch.cuda.synchronize()
+        for a, e in zip((*gr, gdx), (*er, edx)):
+            assert torch.equal(a, e)
