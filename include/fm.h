@@ -431,9 +431,6 @@ int fm_token_logprobs_backward(const void* x, int64_t x_stride, const void* toke
  *                distance with an entry outside [0, num_buckets) has no bias;
  *   key_lengths  [batch] int32 (clamped to [0, k_len]) or NULL: k_len;
  *   query_offset [batch] int32 or NULL: query_offset_value for every entry;
- *   o_rest       NULL, or (16-bit types; strides as o) what rounding o left:
- *                with it the backward has o in twice the bits, which the sums
- *                of the table's gradient profit from;
  *   lse          [batch, heads, q_len] float32, NULL allowed in the forward;
  * backward: grad_o in; grad_q, grad_k, grad_v out (every element written);
  *                grad_table out, [num_buckets, heads] of table_dtype, or NULL.
@@ -450,7 +447,6 @@ typedef struct fm_attention_args {
   const int32_t* key_lengths;
   const int32_t* query_offset;
   void* o;
-  void* o_rest;
   float* lse;
   const void* grad_o;
   void* grad_q;
@@ -465,10 +461,10 @@ typedef struct fm_attention_args {
  * (1); pointers and strides are not looked at. */
 int64_t fm_attention_workspace(const fm_attention_args* args, int backward);
 
-/* o (and o_rest, lse if not NULL). */
+/* o (and lse if not NULL). */
 int fm_attention_forward(const fm_attention_args* args, void* workspace, void* stream);
 
-/* Gradients of sum(grad_o * o); o, o_rest and lse as the forward wrote them. */
+/* Gradients of sum(grad_o * o); o and lse as the forward wrote them. */
 int fm_attention_backward(const fm_attention_args* args, void* workspace, void* stream);
 
 #ifdef __cplusplus

@@ -68,8 +68,7 @@ class AttentionArgs(ctypes.Structure):
                                                 "head_dim", "query_offset_value")] +
                 [("scale", ctypes.c_double)] +
                 [(n, ctypes.c_void_p) for n in ("q", "k", "v", "table", "bucket_map",
-                                                 "key_lengths", "query_offset", "o", "o_rest",
-                                                 "lse", "grad_o", "grad_q", "grad_k", "grad_v",
+                                                 "key_lengths", "query_offset", "o", "lse", "grad_o", "grad_q", "grad_k", "grad_v",
                                                  "grad_table")] +
                 [(f"{t}_stride_{axis}", ctypes.c_int64)
                  for t in ("q", "k", "v", "o", "grad_o", "grad_q", "grad_k", "grad_v")

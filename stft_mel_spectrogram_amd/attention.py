@@ -13,7 +13,6 @@ key gives zeros and zero gradients.
 """
 from __future__ import annotations
 
-import collections
 import ctypes
 import functools
 
@@ -21,12 +20,6 @@ import torch
 
 from . import _native as N
 from . import _tensors as T
-
-# What relative_attention_backward needs besides the inputs and the result:
-# lse [batch, heads, time] float32, and for 16-bit types what rounding the
-# result left.
-AttentionStats = collections.namedtuple("AttentionStats", ["lse", "rest"])
-
 
 @functools.lru_cache(maxsize=64)
 def _bucket_list(num_buckets: int, max_distance: int, bidirectional: bool) -> tuple:
@@ -142,33 +135,24 @@ class _Call:
               or (q.shape[3] > 1 and out.stride(3) != 1)):
             raise ValueError(f"out must be a {q.dtype} tensor of shape {tuple(q.shape)} on "
                              f"{q.device} with a contiguous last axis")
-        lse = rest = None
-        if stats:
-            lse = torch.empty((b, h, tq), dtype=torch.float32, device=q.device)
-            if self.code != N.FM_F32:
-                rest = torch.empty_strided(out.shape, out.stride(), dtype=out.dtype,
-                                           device=out.device)
-        a = N.AttentionArgs(*self.head, out.data_ptr(), T.ptr(rest), T.ptr(lse), None, None, None,
-                            None, None, *self.inputs, *_strides(out))
+        lse = torch.empty((b, h, tq), dtype=torch.float32, device=q.device) if stats else None
+        a = N.AttentionArgs(*self.head, out.data_ptr(), T.ptr(lse), None, None, None, None, None,
+                            *self.inputs, *_strides(out))
         ws = T.workspace(q, N.lib.fm_attention_workspace(ctypes.byref(a), 0))
         T.call(q, N.lib.fm_attention_forward, ctypes.byref(a), T.ptr(ws))
-        return out, AttentionStats(lse, rest)
+        return out, lse
 
-    def backward(self, grad_out, out, stats, need_table=True):
+    def backward(self, grad_out, out, lse, need_table=True):
         q, k, v = self.q, self.k, self.v
-        T.same_device(q, grad_out=grad_out, out=out, lse=stats.lse, rest=stats.rest)
+        T.same_device(q, grad_out=grad_out, out=out, lse=lse)
         for name, t in (("grad_out", grad_out), ("out", out)):
             if t.shape != q.shape or t.dtype != q.dtype or (q.shape[3] > 1 and t.stride(3) != 1):
                 raise ValueError(f"{name} must be a {q.dtype} tensor of shape {tuple(q.shape)} "
                                  "with a contiguous last axis")
-        T.contiguous_f32(stats.lse, q.shape[:3], "stats.lse")
-        if stats.rest is not None and (stats.rest.stride() != out.stride()
-                                       or stats.rest.shape != out.shape
-                                       or stats.rest.dtype != out.dtype):
-            raise ValueError("stats.rest must have the result's layout")
+        T.contiguous_f32(lse, q.shape[:3], "lse")
         dq, dk, dv = _like(q), _like(k), _like(v)
         dt = torch.empty_like(self.table) if need_table else None
-        a = N.AttentionArgs(*self.head, out.data_ptr(), T.ptr(stats.rest), stats.lse.data_ptr(),
+        a = N.AttentionArgs(*self.head, out.data_ptr(), lse.data_ptr(),
                             grad_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
                             T.ptr(dt), *self.inputs, *_strides(out), *_strides(grad_out),
                             *_strides(dq), *_strides(dk), *_strides(dv))
@@ -210,37 +194,38 @@ def relative_attention(q, k, v, table, buckets, *, scale=None, causal: bool = Fa
 
 def relative_attention_forward(q, k, v, table, buckets, *, scale=None, causal: bool = False,
                                key_lengths=None, query_offset=0):
-    """(o, AttentionStats) for relative_attention_backward."""
+    """(o, lse): the result and the float32 log sum exp of every query's scores
+    [batch, heads, time], which relative_attention_backward takes."""
     return _Call(q, k, v, table, buckets, scale, causal, key_lengths, query_offset).forward(True)
 
 
-def relative_attention_backward(grad_out, q, k, v, table, buckets, out, stats, *, scale=None,
+def relative_attention_backward(grad_out, q, k, v, table, buckets, out, lse, *, scale=None,
                                 causal: bool = False, key_lengths=None, query_offset=0):
     """(grad_q, grad_k, grad_v, grad_table) of sum(grad_out * o), from the
-    forward's inputs, result and stats."""
+    forward's inputs and both its results."""
     return _Call(q, k, v, table, buckets, scale, causal, key_lengths,
-                 query_offset).backward(grad_out, out, stats)
+                 query_offset).backward(grad_out, out, lse)
 
 
 class _RelativeAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, table, buckets, scale, causal, key_lengths, query_offset):
-        o, stats = relative_attention_forward(q, k, v, table, buckets, scale=scale, causal=causal,
+        o, lse = relative_attention_forward(q, k, v, table, buckets, scale=scale, causal=causal,
                                               key_lengths=key_lengths, query_offset=query_offset)
         offset = query_offset if isinstance(query_offset, torch.Tensor) else None
         ctx.how = (scale, causal, query_offset if offset is None else None)
-        ctx.save_for_backward(q, k, v, table, buckets, key_lengths, offset, o, *stats)
+        ctx.save_for_backward(q, k, v, table, buckets, key_lengths, offset, o, lse)
         return o
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
-        q, k, v, table, buckets, lengths, offset, o, lse, rest = ctx.saved_tensors
+        q, k, v, table, buckets, lengths, offset, o, lse = ctx.saved_tensors
         scale, causal, value = ctx.how
         if grad.stride(-1) != 1:
             grad = grad.contiguous()
         call = _Call(q, k, v, table, buckets, scale, causal, lengths,
                      value if offset is None else offset)
-        grads = call.backward(grad, o, AttentionStats(lse, rest), ctx.needs_input_grad[3])
+        grads = call.backward(grad, o, lse, ctx.needs_input_grad[3])
         return (*(g if need else None for g, need in zip(grads, ctx.needs_input_grad)),
                 None, None, None, None, None)

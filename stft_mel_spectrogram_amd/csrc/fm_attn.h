@@ -129,30 +129,58 @@ __device__ __forceinline__ Frag<T> acc_frag(const acc16& a, int c) {
 
 // A tile of ROWS rows on its way from memory to LDS: 16-byte groups held by
 // NT threads.  Rows from `valid` on and columns from `dim` on become zero;
-// nothing past them is read.
-template <class T, int DP, int ROWS, int NT>
+// nothing past them is read.  VEC (rows of whole, aligned 16-byte groups):
+// buffer loads whose range ends with the last valid row, so that neither end
+// costs an instruction; a thread's offsets never change.
+template <class T, int DP, int ROWS, int NT, bool VEC>
 struct TileLoad {
   static constexpr int ch = Tile<T, DP>::chunks;
   static constexpr int n = (ROWS * ch + NT - 1) / NT;
   static constexpr int ve = Vec16<T>::n;
-  Vec16<T> v[n];
-  __device__ __forceinline__ void load(const T* base, int64_t stride, int valid, int dim, int tid) {
+  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+  u4 v[n];
+  uint32_t at[VEC ? n : 1];
+  __device__ __forceinline__ void init(int64_t stride, int dim, int tid) {
+    if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const int c = i * NT + tid, row = c / ch, col = (c - row * ch) * ve;
-      const int have = row < valid && row < ROWS ? dim - col : 0;
-      v[i] = load16_part(base + row * stride + col, have, (T)0.f);
+      for (int i = 0; i < n; ++i) {
+        const int c = i * NT + tid, row = c / ch, col = (c - row * ch) * ve;
+        at[i] = row < ROWS && col < dim ? (uint32_t)((row * stride + col) * sizeof(T)) : 0x7ffffff0u;
+      }
+    }
+  }
+  __device__ __forceinline__ void load(const T* base, int64_t stride, int valid, int dim, int tid) {
+    if constexpr (VEC) {
+      const int rows = valid < ROWS ? valid : ROWS;
+      const int bytes = rows <= 0 ? 0 : (int)(((rows - 1) * stride + dim) * sizeof(T));
+      const __amdgpu_buffer_rsrc_t r =
+          __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, bytes, 0x00020000);
+#pragma unroll
+      for (int i = 0; i < n; ++i) v[i] = __builtin_amdgcn_raw_buffer_load_b128(r, at[i], 0, 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const int c = i * NT + tid, row = c / ch, col = (c - row * ch) * ve;
+        const int have = row < valid && row < ROWS ? dim - col : 0;
+        v[i] = __builtin_bit_cast(u4, load16_part(base + row * stride + col, have, (T)0.f));
+      }
     }
   }
   __device__ __forceinline__ void store(T* tile, int tid) const {
 #pragma unroll
     for (int i = 0; i < n; ++i) {
       const int c = i * NT + tid, row = c / ch, col = (c - row * ch) * ve;
-      if (ROWS * ch % NT == 0 || row < ROWS)
-        *(Vec16<T>*)__builtin_assume_aligned(tile + row * Tile<T, DP>::ld + col, 16) = v[i];
+      if (ROWS * ch % NT == 0 || row < ROWS) *(u4*)(tile + row * Tile<T, DP>::ld + col) = v[i];
     }
   }
 };
+
+// Waves per SIMD the big kernels are compiled for.  Two keep their registers
+// within 256, which the products' results then share with the vector unit;
+// beyond, the compiler moves every score between the two register files.
+// float32 fragments of more than 64 columns do not fit.
+template <class T, int DP>
+constexpr int attn_waves() { return sizeof(T) == 2 || DP == 64 ? 2 : 1; }
 
 // Bias by distance, as the accumulators' start: table value / scale, so that
 // one multiplication scales both.  The window covers every distance of a
@@ -178,37 +206,33 @@ __device__ __forceinline__ int position_of_first(const AttnArgs& a, int b) {
   return clamp_int(o, -(1 << 30), 1 << 30);
 }
 
-// Start of a 32x32 tile whose rows are keys and whose columns are queries:
-// dist = first key - first query's position.  Rows 8 (r / 4) + 4 h + r % 4,
-// column n: distance dist + row - n.
-__device__ __forceinline__ acc16 bias_start_keys(const float* bias, int far, int dist, float lo,
-                                                 float hi, int h, int n) {
+// A 32x32 tile's place against the window, dist = first key - first query's
+// position: all of it at or beyond -far or far (one bias for every pair), or
+// not (the window's values start the accumulators).
+__device__ __forceinline__ bool tile_before(int dist, int far) { return dist + 31 <= -far; }
+__device__ __forceinline__ bool tile_behind(int dist, int far) { return dist - 31 >= far; }
+// Rows keys, columns queries: rows 8 (r / 4) + 4 h + r % 4, column n have
+// distance dist + row - n.
+__device__ __forceinline__ acc16 bias_start_keys(const float* bias, int far, int dist, int h, int n) {
+  const float* p = bias + dist + far + kBiasPad + 4 * h - n;
   acc16 acc;
-  if (dist + 31 <= -far || dist - 31 >= far) {
-    const float c = dist < 0 ? lo : hi;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) acc[r] = c;
-  } else {
-    const float* p = bias + dist + far + kBiasPad + 4 * h - n;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) acc[r] = p[8 * (r / 4) + r % 4];
-  }
+  for (int r = 0; r < 16; ++r) acc[r] = p[8 * (r / 4) + r % 4];
   return acc;
 }
-// The same with queries as rows and keys as columns: distance dist + n - row.
-__device__ __forceinline__ acc16 bias_start_queries(const float* bias, int far, int dist, float lo,
-                                                    float hi, int h, int n) {
+// Rows queries, columns keys: distance dist + n - row.
+__device__ __forceinline__ acc16 bias_start_queries(const float* bias, int far, int dist, int h, int n) {
+  const float* p = bias + dist + far + kBiasPad - 4 * h + n;
   acc16 acc;
-  if (dist + 31 <= -far || dist - 31 >= far) {
-    const float c = dist < 0 ? lo : hi;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) acc[r] = c;
-  } else {
-    const float* p = bias + dist + far + kBiasPad - 4 * h + n;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) acc[r] = p[-(8 * (r / 4) + r % 4)];
-  }
+  for (int r = 0; r < 16; ++r) acc[r] = p[-(8 * (r / 4) + r % 4)];
   return acc;
+}
+__device__ __forceinline__ acc16 acc_zero() {
+  acc16 a;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) a[r] = 0.f;
+  return a;
 }
 
 template <class T>

@@ -12,8 +12,13 @@ namespace fm {
 
 constexpr int kAttnThreads = 256;
 constexpr int kAttnBlockKeys = 128;  // keys of a dk, dv workgroup
+// Rows of an LDS tile: two 32-row steps for 16-bit types, one for float32;
+// one in the dq kernel of 128 columns too, whose registers do not hold the
+// next 64 rows.
 template <class T>
 constexpr int attn_step() { return sizeof(T) == 2 ? 64 : 32; }
+template <class T, int DP>
+constexpr int attn_dq_step() { return DP < 128 ? attn_step<T>() : 32; }
 
 // float16 has no room for small gradients: ds is scaled by the power of two
 // that brings the largest |do| into [1, 2), so that ds stays within a few
@@ -34,26 +39,58 @@ constexpr bool kIsF16 = false;
 template <>
 inline constexpr bool kIsF16<f16_t> = true;
 
-// Sums of ds by distance: one array per half wave, so that no two lanes of an
-// instruction add to one address and the order of additions is the program's.
-constexpr int kTableArrays = 8;
+// Sums of ds by distance inside the window.  A 32x32 tile's 63 diagonals come
+// from a wave's scratch in LDS: 16 queries at a time are stored as rows of 32
+// keys with zeros between them, and lane t adds up diagonal t (key - query = t -
+// 31) over the 16 rows, consecutive lanes at consecutive addresses.  The sums
+// are added to the wave's own window without atomics: 16 atomic additions per
+// tile and wave instead cost 170 cycles each (dq at 64 columns, 8 x 16 heads x
+// 1501: 510 us, most of it there).
+constexpr int kDiagRow = 68;  // 32 keys, 36 zeros (at least 31 on either side)
+constexpr int kDiagScratch = 32 + 16 * kDiagRow;
 
 template <class T, int DP>
 constexpr size_t attn_dq_lds(int far, bool table) {
-  return 4 * attn_step<T>() * Tile<T, DP>::ld * sizeof(T) +
-         bias_window(far) * sizeof(float) * (table ? 1 + kTableArrays : 1) + 8 * sizeof(float);
+  return 4 * attn_dq_step<T, DP>() * Tile<T, DP>::ld * sizeof(T) +
+         (table ? 4 * kDiagScratch * sizeof(float) : 0) +
+         bias_window(far) * sizeof(float) * (table ? 5 : 1) + 8 * sizeof(float);
 }
 
-template <class T, int DP, bool TABLE>
-__global__ __launch_bounds__(kAttnThreads) void attn_dq_kernel(const AttnArgs a) {
-  constexpr int BK = attn_step<T>(), NS = BK / 32, LD = Tile<T, DP>::ld, KS = DP / 16, DT = DP / 32;
+__device__ __forceinline__ float tile_diagonals(float* scratch, const acc16& s, int h, int n, int lane) {
+  float sum = 0.f;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    if ((n >> 4) == half) {
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        *(float4*)(scratch + 32 + (n & 15) * kDiagRow + 8 * y + 4 * h) =
+            make_float4(s[4 * y], s[4 * y + 1], s[4 * y + 2], s[4 * y + 3]);
+    }
+    // the lanes' stores above are seen by the wave's reads below
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    const float* p = scratch + 1 + 16 * half + lane;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum += p[(kDiagRow + 1) * i];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+  return sum;
+}
+
+template <class T, int DP, bool TABLE, bool VEC>
+__global__ __launch_bounds__(kAttnThreads, (attn_waves<T, DP>())) void attn_dq_kernel(const AttnArgs a) {
+  constexpr int BK = attn_dq_step<T, DP>(), NS = BK / 32, LD = Tile<T, DP>::ld, KS = DP / 16, DT = DP / 32;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   T* kt = (T*)smem;
   T* vt = kt + 2 * BK * LD;
-  float* bias = (float*)(vt + 2 * BK * LD);
+  float* diag = (float*)(vt + 2 * BK * LD);  // [4][kDiagScratch]
+  float* bias = diag + (TABLE ? 4 * kDiagScratch : 0);
   const int win = bias_window(a.far);
   float* ends = bias + win;  // [4][2]
-  float* sums = ends + 8;    // [kTableArrays][win]
+  float* sums = ends + 8;    // [4][win]
 
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 31, h = lane >> 5;
   const int blocks = (a.q_len + kAttnQueries - 1) / kAttnQueries;
@@ -70,7 +107,9 @@ __global__ __launch_bounds__(kAttnThreads) void attn_dq_kernel(const AttnArgs a)
 
   const T* kp = (const T*)a.k + b * a.ks[0] + kvh * a.ks[1];
   const T* vp = (const T*)a.v + b * a.vs[0] + kvh * a.vs[1];
-  TileLoad<T, DP, BK, kAttnThreads> kl, vl;
+  TileLoad<T, DP, BK, kAttnThreads, VEC> kl, vl;
+  kl.init(a.ks[2], a.dim, tid);
+  vl.init(a.vs[2], a.dim, tid);
   kl.load(kp, a.ks[2], k_end, a.dim, tid);
   vl.load(vp, a.vs[2], k_end, a.dim, tid);
   const int64_t row = (int64_t)(b * a.heads + head) * a.q_len + i;
@@ -91,11 +130,6 @@ __global__ __launch_bounds__(kAttnThreads) void attn_dq_kernel(const AttnArgs a)
         delta = fmaf((float)gf[s][e], (float)of[e], delta);
         amax = fmaxf(amax, fabsf((float)gf[s][e]));
       }
-      if (a.o_rest) {
-        const Frag<T> rf = load_frag((const T*)a.o_rest + off + d, have);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) delta = fmaf((float)gf[s][e], (float)rf[e], delta);
-      }
     }
     delta += __shfl_xor(delta, 32, 64);
     amax = fmaxf(amax, __shfl_xor(amax, 32, 64));
@@ -113,8 +147,10 @@ __global__ __launch_bounds__(kAttnThreads) void attn_dq_kernel(const AttnArgs a)
   const float unit = kIsF16<T> ? unit_scale(amax) : 1.f;
   fill_bias<T>(a, head, bias, tid, kAttnThreads);
   const float lo = bias_of<T>(a, head, -a.far) / a.scale, hi = bias_of<T>(a, head, a.far) / a.scale;
-  if constexpr (TABLE)
-    for (int t = tid; t < kTableArrays * win; t += kAttnThreads) sums[t] = 0.f;
+  if constexpr (TABLE) {
+    for (int t = tid; t < 4 * win; t += kAttnThreads) sums[t] = 0.f;
+    for (int t = tid; t < 4 * kDiagScratch; t += kAttnThreads) diag[t] = 0.f;
+  }
   kl.store(kt, tid);
   vl.store(vt, tid);
   __syncthreads();
@@ -124,8 +160,10 @@ __global__ __launch_bounds__(kAttnThreads) void attn_dq_kernel(const AttnArgs a)
   for (int d = 0; d < DT; ++d)
 #pragma unroll
     for (int r = 0; r < 16; ++r) dq[d][r] = 0.f;
-  float before = 0.f, behind = 0.f;  // ds of the far tiles on either side
-  float* mysums = sums + (wave * 2 + h) * win;
+  // per query: ds and p over the tiles on either side of the window, ds inside
+  float before = 0.f, behind = 0.f, inside = 0.f, p_before = 0.f, p_behind = 0.f;
+  float* mysums = sums + wave * win;
+  float* mydiag = diag + wave * kDiagScratch;
   const float c = a.scale * kLog2e;
   const int mine = a.causal ? min(len, first + i + 1) : len;
   const int least = a.causal ? min(len, first + q0 + 1) : len;
@@ -145,12 +183,20 @@ __global__ __launch_bounds__(kAttnThreads) void attn_dq_kernel(const AttnArgs a)
 #pragma unroll
       for (int u = 0; u < NS; ++u) {
         const int dist = j0 + 32 * u - first - q0;
-        acc16 s = bias_start_keys(bias, a.far, dist, lo, hi, h, n);
-        acc16 dp;
+        const bool is_before = tile_before(dist, a.far), is_behind = tile_behind(dist, a.far);
+        const Frag<T> k0 = tile_rows<T, DP>(ktb, 32 * u + n, 0, h);
+        acc16 s;
+        float far_bias;
+        if (is_before || is_behind) {
+          s = mma32(k0, qf[0], acc_zero());
+          far_bias = dist < 0 ? lo : hi;
+        } else {
+          s = mma32(k0, qf[0], bias_start_keys(bias, a.far, dist, h, n));
+          far_bias = 0.f;
+        }
 #pragma unroll
-        for (int r = 0; r < 16; ++r) dp[r] = 0.f;
-#pragma unroll
-        for (int x = 0; x < KS; ++x) s = mma32(tile_rows<T, DP>(ktb, 32 * u + n, x, h), qf[x], s);
+        for (int x = 1; x < KS; ++x) s = mma32(tile_rows<T, DP>(ktb, 32 * u + n, x, h), qf[x], s);
+        acc16 dp = acc_zero();
 #pragma unroll
         for (int x = 0; x < KS; ++x) dp = mma32(tile_rows<T, DP>(vtb, 32 * u + n, x, h), gf[x], dp);
         if (j0 + 32 * u + 32 > least) {
@@ -158,22 +204,25 @@ __global__ __launch_bounds__(kAttnThreads) void attn_dq_kernel(const AttnArgs a)
           for (int r = 0; r < 16; ++r)
             s[r] = j0 + 32 * u + 8 * (r / 4) + 4 * h + r % 4 < mine ? s[r] : -INFINITY;
         }
+        const float t = fmaf(far_bias, c, -lse2);
+        if (TABLE && (is_before || is_behind)) {
+          float p_sum = 0.f, ds_sum = 0.f;
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse2)) * (dp[r] - delta);
-        if constexpr (TABLE) {
-          if (dist + 31 <= -a.far) {
+          for (int r = 0; r < 16; ++r) {
+            const float p = __builtin_amdgcn_exp2f(fmaf(s[r], c, t));
+            p_sum += p;
+            s[r] = p * (dp[r] - delta);
+            ds_sum += s[r];
+          }
+          (is_before ? before : behind) += ds_sum;
+          (is_before ? p_before : p_behind) += p_sum;
+        } else {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) before += s[r];
-          } else if (dist - 31 >= a.far) {
+          for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, t)) * (dp[r] - delta);
+          if constexpr (TABLE) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) behind += s[r];
-          } else {
-            float* p = mysums + dist + a.far + kBiasPad + 4 * h - n;
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-              __hip_atomic_fetch_add(p + 8 * (r / 4) + r % 4, s[r], __ATOMIC_RELAXED,
-                                     __HIP_MEMORY_SCOPE_WORKGROUP);
+            for (int r = 0; r < 16; ++r) inside += s[r];
+            mysums[dist - 31 + a.far + kBiasPad + lane] += tile_diagonals(mydiag, s, h, n, lane);
           }
         }
         if constexpr (kIsF16<T>) {
@@ -210,8 +259,15 @@ __global__ __launch_bounds__(kAttnThreads) void attn_dq_kernel(const AttnArgs a)
       }
   }
   if constexpr (TABLE) {
-    before = lanes_sum<64>(before);
-    behind = lanes_sum<64>(behind);
+    // A query's ds add up to 0.  What they add up to here is the error of
+    // delta, whose o was rounded (its probabilities before, itself after): as
+    // much times a pair's p is in each ds.  The far sides hold most of a long
+    // row's probability in one bucket each, where these errors would add up;
+    // there they are taken out.
+    const float off = before + behind + inside;
+    const float all = off + __shfl_xor(off, 32, 64);
+    before = lanes_sum<64>(fmaf(-all, p_before, before));
+    behind = lanes_sum<64>(fmaf(-all, p_behind, behind));
     if (lane == 0) {
       ends[2 * wave] = before;
       ends[2 * wave + 1] = behind;
@@ -222,7 +278,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_dq_kernel(const AttnArgs a)
     for (int t = tid; t < win; t += kAttnThreads) {
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kTableArrays; ++w) v += sums[w * win + t];
+      for (int w = 0; w < 4; ++w) v += sums[w * win + t];
       if (t == 0) v += (ends[0] + ends[2]) + (ends[4] + ends[6]);
       if (t == win - 1) v += (ends[1] + ends[3]) + (ends[5] + ends[7]);
       out[t] = v;
@@ -254,22 +310,30 @@ __global__ __launch_bounds__(1024) void attn_table_distances_kernel(const AttnAr
   }
 }
 
-// ... and by bucket, one head per workgroup, one thread per bucket.
+// ... and by bucket, one head per workgroup: the threads beyond one per bucket
+// take further shares of the distances.
 template <class W>
-__global__ __launch_bounds__(kAttnThreads) void attn_table_buckets_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(1024) void attn_table_buckets_kernel(const AttnArgs a) {
   __shared__ float dist[bias_window(kAttnMaxFar)];
-  __shared__ int16_t bucket[bias_window(kAttnMaxFar)];
-  const int win = bias_window(a.far), head = blockIdx.x;
-  for (int t = threadIdx.x; t < win; t += kAttnThreads) {
+  __shared__ int bucket[bias_window(kAttnMaxFar)];
+  __shared__ float red[1024];
+  const int win = bias_window(a.far), head = blockIdx.x, tid = threadIdx.x;
+  for (int t = tid; t < win; t += 1024) {
     dist[t] = a.table_dist[(int64_t)head * win + t];
-    const int b = a.map[clamp_int(t - kBiasPad, 0, 2 * a.far)];
-    bucket[t] = (int16_t)(b < 0 || b >= a.num_buckets ? -1 : b);
+    bucket[t] = a.map[clamp_int(t - kBiasPad, 0, 2 * a.far)];
   }
   __syncthreads();
-  for (int k = threadIdx.x; k < a.num_buckets; k += kAttnThreads) {
-    float s = 0.f;
-    for (int t = 0; t < win; ++t) s += bucket[t] == k ? dist[t] : 0.f;
-    ((W*)a.d_table)[(int64_t)k * a.heads + head] = (W)s;
+  const int shares = 1024 / a.num_buckets, k = tid % a.num_buckets, share = tid / a.num_buckets;
+  const int per = (win + shares - 1) / shares;
+  float s = 0.f;
+  if (share < shares)
+    for (int t = share * per; t < min((share + 1) * per, win); ++t) s += bucket[t] == k ? dist[t] : 0.f;
+  red[tid] = s;
+  __syncthreads();
+  if (tid < a.num_buckets) {
+    float v = 0.f;
+    for (int x = 0; x < shares; ++x) v += red[x * a.num_buckets + tid];
+    ((W*)a.d_table)[(int64_t)tid * a.heads + head] = (W)v;
   }
 }
 
@@ -279,8 +343,8 @@ constexpr size_t attn_dkv_lds(int far) {
          bias_window(far) * sizeof(float);
 }
 
-template <class T, int DP>
-__global__ __launch_bounds__(kAttnThreads) void attn_dkv_kernel(const AttnArgs a) {
+template <class T, int DP, bool VEC>
+__global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 ? 2 : 1)) void attn_dkv_kernel(const AttnArgs a) {
   constexpr int BQ = attn_step<T>(), NS = BQ / 32, LD = Tile<T, DP>::ld, KS = DP / 16, DT = DP / 32;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   // float32 fragments of 128 columns leave no registers for the next tile
@@ -341,7 +405,9 @@ __global__ __launch_bounds__(kAttnThreads) void attn_dkv_kernel(const AttnArgs a
     const T* qp = (const T*)a.q + b * a.qs[0] + head * a.qs[1];
     const T* gp = (const T*)a.d_o + b * a.dos[0] + head * a.dos[1];
     const int64_t row0 = (int64_t)(b * a.heads + head) * a.q_len;
-    TileLoad<T, DP, BQ, kAttnThreads> ql, gl;
+    TileLoad<T, DP, BQ, kAttnThreads, VEC> ql, gl;
+    ql.init(a.qs[2], a.dim, tid);
+    gl.init(a.dos[2], a.dim, tid);
     float l_next = 0.f, d_next = 0.f;
     const auto fetch = [&](int i0) {
       ql.load(qp + (int64_t)i0 * a.qs[2], a.qs[2], i_end - i0, a.dim, tid);
@@ -376,15 +442,22 @@ __global__ __launch_bounds__(kAttnThreads) void attn_dkv_kernel(const AttnArgs a
 #pragma unroll
         for (int u = 0; u < NS; ++u) {
           const int iu = i0 + 32 * u;
-          acc16 s = bias_start_queries(bias, a.far, jw - first - iu, lo, hi, h, n);
-          acc16 dp;
-#pragma unroll
-          for (int r = 0; r < 16; ++r) dp[r] = 0.f;
-#pragma unroll
-          for (int x = 0; x < KS; ++x) {
-            s = mma32(tile_rows<T, DP>(qtb, 32 * u + n, x, h), kf[x], s);
-            dp = mma32(tile_rows<T, DP>(gtb, 32 * u + n, x, h), vf[x], dp);
+          const int dist = jw - first - iu;
+          const Frag<T> q0 = tile_rows<T, DP>(qtb, 32 * u + n, 0, h);
+          acc16 s;
+          float far_bias;
+          if (tile_before(dist, a.far) || tile_behind(dist, a.far)) {
+            s = mma32(q0, kf[0], acc_zero());
+            far_bias = (dist < 0 ? lo : hi) * c;
+          } else {
+            s = mma32(q0, kf[0], bias_start_queries(bias, a.far, dist, h, n));
+            far_bias = 0.f;
           }
+#pragma unroll
+          for (int x = 1; x < KS; ++x) s = mma32(tile_rows<T, DP>(qtb, 32 * u + n, x, h), kf[x], s);
+          acc16 dp = acc_zero();
+#pragma unroll
+          for (int x = 0; x < KS; ++x) dp = mma32(tile_rows<T, DP>(gtb, 32 * u + n, x, h), vf[x], dp);
           if (jw + 32 > len || (a.causal && jw + 31 - first > iu)) {
 #pragma unroll
             for (int r = 0; r < 16; ++r)
@@ -398,7 +471,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_dkv_kernel(const AttnArgs a
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int r = 4 * y + e;
-              s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -ls[e]));
+              s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, far_bias - ls[e]));
               if constexpr (kIsF16<T>)
                 dp[r] = s[r] * ((dp[r] - ds[e]) * back);
               else
@@ -439,22 +512,23 @@ __global__ __launch_bounds__(kAttnThreads) void attn_dkv_kernel(const AttnArgs a
     }
 }
 
-template <class T, int DP>
+template <class T, int DP, bool VEC>
 int attn_backward_dim(const AttnArgs& a, void* stream) {
-  static const int opted = lds_opt_in(attn_dq_kernel<T, DP, false>, attn_dq_lds<T, DP>(kAttnMaxFar, false)) |
-                           lds_opt_in(attn_dq_kernel<T, DP, true>, attn_dq_lds<T, DP>(kAttnMaxFar, true)) |
-                           lds_opt_in(attn_dkv_kernel<T, DP>, attn_dkv_lds<T, DP>(kAttnMaxFar));
+  static const int opted =
+      lds_opt_in(attn_dq_kernel<T, DP, false, VEC>, attn_dq_lds<T, DP>(kAttnMaxFar, false)) |
+      lds_opt_in(attn_dq_kernel<T, DP, true, VEC>, attn_dq_lds<T, DP>(kAttnMaxFar, true)) |
+      lds_opt_in(attn_dkv_kernel<T, DP, VEC>, attn_dkv_lds<T, DP>(kAttnMaxFar));
   if (opted != FM_OK) return set_error(FM_E_HIP, "attention backward: LDS size refused");
   const bool table = a.d_table != nullptr;
   if (a.q_len > 0) {
     const int st = launch("attention backward (dq)",
-                          table ? attn_dq_kernel<T, DP, true> : attn_dq_kernel<T, DP, false>,
+                          table ? attn_dq_kernel<T, DP, true, VEC> : attn_dq_kernel<T, DP, false, VEC>,
                           dim3(place_grid((int64_t)a.batch * a.heads, attn_query_blocks(a))),
                           dim3(kAttnThreads), attn_dq_lds<T, DP>(a.far, table), stream, a);
     if (st != FM_OK) return st;
   }
   if (a.k_len > 0)
-    return launch("attention backward (dk, dv)", attn_dkv_kernel<T, DP>,
+    return launch("attention backward (dk, dv)", attn_dkv_kernel<T, DP, VEC>,
                   dim3(place_grid((int64_t)a.batch * a.kv_heads,
                                   (a.k_len + kAttnBlockKeys - 1) / kAttnBlockKeys)),
                   dim3(kAttnThreads), attn_dkv_lds<T, DP>(a.far), stream, a);
@@ -464,17 +538,24 @@ int attn_backward_dim(const AttnArgs& a, void* stream) {
 template <class T>
 int attn_backward_t(const AttnArgs& a, void* stream) {
   int st = FM_OK;
-  if (a.batch > 0)
-    st = a.dim <= 64   ? attn_backward_dim<T, 64>(a, stream)
-         : a.dim <= 96 ? attn_backward_dim<T, 96>(a, stream)
-                       : attn_backward_dim<T, 128>(a, stream);
+  if (a.batch > 0) {
+    const bool vec = attn_groups(a.q, a.qs, a.dim, sizeof(T)) && attn_groups(a.k, a.ks, a.dim, sizeof(T)) &&
+                     attn_groups(a.v, a.vs, a.dim, sizeof(T)) && attn_groups(a.d_o, a.dos, a.dim, sizeof(T));
+    const auto go = [&](auto narrow, auto wide, auto widest) {
+      return a.dim <= 64 ? narrow(a, stream) : a.dim <= 96 ? wide(a, stream) : widest(a, stream);
+    };
+    st = vec ? go(attn_backward_dim<T, 64, true>, attn_backward_dim<T, 96, true>,
+                  attn_backward_dim<T, 128, true>)
+             : go(attn_backward_dim<T, 64, false>, attn_backward_dim<T, 96, false>,
+                  attn_backward_dim<T, 128, false>);
+  }
   if (st != FM_OK || !a.d_table) return st;
   st = launch("attention backward (distances)", attn_table_distances_kernel<T>,
               dim3((unsigned)(bias_window(a.far) + 63) / 64, (unsigned)a.heads), dim3(1024), 0, stream, a);
   if (st != FM_OK) return st;
   return launch("attention backward (buckets)",
                 a.table32 ? attn_table_buckets_kernel<float> : attn_table_buckets_kernel<T>,
-                dim3((unsigned)a.heads), dim3(kAttnThreads), 0, stream, a);
+                dim3((unsigned)a.heads), dim3(1024), 0, stream, a);
 }
 
 }  // namespace fm

@@ -21,8 +21,8 @@ constexpr size_t attn_forward_lds(int far) {
 // The transposed scores s' = K q' have queries as columns, so that a lane
 // keeps one query's running maximum and sum, and the probabilities are the
 // next product's right operand as they stand: o' = V' p'.
-template <class T, int DP, bool SPLIT>
-__global__ __launch_bounds__(kAttnThreads) void attn_forward_kernel(const AttnArgs a) {
+template <class T, int DP, bool SPLIT, bool VEC>
+__global__ __launch_bounds__(kAttnThreads, (attn_waves<T, DP>())) void attn_forward_kernel(const AttnArgs a) {
   constexpr int BK = attn_keys<T>(), NS = BK / 32, LD = Tile<T, DP>::ld, KS = DP / 16, DT = DP / 32;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   T* kt = (T*)smem;              // [2][BK][LD]
@@ -49,7 +49,9 @@ __global__ __launch_bounds__(kAttnThreads) void attn_forward_kernel(const AttnAr
 
   const T* kp = (const T*)a.k + b * a.ks[0] + kvh * a.ks[1];
   const T* vp = (const T*)a.v + b * a.vs[0] + kvh * a.vs[1];
-  TileLoad<T, DP, BK, kAttnThreads> kl, vl;
+  TileLoad<T, DP, BK, kAttnThreads, VEC> kl, vl;
+  kl.init(a.ks[2], a.dim, tid);
+  vl.init(a.vs[2], a.dim, tid);
   kl.load(kp + k_beg * a.ks[2], a.ks[2], k_end - k_beg, a.dim, tid);
   vl.load(vp + k_beg * a.vs[2], a.vs[2], k_end - k_beg, a.dim, tid);
   Frag<T> qf[KS];
@@ -87,22 +89,34 @@ __global__ __launch_bounds__(kAttnThreads) void attn_forward_kernel(const AttnAr
       const T* ktb = kt + buf * BK * LD;
       const T* vtb = vt + buf * BK * LD;
       acc16 s[NS];
+      float far_bias[NS];  // of a tile that lies outside the window
 #pragma unroll
       for (int u = 0; u < NS; ++u) {
-        s[u] = bias_start_keys(bias, a.far, j0 + 32 * u - first - q0, lo, hi, h, n);
+        const int dist = j0 + 32 * u - first - q0;
+        const Frag<T> k0 = tile_rows<T, DP>(ktb, 32 * u + n, 0, h);
+        if (tile_before(dist, a.far) || tile_behind(dist, a.far)) {
+          s[u] = mma32(k0, qf[0], acc_zero());
+          far_bias[u] = dist < 0 ? lo : hi;
+        } else {
+          s[u] = mma32(k0, qf[0], bias_start_keys(bias, a.far, dist, h, n));
+          far_bias[u] = 0.f;
+        }
 #pragma unroll
-        for (int x = 0; x < KS; ++x) s[u] = mma32(tile_rows<T, DP>(ktb, 32 * u + n, x, h), qf[x], s[u]);
+        for (int x = 1; x < KS; ++x) s[u] = mma32(tile_rows<T, DP>(ktb, 32 * u + n, x, h), qf[x], s[u]);
         if (j0 + 32 * u + 32 > least) {
 #pragma unroll
           for (int r = 0; r < 16; ++r)
             s[u][r] = j0 + 32 * u + 8 * (r / 4) + 4 * h + r % 4 < mine ? s[u][r] : -INFINITY;
         }
       }
-      float mx = s[0][0];
+      float mx = -INFINITY;
 #pragma unroll
-      for (int u = 0; u < NS; ++u)
+      for (int u = 0; u < NS; ++u) {
+        float mu = s[u][0];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[u][r]);
+        for (int r = 1; r < 16; ++r) mu = fmaxf(mu, s[u][r]);
+        mx = fmaxf(mx, mu + far_bias[u]);
+      }
       mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
       const bool raise = mx > m + grow || (m == -INFINITY && mx > m);
       if (__any(raise)) {
@@ -119,12 +133,14 @@ __global__ __launch_bounds__(kAttnThreads) void attn_forward_kernel(const AttnAr
       const float mc = m == -INFINITY ? 0.f : m * c;
       float sum = 0.f;
 #pragma unroll
-      for (int u = 0; u < NS; ++u)
+      for (int u = 0; u < NS; ++u) {
+        const float t = fmaf(far_bias[u], c, -mc);
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          s[u][r] = __builtin_amdgcn_exp2f(fmaf(s[u][r], c, -mc));
+          s[u][r] = __builtin_amdgcn_exp2f(fmaf(s[u][r], c, t));
           sum += s[u][r];
         }
+      }
       l += sum;
 #pragma unroll
       for (int u = 0; u < NS; ++u)
@@ -172,15 +188,9 @@ __global__ __launch_bounds__(kAttnThreads) void attn_forward_kernel(const AttnAr
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         const int at_d = 32 * d + 8 * y + 4 * h;
-        if (at_d < a.dim) {
-          float v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = o[d][4 * y + e] * inv;
-          store4(op + at_d, v[0], v[1], v[2], v[3], a.dim - at_d);
-          if (a.o_rest)
-            store4((T*)a.o_rest + off + at_d, v[0] - (float)(T)v[0], v[1] - (float)(T)v[1],
-                   v[2] - (float)(T)v[2], v[3] - (float)(T)v[3], a.dim - at_d);
-        }
+        if (at_d < a.dim)
+          store4(op + at_d, o[d][4 * y] * inv, o[d][4 * y + 1] * inv, o[d][4 * y + 2] * inv,
+                 o[d][4 * y + 3] * inv, a.dim - at_d);
       }
   }
 }
@@ -198,7 +208,7 @@ constexpr size_t attn_token_lds() {
   return tiles > join ? tiles : join;
 }
 
-template <class T, int DP, bool SPLIT>
+template <class T, int DP, bool SPLIT, bool VEC>
 __global__ __launch_bounds__(kAttnThreads) void attn_token_kernel(const AttnArgs a) {
   constexpr int LD = Tile<T, DP>::ld, KS = DP / 32, DT = DP / 16;
   extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -235,7 +245,8 @@ __global__ __launch_bounds__(kAttnThreads) void attn_token_kernel(const AttnArgs
   float m = -INFINITY, l = 0.f;
 
   Frag<T> kf[2][KS];
-  TileLoad<T, DP, kTokenKeys, 64> vl;
+  TileLoad<T, DP, kTokenKeys, 64, VEC> vl;
+  vl.init(a.vs[2], a.dim, lane);
   const auto fetch = [&](int j) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -365,7 +376,6 @@ __global__ __launch_bounds__(kAttnThreads) void attn_token_kernel(const AttnArgs
     } else {
       const int64_t off = b * a.os[0] + hd * a.os[1] + qi * a.os[2] + d;
       ((T*)a.o)[off] = (T)out;
-      if (a.o_rest) ((T*)a.o_rest)[off] = (T)(out - (float)(T)out);
       if (a.lse && d == 0) a.lse[row] = lse;
     }
   }
@@ -402,43 +412,45 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(const AttnArgs 
   const int64_t off = bh / a.heads * a.os[0] + bh % a.heads * a.os[1] + i * a.os[2];
   v0 *= inv;
   v1 *= inv;
-  if (lane < a.dim) {
-    ((T*)a.o)[off + lane] = (T)v0;
-    if (a.o_rest) ((T*)a.o_rest)[off + lane] = (T)(v0 - (float)(T)v0);
-  }
-  if (lane + 64 < a.dim) {
-    ((T*)a.o)[off + lane + 64] = (T)v1;
-    if (a.o_rest) ((T*)a.o_rest)[off + lane + 64] = (T)(v1 - (float)(T)v1);
-  }
+  if (lane < a.dim) ((T*)a.o)[off + lane] = (T)v0;
+  if (lane + 64 < a.dim) ((T*)a.o)[off + lane + 64] = (T)v1;
   if (a.lse && lane == 0) a.lse[row] = mm == -INFINITY ? mm : ms + logf(sum);
 }
 
-template <class T, int DP>
+template <class T, int DP, bool VEC>
 int attn_forward_dim(const AttnArgs& a, void* stream) {
   if (attn_token_kernel(a)) {
-    static const int opted = lds_opt_in(attn_token_kernel<T, DP, false>, attn_token_lds<T, DP>()) |
-                             lds_opt_in(attn_token_kernel<T, DP, true>, attn_token_lds<T, DP>());
+    static const int opted =
+        lds_opt_in(attn_token_kernel<T, DP, false, VEC>, attn_token_lds<T, DP>()) |
+        lds_opt_in(attn_token_kernel<T, DP, true, VEC>, attn_token_lds<T, DP>());
     if (opted != FM_OK) return set_error(FM_E_HIP, "attention: LDS size refused");
     return launch("attention of single tokens",
-                  a.splits > 1 ? attn_token_kernel<T, DP, true> : attn_token_kernel<T, DP, false>,
+                  a.splits > 1 ? attn_token_kernel<T, DP, true, VEC>
+                               : attn_token_kernel<T, DP, false, VEC>,
                   dim3((unsigned)(a.batch * a.kv_heads), (unsigned)a.splits), dim3(kAttnThreads),
                   attn_token_lds<T, DP>(), stream, a);
   }
   static const int opted =
-      lds_opt_in(attn_forward_kernel<T, DP, false>, attn_forward_lds<T, DP>(kAttnMaxFar)) |
-      lds_opt_in(attn_forward_kernel<T, DP, true>, attn_forward_lds<T, DP>(kAttnMaxFar));
+      lds_opt_in(attn_forward_kernel<T, DP, false, VEC>, attn_forward_lds<T, DP>(kAttnMaxFar)) |
+      lds_opt_in(attn_forward_kernel<T, DP, true, VEC>, attn_forward_lds<T, DP>(kAttnMaxFar));
   if (opted != FM_OK) return set_error(FM_E_HIP, "attention: LDS size refused");
   return launch("attention",
-                a.splits > 1 ? attn_forward_kernel<T, DP, true> : attn_forward_kernel<T, DP, false>,
+                a.splits > 1 ? attn_forward_kernel<T, DP, true, VEC>
+                             : attn_forward_kernel<T, DP, false, VEC>,
                 dim3(place_grid((int64_t)a.batch * a.heads, attn_query_blocks(a)), (unsigned)a.splits),
                 dim3(kAttnThreads), attn_forward_lds<T, DP>(a.far), stream, a);
 }
 
 template <class T>
 int attn_forward_t(const AttnArgs& a, void* stream) {
-  const int st = a.dim <= 64   ? attn_forward_dim<T, 64>(a, stream)
-                 : a.dim <= 96 ? attn_forward_dim<T, 96>(a, stream)
-                               : attn_forward_dim<T, 128>(a, stream);
+  const bool vec = attn_groups(a.k, a.ks, a.dim, sizeof(T)) && attn_groups(a.v, a.vs, a.dim, sizeof(T));
+  const auto go = [&](auto narrow, auto wide, auto widest) {
+    return a.dim <= 64 ? narrow(a, stream) : a.dim <= 96 ? wide(a, stream) : widest(a, stream);
+  };
+  const int st = vec ? go(attn_forward_dim<T, 64, true>, attn_forward_dim<T, 96, true>,
+                          attn_forward_dim<T, 128, true>)
+                     : go(attn_forward_dim<T, 64, false>, attn_forward_dim<T, 96, false>,
+                          attn_forward_dim<T, 128, false>);
   if (st != FM_OK || a.splits == 1) return st;
   return launch("attention (join)", attn_join_kernel<T>, dim3((unsigned)((attn_rows(a) + 3) / 4)),
                 dim3(kAttnThreads), 0, stream, a);

@@ -115,7 +115,6 @@ int attention_args(const fm_attention_args* p, bool backward, AttnArgs& a) {
   if (q_units >= most || k_units >= most || attn_rows(a) >= most)
     return bad("attention: too many rows for one launch");
   a.o = p->o;
-  a.o_rest = p->dtype == FM_F32 ? nullptr : p->o_rest;
   a.lse = p->lse;
   a.d_o = p->grad_o;
   a.dq = p->grad_q;
@@ -134,7 +133,7 @@ int attention_pointers(const AttnArgs& a, int dtype) {
   if (q && (!a.q || !a.o)) return bad("attention: q and o must not be NULL");
   if (k && (!a.k || !a.v)) return bad("attention: k and v must not be NULL");
   if (!aligned(a.q, es) || !aligned(a.k, es) || !aligned(a.v, es) || !aligned(a.o, es) ||
-      !aligned(a.o_rest, es) || !aligned(a.d_o, es) || !aligned(a.dq, es) || !aligned(a.dk, es) ||
+      !aligned(a.d_o, es) || !aligned(a.dq, es) || !aligned(a.dk, es) ||
       !aligned(a.dv, es) || !aligned(a.map, 4) || !aligned(a.key_lengths, 4) ||
       !aligned(a.query_offset, 4))
     return bad("attention: misaligned pointer");

@@ -166,7 +166,6 @@ struct AttnArgs {
   float scale;
   int64_t qs[3], ks[3], vs[3], os[3];
   void* o;
-  void* o_rest;  // what rounding o to 16 bits left, or NULL
   float* lse;    // [batch, heads, q_len] or NULL
   // backward
   const void* d_o;
@@ -232,6 +231,15 @@ inline AttnBackwardSpace attn_backward_space(const AttnArgs& a, bool f16) {
   s.dist = s.part + attn_round16(4 * (int64_t)a.batch * a.heads * attn_query_blocks(a) * bias_window(a.far));
   s.total = s.dist + attn_round16(4 * (int64_t)a.heads * bias_window(a.far));
   return s;
+}
+
+// Whether rows are whole, aligned 16-byte groups and a tile of them lies
+// within a buffer load's reach (64 rows, 31-bit byte offsets).
+inline bool attn_groups(const void* p, const int64_t* stride, int dim, int size) {
+  const int n = 16 / size;
+  return dim % n == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride[0] % n == 0 &&
+         stride[1] % n == 0 && stride[2] % n == 0 &&
+         (63 * stride[2] + dim) * size < 0x7fff0000;
 }
 
 int attn_forward_f32(const AttnArgs& a, void* stream);

@@ -132,10 +132,10 @@ def run_case(q, k, v, table, m, do, scale=None, causal=False, lengths=None, offs
                                                      causal, full, off)
     close("o", o, ro, o_tol)
     empty = lse == -math.inf
-    assert torch.equal(stats.lse == -math.inf, empty)
+    assert torch.equal(stats == -math.inf, empty)
     assert (o[empty] == 0).all()
     fin = ~empty
-    close("lse", torch.where(fin, stats.lse, torch.zeros_like(stats.lse)),
+    close("lse", torch.where(fin, stats, torch.zeros_like(stats)),
           torch.where(fin, lse, torch.zeros_like(lse)), lse_tol + 64 * U * (1 + lse.abs().nan_to_num(posinf=0)))
     assert torch.equal(relative_attention(q, k, v, table, m, **how), o)
     if not backward:
