@@ -127,50 +127,71 @@ __device__ __forceinline__ Frag<T> acc_frag(const acc16& a, int c) {
   return __builtin_convertvector(v, Frag<T>);
 }
 
-// A tile of ROWS rows on its way from memory to LDS: 16-byte groups held by
-// NT threads.  Rows from `valid` on and columns from `dim` on become zero;
-// nothing past them is read.  VEC (rows of whole, aligned 16-byte groups):
-// buffer loads whose range ends with the last valid row, so that neither end
-// costs an instruction; a thread's offsets never change.
+// A tile of ROWS rows on its way from memory to LDS.  Rows from `valid` on and
+// columns from `dim` on become zero; nothing past them is read.
+//
+// VEC (rows of whole, aligned 16-byte groups): buffer loads whose range ends
+// with the last valid row, so that neither end costs an instruction, held in
+// registers until store().  A thread's groups lie a whole number of rows apart
+// where they can: then one offset serves all, with the step as the load's
+// scalar offset.
 template <class T, int DP, int ROWS, int NT, bool VEC>
 struct TileLoad {
   static constexpr int ch = Tile<T, DP>::chunks;
   static constexpr int n = (ROWS * ch + NT - 1) / NT;
   static constexpr int ve = Vec16<T>::n;
+  static constexpr bool even = NT % ch == 0 && ROWS % (NT / ch) == 0;
   typedef uint32_t u4 __attribute__((ext_vector_type(4)));
   u4 v[n];
-  uint32_t at[VEC ? n : 1];
+  uint32_t at[even ? 1 : n];
+  uint32_t step;
   __device__ __forceinline__ void init(int64_t stride, int dim, int tid) {
-    if constexpr (VEC) {
+    step = even ? (uint32_t)(NT / ch * stride * sizeof(T)) : 0u;
 #pragma unroll
-      for (int i = 0; i < n; ++i) {
-        const int c = i * NT + tid, row = c / ch, col = (c - row * ch) * ve;
-        at[i] = row < ROWS && col < dim ? (uint32_t)((row * stride + col) * sizeof(T)) : 0x7ffffff0u;
-      }
+    for (int i = 0; i < (even ? 1 : n); ++i) {
+      const int c = i * NT + tid, row = c / ch, col = (c - row * ch) * ve;
+      at[i] = row < ROWS && col < dim ? (uint32_t)((row * stride + col) * sizeof(T)) : 0x7ffffff0u;
     }
   }
   __device__ __forceinline__ void load(const T* base, int64_t stride, int valid, int dim, int tid) {
-    if constexpr (VEC) {
-      const int rows = valid < ROWS ? valid : ROWS;
-      const int bytes = rows <= 0 ? 0 : (int)(((rows - 1) * stride + dim) * sizeof(T));
-      const __amdgpu_buffer_rsrc_t r =
-          __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, bytes, 0x00020000);
+    const int rows = valid < ROWS ? valid : ROWS;
+    const int bytes = rows <= 0 ? 0 : (int)(((rows - 1) * stride + dim) * sizeof(T));
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, bytes, 0x00020000);
 #pragma unroll
-      for (int i = 0; i < n; ++i) v[i] = __builtin_amdgcn_raw_buffer_load_b128(r, at[i], 0, 0);
-    } else {
-#pragma unroll
-      for (int i = 0; i < n; ++i) {
-        const int c = i * NT + tid, row = c / ch, col = (c - row * ch) * ve;
-        const int have = row < valid && row < ROWS ? dim - col : 0;
-        v[i] = __builtin_bit_cast(u4, load16_part(base + row * stride + col, have, (T)0.f));
-      }
-    }
+    for (int i = 0; i < n; ++i)
+      v[i] = __builtin_amdgcn_raw_buffer_load_b128(r, at[even ? 0 : i], even ? i * step : 0, 0);
   }
   __device__ __forceinline__ void store(T* tile, int tid) const {
 #pragma unroll
     for (int i = 0; i < n; ++i) {
       const int c = i * NT + tid, row = c / ch, col = (c - row * ch) * ve;
       if (ROWS * ch % NT == 0 || row < ROWS) *(u4*)(tile + row * Tile<T, DP>::ld + col) = v[i];
+    }
+  }
+};
+// Rows of any width, stride and alignment: nothing is held, store() copies
+// group by group.
+template <class T, int DP, int ROWS, int NT>
+struct TileLoad<T, DP, ROWS, NT, false> {
+  static constexpr int ch = Tile<T, DP>::chunks;
+  static constexpr int ve = Vec16<T>::n;
+  const T* base;
+  int64_t stride;
+  int valid, dim;
+  __device__ __forceinline__ void init(int64_t, int, int) {}
+  __device__ __forceinline__ void load(const T* base_, int64_t stride_, int valid_, int dim_, int) {
+    base = base_;
+    stride = stride_;
+    valid = valid_;
+    dim = dim_;
+  }
+  __device__ __forceinline__ void store(T* tile, int tid) const {
+#pragma unroll 1
+    for (int c = tid; c < ROWS * ch; c += NT) {
+      const int row = c / ch, col = (c - row * ch) * ve;
+      *(Vec16<T>*)__builtin_assume_aligned(tile + row * Tile<T, DP>::ld + col, 16) =
+          load16_part(base + row * stride + col, row < valid ? dim - col : 0, (T)0.f);
     }
   }
 };
@@ -242,25 +263,45 @@ __device__ __forceinline__ void fill_bias(const AttnArgs& a, int head, float* bi
     bias[i] = bias_of<T>(a, head, i - a.far - kBiasPad) * inv;
 }
 
-// Which (entry, head) and block a workgroup takes.  Workgroups go round the 8
-// XCDs one by one; where the heads divide among them, an XCD keeps whole
-// heads (neighbouring ones, which share keys), so that their keys and values
-// stay in its L2.
+// Which unit (entry, key head) and which of its blocks a workgroup takes.
+// Workgroups go round the 8 XCDs one by one; where the units divide among them,
+// an XCD keeps whole units, whose keys and values then stay in its L2.  Units
+// go round the XCDs too: the heads of a long entry would otherwise share one
+// XCD (8 entries of 1501 to 845 keys, 16 heads, forward: 102 us against ...).
 struct Place {
   int unit, block;
   bool none;
 };
+__host__ __device__ inline bool place_by_xcd(int64_t units) { return units % 8 == 0 || units >= 64; }
 __device__ __forceinline__ Place place_of(int units, int blocks, int id) {
-  if (units % 8 == 0 || units >= 64) {
-    const int per = (units + 7) / 8;
-    const int x = id & 7, t = id >> 3;
-    const int u = x * per + t / blocks;
-    return {u, t % blocks, u >= units || t / blocks >= per};
+  if (place_by_xcd(units)) {
+    const int t = id >> 3, u = t / blocks * 8 + (id & 7);
+    return {u, t % blocks, u >= units};
   }
   return {id / blocks, id % blocks, id / blocks >= units};
 }
 inline unsigned place_grid(int64_t units, int64_t blocks) {
-  return (unsigned)((units % 8 == 0 || units >= 64) ? (units + 7) / 8 * 8 * blocks : units * blocks);
+  return (unsigned)(place_by_xcd(units) ? (units + 7) / 8 * 8 * blocks : units * blocks);
+}
+
+// The wave of a thread as a scalar: what depends on it alone then branches
+// without touching the lane mask.
+__device__ __forceinline__ int wave_index() {
+  return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+}
+
+__device__ __forceinline__ float as_scalar(float x) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
+}
+
+// Over the two halves of a wave, in every lane.
+__device__ __forceinline__ float halves_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float halves_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
 // Stores 4 consecutive elements of a result column's rows.

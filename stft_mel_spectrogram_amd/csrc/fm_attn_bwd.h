@@ -12,13 +12,12 @@ namespace fm {
 
 constexpr int kAttnThreads = 256;
 constexpr int kAttnBlockKeys = 128;  // keys of a dk, dv workgroup
-// Rows of an LDS tile: two 32-row steps for 16-bit types, one for float32;
-// one in the dq kernel of 128 columns too, whose registers do not hold the
-// next 64 rows.
+// Rows of an LDS tile: two 32-row steps for 16-bit types in the dk, dv kernel,
+// one for float32 and in the dq kernel (at 64 columns three waves per SIMD
+// then fit, by registers and by LDS: 157 us against 166 with 64 rows).
 template <class T>
 constexpr int attn_step() { return sizeof(T) == 2 ? 64 : 32; }
-template <class T, int DP>
-constexpr int attn_dq_step() { return DP < 128 ? attn_step<T>() : 32; }
+constexpr int kDqStep = 32;
 
 // float16 has no room for small gradients: ds is scaled by the power of two
 // that brings the largest |do| into [1, 2), so that ds stays within a few
@@ -49,9 +48,13 @@ inline constexpr bool kIsF16<f16_t> = true;
 constexpr int kDiagRow = 68;  // 32 keys, 36 zeros (at least 31 on either side)
 constexpr int kDiagScratch = 32 + 16 * kDiagRow;
 
+// float16's scale takes the registers that a third wave would need.
+template <class T, int DP, bool VEC>
+constexpr int kDqWaves = sizeof(T) == 2 && DP == 64 && VEC && !kIsF16<T> ? 3 : attn_waves<T, DP>();
+
 template <class T, int DP>
 constexpr size_t attn_dq_lds(int far, bool table) {
-  return 4 * attn_dq_step<T, DP>() * Tile<T, DP>::ld * sizeof(T) +
+  return 4 * kDqStep * Tile<T, DP>::ld * sizeof(T) +
          (table ? 4 * kDiagScratch * sizeof(float) : 0) +
          bias_window(far) * sizeof(float) * (table ? 5 : 1) + 8 * sizeof(float);
 }
@@ -81,8 +84,8 @@ __device__ __forceinline__ float tile_diagonals(float* scratch, const acc16& s, 
 }
 
 template <class T, int DP, bool TABLE, bool VEC>
-__global__ __launch_bounds__(kAttnThreads, (attn_waves<T, DP>())) void attn_dq_kernel(const AttnArgs a) {
-  constexpr int BK = attn_dq_step<T, DP>(), NS = BK / 32, LD = Tile<T, DP>::ld, KS = DP / 16, DT = DP / 32;
+__global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_kernel(const AttnArgs a) {
+  constexpr int BK = kDqStep, NS = BK / 32, LD = Tile<T, DP>::ld, KS = DP / 16, DT = DP / 32;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   T* kt = (T*)smem;
   T* vt = kt + 2 * BK * LD;
@@ -92,12 +95,13 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<T, DP>())) void attn_dq_k
   float* ends = bias + win;  // [4][2]
   float* sums = ends + 8;    // [4][win]
 
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 31, h = lane >> 5;
+  const int tid = threadIdx.x, wave = wave_index(), lane = tid & 63, n = lane & 31, h = lane >> 5;
   const int blocks = (a.q_len + kAttnQueries - 1) / kAttnQueries;
-  const Place at = place_of(a.batch * a.heads, blocks, blockIdx.x);
+  const int group = a.heads / a.kv_heads;
+  const Place at = place_of(a.batch * a.kv_heads, blocks * group, blockIdx.x);
   if (at.none) return;
-  const int b = at.unit / a.heads, head = at.unit % a.heads, kvh = head / (a.heads / a.kv_heads);
-  const int qb = a.causal ? blocks - 1 - at.block : at.block;
+  const int b = at.unit / a.kv_heads, kvh = at.unit % a.kv_heads, head = kvh * group + at.block % group;
+  const int qb = a.causal ? blocks - 1 - at.block / group : at.block / group;
   const int q0 = qb * kAttnQueries + wave * 32;
   const int i = q0 + n;
   const bool real = i < a.q_len;
@@ -131,8 +135,8 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<T, DP>())) void attn_dq_k
         amax = fmaxf(amax, fabsf((float)gf[s][e]));
       }
     }
-    delta += __shfl_xor(delta, 32, 64);
-    amax = fmaxf(amax, __shfl_xor(amax, 32, 64));
+    delta = halves_sum(delta);
+    amax = halves_max(amax);
   }
   // empty rows and rows past the end: every probability is 0
   float lse2 = INFINITY;
@@ -146,7 +150,8 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<T, DP>())) void attn_dq_k
   }
   const float unit = kIsF16<T> ? unit_scale(amax) : 1.f;
   fill_bias<T>(a, head, bias, tid, kAttnThreads);
-  const float lo = bias_of<T>(a, head, -a.far) / a.scale, hi = bias_of<T>(a, head, a.far) / a.scale;
+  const float lo = as_scalar(bias_of<T>(a, head, -a.far) * kLog2e);
+  const float hi = as_scalar(bias_of<T>(a, head, a.far) * kLog2e);
   if constexpr (TABLE) {
     for (int t = tid; t < 4 * win; t += kAttnThreads) sums[t] = 0.f;
     for (int t = tid; t < 4 * kDiagScratch; t += kAttnThreads) diag[t] = 0.f;
@@ -204,7 +209,7 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<T, DP>())) void attn_dq_k
           for (int r = 0; r < 16; ++r)
             s[r] = j0 + 32 * u + 8 * (r / 4) + 4 * h + r % 4 < mine ? s[r] : -INFINITY;
         }
-        const float t = fmaf(far_bias, c, -lse2);
+        const float t = far_bias - lse2;
         if (TABLE && (is_before || is_behind)) {
           float p_sum = 0.f, ds_sum = 0.f;
 #pragma unroll
@@ -265,7 +270,7 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<T, DP>())) void attn_dq_k
     // row's probability in one bucket each, where these errors would add up;
     // there they are taken out.
     const float off = before + behind + inside;
-    const float all = off + __shfl_xor(off, 32, 64);
+    const float all = halves_sum(off);
     before = lanes_sum<64>(fmaf(-all, p_before, before));
     behind = lanes_sum<64>(fmaf(-all, p_behind, behind));
     if (lane == 0) {
@@ -274,7 +279,7 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<T, DP>())) void attn_dq_k
     }
     __syncthreads();
     // the window's first and last distances lie beyond +-far like the far tiles
-    float* out = a.table_part + ((int64_t)at.unit * blocks + qb) * win;
+    float* out = a.table_part + ((int64_t)(b * a.heads + head) * blocks + qb) * win;
     for (int t = tid; t < win; t += kAttnThreads) {
       float v = 0.f;
 #pragma unroll
@@ -344,18 +349,19 @@ constexpr size_t attn_dkv_lds(int far) {
 }
 
 template <class T, int DP, bool VEC>
-__global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 ? 2 : 1)) void attn_dkv_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 2 : 1)) void attn_dkv_kernel(const AttnArgs a) {
   constexpr int BQ = attn_step<T>(), NS = BQ / 32, LD = Tile<T, DP>::ld, KS = DP / 16, DT = DP / 32;
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  // float32 fragments of 128 columns leave no registers for the next tile
-  constexpr bool AHEAD = !(sizeof(T) == 4 && DP == 128);
+  // float32 fragments of 128 columns leave no registers for the next tile, and
+  // neither do loads of odd rows
+  constexpr bool AHEAD = VEC && !(sizeof(T) == 4 && DP == 128);
   T* qt = (T*)smem;
   T* gt = qt + 2 * BQ * LD;
   float* lse2 = (float*)(gt + 2 * BQ * LD);  // [2][BQ]
   float* delta = lse2 + 2 * BQ;              // [2][BQ]
   float* bias = delta + 2 * BQ;
 
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 31, h = lane >> 5;
+  const int tid = threadIdx.x, wave = wave_index(), lane = tid & 63, n = lane & 31, h = lane >> 5;
   const int blocks = (a.k_len + kAttnBlockKeys - 1) / kAttnBlockKeys;
   const Place at = place_of(a.batch * a.kv_heads, blocks, blockIdx.x);
   if (at.none) return;
@@ -409,7 +415,7 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 ? 2 : 1))
     ql.init(a.qs[2], a.dim, tid);
     gl.init(a.dos[2], a.dim, tid);
     float l_next = 0.f, d_next = 0.f;
-    const auto fetch = [&](int i0) {
+    const auto fetch = [&](int i0) __attribute__((always_inline)) {
       ql.load(qp + (int64_t)i0 * a.qs[2], a.qs[2], i_end - i0, a.dim, tid);
       gl.load(gp + (int64_t)i0 * a.dos[2], a.dos[2], i_end - i0, a.dim, tid);
       if (tid < BQ) {
@@ -419,7 +425,7 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 ? 2 : 1))
         d_next = in ? a.delta[row0 + i0 + tid] : 0.f;
       }
     };
-    const auto put = [&](int buf) {
+    const auto put = [&](int buf) __attribute__((always_inline)) {
       ql.store(qt + buf * BQ * LD, tid);
       gl.store(gt + buf * BQ * LD, tid);
       if (tid < BQ) {
@@ -429,7 +435,8 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 ? 2 : 1))
     };
     fetch(i_beg);
     fill_bias<T>(a, head, bias, tid, kAttnThreads);
-    const float lo = bias_of<T>(a, head, -a.far) / a.scale, hi = bias_of<T>(a, head, a.far) / a.scale;
+    const float lo = as_scalar(bias_of<T>(a, head, -a.far) * kLog2e);
+  const float hi = as_scalar(bias_of<T>(a, head, a.far) * kLog2e);
     put(0);
     __syncthreads();
     int buf = 0;
@@ -448,7 +455,7 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 ? 2 : 1))
           float far_bias;
           if (tile_before(dist, a.far) || tile_behind(dist, a.far)) {
             s = mma32(q0, kf[0], acc_zero());
-            far_bias = (dist < 0 ? lo : hi) * c;
+            far_bias = dist < 0 ? lo : hi;
           } else {
             s = mma32(q0, kf[0], bias_start_queries(bias, a.far, dist, h, n));
             far_bias = 0.f;
@@ -523,7 +530,8 @@ int attn_backward_dim(const AttnArgs& a, void* stream) {
   if (a.q_len > 0) {
     const int st = launch("attention backward (dq)",
                           table ? attn_dq_kernel<T, DP, true, VEC> : attn_dq_kernel<T, DP, false, VEC>,
-                          dim3(place_grid((int64_t)a.batch * a.heads, attn_query_blocks(a))),
+                          dim3(place_grid((int64_t)a.batch * a.kv_heads,
+                                          (int64_t)attn_query_blocks(a) * (a.heads / a.kv_heads))),
                           dim3(kAttnThreads), attn_dq_lds<T, DP>(a.far, table), stream, a);
     if (st != FM_OK) return st;
   }

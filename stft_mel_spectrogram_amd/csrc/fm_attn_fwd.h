@@ -22,20 +22,21 @@ constexpr size_t attn_forward_lds(int far) {
 // keeps one query's running maximum and sum, and the probabilities are the
 // next product's right operand as they stand: o' = V' p'.
 template <class T, int DP, bool SPLIT, bool VEC>
-__global__ __launch_bounds__(kAttnThreads, (attn_waves<T, DP>())) void attn_forward_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 4 : attn_waves<T, DP>())) void attn_forward_kernel(const AttnArgs a) {
   constexpr int BK = attn_keys<T>(), NS = BK / 32, LD = Tile<T, DP>::ld, KS = DP / 16, DT = DP / 32;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   T* kt = (T*)smem;              // [2][BK][LD]
   T* vt = kt + 2 * BK * LD;      // [2][BK][LD]
   float* bias = (float*)(vt + 2 * BK * LD);
 
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 31, h = lane >> 5;
+  const int tid = threadIdx.x, wave = wave_index(), lane = tid & 63, n = lane & 31, h = lane >> 5;
   const int blocks = (a.q_len + kAttnQueries - 1) / kAttnQueries;
-  const Place at = place_of(a.batch * a.heads, blocks, blockIdx.x);
+  const int group = a.heads / a.kv_heads;
+  const Place at = place_of(a.batch * a.kv_heads, blocks * group, blockIdx.x);
   if (at.none) return;
-  const int b = at.unit / a.heads, head = at.unit % a.heads, kvh = head / (a.heads / a.kv_heads);
+  const int b = at.unit / a.kv_heads, kvh = at.unit % a.kv_heads, head = kvh * group + at.block % group;
   // the last queries see the most keys when causal: they start first
-  const int qb = a.causal ? blocks - 1 - at.block : at.block;
+  const int qb = a.causal ? blocks - 1 - at.block / group : at.block / group;
   const int q0 = qb * kAttnQueries + wave * 32;
   const int i = q0 + n;
   const int len = key_count(a, b), first = position_of_first(a, b);
@@ -60,7 +61,9 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<T, DP>())) void attn_forw
   for (int s = 0; s < KS; ++s)
     qf[s] = load_frag(qp + 16 * s + 8 * h, i < a.q_len ? a.dim - 16 * s - 8 * h : 0);
   fill_bias<T>(a, head, bias, tid, kAttnThreads);
-  const float lo = bias_of<T>(a, head, -a.far) / a.scale, hi = bias_of<T>(a, head, a.far) / a.scale;
+  const float c = a.scale * kLog2e;
+  const float lo = as_scalar(bias_of<T>(a, head, -a.far) * kLog2e);
+  const float hi = as_scalar(bias_of<T>(a, head, a.far) * kLog2e);
   kl.store(kt, tid);
   vl.store(vt, tid);
   __syncthreads();
@@ -70,9 +73,8 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<T, DP>())) void attn_forw
   for (int d = 0; d < DT; ++d)
 #pragma unroll
     for (int r = 0; r < 16; ++r) o[d][r] = 0.f;
-  float m = -INFINITY, l = 0.f;
-  const float c = a.scale * kLog2e;
-  const float grow = 8.f / c;  // a maximum raised by less than 2^8 leaves m as it is
+  // running maximum of the scores in base 2, its finite negative, and the sum
+  float m = -INFINITY, neg = 0.f, l = 0.f;
   const int mine = a.causal ? min(len, first + i + 1) : len;   // keys this lane's query sees
   const int least = a.causal ? min(len, first + q0 + 1) : len; // of the wave's first query
   const int wave_end = a.causal ? min(k_end, first + q0 + 32) : k_end;
@@ -89,7 +91,7 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<T, DP>())) void attn_forw
       const T* ktb = kt + buf * BK * LD;
       const T* vtb = vt + buf * BK * LD;
       acc16 s[NS];
-      float far_bias[NS];  // of a tile that lies outside the window
+      float far_bias[NS];  // of a tile that lies outside the window, in base 2
 #pragma unroll
       for (int u = 0; u < NS; ++u) {
         const int dist = j0 + 32 * u - first - q0;
@@ -115,26 +117,28 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<T, DP>())) void attn_forw
         float mu = s[u][0];
 #pragma unroll
         for (int r = 1; r < 16; ++r) mu = fmaxf(mu, s[u][r]);
-        mx = fmaxf(mx, mu + far_bias[u]);
+        mx = fmaxf(mx, fmaf(mu, c, far_bias[u]));
       }
-      mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-      const bool raise = mx > m + grow || (m == -INFINITY && mx > m);
+      mx = halves_max(mx);
+      // a maximum raised by less than 2^8 leaves m as it is: every later
+      // product with o and l waits for it
+      const bool raise = mx > m + 8.f;
       if (__any(raise)) {
         const float m2 = raise ? mx : m;
         // nothing seen yet: o and l are 0
-        const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - m2) * c);
+        const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - m2);
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
           for (int r = 0; r < 16; ++r) o[d][r] *= f;
         l *= f;
         m = m2;
+        neg = m == -INFINITY ? 0.f : -m;
       }
-      const float mc = m == -INFINITY ? 0.f : m * c;
       float sum = 0.f;
 #pragma unroll
       for (int u = 0; u < NS; ++u) {
-        const float t = fmaf(far_bias[u], c, -mc);
+        const float t = far_bias[u] + neg;
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           s[u][r] = __builtin_amdgcn_exp2f(fmaf(s[u][r], c, t));
@@ -161,11 +165,11 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<T, DP>())) void attn_forw
     __syncthreads();
   }
 
-  l += __shfl_xor(l, 32, 64);
+  l = halves_sum(l);
   if (i >= a.q_len) return;
   const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
   const int64_t row = (int64_t)(b * a.heads + head) * a.q_len + i;
-  const float lse = l != l ? l : m == -INFINITY ? -INFINITY : fmaf(m, a.scale, logf(l));
+  const float lse = l != l ? l : m == -INFINITY ? -INFINITY : fmaf(m, kLn2, logf(l));
   if constexpr (SPLIT) {
     const int64_t rows = (int64_t)a.batch * a.heads * a.q_len;
     if (h == 0) a.part_lse[blockIdx.y * rows + row] = lse;
@@ -196,23 +200,32 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<T, DP>())) void attn_forw
 }
 
 // Few query rows per key head (rows = heads of the group x queries, at most
-// 16): one 16-column fragment holds them all; the 4 waves take 32 keys each
-// in turn, straight from memory, and join at the end.  Memory bound: keys are
-// the left operand as they lie in memory, values pass through a wave's own
-// LDS tile to be read by columns.
+// 16): one 16-column fragment holds them all; the waves take 32 keys each in
+// turn, straight from memory, and join at the end.  Memory bound: keys are the
+// left operand as they lie in memory, values pass through a wave's own LDS
+// tile to be read by columns.
 constexpr int kTokenKeys = 32;
+// The group's bias windows are kept in LDS where they take at most this much;
+// larger ones are looked up in memory by the few tiles that need them.
+constexpr int kTokenBias = 16384;
+inline int attn_token_bias(const AttnArgs& a) {
+  const int64_t n = 4 * (int64_t)(2 * a.far + 1) * (a.heads / a.kv_heads);
+  return n <= kTokenBias ? (int)n : 0;
+}
 template <class T, int DP>
-constexpr size_t attn_token_lds() {
-  constexpr size_t tiles = 4 * kTokenKeys * Tile<T, DP>::ld * sizeof(T);
-  constexpr size_t join = 4 * 16 * (DP + 2) * sizeof(float);
-  return tiles > join ? tiles : join;
+constexpr size_t attn_token_lds(int bias) {
+  constexpr int nw = attn_token_waves(sizeof(T), DP);
+  constexpr size_t tiles = nw * kTokenKeys * Tile<T, DP>::ld * sizeof(T);
+  constexpr size_t join = nw * 16 * (DP + 2) * sizeof(float);
+  return (tiles > join ? tiles : join) + bias;
 }
 
 template <class T, int DP, bool SPLIT, bool VEC>
-__global__ __launch_bounds__(kAttnThreads) void attn_token_kernel(const AttnArgs a) {
+__global__ __launch_bounds__((attn_token_waves(sizeof(T), DP) * 64)) void attn_token_kernel(const AttnArgs a) {
+  constexpr int NW = attn_token_waves(sizeof(T), DP), NT = NW * 64;
   constexpr int LD = Tile<T, DP>::ld, KS = DP / 32, DT = DP / 16;
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, wave = wave_index(), lane = tid & 63, n = lane & 15, g = lane >> 4;
   T* vt = (T*)smem + wave * kTokenKeys * LD;
   const int group = a.heads / a.kv_heads, rows = group * a.q_len;
   const int b = blockIdx.x / a.kv_heads, kvh = blockIdx.x % a.kv_heads;
@@ -221,33 +234,18 @@ __global__ __launch_bounds__(kAttnThreads) void attn_token_kernel(const AttnArgs
   const int len = key_count(a, b), first = position_of_first(a, b);
   int k_beg = 0, k_end = a.causal ? clamp_int(first + a.q_len, 0, len) : len;
   if constexpr (SPLIT) {
-    const int per = ((k_end + a.splits - 1) / a.splits + 127) / 128 * 128;
+    const int per = ((k_end + a.splits - 1) / a.splits + kTokenKeys - 1) / kTokenKeys * kTokenKeys;
     k_beg = min((int)blockIdx.y * per, k_end);
     k_end = min(k_beg + per, k_end);
   }
   const T* kp = (const T*)a.k + b * a.ks[0] + kvh * a.ks[1];
   const T* vp = (const T*)a.v + b * a.vs[0] + kvh * a.vs[1];
 
-  Frag<T> qf[KS];
-  const T* qp = (const T*)a.q + b * a.qs[0] + (real ? head : 0) * a.qs[1] + i * a.qs[2];
-#pragma unroll
-  for (int s = 0; s < KS; ++s) qf[s] = load_frag(qp + 32 * s + 8 * g, real ? a.dim - 32 * s - 8 * g : 0);
-  const float lo = real ? bias_of<T>(a, head, -a.far) / a.scale : 0.f;
-  const float hi = real ? bias_of<T>(a, head, a.far) / a.scale : 0.f;
-  const int pos = first + i;
-  const int mine = real ? (a.causal ? min(len, pos + 1) : len) : 0;
-  const int least = a.causal ? min(len, first + 1) : len;
   const float c = a.scale * kLog2e;
-
-  acc4 o[DT];
-#pragma unroll
-  for (int d = 0; d < DT; ++d) o[d] = acc4{0.f, 0.f, 0.f, 0.f};
-  float m = -INFINITY, l = 0.f;
-
   Frag<T> kf[2][KS];
   TileLoad<T, DP, kTokenKeys, 64, VEC> vl;
   vl.init(a.vs[2], a.dim, lane);
-  const auto fetch = [&](int j) {
+  const auto fetch = [&](int j) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int key = j + 16 * u + n;
@@ -259,7 +257,37 @@ __global__ __launch_bounds__(kAttnThreads) void attn_token_kernel(const AttnArgs
   };
   int j0 = k_beg + wave * kTokenKeys;
   if (j0 < k_end) fetch(j0);
-  for (; j0 < k_end; j0 += 4 * kTokenKeys) {
+  Frag<T> qf[KS];
+  const T* qp = (const T*)a.q + b * a.qs[0] + (real ? head : 0) * a.qs[1] + i * a.qs[2];
+#pragma unroll
+  for (int s = 0; s < KS; ++s) qf[s] = load_frag(qp + 32 * s + 8 * g, real ? a.dim - 32 * s - 8 * g : 0);
+  // the bias in units of the product: [group][2 far + 1]
+  const int dists = 2 * a.far + 1;
+  const bool table = (int64_t)dists * group * 4 <= kTokenBias;
+  float* bias = (float*)(smem + attn_token_lds<T, DP>(0));
+  const float inv_scale = 1.f / a.scale;
+  if (table) {
+    for (int t = tid; t < dists * group; t += NT) {
+      const int x = t / dists;
+      bias[t] = bias_of<T>(a, kvh * group + x, t - x * dists - a.far) * inv_scale;
+    }
+    __syncthreads();
+  }
+  const auto bias_at = [&](int d) {
+    return table ? bias[n / a.q_len * dists + clamp_int(d + a.far, 0, dists - 1)]
+                 : bias_of<T>(a, head, d) * inv_scale;
+  };
+  const float lo = real ? bias_at(-a.far) : 0.f, hi = real ? bias_at(a.far) : 0.f;
+  const int pos = first + i;
+  const int mine = real ? (a.causal ? min(len, pos + 1) : len) : 0;
+  const int least = a.causal ? min(len, first + 1) : len;
+
+  acc4 o[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d) o[d] = acc4{0.f, 0.f, 0.f, 0.f};
+  float m = -INFINITY, l = 0.f;
+
+  for (; j0 < k_end; j0 += NW * kTokenKeys) {
     // the wave's own tile: its reads of the last round are done
     vl.store(vt, lane);
     acc4 s[2];
@@ -273,13 +301,13 @@ __global__ __launch_bounds__(kAttnThreads) void attn_token_kernel(const AttnArgs
       } else {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          s[u][r] = real ? bias_of<T>(a, head, j0 + 16 * u + 4 * g + r - pos) / a.scale : 0.f;
+          s[u][r] = real ? bias_at(j0 + 16 * u + 4 * g + r - pos) : 0.f;
       }
 #pragma unroll
       for (int x = 0; x < KS; ++x) s[u] = mma16(kf[u][x], qf[x], s[u]);
     }
     const int j = j0;
-    if (j0 + 4 * kTokenKeys < k_end) fetch(j0 + 4 * kTokenKeys);
+    if (j0 + NW * kTokenKeys < k_end) fetch(j0 + NW * kTokenKeys);
     if (j + kTokenKeys > least || rows < 16) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
@@ -289,7 +317,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_token_kernel(const AttnArgs
     float mx = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
                      fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
     mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+    mx = halves_max(mx);
     if (__any(mx > m)) {
       const float m2 = fmaxf(m, mx);
       const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - m2) * c);
@@ -334,7 +362,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_token_kernel(const AttnArgs
     }
   }
   l += __shfl_xor(l, 16, 64);
-  l += __shfl_xor(l, 32, 64);
+  l = halves_sum(l);
 
   // the waves' shares: o[row][d], m and l per row
   __syncthreads();
@@ -350,15 +378,15 @@ __global__ __launch_bounds__(kAttnThreads) void attn_token_kernel(const AttnArgs
     jw[DP + 1] = l;
   }
   __syncthreads();
-  for (int t = tid; t < rows * DP; t += kAttnThreads) {
+  for (int t = tid; t < rows * DP; t += NT) {
     const int r = t / DP, d = t - r * DP;
     if (d >= a.dim) continue;
     float mm = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) mm = fmaxf(mm, join[(w * 16 + r) * JL + DP]);
+    for (int w = 0; w < NW; ++w) mm = fmaxf(mm, join[(w * 16 + r) * JL + DP]);
     float sum = 0.f, val = 0.f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < NW; ++w) {
       const float* p = join + (w * 16 + r) * JL;
       const float f = p[DP] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((p[DP] - mm) * c);
       // a NaN sum has to survive a maximum that never was one
@@ -381,54 +409,66 @@ __global__ __launch_bounds__(kAttnThreads) void attn_token_kernel(const AttnArgs
   }
 }
 
-// Joins the key ranges of a row: one wave per row.
+// Joins the key ranges of a row: one workgroup per row, groups of threads over
+// shares of the ranges.
 template <class T>
 __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(const AttnArgs a) {
-  const int64_t rows = (int64_t)a.batch * a.heads * a.q_len;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (row >= rows) return;
-  float mm = -INFINITY;
-  bool bad = false;
-  for (int s = lane; s < a.splits; s += 64) {
-    const float v = a.part_lse[s * rows + row];
-    mm = fmaxf(mm, v);
-    bad |= v != v;
+  __shared__ float weight[kAttnMaxSplits];
+  __shared__ float red[8];
+  __shared__ float acc[kAttnThreads];
+  const int64_t rows = (int64_t)a.batch * a.heads * a.q_len, row = blockIdx.x;
+  const int tid = threadIdx.x, wave = tid >> 6;
+  // thread (share, column)
+  const int cols = a.dim <= 64 ? 64 : 128, shares = kAttnThreads / cols;
+  const int d = tid & (cols - 1), share = tid / cols;
+  float v = tid < a.splits ? a.part_lse[tid * rows + row] : -INFINITY;
+  float v2 = tid + kAttnThreads < a.splits ? a.part_lse[(tid + kAttnThreads) * rows + row] : -INFINITY;
+  const bool bad = v != v || v2 != v2;
+  float m = lanes_max<64>(fmaxf(v, v2));
+  if ((tid & 63) == 0) red[wave] = m;
+  if (tid < 4) red[4 + tid] = 0.f;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const float ms = m == -INFINITY ? 0.f : m;
+  v = __builtin_amdgcn_exp2f((v - ms) * kLog2e);
+  v2 = __builtin_amdgcn_exp2f((v2 - ms) * kLog2e);
+  if (tid < a.splits) weight[tid] = v;
+  if (tid + kAttnThreads < a.splits) weight[tid + kAttnThreads] = v2;
+  // a NaN weight makes the sum NaN, and with it the row
+  const float part = lanes_sum<64>(bad ? NAN : v + v2);
+  if ((tid & 63) == 0) red[4 + wave] = part;
+  __syncthreads();
+  const float sum = (red[4] + red[5]) + (red[6] + red[7]);
+  float o = 0.f;
+  if (d < a.dim) {
+    const float* p = a.part_o + row * a.dim + d;
+    const int64_t step = rows * a.dim;
+#pragma unroll 8
+    for (int s = share; s < a.splits; s += shares) o = fmaf(weight[s], p[s * step], o);
   }
-  mm = lanes_max<64>(mm);
-  if (__any(bad)) mm = NAN;
-  const float ms = mm == -INFINITY ? 0.f : mm;
-  float sum = 0.f, v0 = 0.f, v1 = 0.f;
-  for (int s = 0; s < a.splits; ++s) {
-    const float f = __builtin_amdgcn_exp2f((a.part_lse[s * rows + row] - ms) * kLog2e);
-    const float* p = a.part_o + (s * rows + row) * a.dim;
-    sum += f;
-    if (lane < a.dim) v0 = fmaf(f, p[lane], v0);
-    if (lane + 64 < a.dim) v1 = fmaf(f, p[lane + 64], v1);
+  acc[tid] = o;
+  __syncthreads();
+  if (share == 0 && d < a.dim) {
+    for (int x = 1; x < shares; ++x) o += acc[x * cols + d];
+    const int64_t bh = row / a.q_len, i = row - bh * a.q_len;
+    const int64_t off = bh / a.heads * a.os[0] + bh % a.heads * a.os[1] + i * a.os[2];
+    ((T*)a.o)[off + d] = (T)(sum == 0.f ? 0.f : o / sum);
+    if (a.lse && d == 0) a.lse[row] = sum == 0.f ? -INFINITY : ms + logf(sum);
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int i = (int)(row % a.q_len);
-  const int64_t bh = row / a.q_len;
-  const int64_t off = bh / a.heads * a.os[0] + bh % a.heads * a.os[1] + i * a.os[2];
-  v0 *= inv;
-  v1 *= inv;
-  if (lane < a.dim) ((T*)a.o)[off + lane] = (T)v0;
-  if (lane + 64 < a.dim) ((T*)a.o)[off + lane + 64] = (T)v1;
-  if (a.lse && lane == 0) a.lse[row] = mm == -INFINITY ? mm : ms + logf(sum);
 }
 
 template <class T, int DP, bool VEC>
 int attn_forward_dim(const AttnArgs& a, void* stream) {
   if (attn_token_kernel(a)) {
     static const int opted =
-        lds_opt_in(attn_token_kernel<T, DP, false, VEC>, attn_token_lds<T, DP>()) |
-        lds_opt_in(attn_token_kernel<T, DP, true, VEC>, attn_token_lds<T, DP>());
+        lds_opt_in(attn_token_kernel<T, DP, false, VEC>, attn_token_lds<T, DP>(kTokenBias)) |
+        lds_opt_in(attn_token_kernel<T, DP, true, VEC>, attn_token_lds<T, DP>(kTokenBias));
     if (opted != FM_OK) return set_error(FM_E_HIP, "attention: LDS size refused");
     return launch("attention of single tokens",
                   a.splits > 1 ? attn_token_kernel<T, DP, true, VEC>
                                : attn_token_kernel<T, DP, false, VEC>,
-                  dim3((unsigned)(a.batch * a.kv_heads), (unsigned)a.splits), dim3(kAttnThreads),
-                  attn_token_lds<T, DP>(), stream, a);
+                  dim3((unsigned)(a.batch * a.kv_heads), (unsigned)a.splits), dim3(64 * attn_token_waves(sizeof(T), DP)),
+                  attn_token_lds<T, DP>(attn_token_bias(a)), stream, a);
   }
   static const int opted =
       lds_opt_in(attn_forward_kernel<T, DP, false, VEC>, attn_forward_lds<T, DP>(kAttnMaxFar)) |
@@ -437,7 +477,9 @@ int attn_forward_dim(const AttnArgs& a, void* stream) {
   return launch("attention",
                 a.splits > 1 ? attn_forward_kernel<T, DP, true, VEC>
                              : attn_forward_kernel<T, DP, false, VEC>,
-                dim3(place_grid((int64_t)a.batch * a.heads, attn_query_blocks(a)), (unsigned)a.splits),
+                dim3(place_grid((int64_t)a.batch * a.kv_heads,
+                                (int64_t)attn_query_blocks(a) * (a.heads / a.kv_heads)),
+                     (unsigned)a.splits),
                 dim3(kAttnThreads), attn_forward_lds<T, DP>(a.far), stream, a);
 }
 
@@ -452,8 +494,8 @@ int attn_forward_t(const AttnArgs& a, void* stream) {
                      : go(attn_forward_dim<T, 64, false>, attn_forward_dim<T, 96, false>,
                           attn_forward_dim<T, 128, false>);
   if (st != FM_OK || a.splits == 1) return st;
-  return launch("attention (join)", attn_join_kernel<T>, dim3((unsigned)((attn_rows(a) + 3) / 4)),
-                dim3(kAttnThreads), 0, stream, a);
+  return launch("attention (join)", attn_join_kernel<T>, dim3((unsigned)attn_rows(a)), dim3(kAttnThreads),
+                0, stream, a);
 }
 
 }  // namespace fm

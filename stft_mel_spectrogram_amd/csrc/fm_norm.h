@@ -9,9 +9,10 @@
 //
 // One row is held in registers by LPR lanes, VPL groups of 16 bytes each, so
 // x (and dy) are read from memory once per pass; a wave takes 64 / LPR rows
-// where LPR < 64.  Memory bound: the backward adds dw and db up in registers
-// over a workgroup's rows, writes one partial row per workgroup and a second
-// launch adds the partials in a fixed order.
+// where LPR < 64.  Memory bound: workgroups walk over rows and keep their
+// columns' weight and bias in registers; the backward adds dw and db up there
+// too, writes one partial row per workgroup and a second launch adds the
+// partials in a fixed order.
 #pragma once
 
 #include "fm_op.h"
@@ -23,11 +24,8 @@ namespace fm {
 template <int LPR>
 __device__ __forceinline__ float2 row_sum2(float2 v, float2* red) {
   constexpr int L = LPR < 64 ? LPR : 64;
-#pragma unroll
-  for (int m = L / 2; m >= 1; m >>= 1) {
-    v.x += __shfl_xor(v.x, m, 64);
-    v.y += __shfl_xor(v.y, m, 64);
-  }
+  v.x = lanes_sum<L>(v.x);
+  v.y = lanes_sum<L>(v.y);
   if constexpr (LPR > 64) {
     const int wave = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0) red[wave] = v;
@@ -54,64 +52,72 @@ __global__ __launch_bounds__(kNormThreads) void norm_forward_kernel(
     T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int width,
     float eps) {
   constexpr int VE = Vec16<T>::n;
-  constexpr int NT = kNormThreads;
+  constexpr int RPB = kNormThreads / LPR;
   __shared__ float2 red[LPR > 64 ? LPR / 64 : 1];
-  const int lane = threadIdx.x % LPR;
-  const int64_t row = (int64_t)blockIdx.x * (NT / LPR) + threadIdx.x / LPR;
-  // rows past the end (whole lane groups; never in kernels with barriers,
-  // where a workgroup is one row) run on an empty width
-  const int have_all = row < rows ? width : 0;
-  const T* xr = x + row * x_stride;
-  Vec16<T> raw[VPL];
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int c = (i * LPR + lane) * VE;
-    raw[i] = load16_part(xr + c, have_all - c, (T)0.f);
-  }
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i)
-#pragma unroll
-    for (int e = 0; e < VE; ++e) s += (float)raw[i].v[e];
+  const int lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
   // divided, not multiplied by 1 / n: a constant row has exactly that mean
   const float n = (float)width;
-  const float mu = row_sum<LPR>(s, red) / n;
-  float q = 0.f;
+  Group<W, VE> wv[VPL], bv[VPL];
+  bool first = true;
+  // rows past the end (whole lane groups; a workgroup of one row has none) run
+  // on an empty width
+  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < rows; r0 += (int64_t)gridDim.x * RPB) {
+    const int64_t row = r0 + sub;
+    const int have_all = row < rows ? width : 0;
+    const T* xr = x + row * x_stride;
+    Vec16<T> raw[VPL];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int c = (i * LPR + lane) * VE;
-#pragma unroll
-    for (int e = 0; e < VE; ++e) {
-      const float d = c + e < width ? (float)raw[i].v[e] - mu : 0.f;
-      q = fmaf(d, d, q);
+    for (int i = 0; i < VPL; ++i) {
+      const int c = (i * LPR + lane) * VE;
+      raw[i] = load16_part(xr + c, have_all - c, (T)0.f);
     }
-  }
-  const float rs = 1.f / sqrtf(row_sum<LPR>(q, red) / n + eps);
-  if (row >= rows) return;
-  if (lane == 0) {
-    if (mean) mean[row] = mu;
-    if (rstd) rstd[row] = rs;
-  }
-  T* yr = y + row * width;
+    if (first) {
+      first = false;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int c = (i * LPR + lane) * VE;
-    const int have = width - c;
-    if (have <= 0) break;
-    Vec16<T> out;
-#pragma unroll
-    for (int e = 0; e < VE; ++e) {
-      const int ce = e < have ? c + e : c;
-      float u = ((float)raw[i].v[e] - mu) * rs;
-      if (w) u = fmaf(u, (float)w[ce], b ? (float)b[ce] : 0.f);
-      out.v[e] = (T)u;
+      for (int i = 0; i < VPL; ++i) {
+        const int c = (i * LPR + lane) * VE;
+        wv[i] = load_group<W, VE>(w + c, w ? width - c : 0, (W)1.f);
+        bv[i] = load_group<W, VE>(b + c, b ? width - c : 0, (W)0.f);
+      }
     }
-    store16_part(yr + c, out, have);
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+#pragma unroll
+      for (int e = 0; e < VE; ++e) s += (float)raw[i].v[e];
+    const float mu = row_sum<LPR>(s, red) / n;
+    float q = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int c = (i * LPR + lane) * VE;
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        const float d = c + e < width ? (float)raw[i].v[e] - mu : 0.f;
+        q = fmaf(d, d, q);
+      }
+    }
+    const float rs = 1.f / sqrtf(row_sum<LPR>(q, red) / n + eps);
+    if (lane == 0 && row < rows) {
+      if (mean) mean[row] = mu;
+      if (rstd) rstd[row] = rs;
+    }
+    T* yr = y + row * width;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int c = (i * LPR + lane) * VE;
+      if (have_all - c > 0) {
+        Vec16<T> out;
+#pragma unroll
+        for (int e = 0; e < VE; ++e)
+          out.v[e] = (T)fmaf(((float)raw[i].v[e] - mu) * rs, (float)wv[i].v[e], (float)bv[i].v[e]);
+        store16_part(yr + c, out, have_all - c);
+      }
+    }
   }
 }
 
-// grid-stride over rows; PARTS: also add up dw and db (part: one row of
-// [dw | db], 2 * width floats, per workgroup).
+// PARTS: also add up dw and db (part: one row of [dw | db], 2 * width floats,
+// per workgroup).
 template <class T, class W, int LPR, int VPL, bool PARTS>
 __global__ __launch_bounds__(kNormThreads) void norm_backward_kernel(
     const T* __restrict__ dy, int64_t dy_stride, const T* __restrict__ x, int64_t x_stride,
@@ -129,6 +135,12 @@ __global__ __launch_bounds__(kNormThreads) void norm_backward_kernel(
 #pragma unroll
     for (int i = 0; i < VPL * VE; ++i) aw[i] = ab[i] = 0.f;
   }
+  Group<W, VE> wv[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int c = (i * LPR + lane) * VE;
+    wv[i] = load_group<W, VE>(w + c, w ? width - c : 0, (W)1.f);
+  }
   for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < rows; r0 += (int64_t)gridDim.x * RPB) {
     const int64_t row = r0 + sub;
     const int have_all = row < rows ? width : 0;
@@ -145,14 +157,13 @@ __global__ __launch_bounds__(kNormThreads) void norm_backward_kernel(
     const float rs = row < rows ? rstd[row] : 0.f;
     float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int c = (i * LPR + lane) * VE;
+    for (int i = 0; i < VPL; ++i)
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
-        const bool in = c + e < have_all;
+        // past the end dy is 0
         const float d = (float)gv[i].v[e];
-        const float u = in ? ((float)xv[i].v[e] - mu) * rs : 0.f;
-        const float g = (w && in) ? d * (float)w[c + e] : d;
+        const float u = ((float)xv[i].v[e] - mu) * rs;
+        const float g = d * (float)wv[i].v[e];
         s.x += g;
         s.y = fmaf(g, u, s.y);
         if constexpr (PARTS) {
@@ -160,25 +171,21 @@ __global__ __launch_bounds__(kNormThreads) void norm_backward_kernel(
           ab[i * VE + e] += d;
         }
       }
-    }
     s = row_sum2<LPR>(s, red);
     const float m1 = s.x * inv_n, m2 = s.y * inv_n;
     T* dr = dx + row * width;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const int c = (i * LPR + lane) * VE;
-      const int have = have_all - c;
-      if (have > 0) {
+      if (have_all - c > 0) {
         Vec16<T> out;
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
-          const int ce = e < have ? c + e : c;
-          const float d = (float)gv[i].v[e];
           const float u = ((float)xv[i].v[e] - mu) * rs;
-          const float g = w ? d * (float)w[ce] : d;
+          const float g = (float)gv[i].v[e] * (float)wv[i].v[e];
           out.v[e] = (T)(rs * (g - m1 - u * m2));
         }
-        store16_part(dr + c, out, have);
+        store16_part(dr + c, out, have_all - c);
       }
     }
   }
@@ -343,8 +350,20 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* __restri
   const int64_t c = (int64_t)blockIdx.x * 64 + lane;
   const bool in = c < 2 * (int64_t)width;
   float s = 0.f;
-  if (in)
-    for (int p = set; p < parts; p += 16) s += part[(int64_t)p * 2 * width + c];
+  if (in) {
+    const float* q = part + c;
+    const int64_t row = 2 * (int64_t)width;
+    int p = set;
+    // eight loads on their way at a time
+    for (; p + 112 < parts; p += 128) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = q[(p + 16 * k) * row];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += v[k];
+    }
+    for (; p < parts; p += 16) s += q[p * row];
+  }
   red[set][lane] = s;
   __syncthreads();
   if (set == 0 && in) {
@@ -360,16 +379,18 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* __restri
 
 template <class T, class W>
 int norm_forward_t(const NormForward& a) {
-  const NormShape s = norm_shape(a.width, Vec16<T>::n);
-#define FM_NORM_FWD(L, V)                                                                  \
-  if (s.lpr == L && s.vpl == V) {                                                          \
-    constexpr int nt = kNormThreads;                                \
-    const int64_t blocks = (a.rows + nt / L - 1) / (nt / L);                               \
-    return launch("layer norm forward", norm_forward_kernel<T, W, L, V>,                   \
-                  dim3((unsigned)blocks), dim3(nt), 0, a.stream, (const T*)a.x, a.x_stride, \
-                  (const W*)a.weight, (const W*)a.bias, (T*)a.y, a.mean, a.rstd, a.rows,   \
-                  a.width, a.eps);                                                         \
-  }
+  constexpr int VE = Vec16<T>::n;
+  const NormShape s = norm_shape(a.width, VE);
+#define FM_NORM_FWD(L, V)                                                                     \
+  if constexpr (V * VE <= 32)                                                                 \
+    if (s.lpr == L && s.vpl == V) {                                                           \
+      const int64_t need = (a.rows + kNormThreads / L - 1) / (kNormThreads / L);              \
+      return launch("layer norm forward", norm_forward_kernel<T, W, L, V>,                    \
+                    dim3((unsigned)(need < kNormBlocks ? need : kNormBlocks)),                \
+                    dim3(kNormThreads), 0, a.stream, (const T*)a.x, a.x_stride,               \
+                    (const W*)a.weight, (const W*)a.bias, (T*)a.y, a.mean, a.rstd, a.rows,    \
+                    a.width, a.eps);                                                          \
+    }
   FM_NORM_SHAPES(FM_NORM_FWD)
 #undef FM_NORM_FWD
   return launch("layer norm forward", norm_forward_wide_kernel<T, W>, dim3((unsigned)a.rows),
@@ -390,22 +411,19 @@ int norm_backward_t(const NormBackward& a) {
       st = launch("layer norm backward", norm_backward_wide_kernel<T, W>, dim3((unsigned)a.rows),
                   dim3(kNormWide), 0, a.stream, (const T*)a.dy, a.dy_stride, (const T*)a.x,
                   a.x_stride, (const W*)a.weight, a.mean, a.rstd, (T*)a.dx, a.rows, a.width);
-#define FM_NORM_BWD(L, V)                                                                       \
-  if (s.lpr == L && s.vpl == V) {                                                               \
-    constexpr int nt = kNormThreads;                                     \
-    constexpr bool in = V * VE <= 32;                                               \
-    const int64_t need = (a.rows + nt / L - 1) / (nt / L);                                      \
-    const bool sums = in && want;                                                               \
-    st = launch("layer norm backward",                                                          \
-                sums ? norm_backward_kernel<T, W, L, V, in> : norm_backward_kernel<T, W, L, V, false>, \
-                dim3(sums ? (unsigned)parts : (unsigned)(need < 65536 ? need : 65536)), dim3(nt), 0, \
-                a.stream, (const T*)a.dy, a.dy_stride, (const T*)a.x, a.x_stride,               \
-                (const W*)a.weight, a.mean, a.rstd, (T*)a.dx, part, a.rows, a.width);           \
-  }
+#define FM_NORM_BWD(L, V)                                                                      \
+  if constexpr (V * VE <= 32)                                                                  \
+    if (s.lpr == L && s.vpl == V)                                                              \
+      st = launch("layer norm backward",                                                       \
+                  want ? norm_backward_kernel<T, W, L, V, true>                                \
+                       : norm_backward_kernel<T, W, L, V, false>,                              \
+                  dim3((unsigned)parts), dim3(kNormThreads), 0, a.stream, (const T*)a.dy,      \
+                  a.dy_stride, (const T*)a.x, a.x_stride, (const W*)a.weight, a.mean, a.rstd,  \
+                  (T*)a.dx, part, a.rows, a.width);
     FM_NORM_SHAPES(FM_NORM_BWD)
 #undef FM_NORM_BWD
     if (st != FM_OK) return st;
-    if (want && !norm_parts_inline(s, VE)) {
+    if (want && s.vpl == 0) {
       st = launch("layer norm backward columns", norm_columns_kernel<T>,
                   dim3((a.width + kNormThreads - 1) / kNormThreads, parts), dim3(kNormThreads), 0,
                   a.stream, (const T*)a.dy, a.dy_stride, (const T*)a.x, a.x_stride, a.mean, a.rstd,

@@ -85,6 +85,23 @@ __device__ __forceinline__ Vec16<T> load16_part(const T* p, int have, T fill) {
   return r;
 }
 
+// N elements from any element-aligned address, of which `have` exist.
+template <class W, int N>
+struct Group {
+  W v[N];
+};
+template <class W, int N>
+__device__ __forceinline__ Group<W, N> load_group(const W* p, int have, W fill) {
+  Group<W, N> r;
+  if (have >= N) {
+    __builtin_memcpy(&r, p, sizeof(r));
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) r.v[e] = e < have ? p[e] : fill;
+  }
+  return r;
+}
+
 template <class T>
 __device__ __forceinline__ void store16_part(T* p, const Vec16<T>& r, int have) {
   if (have >= Vec16<T>::n) {
@@ -96,20 +113,37 @@ __device__ __forceinline__ void store16_part(T* p, const Vec16<T>& r, int have) 
   }
 }
 
-// Sum over aligned groups of LANES lanes of a wave (every lane gets it); the
-// order of the additions is fixed.
-template <int LANES>
-__device__ __forceinline__ float lanes_sum(float v) {
-#pragma unroll
-  for (int m = LANES / 2; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
+// Reductions over aligned groups of LANES (16, 32 or 64) lanes; every lane gets
+// the result, and the order of the operations is fixed.  Within 16 lanes by
+// rotations, beyond by exchanges of rows: vector instructions only.
+template <int ROT>
+__device__ __forceinline__ float lanes_rotate(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+      0, (int)__float_as_uint(v), 0x120 + ROT, 0xf, 0xf, false));
+}
+template <int LANES, class F>
+__device__ __forceinline__ float lanes_reduce(float v, F f) {
+  v = f(v, lanes_rotate<8>(v));
+  v = f(v, lanes_rotate<4>(v));
+  v = f(v, lanes_rotate<2>(v));
+  v = f(v, lanes_rotate<1>(v));
+  if constexpr (LANES >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  if constexpr (LANES >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
   return v;
 }
-
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+  return lanes_reduce<LANES>(v, [](float a, float b) { return a + b; });
+}
 template <int LANES>
 __device__ __forceinline__ float lanes_max(float v) {
-#pragma unroll
-  for (int m = LANES / 2; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor(v, m, 64));
-  return v;
+  return lanes_reduce<LANES>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
 }  // namespace fm

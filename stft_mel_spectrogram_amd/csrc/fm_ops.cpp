@@ -43,7 +43,7 @@ int check_scores(int64_t rows, int64_t vocab, int top, int dtype) {
     return bad("token log probabilities: vocab must be in [1, 2^31 - 65536)");
   if (top < 0 || top > kScoreMaxTop || top > vocab)
     return bad("token log probabilities: top must be in [0, min(64, vocab)]");
-  const ScoreSplit p = score_split(rows, static_cast<int>(vocab), vec_elems(dtype));
+  const ScoreSplit p = score_split(rows, static_cast<int>(vocab), vec_elems(dtype), top);
   if (rows >= (int64_t(1) << 31) / p.segs)
     return bad("token log probabilities: too many rows for one launch");
   return FM_OK;

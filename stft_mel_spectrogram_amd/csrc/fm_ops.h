@@ -43,9 +43,11 @@ struct NormBackward {
 
 constexpr int kNormMaxWidth = 1 << 20;
 constexpr int kNormThreads = 256;
+constexpr int kNormBlocks = 2048;  // workgroups that walk over rows: 8 per CU
 
-// Lane layout of a width: lanes per row and 16-byte groups per lane.  Rows of
-// more than 2048 groups do not stay in registers: {1024, 0}, sweeps that read
+// Lane layout of a width: lanes per row and 16-byte groups per lane, at most
+// 32 elements per lane, so that the backward's two sums per column fit beside
+// the row.  Wider rows do not stay in registers: {1024, 0}, sweeps that read
 // the row again from the cache.
 struct NormShape {
   int lpr, vpl;
@@ -56,18 +58,13 @@ inline NormShape norm_shape(int width, int ve) {
   if (nvec <= 32) return {16, 2};
   if (nvec <= 64) return {64, 1};
   if (nvec <= 128) return {64, 2};
-  if (nvec <= 256) return {64, 4};
+  if (nvec <= 256) return {256, 1};
   if (nvec <= 512) return {256, 2};
   if (nvec <= 1024) return {256, 4};
-  if (nvec <= 2048) return {256, 8};
+  if (nvec <= 2048 && ve == 4) return {256, 8};
   return {1024, 0};
 }
-#define FM_NORM_SHAPES(X) \
-  X(16, 1) X(16, 2) X(64, 1) X(64, 2) X(64, 4) X(256, 2) X(256, 4) X(256, 8)
-
-// Whether the backward adds dw and db up beside the row (else in a launch of
-// its own): 2 * vpl * ve accumulators per lane.
-inline bool norm_parts_inline(NormShape s, int ve) { return s.vpl > 0 && s.vpl * ve <= 32; }
+#define FM_NORM_SHAPES(X) X(16, 1) X(16, 2) X(64, 1) X(64, 2) X(256, 1) X(256, 2) X(256, 4) X(256, 8)
 
 // Partial rows (workgroups of the backward): enough to fill the chip several
 // times over, few enough that their sum stays small.
@@ -75,7 +72,7 @@ inline int norm_parts(int64_t rows, int width, int ve) {
   const NormShape s = norm_shape(width, ve);
   const int rpb = s.lpr > kNormThreads ? 1 : kNormThreads / s.lpr;
   const int64_t need = (rows + rpb - 1) / rpb;
-  const int64_t most = norm_parts_inline(s, ve) ? 1024 : 64;
+  const int64_t most = s.vpl > 0 ? 1024 : 64;
   return (int)(need < most ? need : most);
 }
 
@@ -125,28 +122,38 @@ struct ScoreBackward {
 
 constexpr int kScoreMaxTop = 64;  // one kept entry per lane of a wave
 
-// Work split of a call: waves per workgroup and row segments.  A row that one
-// wave holds in its registers takes one wave; longer rows take four, and are
-// cut into segments while the rows alone give fewer than 1024 workgroups.
+// Work split of a call: lanes of a row (256: a workgroup per row segment), 16-
+// byte groups of a lane, segments and their length.  Top alternatives need a
+// whole wave per row.  Long rows take segments of one chunk of 4 groups per
+// lane while the rows alone give fewer than 1024 workgroups, of one group where
+// even those leave compute units idle (8 x 50001, 5 alternatives: ...).
 struct ScoreSplit {
-  int waves, segs, seg_len;
+  int lanes, vecs, segs, seg_len;
 };
-inline ScoreSplit score_split(int64_t rows, int vocab, int ve) {
-  const int wave_chunk = 64 * ve * 4;
-  if (vocab <= wave_chunk) return {1, 1, vocab};
-  const int chunk = 4 * wave_chunk;
-  const int chunks = (vocab + chunk - 1) / chunk;
+inline ScoreSplit score_split(int64_t rows, int vocab, int ve, int top) {
+  const int groups = (vocab + ve - 1) / ve;
+  if (groups <= 256) {
+    if (top > 0) return {64, groups <= 64 ? 1 : groups <= 128 ? 2 : 4, 1, vocab};
+    if (groups <= 64) return {16, groups <= 16 ? 1 : groups <= 32 ? 2 : 4, 1, vocab};
+    return {64, groups <= 128 ? 2 : 4, 1, vocab};
+  }
+  int vecs = 4, chunk = 256 * ve * 4, chunks = (vocab + chunk - 1) / chunk;
+  if (rows * chunks < 256) {
+    vecs = 1;
+    chunk = 256 * ve;
+    chunks = (vocab + chunk - 1) / chunk;
+  }
   int64_t segs = rows > 0 ? (1024 + rows - 1) / rows : 1;
   if (segs > chunks) segs = chunks;
   if (segs < 1) segs = 1;
   const int per = (chunks + (int)segs - 1) / (int)segs;
-  return {4, (chunks + per - 1) / per, per * chunk};
+  return {256, vecs, (chunks + per - 1) / per, per * chunk};
 }
 inline int64_t score_part_bytes(int64_t rows, int segs) {
   return (rows * segs * 3 * (int64_t)sizeof(float) + 15) / 16 * 16;
 }
 inline int64_t score_workspace(int64_t rows, int vocab, int top, int ve) {
-  const ScoreSplit p = score_split(rows, vocab, ve);
+  const ScoreSplit p = score_split(rows, vocab, ve, top);
   return p.segs == 1 ? 0 : score_part_bytes(rows, p.segs) + rows * p.segs * (int64_t)top * 8;
 }
 
@@ -187,6 +194,7 @@ struct AttnArgs {
 constexpr int kAttnMaxDim = 128;
 constexpr int kAttnMaxFar = 1024;
 constexpr int kAttnMaxBuckets = 1024;
+constexpr int kAttnMaxSplits = 512; // key ranges of a forward call
 constexpr int kAttnQueries = 128;   // queries of a workgroup
 constexpr int kAttnTokenRows = 16;  // query rows of the single-token kernel
 
@@ -195,16 +203,22 @@ constexpr int kAttnTokenRows = 16;  // query rows of the single-token kernel
 inline bool attn_token_kernel(const AttnArgs& a) {
   return (int64_t)a.q_len * (a.heads / a.kv_heads) <= kAttnTokenRows;
 }
+// Waves of a single-token workgroup: as many as its registers and LDS let one
+// compute unit hold, since they join without a second launch.
+constexpr int attn_token_waves(int size, int dp) {
+  return size == 2 ? (dp == 64 ? 16 : 8) : (dp == 64 ? 8 : 4);
+}
 // Key ranges a forward call is cut into while its workgroups alone do not
-// fill the chip (256 compute units): four workgroups per unit for the
-// single-token kernel, two for the other; at least 256 keys (512) each.
+// fill the chip (256 compute units): two workgroups per unit; at least 2048
+// keys each for the single-token kernel (shorter ranges cost more in the join
+// than they gain: ...), 512 for the other.
 inline int attn_splits(const AttnArgs& a) {
   const bool token = attn_token_kernel(a);
   const int64_t wgs = token ? (int64_t)a.batch * a.kv_heads
                             : (int64_t)a.batch * a.heads * ((a.q_len + kAttnQueries - 1) / kAttnQueries);
   if (wgs == 0) return 1;
-  int64_t s = (token ? 1024 : 512) / wgs;
-  const int64_t most = (a.k_len + (token ? 255 : 511)) / (token ? 256 : 512);
+  int64_t s = 512 / wgs;
+  const int64_t least = token ? 2048 : 512, most = (a.k_len + least - 1) / least;
   if (s > most) s = most;
   return s < 1 ? 1 : (int)s;
 }

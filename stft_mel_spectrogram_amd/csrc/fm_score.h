@@ -17,15 +17,15 @@
 // ties go to the lower index), one per lane in descending order; a chunk's
 // entries are taken in descending order while they beat the last one kept.
 //
-// Memory bound.  Few rows with a long vocabulary are cut into segments, one
-// workgroup each, whose partial results a second launch joins.
+// Memory bound.  A row that 16 or 64 lanes hold in registers is read once, its
+// maximum taken first.  Longer rows go through 4 waves chunk by chunk, the next
+// chunk on its way; few of them are cut into segments, one workgroup each,
+// whose partial results a second launch joins.
 #pragma once
 
 #include "fm_op.h"
 
 namespace fm {
-
-constexpr int kScoreVecs = 4;  // 16-byte groups a lane holds at a time
 
 typedef unsigned long long key_t;
 
@@ -81,12 +81,22 @@ struct ScoreOut {
   float* top_lp;
 };
 
-// Writes a row's results; one wave, `list` its descending keys.
+// Joins the triples of LANES lanes around their common maximum.
+template <int LANES>
+__device__ __forceinline__ ScoreSum score_join_lanes(ScoreSum a) {
+  const float m = lanes_max<LANES>(a.m);
+  const float d = a.m == -INFINITY ? 0.f : fmaxf(a.m - m, -200.f);
+  const float r = __builtin_amdgcn_exp2f(d * kLog2e);
+  return {m, lanes_sum<LANES>(a.s * r), lanes_sum<LANES>((a.t + a.s * d) * r)};
+}
+
+// Writes a row's results: lane 0, and lane i the i-th of the `top` keys.
 template <class T>
 __device__ __forceinline__ void score_finish(const ScoreSum& r, const T* xr, int64_t row, int vocab,
                                              const void* tokens, int tok64, key_t list, int top,
                                              const ScoreOut& o, int lane) {
-  const float lse = r.m == -INFINITY ? (r.s == 0.f ? -INFINITY : NAN) : r.m + logf(r.s);
+  const float log_s = logf(r.s);
+  const float lse = r.m == -INFINITY ? (r.s == 0.f ? -INFINITY : NAN) : r.m + log_s;
   if (lane == 0) {
     const int64_t t = tok64 ? ((const int64_t*)tokens)[row] : ((const int32_t*)tokens)[row];
     float lp;
@@ -97,116 +107,160 @@ __device__ __forceinline__ void score_finish(const ScoreSum& r, const T* xr, int
     else if (lse == -INFINITY)
       lp = -INFINITY;
     else
-      lp = ((float)xr[t] - r.m) - logf(r.s);
+      lp = ((float)xr[t] - r.m) - log_s;
     if (o.lp) o.lp[row] = lp;
-    if (o.ent) o.ent[row] = lse == -INFINITY ? 0.f : logf(r.s) - r.t / r.s;
+    if (o.ent) o.ent[row] = lse == -INFINITY ? 0.f : log_s - r.t / r.s;
     if (o.lse) o.lse[row] = lse;
   }
   if (lane < top) {
     const float v = key_value(list);
     o.top_ids[row * top + lane] = key_index(list);
-    o.top_lp[row * top + lane] = v == -INFINITY && lse == -INFINITY ? -INFINITY : (v - r.m) - logf(r.s);
+    o.top_lp[row * top + lane] = v == -INFINITY && lse == -INFINITY ? -INFINITY : (v - r.m) - log_s;
   }
 }
 
-// WAVES waves per row segment; WAVES == 1: four rows per workgroup.  With
-// several segments, `part` gets (m, s, t) and the keys of each.
-template <class T, int WAVES, bool TOP>
-__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void score_forward_kernel(
-    const T* __restrict__ x, int64_t x_stride, const void* __restrict__ tokens, int tok64,
-    ScoreOut out, float* __restrict__ part, key_t* __restrict__ part_keys, int64_t rows, int vocab,
-    int top, int seg_len, int segs) {
+// exp(x - m) of a register chunk added to s and t; entries of -inf add 0.
+template <class T, int V>
+__device__ __forceinline__ void score_add(const Vec16<T> (&v)[V], float m, float& s, float& t) {
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int e = 0; e < Vec16<T>::n; ++e) {
+      const float d = (float)v[i].v[e] - m;
+      const float p = __builtin_amdgcn_exp2f(d * kLog2e);
+      s += p;
+      // p is 0 long before -200, where the product with -inf would be NaN
+      t = fmaf(p, fmaxf(d, -200.f), t);
+    }
+}
+template <class T, int V>
+__device__ __forceinline__ float score_max(const Vec16<T> (&v)[V]) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int e = 0; e < Vec16<T>::n; ++e) m = fmaxf(m, (float)v[i].v[e]);
+  return m;
+}
+
+// The best entries of a chunk (group i of this lane starts at c0 + (i * nt +
+// tid) * VE) into the wave's list, in descending order: `last` is what has
+// been taken so far.
+template <class T, int V>
+__device__ __forceinline__ void score_best(const Vec16<T> (&v)[V], int c0, int nt, int tid, int end,
+                                           int top, key_t& list, int lane) {
   constexpr int VE = Vec16<T>::n;
-  constexpr int NT = WAVES * 64;
-  constexpr int CH = NT * VE * kScoreVecs;
-  const int lane = threadIdx.x & 63;
-  const int wave = WAVES == 1 ? 0 : threadIdx.x >> 6;
-  const int tid = WAVES == 1 ? lane : threadIdx.x;
-  const int64_t unit = WAVES == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  key_t last = ~(key_t)0;
+  while (true) {
+    key_t best = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        const int c = c0 + (i * nt + tid) * VE + e;
+        const key_t k = c < end ? score_key((float)v[i].v[e], c) : 0;
+        if (k < last && k > best) best = k;
+      }
+    best = wave_max_key(best);
+    const key_t worst = __shfl(list, top - 1, 64);
+    if (best <= worst) break;
+    list_insert(list, best, lane);
+    last = best;
+  }
+}
+
+// Rows that L lanes hold, V groups each.
+template <class T, int L, int V, bool TOP>
+__global__ __launch_bounds__(256) void score_row_kernel(const T* __restrict__ x, int64_t x_stride,
+                                                        const void* __restrict__ tokens, int tok64,
+                                                        ScoreOut out, int64_t rows, int vocab,
+                                                        int top) {
+  constexpr int VE = Vec16<T>::n;
+  const int lane = threadIdx.x % L;
+  const int64_t row = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  const T* xr = x + row * x_stride;
+  const int end = row < rows ? vocab : 0;
+  Vec16<T> v[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = (i * L + lane) * VE;
+    v[i] = load16_part(xr + c, end - c, (T)-INFINITY);
+  }
+  ScoreSum r;
+  r.m = lanes_max<L>(score_max(v));
+  float s = 0.f, t = 0.f;
+  score_add(v, r.m == -INFINITY ? 0.f : r.m, s, t);
+  r.s = lanes_sum<L>(s);
+  r.t = lanes_sum<L>(t);
+  key_t list = 0;
+  if constexpr (TOP) score_best(v, 0, L, lane, end, top, list, lane);
+  if (row < rows) score_finish(r, xr, row, vocab, tokens, tok64, list, TOP ? top : 0, out, lane);
+}
+
+// 4 waves per row segment.  With several segments, `part` gets (m, s, t) and
+// the keys of each.
+template <class T, int V, bool TOP>
+__global__ __launch_bounds__(256) void score_forward_kernel(
+    const T* __restrict__ x, int64_t x_stride, const void* __restrict__ tokens, int tok64,
+    ScoreOut out, float* __restrict__ part, key_t* __restrict__ part_keys, int vocab, int top,
+    int seg_len, int segs) {
+  constexpr int VE = Vec16<T>::n;
+  constexpr int NT = 256, CH = NT * VE * V;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t unit = blockIdx.x;
   const int64_t row = unit / segs;
   const int seg = (int)(unit - row * segs);
-  if (WAVES == 1 && row >= rows) return;  // whole waves, no barriers there
   const T* xr = x + row * x_stride;
   const int beg = seg * seg_len;
   const int end = beg + seg_len < vocab ? beg + seg_len : vocab;
 
   ScoreSum acc = {-INFINITY, 0.f, 0.f};
   key_t list = 0;
+  Vec16<T> next[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = beg + (i * NT + tid) * VE;
+    next[i] = load16_part(xr + c, end - c, (T)-INFINITY);
+  }
   for (int c0 = beg; c0 < end; c0 += CH) {
-    Vec16<T> v[kScoreVecs];
+    Vec16<T> v[V];
 #pragma unroll
-    for (int i = 0; i < kScoreVecs; ++i) {
-      const int c = c0 + (i * NT + tid) * VE;
-      v[i] = load16_part(xr + c, end - c, (T)-INFINITY);
+    for (int i = 0; i < V; ++i) v[i] = next[i];
+    if (c0 + CH < end) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = c0 + CH + (i * NT + tid) * VE;
+        next[i] = load16_part(xr + c, end - c, (T)-INFINITY);
+      }
     }
-    float cm = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kScoreVecs; ++i)
-#pragma unroll
-      for (int e = 0; e < VE; ++e) cm = fmaxf(cm, (float)v[i].v[e]);
-    const float m = fmaxf(acc.m, cm);
+    const float m = fmaxf(acc.m, score_max(v));
     const float ms = m == -INFINITY ? 0.f : m;
     const float d0 = acc.m == -INFINITY ? 0.f : fmaxf(acc.m - ms, -200.f);
     const float r0 = __builtin_amdgcn_exp2f(d0 * kLog2e);
     float s = 0.f, t = 0.f;
-#pragma unroll
-    for (int i = 0; i < kScoreVecs; ++i)
-#pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        const float d = (float)v[i].v[e] - ms;
-        const float p = __builtin_amdgcn_exp2f(d * kLog2e);
-        s += p;
-        // p is 0 long before -200, where the product with -inf would be NaN
-        t = fmaf(p, fmaxf(d, -200.f), t);
-      }
+    score_add(v, ms, s, t);
     acc.t = (acc.t + acc.s * d0) * r0 + t;
     acc.s = acc.s * r0 + s;
     acc.m = m;
-    if constexpr (TOP) {
-      // descending over the chunk: `last` is what has been taken so far
-      key_t last = ~(key_t)0;
-      while (true) {
-        key_t best = 0;
+    if constexpr (TOP) score_best(v, c0, NT, tid, end, top, list, lane);
+  }
+  acc = score_join_lanes<64>(acc);
+  __shared__ ScoreSum sums[4];
+  __shared__ key_t keys[TOP ? 256 : 1];
+  if (lane == 0) sums[wave] = acc;
+  if constexpr (TOP) keys[tid] = lane < top ? list : 0;
+  __syncthreads();
+  if (wave != 0) return;
+  acc = sums[0];
 #pragma unroll
-        for (int i = 0; i < kScoreVecs; ++i)
-#pragma unroll
-          for (int e = 0; e < VE; ++e) {
-            const int c = c0 + (i * NT + tid) * VE + e;
-            const key_t k = c < end ? score_key((float)v[i].v[e], c) : 0;
-            if (k < last && k > best) best = k;
-          }
-        best = wave_max_key(best);
-        const key_t worst = __shfl(list, top - 1, 64);
-        if (best <= worst) break;
-        list_insert(list, best, lane);
-        last = best;
+  for (int w = 1; w < 4; ++w) acc = score_join(acc, sums[w]);
+  if constexpr (TOP) {
+    for (int w = 1; w < 4; ++w)
+      for (int i = 0; i < top; ++i) {
+        const key_t k = keys[w * 64 + i];
+        if (k <= __shfl(list, top - 1, 64)) break;
+        list_insert(list, k, lane);
       }
-    }
-  }
-#pragma unroll
-  for (int mk = 32; mk >= 1; mk >>= 1) {
-    const ScoreSum o = {__shfl_xor(acc.m, mk, 64), __shfl_xor(acc.s, mk, 64),
-                        __shfl_xor(acc.t, mk, 64)};
-    acc = score_join(acc, o);
-  }
-  if constexpr (WAVES > 1) {
-    __shared__ ScoreSum sums[WAVES];
-    __shared__ key_t keys[TOP ? WAVES * 64 : 1];
-    if (lane == 0) sums[wave] = acc;
-    if constexpr (TOP) keys[wave * 64 + lane] = lane < top ? list : 0;
-    __syncthreads();
-    if (wave != 0) return;
-    acc = sums[0];
-#pragma unroll
-    for (int w = 1; w < WAVES; ++w) acc = score_join(acc, sums[w]);
-    if constexpr (TOP) {
-      for (int w = 1; w < WAVES; ++w)
-        for (int i = 0; i < top; ++i) {
-          const key_t k = keys[w * 64 + i];
-          if (k <= __shfl(list, top - 1, 64)) break;
-          list_insert(list, k, lane);
-        }
-    }
   }
   if (segs == 1) {
     score_finish(acc, xr, row, vocab, tokens, tok64, list, TOP ? top : 0, out, lane);
@@ -233,12 +287,7 @@ __global__ __launch_bounds__(64) void score_join_kernel(
     const float* p = part + (row * segs + s) * 3;
     acc = score_join(acc, ScoreSum{p[0], p[1], p[2]});
   }
-#pragma unroll
-  for (int mk = 32; mk >= 1; mk >>= 1) {
-    const ScoreSum o = {__shfl_xor(acc.m, mk, 64), __shfl_xor(acc.s, mk, 64),
-                        __shfl_xor(acc.t, mk, 64)};
-    acc = score_join(acc, o);
-  }
+  acc = score_join_lanes<64>(acc);
   key_t list = 0;
   if (top > 0) {
     const int64_t n = (int64_t)segs * top;
@@ -256,25 +305,31 @@ __global__ __launch_bounds__(64) void score_join_kernel(
   score_finish(acc, x + row * x_stride, row, vocab, tokens, tok64, list, top, out, lane);
 }
 
-// dx of one row segment; see the formula above.
-template <class T, int WAVES>
-__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void score_backward_kernel(
+// dx of one row segment (L = 256), or of whole rows that L < 256 lanes hold
+// with V groups each; see the formula above.
+template <class T, int L, int V>
+__global__ __launch_bounds__(256) void score_backward_kernel(
     const T* __restrict__ x, int64_t x_stride, const void* __restrict__ tokens, int tok64,
     const float* __restrict__ lse_, const float* __restrict__ ent, const float* __restrict__ g_lp,
     const float* __restrict__ g_ent, const int64_t* __restrict__ top_ids,
     const float* __restrict__ g_top, T* __restrict__ dx, int64_t rows, int vocab, int top,
     int seg_len, int segs) {
   constexpr int VE = Vec16<T>::n;
-  constexpr int NT = WAVES * 64;
-  const int tid = WAVES == 1 ? threadIdx.x & 63 : threadIdx.x;
-  const int64_t unit = WAVES == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
-  const int64_t row = unit / segs;
-  const int seg = (int)(unit - row * segs);
-  if (WAVES == 1 && row >= rows) return;
+  const int tid = threadIdx.x % L;
+  const int64_t unit = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  const int64_t row = L == 256 ? unit / segs : unit;
+  const int seg = L == 256 ? (int)(unit - row * segs) : 0;
+  if (row >= rows) return;
   const T* xr = x + row * x_stride;
   T* dr = dx + row * vocab;
   const int beg = seg * seg_len;
   const int end = beg + seg_len < vocab ? beg + seg_len : vocab;
+  Vec16<T> v[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = beg + (i * L + tid) * VE;
+    v[i] = load16_part(xr + c, end - c, (T)0.f);
+  }
   const float lse = lse_[row];
   const bool empty = lse == -INFINITY;
   const float ls = empty ? 0.f : lse;
@@ -291,26 +346,28 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void score_backward_
     const float p = exp2f(l * kLog2e);  // with the subnormal ones, which a gradient may lift
     return -p * fmaf(ge, fmaxf(l, -200.f) + h, all);
   };
-  for (int c0 = beg; c0 < end; c0 += NT * VE * kScoreVecs) {
-    Vec16<T> v[kScoreVecs];
+  for (int c0 = beg; c0 < end; c0 += L * VE * V) {
+    if (c0 > beg) {
 #pragma unroll
-    for (int i = 0; i < kScoreVecs; ++i) {
-      const int c = c0 + (i * NT + tid) * VE;
-      v[i] = load16_part(xr + c, end - c, (T)0.f);
+      for (int i = 0; i < V; ++i) {
+        const int c = c0 + (i * L + tid) * VE;
+        v[i] = load16_part(xr + c, end - c, (T)0.f);
+      }
     }
 #pragma unroll
-    for (int i = 0; i < kScoreVecs; ++i) {
-      const int c = c0 + (i * NT + tid) * VE;
+    for (int i = 0; i < V; ++i) {
+      const int c = c0 + (i * L + tid) * VE;
 #pragma unroll
       for (int e = 0; e < VE; ++e) v[i].v[e] = (T)dense((float)v[i].v[e]);
       store16_part(dr + c, v[i], end - c);
     }
+    if constexpr (L < 256) break;
   }
   // The named tokens' entries, written again by the lane that wrote them
   // above (one thread's stores to one address stay in order), from the
   // unrounded sum.
   const auto named = [&](int64_t j) {
-    if (j < beg || j >= end || (int)(((j - beg) / VE) % NT) != tid) return;
+    if (j < beg || j >= end || (int)(((j - beg) / VE) % L) != tid) return;
     float d = dense((float)xr[j]);
     if (tok == j) d += g;
     if (g_top)
@@ -324,24 +381,41 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void score_backward_
     for (int i = 0; i < top; ++i) named(top_ids[row * top + i]);
 }
 
+#define FM_SCORE_SHAPES(X) X(16, 1) X(16, 2) X(16, 4) X(64, 2) X(64, 4)
+#define FM_SCORE_TOP_SHAPES(X) X(64, 1) X(64, 2) X(64, 4)
+
 template <class T>
 int score_forward_t(const ScoreForward& a) {
-  const ScoreSplit p = score_split(a.rows, a.vocab, Vec16<T>::n);
+  const ScoreSplit p = score_split(a.rows, a.vocab, Vec16<T>::n, a.top);
   ScoreOut out = {a.lp, a.ent, a.lse, a.top_ids, a.top_lp};
+#define FM_SCORE_ROW(L, V)                                                                        \
+  if (p.lanes == L && p.vecs == V)                                                                \
+    return launch("token log probabilities", score_row_kernel<T, L, V, false>,                    \
+                  dim3((unsigned)((a.rows + 256 / L - 1) / (256 / L))), dim3(256), 0, a.stream,   \
+                  (const T*)a.x, a.x_stride, a.tokens, a.tok64, out, a.rows, a.vocab, a.top);
+#define FM_SCORE_TOP_ROW(L, V)                                                                    \
+  if (p.lanes == L && p.vecs == V)                                                                \
+    return launch("token log probabilities", score_row_kernel<T, L, V, true>,                     \
+                  dim3((unsigned)((a.rows + 256 / L - 1) / (256 / L))), dim3(256), 0, a.stream,   \
+                  (const T*)a.x, a.x_stride, a.tokens, a.tok64, out, a.rows, a.vocab, a.top);
+  if (a.top == 0) {
+    FM_SCORE_SHAPES(FM_SCORE_ROW)
+  } else {
+    FM_SCORE_TOP_SHAPES(FM_SCORE_TOP_ROW)
+  }
+#undef FM_SCORE_ROW
+#undef FM_SCORE_TOP_ROW
   float* part = (float*)a.workspace;
   key_t* keys = (key_t*)((char*)a.workspace + score_part_bytes(a.rows, p.segs));
-  const int64_t units = a.rows * p.segs;
   const auto go = [&](auto kernel) {
-    const int64_t blocks = p.waves == 1 ? (units + 3) / 4 : units;
-    return launch("token log probabilities", kernel, dim3((unsigned)blocks),
-                  dim3(p.waves == 1 ? 256 : 256), 0, a.stream, (const T*)a.x, a.x_stride, a.tokens,
-                  a.tok64, out, part, keys, a.rows, a.vocab, a.top, p.seg_len, p.segs);
+    return launch("token log probabilities", kernel, dim3((unsigned)(a.rows * p.segs)), dim3(256), 0,
+                  a.stream, (const T*)a.x, a.x_stride, a.tokens, a.tok64, out, part, keys, a.vocab,
+                  a.top, p.seg_len, p.segs);
   };
-  int st;
-  if (p.waves == 1)
-    st = a.top ? go(score_forward_kernel<T, 1, true>) : go(score_forward_kernel<T, 1, false>);
-  else
-    st = a.top ? go(score_forward_kernel<T, 4, true>) : go(score_forward_kernel<T, 4, false>);
+  const int st = p.vecs == 1 ? (a.top ? go(score_forward_kernel<T, 1, true>)
+                                      : go(score_forward_kernel<T, 1, false>))
+                             : (a.top ? go(score_forward_kernel<T, 4, true>)
+                                      : go(score_forward_kernel<T, 4, false>));
   if (st != FM_OK || p.segs == 1) return st;
   return launch("token log probabilities (join)", score_join_kernel<T>, dim3((unsigned)a.rows),
                 dim3(64), 0, a.stream, (const T*)a.x, a.x_stride, a.tokens, a.tok64, out, part, keys,
@@ -350,14 +424,18 @@ int score_forward_t(const ScoreForward& a) {
 
 template <class T>
 int score_backward_t(const ScoreBackward& a) {
-  const ScoreSplit p = score_split(a.rows, a.vocab, Vec16<T>::n);
-  const int64_t units = a.rows * p.segs;
-  const int64_t blocks = p.waves == 1 ? (units + 3) / 4 : units;
-  return launch("token log probabilities backward",
-                p.waves == 1 ? score_backward_kernel<T, 1> : score_backward_kernel<T, 4>,
-                dim3((unsigned)blocks), dim3(256), 0, a.stream, (const T*)a.x, a.x_stride, a.tokens,
-                a.tok64, a.lse, a.ent, a.g_lp, a.g_ent, a.top_ids, a.g_top, (T*)a.dx, a.rows,
-                a.vocab, a.top, p.seg_len, p.segs);
+  const ScoreSplit p = score_split(a.rows, a.vocab, Vec16<T>::n, 0);
+#define FM_SCORE_BWD(L, V)                                                                        \
+  if (p.lanes == L && (L < 256 ? p.vecs == V : true))                                             \
+    return launch("token log probabilities backward", score_backward_kernel<T, L, V>,             \
+                  dim3((unsigned)((a.rows * p.segs + 256 / L - 1) / (256 / L))), dim3(256), 0,    \
+                  a.stream, (const T*)a.x, a.x_stride, a.tokens, a.tok64, a.lse, a.ent, a.g_lp,   \
+                  a.g_ent, a.top_ids, a.g_top, (T*)a.dx, a.rows, a.vocab, a.top, p.seg_len,       \
+                  p.segs);
+  FM_SCORE_SHAPES(FM_SCORE_BWD)
+  FM_SCORE_BWD(256, 4)
+#undef FM_SCORE_BWD
+  return set_error(FM_E_UNSUPPORTED, "token log probabilities: no kernel for this shape");
 }
 
 }  // namespace fm
