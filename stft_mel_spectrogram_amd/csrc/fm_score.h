@@ -18,8 +18,9 @@
 // entries are taken in descending order while they beat the last one kept.
 //
 // Memory bound.  A row that 16 or 64 lanes hold in registers is read once, its
-// maximum taken first.  Longer rows go through 4 waves chunk by chunk, the next
-// chunk on its way; few of them are cut into segments, one workgroup each,
+// maximum taken first.  Longer rows go through 4 waves chunk by chunk (8 waves
+// per SIMD hide the loads better than a chunk fetched ahead: 75 us against 80 at
+// 4096 x 32000 bf16); few of them are cut into segments, one workgroup each,
 // whose partial results a second launch joins.
 #pragma once
 
@@ -58,18 +59,21 @@ __device__ __forceinline__ void list_insert(key_t& list, key_t k, int lane) {
   list = below ? (above_too ? up : k) : list;
 }
 
-// (m, s, t) of two disjoint sets of entries.
+// m = max x, s = sum exp2(y), t = sum exp2(y) y of a set of entries, y = (x - m)
+// log2 e (x log2 e alone would overflow for masks of the type's lowest value).
+// The distance of two maxima is cut at -300: the factor is 0 there, and so must
+// its product with the distance be.
 struct ScoreSum {
   float m, s, t;
 };
+__device__ __forceinline__ float score_shift(float from, float to) {
+  // a set of -inf has s = t = 0
+  return from == -INFINITY ? 0.f : fmaxf((from - to) * kLog2e, -300.f);
+}
 __device__ __forceinline__ ScoreSum score_join(ScoreSum a, ScoreSum b) {
   const float m = fmaxf(a.m, b.m);
-  if (m == -INFINITY) return {m, a.s + b.s, a.t + b.t};
-  // a set of -inf only has s = t = 0.  Past -200 the factor is 0, and so must
-  // its product with the distance be, however far the maxima are apart.
-  const float da = a.m == -INFINITY ? 0.f : fmaxf(a.m - m, -200.f);
-  const float db = b.m == -INFINITY ? 0.f : fmaxf(b.m - m, -200.f);
-  const float ra = __builtin_amdgcn_exp2f(da * kLog2e), rb = __builtin_amdgcn_exp2f(db * kLog2e);
+  const float da = score_shift(a.m, m), db = score_shift(b.m, m);
+  const float ra = __builtin_amdgcn_exp2f(da), rb = __builtin_amdgcn_exp2f(db);
   return {m, a.s * ra + b.s * rb, (a.t + a.s * da) * ra + (b.t + b.s * db) * rb};
 }
 
@@ -85,8 +89,8 @@ struct ScoreOut {
 template <int LANES>
 __device__ __forceinline__ ScoreSum score_join_lanes(ScoreSum a) {
   const float m = lanes_max<LANES>(a.m);
-  const float d = a.m == -INFINITY ? 0.f : fmaxf(a.m - m, -200.f);
-  const float r = __builtin_amdgcn_exp2f(d * kLog2e);
+  const float d = score_shift(a.m, m);
+  const float r = __builtin_amdgcn_exp2f(d);
   return {m, lanes_sum<LANES>(a.s * r), lanes_sum<LANES>((a.t + a.s * d) * r)};
 }
 
@@ -96,41 +100,34 @@ __device__ __forceinline__ void score_finish(const ScoreSum& r, const T* xr, int
                                              const void* tokens, int tok64, key_t list, int top,
                                              const ScoreOut& o, int lane) {
   const float log_s = logf(r.s);
-  const float lse = r.m == -INFINITY ? (r.s == 0.f ? -INFINITY : NAN) : r.m + log_s;
+  // nothing but -inf; NaN if there was one
+  const bool empty = r.m == -INFINITY && r.s == 0.f;
+  const auto log_prob = [&](float v) { return empty ? -INFINITY : (v - r.m) - log_s; };
   if (lane == 0) {
     const int64_t t = tok64 ? ((const int64_t*)tokens)[row] : ((const int32_t*)tokens)[row];
-    float lp;
-    if (t < 0)
-      lp = 0.f;  // no token asked for
-    else if (t >= vocab)
-      lp = NAN;
-    else if (lse == -INFINITY)
-      lp = -INFINITY;
-    else
-      lp = ((float)xr[t] - r.m) - log_s;
-    if (o.lp) o.lp[row] = lp;
-    if (o.ent) o.ent[row] = lse == -INFINITY ? 0.f : log_s - r.t / r.s;
-    if (o.lse) o.lse[row] = lse;
+    // no token asked for, or none that exists
+    if (o.lp) o.lp[row] = t < 0 ? 0.f : t >= vocab ? NAN : log_prob((float)xr[t]);
+    if (o.ent) o.ent[row] = empty ? 0.f : fmaf(r.t / r.s, -kLn2, log_s);
+    if (o.lse) o.lse[row] = empty ? -INFINITY : r.m == -INFINITY ? NAN : r.m + log_s;
   }
   if (lane < top) {
-    const float v = key_value(list);
     o.top_ids[row * top + lane] = key_index(list);
-    o.top_lp[row * top + lane] = v == -INFINITY && lse == -INFINITY ? -INFINITY : (v - r.m) - log_s;
+    o.top_lp[row * top + lane] = log_prob(key_value(list));
   }
 }
 
-// exp(x - m) of a register chunk added to s and t; entries of -inf add 0.
+// A register chunk added to s and t, m finite; entries of -inf add 0.
 template <class T, int V>
 __device__ __forceinline__ void score_add(const Vec16<T> (&v)[V], float m, float& s, float& t) {
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int e = 0; e < Vec16<T>::n; ++e) {
-      const float d = (float)v[i].v[e] - m;
-      const float p = __builtin_amdgcn_exp2f(d * kLog2e);
+      const float y = ((float)v[i].v[e] - m) * kLog2e;
+      const float p = __builtin_amdgcn_exp2f(y);
       s += p;
-      // p is 0 long before -200, where the product with -inf would be NaN
-      t = fmaf(p, fmaxf(d, -200.f), t);
+      // p is 0 long before -300, where the product with -inf would be NaN
+      t = fmaf(p, fmaxf(y, -300.f), t);
     }
 }
 template <class T, int V>
@@ -216,29 +213,18 @@ __global__ __launch_bounds__(256) void score_forward_kernel(
 
   ScoreSum acc = {-INFINITY, 0.f, 0.f};
   key_t list = 0;
-  Vec16<T> next[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = beg + (i * NT + tid) * VE;
-    next[i] = load16_part(xr + c, end - c, (T)-INFINITY);
-  }
   for (int c0 = beg; c0 < end; c0 += CH) {
     Vec16<T> v[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = next[i];
-    if (c0 + CH < end) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = c0 + CH + (i * NT + tid) * VE;
-        next[i] = load16_part(xr + c, end - c, (T)-INFINITY);
-      }
+    for (int i = 0; i < V; ++i) {
+      const int c = c0 + (i * NT + tid) * VE;
+      v[i] = load16_part(xr + c, end - c, (T)-INFINITY);
     }
     const float m = fmaxf(acc.m, score_max(v));
-    const float ms = m == -INFINITY ? 0.f : m;
-    const float d0 = acc.m == -INFINITY ? 0.f : fmaxf(acc.m - ms, -200.f);
-    const float r0 = __builtin_amdgcn_exp2f(d0 * kLog2e);
+    const float d0 = score_shift(acc.m, m);
+    const float r0 = __builtin_amdgcn_exp2f(d0);
     float s = 0.f, t = 0.f;
-    score_add(v, ms, s, t);
+    score_add(v, m == -INFINITY ? 0.f : m, s, t);
     acc.t = (acc.t + acc.s * d0) * r0 + t;
     acc.s = acc.s * r0 + s;
     acc.m = m;
@@ -340,11 +326,14 @@ __global__ __launch_bounds__(256) void score_backward_kernel(
   if (g_top && !empty)
     for (int i = 0; i < top; ++i) all += g_top[row * top + i];
   const float ge = g_ent && !empty ? g_ent[row] : 0.f;
-  const float h = ge != 0.f ? ent[row] : 0.f;
+  // -p (g_H (lp + H) + all) from y = lp in base 2 plus 64: the exponential then
+  // stays a normal number down to p = 2^-190, and 2^-64 goes into the factor
+  // (a gradient may lift what float32 holds as subnormal)
+  const float slope = -ge * kLn2 * 0x1p-64f;
+  const float base = -0x1p-64f * (all + (ge != 0.f ? ge * (ent[row] - 64.f * kLn2) : 0.f));
   const auto dense = [&](float xv) {
-    const float l = xv - ls;
-    const float p = exp2f(l * kLog2e);  // with the subnormal ones, which a gradient may lift
-    return -p * fmaf(ge, fmaxf(l, -200.f) + h, all);
+    const float y = fmaf(xv - ls, kLog2e, 64.f);
+    return __builtin_amdgcn_exp2f(y) * fmaf(slope, fmaxf(y, -300.f), base);
   };
   for (int c0 = beg; c0 < end; c0 += L * VE * V) {
     if (c0 > beg) {
