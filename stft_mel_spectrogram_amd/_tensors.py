@@ -48,12 +48,13 @@ def rows_of(x: torch.Tensor, name: str):
 
 
 def same_device(x: torch.Tensor, **others) -> None:
+    dev = x.get_device()
     for name, t in others.items():
         if t is None:
             continue
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} must be a tensor, got {type(t).__name__}")
-        if t.device != x.device:
+        if t.get_device() != dev:
             raise ValueError(f"{name} must be on {x.device}, got {t.device}")
 
 
@@ -67,15 +68,17 @@ def contiguous_f32(t, shape, name: str) -> None:
         raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}")
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream() builds a Stream object first
+
+
 def call(x: torch.Tensor, fn, *args) -> None:
     """fn(*args, stream) on x's device, on torch's current stream there."""
-    dev = x.device
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args, stream)
+    dev = x.get_device()
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, stream)
+            st = fn(*args, _raw_stream(dev))
     if st < 0:
         N.check(st)
 
@@ -86,7 +89,7 @@ def workspace(x: torch.Tensor, nbytes: int):
     again in stream order."""
     if nbytes < 0:
         N.check(nbytes)
-    return torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
+    return x.new_empty((nbytes,), dtype=torch.uint8) if nbytes else None
 
 
 def ptr(t):

@@ -61,85 +61,82 @@ def relative_buckets(num_buckets: int = 32, max_distance: int = 128, bidirection
                         dtype=torch.int32, device=dev)
 
 
-def _strides(x):
-    s = x.stride()
-    return s[0], s[1], s[2]
-
-
-_NO_STRIDES = (0, 0, 0)
-
-
 class _Call:
     """Checked arguments of a call."""
 
+    __slots__ = ("q", "k", "v", "table", "code", "head", "inputs", "shape")
+
     def __init__(self, q, k, v, table, buckets, scale, causal, key_lengths, query_offset):
-        self.code = T.dtype_code(q, "q")
-        T.same_device(q, k=k, v=v, table=table, buckets=buckets, key_lengths=key_lengths)
-        if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        code = T.dtype_code(q, "q")
+        offset, offset_value = None, 0
+        if isinstance(query_offset, torch.Tensor):
+            offset = query_offset
+        else:
+            offset_value = int(query_offset)
+        T.same_device(q, k=k, v=v, table=table, buckets=buckets, key_lengths=key_lengths,
+                      query_offset=offset)
+        shape, kshape = q.shape, k.shape
+        if len(shape) != 4 or len(kshape) != 4 or v.dim() != 4:
             raise ValueError("q, k and v must be [batch, heads, time, head_dim]")
-        if k.dtype != q.dtype or v.dtype != q.dtype:
-            raise TypeError(f"k and v must be {q.dtype} like q, got {k.dtype} and {v.dtype}")
-        b, h, tq, d = q.shape
-        _, hk, tk, _ = k.shape
-        if k.shape != v.shape or k.shape[0] != b or k.shape[3] != d:
+        dtype = q.dtype
+        if k.dtype != dtype or v.dtype != dtype:
+            raise TypeError(f"k and v must be {dtype} like q, got {k.dtype} and {v.dtype}")
+        b, h, tq, d = shape
+        kb, hk, tk, kd = kshape
+        if kshape != v.shape or kb != b or kd != d:
             raise ValueError(f"k and v must be [{b}, key heads, key time, {d}], got "
-                             f"{tuple(k.shape)} and {tuple(v.shape)}")
+                             f"{tuple(kshape)} and {tuple(v.shape)}")
         if hk == 0 or h % hk:
             raise ValueError(f"{h} query heads do not divide among {hk} key heads")
         if d < 1 or d > 128:
             raise ValueError(f"head_dim must be in 1 .. 128, got {d}")
-        if d > 1 and not (q.stride(3) == k.stride(3) == v.stride(3) == 1):
+        qs, ks, vs = q.stride(), k.stride(), v.stride()
+        if d > 1 and not qs[3] == ks[3] == vs[3] == 1:
             raise ValueError("the last axis of q, k and v must be contiguous")
-        self.table_code = T.dtype_code(table, "table")
-        if self.table_code not in (self.code, N.FM_F32):
-            raise TypeError(f"table must be {q.dtype} or float32, got {table.dtype}")
-        if table.dim() != 2 or table.shape[1] != h or not table.is_contiguous():
+        table_code = T.dtype_code(table, "table")
+        if table_code != code and table_code != N.FM_F32:
+            raise TypeError(f"table must be {dtype} or float32, got {table.dtype}")
+        tshape = table.shape
+        if len(tshape) != 2 or tshape[1] != h or not table.is_contiguous():
             raise ValueError(f"table must be a contiguous tensor of shape [buckets, {h}], "
-                             f"got {tuple(table.shape)}")
-        if not 1 <= table.shape[0] <= 1024:
-            raise ValueError(f"table must have 1 .. 1024 buckets, got {table.shape[0]}")
-        size = buckets.numel()
+                             f"got {tuple(tshape)}")
+        if not 1 <= tshape[0] <= 1024:
+            raise ValueError(f"table must have 1 .. 1024 buckets, got {tshape[0]}")
         if buckets.dtype != torch.int32 or buckets.dim() != 1 or not buckets.is_contiguous():
             raise TypeError("buckets must be a contiguous one-dimensional int32 tensor")
+        size = buckets.shape[0]
         if size % 2 == 0 or size > 2049:
             raise ValueError(f"buckets must have an odd length of at most 2049, got {size}")
         if key_lengths is not None and (key_lengths.dtype != torch.int32
                                         or key_lengths.shape != (b,)
                                         or not key_lengths.is_contiguous()):
             raise ValueError(f"key_lengths must be a contiguous int32 tensor of shape ({b},)")
-        self.offset, self.offset_value = None, 0
-        if isinstance(query_offset, torch.Tensor):
-            T.same_device(q, query_offset=query_offset)
-            if (query_offset.dtype != torch.int32 or query_offset.shape != (b,)
-                    or not query_offset.is_contiguous()):
-                raise ValueError(f"query_offset must be an int or a contiguous int32 tensor of "
-                                 f"shape ({b},)")
-            self.offset = query_offset
-        else:
-            self.offset_value = int(query_offset)
-        self.q, self.k, self.v, self.table, self.buckets = q, k, v, table, buckets
-        self.lengths = key_lengths
-        self.head = (self.code, self.table_code, 1 if causal else 0, size // 2, table.shape[0], 0,
-                     b, h, hk, tq, tk, d, self.offset_value,
+        if offset is not None and (offset.dtype != torch.int32 or offset.shape != (b,)
+                                   or not offset.is_contiguous()):
+            raise ValueError("query_offset must be an int or a contiguous int32 tensor of "
+                             f"shape ({b},)")
+        self.q, self.k, self.v, self.table, self.code, self.shape = q, k, v, table, code, shape
+        self.head = (code, table_code, 1 if causal else 0, size // 2, tshape[0], 0,
+                     b, h, hk, tq, tk, d, offset_value,
                      d ** -0.5 if scale is None else float(scale),
                      q.data_ptr(), k.data_ptr(), v.data_ptr(), table.data_ptr(),
-                     buckets.data_ptr(), T.ptr(key_lengths), T.ptr(self.offset))
-        self.inputs = (*_strides(q), *_strides(k), *_strides(v))
+                     buckets.data_ptr(), T.ptr(key_lengths), T.ptr(offset))
+        self.inputs = qs[:3] + ks[:3] + vs[:3]
 
     def forward(self, stats: bool, out=None):
         q = self.q
-        b, h, tq, _ = q.shape
         if out is None:
             out = _like(q)
         elif (out.shape != q.shape or out.dtype != q.dtype or out.device != q.device
               or (q.shape[3] > 1 and out.stride(3) != 1)):
             raise ValueError(f"out must be a {q.dtype} tensor of shape {tuple(q.shape)} on "
                              f"{q.device} with a contiguous last axis")
-        lse = torch.empty((b, h, tq), dtype=torch.float32, device=q.device) if stats else None
+        lse = q.new_empty(self.shape[:3], dtype=torch.float32) if stats else None
         a = N.AttentionArgs(*self.head, out.data_ptr(), T.ptr(lse), None, None, None, None, None,
-                            *self.inputs, *_strides(out))
-        ws = T.workspace(q, N.lib.fm_attention_workspace(ctypes.byref(a), 0))
-        T.call(q, N.lib.fm_attention_forward, ctypes.byref(a), T.ptr(ws))
+                            *self.inputs, *out.stride()[:3])
+        ref = ctypes.byref(a)
+        ws = T.workspace(q, N.lib.fm_attention_workspace(ref, 0))
+        T.call(q, N.lib.fm_attention_forward, ref, T.ptr(ws))
         return out, lse
 
     def backward(self, grad_out, out, lse, need_table=True):
@@ -154,10 +151,11 @@ class _Call:
         dt = torch.empty_like(self.table) if need_table else None
         a = N.AttentionArgs(*self.head, out.data_ptr(), lse.data_ptr(),
                             grad_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                            T.ptr(dt), *self.inputs, *_strides(out), *_strides(grad_out),
-                            *_strides(dq), *_strides(dk), *_strides(dv))
-        ws = T.workspace(q, N.lib.fm_attention_workspace(ctypes.byref(a), 1))
-        T.call(q, N.lib.fm_attention_backward, ctypes.byref(a), T.ptr(ws))
+                            T.ptr(dt), *self.inputs, *out.stride()[:3], *grad_out.stride()[:3],
+                            *dq.stride()[:3], *dk.stride()[:3], *dv.stride()[:3])
+        ref = ctypes.byref(a)
+        ws = T.workspace(q, N.lib.fm_attention_workspace(ref, 1))
+        T.call(q, N.lib.fm_attention_backward, ref, T.ptr(ws))
         return dq, dk, dv, dt
 
 
@@ -165,9 +163,10 @@ def _like(x):
     """A dense tensor of x's shape with time outside the heads where x has it
     so (the layout of a projection's output)."""
     b, h, t, d = x.shape
-    if h > 1 and x.stride(2) > x.stride(1):
-        return torch.empty((b, t, h, d), dtype=x.dtype, device=x.device).transpose(1, 2)
-    return torch.empty((b, h, t, d), dtype=x.dtype, device=x.device)
+    s = x.stride()
+    if h > 1 and s[2] > s[1]:
+        return x.new_empty((b, t, h, d)).transpose(1, 2)
+    return x.new_empty((b, h, t, d))
 
 
 def relative_attention(q, k, v, table, buckets, *, scale=None, causal: bool = False,

@@ -38,14 +38,14 @@ def _check(x, weight, bias):
 def _forward(x, weight, bias, eps, stats: bool, out=None):
     code, pcode, rows, width, stride = _check(x, weight, bias)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = x.new_empty(x.shape)
     elif (out.shape != x.shape or out.dtype != x.dtype or out.device != x.device
           or not out.is_contiguous()):
         raise ValueError(f"out must be a contiguous {x.dtype} tensor of shape {tuple(x.shape)} "
                          f"on {x.device}")
     mean = rstd = None
     if stats:
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
         rstd = torch.empty_like(mean)
     T.call(x, N.lib.fm_layer_norm_forward, x.data_ptr(), stride, T.ptr(weight), T.ptr(bias),
            out.data_ptr(), T.ptr(mean), T.ptr(rstd), rows, width, float(eps), code, pcode)
@@ -80,7 +80,7 @@ def layer_norm_backward(grad_out, x, weight, mean, rstd, params: bool = True):
     _, _, g_stride = T.rows_of(grad_out, "grad_out")
     T.contiguous_f32(mean, x.shape[:-1], "mean")
     T.contiguous_f32(rstd, x.shape[:-1], "rstd")
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dx = x.new_empty(x.shape)
     dw = db = ws = None
     if weight is not None and params:
         dw, db = torch.empty_like(weight), torch.empty_like(weight)

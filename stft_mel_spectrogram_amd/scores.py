@@ -35,21 +35,27 @@ def _check(logits, tokens, top_k):
     return code, rows, vocab, stride, 64 if tokens.dtype == torch.int64 else 32, top_k
 
 
+def _forward(logits, tokens, top_k, need_lse):
+    code, rows, vocab, stride, bits, top_k = _check(logits, tokens, top_k)
+    lead = logits.shape[:-1]
+    lp = logits.new_empty(lead, dtype=torch.float32)
+    ent = torch.empty_like(lp)
+    lse = torch.empty_like(lp) if need_lse else None
+    ids = tops = None
+    if top_k:
+        tops = logits.new_empty((*lead, top_k), dtype=torch.float32)
+        ids = logits.new_empty((*lead, top_k), dtype=torch.int64)
+    ws = T.workspace(logits, N.lib.fm_token_logprobs_workspace(rows, vocab, top_k, code))
+    T.call(logits, N.lib.fm_token_logprobs, logits.data_ptr(), stride, tokens.data_ptr(), bits,
+           lp.data_ptr(), ent.data_ptr(), T.ptr(lse), T.ptr(ids), T.ptr(tops), T.ptr(ws), rows,
+           vocab, top_k, code)
+    return TokenLogprobs(lp, ent, ids, tops), lse
+
+
 def token_logprobs_forward(logits, tokens, top_k: int = 0):
     """(TokenLogprobs, lse): the results and the float32 log sum exp of every
     row, which token_logprobs_backward takes."""
-    code, rows, vocab, stride, bits, top_k = _check(logits, tokens, top_k)
-    lead = logits.shape[:-1]
-    lp, ent, lse = torch.empty((3, *lead), dtype=torch.float32, device=logits.device).unbind(0)
-    ids = tops = None
-    if top_k:
-        ids = torch.empty((*lead, top_k), dtype=torch.int64, device=logits.device)
-        tops = torch.empty((*lead, top_k), dtype=torch.float32, device=logits.device)
-    ws = T.workspace(logits, N.lib.fm_token_logprobs_workspace(rows, vocab, top_k, code))
-    T.call(logits, N.lib.fm_token_logprobs, logits.data_ptr(), stride, tokens.data_ptr(), bits,
-           lp.data_ptr(), ent.data_ptr(), lse.data_ptr(), T.ptr(ids), T.ptr(tops), T.ptr(ws), rows,
-           vocab, top_k, code)
-    return TokenLogprobs(lp, ent, ids, tops), lse
+    return _forward(logits, tokens, top_k, True)
 
 
 def token_logprobs(logits, tokens, top_k: int = 0) -> TokenLogprobs:
@@ -58,7 +64,7 @@ def token_logprobs(logits, tokens, top_k: int = 0) -> TokenLogprobs:
     Differentiable with respect to the logits."""
     if isinstance(logits, torch.Tensor) and logits.requires_grad and torch.is_grad_enabled():
         return TokenLogprobs(*_TokenLogprobs.apply(logits, tokens, top_k))
-    return token_logprobs_forward(logits, tokens, top_k)[0]
+    return _forward(logits, tokens, top_k, False)[0]
 
 
 def token_logprobs_backward(logits, tokens, lse, entropy, grad_logprobs=None, grad_entropy=None,
@@ -81,7 +87,7 @@ def token_logprobs_backward(logits, tokens, lse, entropy, grad_logprobs=None, gr
     if top_ids is not None and (top_ids.dtype != torch.int64 or not top_ids.is_contiguous()
                                 or tuple(top_ids.shape) != (*lead, top_k)):
         raise ValueError(f"top_ids must be a contiguous int64 tensor of shape {(*lead, top_k)}")
-    dx = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    dx = logits.new_empty(logits.shape)
     T.call(logits, N.lib.fm_token_logprobs_backward, logits.data_ptr(), stride, tokens.data_ptr(),
            bits, lse.data_ptr(), T.ptr(entropy), T.ptr(grad_logprobs), T.ptr(grad_entropy),
            T.ptr(top_ids), T.ptr(grad_top_logprobs), dx.data_ptr(), rows, vocab, top_k, code)
