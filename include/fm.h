@@ -424,6 +424,7 @@ int fm_token_logprobs_backward(const void* x, int64_t x_stride, const void* toke
  *                head_dim]: strides in elements of (entry, head, time), >= 0,
  *                the last axis contiguous; heads a multiple of kv_heads, query
  *                head h reads key head h / (heads / kv_heads); head_dim <= 128;
+ *   scale        in [2^-60, 2^60];
  *   table        [num_buckets, heads] contiguous, table_dtype (dtype or
  *                FM_F32), num_buckets <= 1024;
  *   bucket_map   [2 far + 1] int32, the bucket of each distance key - query

@@ -249,6 +249,19 @@ __device__ __forceinline__ acc16 bias_start_queries(const float* bias, int far, 
   for (int r = 0; r < 16; ++r) acc[r] = p[-(8 * (r / 4) + r % 4)];
   return acc;
 }
+// An accumulator whose rows start at the values of an LDS row vector.
+__device__ __forceinline__ acc16 acc_rows(const float* p, int h) {
+  acc16 a;
+#pragma unroll
+  for (int y = 0; y < 4; ++y) {
+    const float4 v = *(const float4*)(p + 8 * y + 4 * h);
+    a[4 * y] = v.x;
+    a[4 * y + 1] = v.y;
+    a[4 * y + 2] = v.z;
+    a[4 * y + 3] = v.w;
+  }
+  return a;
+}
 __device__ __forceinline__ acc16 acc_zero() {
   acc16 a;
 #pragma unroll
@@ -302,6 +315,20 @@ __device__ __forceinline__ float halves_max(float x) {
 __device__ __forceinline__ float halves_sum(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// A border for the compiler's scheduler, which by itself puts every LDS read
+// right before the product that waits for it.  The kernels read the operands of
+// one stage's products in the stage before.
+__device__ __forceinline__ void stage() { __builtin_amdgcn_sched_barrier(0); }
+// Within a stage: N times a product and VALU vector instructions.
+template <int N, int VALU>
+__device__ __forceinline__ void alternate() {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+  }
 }
 
 // Stores 4 consecutive elements of a result column's rows.

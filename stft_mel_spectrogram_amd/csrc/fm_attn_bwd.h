@@ -357,9 +357,11 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
   constexpr bool AHEAD = VEC && !(sizeof(T) == 4 && DP == 128);
   T* qt = (T*)smem;
   T* gt = qt + 2 * BQ * LD;
-  float* lse2 = (float*)(gt + 2 * BQ * LD);  // [2][BQ]
-  float* delta = lse2 + 2 * BQ;              // [2][BQ]
-  float* bias = delta + 2 * BQ;
+  // -lse in units of the product and -delta start the accumulators: exp2 of the
+  // scaled scores then is p, and dp comes out less delta
+  float* neg_lse = (float*)(gt + 2 * BQ * LD);  // [2][BQ]
+  float* neg_delta = neg_lse + 2 * BQ;          // [2][BQ]
+  float* bias = neg_delta + 2 * BQ;
 
   const int tid = threadIdx.x, wave = wave_index(), lane = tid & 63, n = lane & 31, h = lane >> 5;
   const int blocks = (a.k_len + kAttnBlockKeys - 1) / kAttnBlockKeys;
@@ -396,12 +398,12 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
     const float* am = a.amax + (int64_t)(b * a.heads + kvh * group) * a.q_len;
     for (int64_t t = tid; t < (int64_t)group * a.q_len; t += kAttnThreads) m = fmaxf(m, am[t]);
     m = lanes_max<64>(m);
-    if (lane == 0) lse2[wave] = m;
+    if (lane == 0) neg_lse[wave] = m;
     __syncthreads();
-    unit = unit_scale(fmaxf(fmaxf(lse2[0], lse2[1]), fmaxf(lse2[2], lse2[3])));
+    unit = unit_scale(fmaxf(fmaxf(neg_lse[0], neg_lse[1]), fmaxf(neg_lse[2], neg_lse[3])));
     __syncthreads();
   }
-  const float c = a.scale * kLog2e;
+  const float c = a.scale * kLog2e, inv_c = 1.f / c;
   const float back = kIsF16<T> ? unit * __builtin_amdgcn_exp2f(-kProbShift<T>) : 1.f;
   // row i of the tile at i0 sees this lane's key if i >= need
   const int need = j >= len ? a.q_len : a.causal ? max(j - first, 0) : 0;
@@ -421,22 +423,22 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
       if (tid < BQ) {
         const bool in = i0 + tid < i_end;
         const float v = in ? a.lse[row0 + i0 + tid] : -INFINITY;
-        l_next = v == -INFINITY ? INFINITY : fmaf(v, kLog2e, -kProbShift<T>);
-        d_next = in ? a.delta[row0 + i0 + tid] : 0.f;
+        l_next = v == -INFINITY ? v : fmaf(v, -kLog2e, kProbShift<T>) * inv_c;
+        d_next = in ? -a.delta[row0 + i0 + tid] : 0.f;
       }
     };
     const auto put = [&](int buf) __attribute__((always_inline)) {
       ql.store(qt + buf * BQ * LD, tid);
       gl.store(gt + buf * BQ * LD, tid);
       if (tid < BQ) {
-        lse2[buf * BQ + tid] = l_next;
-        delta[buf * BQ + tid] = d_next;
+        neg_lse[buf * BQ + tid] = l_next;
+        neg_delta[buf * BQ + tid] = d_next;
       }
     };
     fetch(i_beg);
     fill_bias<T>(a, head, bias, tid, kAttnThreads);
     const float lo = as_scalar(bias_of<T>(a, head, -a.far) * kLog2e);
-  const float hi = as_scalar(bias_of<T>(a, head, a.far) * kLog2e);
+    const float hi = as_scalar(bias_of<T>(a, head, a.far) * kLog2e);
     put(0);
     __syncthreads();
     int buf = 0;
@@ -446,54 +448,90 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
       if (jw < len && !(a.causal && i0 + BQ - 1 + first < jw)) {
         const T* qtb = qt + buf * BQ * LD;
         const T* gtb = gt + buf * BQ * LD;
+        acc16 s[NS], ds[NS];
+        float far_bias[NS];
 #pragma unroll
         for (int u = 0; u < NS; ++u) {
-          const int iu = i0 + 32 * u;
-          const int dist = jw - first - iu;
-          const Frag<T> q0 = tile_rows<T, DP>(qtb, 32 * u + n, 0, h);
-          acc16 s;
-          float far_bias;
+          const int dist = jw - first - i0 - 32 * u;
+          s[u] = acc_rows(neg_lse + buf * BQ + 32 * u, h);
           if (tile_before(dist, a.far) || tile_behind(dist, a.far)) {
-            s = mma32(q0, kf[0], acc_zero());
-            far_bias = dist < 0 ? lo : hi;
+            far_bias[u] = dist < 0 ? lo : hi;
           } else {
-            s = mma32(q0, kf[0], bias_start_queries(bias, a.far, dist, h, n));
-            far_bias = 0.f;
+            s[u] += bias_start_queries(bias, a.far, dist, h, n);
+            far_bias[u] = 0.f;
           }
+        }
+        // Products in stages, each reading the next one's operands: queries and
+        // gradients by rows, then by columns.
+        Frag<T> rows[2][KS];
+        const auto read_rows = [&](const T* tile, int u, Frag<T>(&f)[KS]) __attribute__((always_inline)) {
 #pragma unroll
-          for (int x = 1; x < KS; ++x) s = mma32(tile_rows<T, DP>(qtb, 32 * u + n, x, h), kf[x], s);
-          acc16 dp = acc_zero();
+          for (int x = 0; x < KS; ++x) f[x] = tile_rows<T, DP>(tile, 32 * u + n, x, h);
+        };
+        read_rows(qtb, 0, rows[0]);
+        ds[0] = acc_rows(neg_delta + buf * BQ, h);
+        stage();
 #pragma unroll
-          for (int x = 0; x < KS; ++x) dp = mma32(tile_rows<T, DP>(gtb, 32 * u + n, x, h), vf[x], dp);
-          if (jw + 32 > len || (a.causal && jw + 31 - first > iu)) {
+        for (int u = 0; u < NS; ++u) {
+          read_rows(gtb, u, rows[1]);
+          stage();
+#pragma unroll
+          for (int x = 0; x < KS; ++x) s[u] = mma32(rows[0][x], kf[x], s[u]);
+          stage();
+          if (u + 1 < NS) {
+            read_rows(qtb, u + 1, rows[0]);
+            ds[u + 1] = acc_rows(neg_delta + buf * BQ + 32 * (u + 1), h);
+          }
+          stage();
+#pragma unroll
+          for (int x = 0; x < KS; ++x) ds[u] = mma32(rows[1][x], vf[x], ds[u]);
+          stage();
+        }
+        if (jw + 32 > len || (a.causal && jw + 31 - first > i0)) {
+#pragma unroll
+          for (int u = 0; u < NS; ++u)
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-              s[r] = iu + 8 * (r / 4) + 4 * h + r % 4 >= need ? s[r] : -INFINITY;
+              s[u][r] = i0 + 32 * u + 8 * (r / 4) + 4 * h + r % 4 >= need ? s[u][r] : -INFINITY;
+        }
+        // step t: rows 16 t .. 16 t + 15 of the tile
+        Frag<T> cols[2][2 * DT], p[2], f[2];
+        const auto read_cols = [&](int t, Frag<T>(&c)[2 * DT]) __attribute__((always_inline)) {
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            c[d] = tile_cols<T, DP>(gtb, 16 * t, 32 * d, lane);
+            c[DT + d] = tile_cols<T, DP>(qtb, 16 * t, 32 * d, lane);
           }
+        };
+        const auto scores = [&](int t) __attribute__((always_inline)) {
+          const int u = t >> 1, x = t & 1;
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const float4 l4 = *(const float4*)(lse2 + buf * BQ + 32 * u + 8 * y + 4 * h);
-            const float4 d4 = *(const float4*)(delta + buf * BQ + 32 * u + 8 * y + 4 * h);
-            const float ls[4] = {l4.x, l4.y, l4.z, l4.w}, ds[4] = {d4.x, d4.y, d4.z, d4.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int r = 4 * y + e;
-              s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, far_bias - ls[e]));
-              if constexpr (kIsF16<T>)
-                dp[r] = s[r] * ((dp[r] - ds[e]) * back);
-              else
-                dp[r] = s[r] * (dp[r] - ds[e]);
-            }
+          for (int r = 8 * x; r < 8 * x + 8; ++r) {
+            s[u][r] = __builtin_amdgcn_exp2f(fmaf(s[u][r], c, far_bias[u]));
+            if constexpr (kIsF16<T>)
+              ds[u][r] *= s[u][r] * back;
+            else
+              ds[u][r] *= s[u][r];
           }
+          p[t & 1] = acc_frag<T>(s[u], x);
+          f[t & 1] = acc_frag<T>(ds[u], x);
+        };
+        read_cols(0, cols[0]);
+        stage();
+        scores(0);
+        stage();
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const Frag<T> p = acc_frag<T>(s, x), f = acc_frag<T>(dp, x);
+        for (int t = 0; t < 2 * NS; ++t) {
+          if (t + 1 < 2 * NS) read_cols(t + 1, cols[(t + 1) & 1]);
+          stage();
+          if (t + 1 < 2 * NS) scores(t + 1);
 #pragma unroll
-            for (int d = 0; d < DT; ++d) {
-              dv[d] = mma32(tile_cols<T, DP>(gtb, 32 * u + 16 * x, 32 * d, lane), p, dv[d]);
-              dk[d] = mma32(tile_cols<T, DP>(qtb, 32 * u + 16 * x, 32 * d, lane), f, dk[d]);
-            }
+          for (int d = 0; d < DT; ++d) {
+            dv[d] = mma32(cols[t & 1][d], p[t & 1], dv[d]);
+            dk[d] = mma32(cols[t & 1][DT + d], f[t & 1], dk[d]);
           }
+          if constexpr (sizeof(T) == 2) alternate<2 * DT, 32 / (2 * DT)>();
+          stage();
         }
       }
       if (!AHEAD && more) fetch(i0 + BQ);

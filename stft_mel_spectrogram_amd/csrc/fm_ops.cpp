@@ -69,7 +69,9 @@ int attention_args(const fm_attention_args* p, bool backward, AttnArgs& a) {
     return bad("attention: q_len and k_len must be in [0, 2^30)");
   if (p->head_dim < 1) return bad("attention: head_dim must be >= 1");
   if (p->head_dim > kAttnMaxDim) return set_error(FM_E_UNSUPPORTED, "attention: head_dim must be <= 128");
-  if (!(p->scale > 0.0) || !std::isfinite(p->scale)) return bad("attention: scale must be finite and > 0");
+  // its reciprocal times a bias or a log sum exp has to stay in float32's range
+  if (!(p->scale >= 0x1p-60 && p->scale <= 0x1p60))
+    return bad("attention: scale must be in [2^-60, 2^60]");
   if (p->far < 0 || p->num_buckets < 1) return bad("attention: far >= 0 and num_buckets >= 1 are wanted");
   if (p->far > kAttnMaxFar || p->num_buckets > kAttnMaxBuckets)
     return set_error(FM_E_UNSUPPORTED, "attention: far and num_buckets must be <= 1024");
@@ -95,7 +97,6 @@ int attention_args(const fm_attention_args* p, bool backward, AttnArgs& a) {
   a.k_len = static_cast<int>(p->k_len);
   a.dim = static_cast<int>(p->head_dim);
   a.scale = static_cast<float>(p->scale);
-  if (!(a.scale > 0.f) || !std::isfinite(a.scale)) return bad("attention: scale is out of float32's range");
   for (int i = 0; i < 3; ++i) {
     a.qs[i] = p->q_stride[i];
     a.ks[i] = p->k_stride[i];
