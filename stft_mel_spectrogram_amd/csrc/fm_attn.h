@@ -307,6 +307,13 @@ __device__ __forceinline__ float as_scalar(float x) {
   return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
 }
 
+// The same value to the compiler as a new one: what is computed from it after
+// a loop is not kept in registers across the loop.
+__device__ __forceinline__ int afresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // Over the two halves of a wave, in every lane.
 __device__ __forceinline__ float halves_max(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);

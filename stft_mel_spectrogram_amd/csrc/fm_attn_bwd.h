@@ -12,11 +12,16 @@ namespace fm {
 
 constexpr int kAttnThreads = 256;
 constexpr int kAttnBlockKeys = 128;  // keys of a dk, dv workgroup
-// Rows of an LDS tile: two 32-row steps for 16-bit types in the dk, dv kernel,
-// one for float32 and in the dq kernel (at 64 columns three waves per SIMD
-// then fit, by registers and by LDS: 157 us against 166 with 64 rows).
 template <class T>
-constexpr int attn_step() { return sizeof(T) == 2 ? 64 : 32; }
+constexpr bool kIsF16 = false;
+template <>
+inline constexpr bool kIsF16<f16_t> = true;
+// Rows of an LDS tile: two 32-row steps for bfloat16 in the dk, dv kernel (211
+// us with one, 197 with two), one where the registers do not hold two (float16
+// needs some for its scales) and in the dq kernel (at 64 columns three waves per
+// SIMD then fit, by registers and by LDS: 157 us against 166 with 64 rows).
+template <class T>
+constexpr int attn_step() { return sizeof(T) == 2 && !kIsF16<T> ? 64 : 32; }
 constexpr int kDqStep = 32;
 
 // float16 has no room for small gradients: ds is scaled by the power of two
@@ -33,11 +38,6 @@ template <class T>
 constexpr float kProbShift = 0.f;
 template <>
 inline constexpr float kProbShift<f16_t> = 8.f;
-template <class T>
-constexpr bool kIsF16 = false;
-template <>
-inline constexpr bool kIsF16<f16_t> = true;
-
 // Sums of ds by distance inside the window.  A 32x32 tile's 63 diagonals come
 // from a wave's scratch in LDS: 16 queries at a time are stored as rows of 32
 // keys with zeros between them, and lane t adds up diagonal t (key - query = t -
@@ -55,7 +55,7 @@ constexpr int kDqWaves = sizeof(T) == 2 && DP == 64 && VEC && !kIsF16<T> ? 3 : a
 template <class T, int DP>
 constexpr size_t attn_dq_lds(int far, bool table) {
   return 4 * kDqStep * Tile<T, DP>::ld * sizeof(T) +
-         (table ? 4 * kDiagScratch * sizeof(float) : 0) +
+         (table ? (4 * kDiagScratch + 2 * kAttnThreads) * sizeof(float) : 0) +
          bias_window(far) * sizeof(float) * (table ? 5 : 1) + 8 * sizeof(float);
 }
 
@@ -92,8 +92,9 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
   float* diag = (float*)(vt + 2 * BK * LD);  // [4][kDiagScratch]
   float* bias = diag + (TABLE ? 4 * kDiagScratch : 0);
   const int win = bias_window(a.far);
-  float* ends = bias + win;  // [4][2]
-  float* sums = ends + 8;    // [4][win]
+  float* ends = bias + win;      // [4][2]
+  float* before = ends + 8;      // [2][256]
+  float* sums = before + 2 * kAttnThreads;  // [4][win]
 
   const int tid = threadIdx.x, wave = wave_index(), lane = tid & 63, n = lane & 31, h = lane >> 5;
   const int blocks = (a.q_len + kAttnQueries - 1) / kAttnQueries;
@@ -143,10 +144,7 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
   if (real) {
     const float v = a.lse[row];
     if (v != -INFINITY) lse2 = v * kLog2e;
-    if (h == 0) {
-      a.delta[row] = delta;
-      if (kIsF16<T>) a.amax[row] = amax;
-    }
+    if (kIsF16<T> && h == 0) a.amax[row] = amax;
   }
   const float unit = kIsF16<T> ? unit_scale(amax) : 1.f;
   fill_bias<T>(a, head, bias, tid, kAttnThreads);
@@ -160,21 +158,44 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
   vl.store(vt, tid);
   __syncthreads();
 
-  acc16 dq[DT];
-#pragma unroll
-  for (int d = 0; d < DT; ++d)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) dq[d][r] = 0.f;
-  // per query: ds and p over the tiles on either side of the window, ds inside
-  float before = 0.f, behind = 0.f, inside = 0.f, p_before = 0.f, p_behind = 0.f;
-  float* mysums = sums + wave * win;
-  float* mydiag = diag + wave * kDiagScratch;
   const float c = a.scale * kLog2e;
   const int mine = a.causal ? min(len, first + i + 1) : len;
   const int least = a.causal ? min(len, first + q0 + 1) : len;
   const int wave_end = a.causal ? min(k_end, first + q0 + 32) : k_end;
   const bool idle = q0 >= a.q_len;
+  if (!idle && wave_end <= 32) {
+    // All keys of these queries lie in the first tile: delta from p and dp
+    // themselves.  Their few probabilities are large, and so would be the error
+    // that the rounding of o leaves in delta.
+    const int dist = -first - q0;
+    const bool far = tile_before(dist, a.far) || tile_behind(dist, a.far);
+    acc16 s = far ? acc_zero() : bias_start_keys(bias, a.far, dist, h, n), dp = acc_zero();
+#pragma unroll
+    for (int x = 0; x < KS; ++x) {
+      s = mma32(tile_rows<T, DP>(kt, n, x, h), qf[x], s);
+      dp = mma32(tile_rows<T, DP>(vt, n, x, h), gf[x], dp);
+    }
+    const float t = (far ? (dist < 0 ? lo : hi) : 0.f) - lse2;
+    float sum = 0.f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      if (8 * (r / 4) + 4 * h + r % 4 < mine)
+        sum = fmaf(__builtin_amdgcn_exp2f(fmaf(s[r], c, t)), dp[r], sum);
+    delta = halves_sum(sum);
+  }
 
+  acc16 dq[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) dq[d][r] = 0.f;
+  // per query: ds and p over the tiles on one side of the window (keys come in
+  // order: those before it are put away when the first other tile comes), and
+  // ds over all tiles
+  float far_ds = 0.f, far_p = 0.f, all = 0.f;
+  bool put_away = false;
+  float* mysums = sums + wave * win;
+  float* mydiag = diag + wave * kDiagScratch;
   int buf = 0;
   for (int j0 = 0; j0 < k_end; j0 += BK, buf ^= 1) {
     const bool more = j0 + BK < k_end;
@@ -210,23 +231,29 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
             s[r] = j0 + 32 * u + 8 * (r / 4) + 4 * h + r % 4 < mine ? s[r] : -INFINITY;
         }
         const float t = far_bias - lse2;
+        if (TABLE && !is_before && !put_away) {
+          before[tid] = far_ds;
+          before[kAttnThreads + tid] = far_p;
+          far_ds = far_p = 0.f;
+          put_away = true;
+        }
         if (TABLE && (is_before || is_behind)) {
-          float p_sum = 0.f, ds_sum = 0.f;
+          float ds_sum = 0.f;
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             const float p = __builtin_amdgcn_exp2f(fmaf(s[r], c, t));
-            p_sum += p;
+            far_p += p;
             s[r] = p * (dp[r] - delta);
             ds_sum += s[r];
           }
-          (is_before ? before : behind) += ds_sum;
-          (is_before ? p_before : p_behind) += p_sum;
+          far_ds += ds_sum;
+          all += ds_sum;
         } else {
 #pragma unroll
           for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, t)) * (dp[r] - delta);
           if constexpr (TABLE) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) inside += s[r];
+            for (int r = 0; r < 16; ++r) all += s[r];
             mysums[dist - 31 + a.far + kBiasPad + lane] += tile_diagonals(mydiag, s, h, n, lane);
           }
         }
@@ -250,14 +277,16 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
     __syncthreads();
   }
 
-  if (real) {
+  const int ie = afresh(q0 + n), he = afresh(lane >> 5);
+  if (ie < a.q_len) {
+    if (he == 0) a.delta[(int64_t)(b * a.heads + head) * a.q_len + ie] = delta;
     const float f = a.scale / unit;
-    T* out = (T*)a.dq + b * a.dqs[0] + head * a.dqs[1] + i * a.dqs[2];
+    T* out = (T*)a.dq + b * a.dqs[0] + head * a.dqs[1] + ie * a.dqs[2];
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        const int at_d = 32 * d + 8 * y + 4 * h;
+        const int at_d = 32 * d + 8 * y + 4 * he;
         if (at_d < a.dim)
           store4(out + at_d, dq[d][4 * y] * f, dq[d][4 * y + 1] * f, dq[d][4 * y + 2] * f,
                  dq[d][4 * y + 3] * f, a.dim - at_d);
@@ -269,13 +298,19 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
     // much times a pair's p is in each ds.  The far sides hold most of a long
     // row's probability in one bucket each, where these errors would add up;
     // there they are taken out.
-    const float off = before + behind + inside;
-    const float all = halves_sum(off);
-    before = lanes_sum<64>(fmaf(-all, p_before, before));
-    behind = lanes_sum<64>(fmaf(-all, p_behind, behind));
+    const float off = halves_sum(all);
+    float left = far_ds, left_p = far_p, right = 0.f, right_p = 0.f;
+    if (put_away) {
+      right = far_ds;
+      right_p = far_p;
+      left = before[tid];
+      left_p = before[kAttnThreads + tid];
+    }
+    left = lanes_sum<64>(fmaf(-off, left_p, left));
+    right = lanes_sum<64>(fmaf(-off, right_p, right));
     if (lane == 0) {
-      ends[2 * wave] = before;
-      ends[2 * wave + 1] = behind;
+      ends[2 * wave] = left;
+      ends[2 * wave + 1] = right;
     }
     __syncthreads();
     // the window's first and last distances lie beyond +-far like the far tiles

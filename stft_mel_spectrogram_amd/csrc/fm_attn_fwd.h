@@ -92,19 +92,37 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
       const T* vtb = vt + buf * BK * LD;
       acc16 s[NS];
       float far_bias[NS];  // of a tile that lies outside the window, in base 2
+      // the two tiles' products in turn: one that continues the last one's
+      // accumulator waits for all of its passes
+      Frag<T> k0[NS];
+      bool near = false;
 #pragma unroll
       for (int u = 0; u < NS; ++u) {
         const int dist = j0 + 32 * u - first - q0;
-        const Frag<T> k0 = tile_rows<T, DP>(ktb, 32 * u + n, 0, h);
-        if (tile_before(dist, a.far) || tile_behind(dist, a.far)) {
-          s[u] = mma32(k0, qf[0], acc_zero());
-          far_bias[u] = dist < 0 ? lo : hi;
-        } else {
-          s[u] = mma32(k0, qf[0], bias_start_keys(bias, a.far, dist, h, n));
-          far_bias[u] = 0.f;
-        }
+        k0[u] = tile_rows<T, DP>(ktb, 32 * u + n, 0, h);
+        const bool far = tile_before(dist, a.far) || tile_behind(dist, a.far);
+        far_bias[u] = far ? (dist < 0 ? lo : hi) : 0.f;
+        near |= !far;
+      }
+      if (near) {
 #pragma unroll
-        for (int x = 1; x < KS; ++x) s[u] = mma32(tile_rows<T, DP>(ktb, 32 * u + n, x, h), qf[x], s[u]);
+        for (int u = 0; u < NS; ++u) {
+          const int dist = j0 + 32 * u - first - q0;
+          if (tile_before(dist, a.far) || tile_behind(dist, a.far))
+            s[u] = mma32(k0[u], qf[0], acc_zero());
+          else
+            s[u] = mma32(k0[u], qf[0], bias_start_keys(bias, a.far, dist, h, n));
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < NS; ++u) s[u] = mma32(k0[u], qf[0], acc_zero());
+      }
+#pragma unroll
+      for (int x = 1; x < KS; ++x)
+#pragma unroll
+        for (int u = 0; u < NS; ++u) s[u] = mma32(tile_rows<T, DP>(ktb, 32 * u + n, x, h), qf[x], s[u]);
+#pragma unroll
+      for (int u = 0; u < NS; ++u) {
         if (j0 + 32 * u + 32 > least) {
 #pragma unroll
           for (int r = 0; r < 16; ++r)

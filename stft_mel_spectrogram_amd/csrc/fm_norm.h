@@ -117,12 +117,13 @@ __global__ __launch_bounds__(kNormThreads) void norm_forward_kernel(
 }
 
 // PARTS: also add up dw and db (part: one row of [dw | db], 2 * width floats,
-// per workgroup).
+// per workgroup; a single workgroup writes dw and db themselves).
 template <class T, class W, int LPR, int VPL, bool PARTS>
 __global__ __launch_bounds__(kNormThreads) void norm_backward_kernel(
     const T* __restrict__ dy, int64_t dy_stride, const T* __restrict__ x, int64_t x_stride,
     const W* __restrict__ w, const float* __restrict__ mean, const float* __restrict__ rstd,
-    T* __restrict__ dx, float* __restrict__ part, int64_t rows, int width) {
+    T* __restrict__ dx, float* __restrict__ part, W* __restrict__ dw, W* __restrict__ db,
+    int64_t rows, int width) {
   constexpr int VE = Vec16<T>::n;
   constexpr int NT = kNormThreads;
   constexpr int RPB = NT / LPR;
@@ -190,6 +191,15 @@ __global__ __launch_bounds__(kNormThreads) void norm_backward_kernel(
     }
   }
   if constexpr (PARTS) {
+    const auto put = [&](int k, int c, float s) {
+      if (c >= width) return;
+      if (gridDim.x > 1)
+        part[((int64_t)blockIdx.x * 2 + k) * width + c] = s;
+      else if (k == 0)
+        dw[c] = (W)s;
+      else if (db)
+        db[c] = (W)s;
+    };
     // lanes of the same columns: RPB groups of LPR lanes
     if constexpr (RPB > 1) {
       __shared__ float col[RPB > 1 ? NT * VE : 1];
@@ -206,8 +216,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_backward_kernel(
             float s = 0.f;
 #pragma unroll
             for (int r = 0; r < RPB; ++r) s += col[r * LPR * VE + t];
-            const int c = i * LPR * VE + t;
-            if (c < width) part[((int64_t)blockIdx.x * 2 + k) * width + c] = s;
+            put(k, i * LPR * VE + t, s);
           }
         }
     } else {
@@ -216,10 +225,8 @@ __global__ __launch_bounds__(kNormThreads) void norm_backward_kernel(
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
           const int c = (i * LPR + lane) * VE + e;
-          if (c < width) {
-            part[((int64_t)blockIdx.x * 2 + 0) * width + c] = aw[i * VE + e];
-            part[((int64_t)blockIdx.x * 2 + 1) * width + c] = ab[i * VE + e];
-          }
+          put(0, c, aw[i * VE + e]);
+          put(1, c, ab[i * VE + e]);
         }
     }
   }
@@ -419,7 +426,7 @@ int norm_backward_t(const NormBackward& a) {
                        : norm_backward_kernel<T, W, L, V, false>,                              \
                   dim3((unsigned)parts), dim3(kNormThreads), 0, a.stream, (const T*)a.dy,      \
                   a.dy_stride, (const T*)a.x, a.x_stride, (const W*)a.weight, a.mean, a.rstd,  \
-                  (T*)a.dx, part, a.rows, a.width);
+                  (T*)a.dx, part, (W*)a.dw, (W*)a.db, a.rows, a.width);
     FM_NORM_SHAPES(FM_NORM_BWD)
 #undef FM_NORM_BWD
     if (st != FM_OK) return st;
@@ -431,7 +438,7 @@ int norm_backward_t(const NormBackward& a) {
       if (st != FM_OK) return st;
     }
   }
-  if (!want) return FM_OK;
+  if (!want || norm_single(a.rows, a.width, VE)) return FM_OK;
   const int64_t cols = 2 * (int64_t)a.width;
   return launch("layer norm backward sums", norm_reduce_kernel<W>, dim3((unsigned)((cols + 63) / 64)),
                 dim3(1024), 0, a.stream, part, a.rows > 0 ? parts : 0, (W*)a.dw, (W*)a.db, a.width);

@@ -141,6 +141,14 @@ template <int LANES>
 __device__ __forceinline__ float lanes_sum(float v) {
   return lanes_reduce<LANES>(v, [](float a, float b) { return a + b; });
 }
+// The largest of the wave's unsigned integers.
+__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+  const float r = lanes_reduce<64>(__uint_as_float(v), [](float a, float b) {
+    const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+    return __uint_as_float(x > y ? x : y);
+  });
+  return __float_as_uint(r);
+}
 template <int LANES>
 __device__ __forceinline__ float lanes_max(float v) {
   return lanes_reduce<LANES>(v, [](float a, float b) { return fmaxf(a, b); });

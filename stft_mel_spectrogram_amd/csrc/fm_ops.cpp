@@ -170,6 +170,7 @@ int fm_layer_norm_forward(const void* x, int64_t x_stride, const void* weight, c
 
 int64_t fm_layer_norm_backward_workspace(int64_t rows, int64_t width, int dtype) try {
   if (int st = fm::check_norm(rows, width, dtype)) return st;
+  if (fm::norm_single(rows, static_cast<int>(width), fm::vec_elems(dtype))) return 0;
   return int64_t(2) * fm::norm_parts(rows, static_cast<int>(width), fm::vec_elems(dtype)) * width *
          static_cast<int64_t>(sizeof(float));
 } catch (...) {
@@ -187,7 +188,8 @@ int fm_layer_norm_backward(const void* dy, int64_t dy_stride, const void* x, int
   if (rows > 0) {
     if (!dy || !x || !dx || !mean || !rstd)
       return bad("layer norm: dy, x, mean, rstd and dx must not be NULL");
-    if (dw && (!workspace || !fm::aligned(workspace, 16)))
+    if (dw && !fm::norm_single(rows, static_cast<int>(width), fm::vec_elems(dtype)) &&
+        (!workspace || !fm::aligned(workspace, 16)))
       return bad("layer norm: the workspace must be 16-byte aligned device memory");
     if (rows > 1 && (x_stride < 0 || dy_stride < 0)) return bad("layer norm: strides must be >= 0");
     const int es = fm::elem_size(dtype);

@@ -66,11 +66,19 @@ inline NormShape norm_shape(int width, int ve) {
 }
 #define FM_NORM_SHAPES(X) X(16, 1) X(16, 2) X(64, 1) X(64, 2) X(256, 1) X(256, 2) X(256, 4) X(256, 8)
 
+// Whether one workgroup of the backward takes all rows: four passes over its
+// rows cost less than the second launch (64 x 122: 29 us of host time against
+// ...).
+inline bool norm_single(int64_t rows, int width, int ve) {
+  const NormShape s = norm_shape(width, ve);
+  return s.vpl > 0 && rows > 0 && rows <= 4 * (kNormThreads / s.lpr);
+}
 // Partial rows (workgroups of the backward): enough to fill the chip several
 // times over, few enough that their sum stays small.
 inline int norm_parts(int64_t rows, int width, int ve) {
   const NormShape s = norm_shape(width, ve);
-  const int rpb = s.lpr > kNormThreads ? 1 : kNormThreads / s.lpr;
+  if (norm_single(rows, width, ve)) return 1;
+  const int rpb = s.vpl > 0 ? kNormThreads / s.lpr : 1;
   const int64_t need = (rows + rpb - 1) / rpb;
   const int64_t most = s.vpl > 0 ? 1024 : 64;
   return (int)(need < most ? need : most);

@@ -15,7 +15,8 @@
 // Top alternatives: a wave keeps its best `top` entries as 64-bit keys
 // (value in an ordered integer, then the complement of the index, so that
 // ties go to the lower index), one per lane in descending order; a chunk's
-// entries are taken in descending order while they beat the last one kept.
+// entries are taken in descending order while they beat the last one kept (the
+// wave's best by rotations of lanes, the next one looked for by its lane alone).
 //
 // Memory bound.  A row that 16 or 64 lanes hold in registers is read once, its
 // maximum taken first.  Longer rows go through 4 waves chunk by chunk (8 waves
@@ -42,13 +43,12 @@ __device__ __forceinline__ float key_value(key_t k) {
 }
 __device__ __forceinline__ int key_index(key_t k) { return (int)~(uint32_t)k; }
 
+// The largest key of the wave: the largest value, then among its holders the
+// largest rest (the lowest index).
 __device__ __forceinline__ key_t wave_max_key(key_t k) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) {
-    const key_t o = __shfl_xor(k, m, 64);
-    k = o > k ? o : k;
-  }
-  return k;
+  const uint32_t hi = wave_umax((uint32_t)(k >> 32));
+  const uint32_t lo = wave_umax((uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+  return (key_t)hi << 32 | lo;
 }
 
 // Inserts `k` (the same in every lane) into the wave's descending list.
@@ -140,29 +140,47 @@ __device__ __forceinline__ float score_max(const Vec16<T> (&v)[V]) {
   return m;
 }
 
-// The best entries of a chunk (group i of this lane starts at c0 + (i * nt +
-// tid) * VE) into the wave's list, in descending order: `last` is what has
-// been taken so far.
+// This lane's best entry of a chunk below `last` (group i starts at c0 + (i * nt
+// + tid) * VE).
 template <class T, int V>
-__device__ __forceinline__ void score_best(const Vec16<T> (&v)[V], int c0, int nt, int tid, int end,
-                                           int top, key_t& list, int lane) {
+__device__ __forceinline__ key_t score_best(const Vec16<T> (&v)[V], int c0, int nt, int tid, int end,
+                                            key_t last) {
   constexpr int VE = Vec16<T>::n;
-  key_t last = ~(key_t)0;
-  while (true) {
-    key_t best = 0;
+  key_t best = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+  for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        const int c = c0 + (i * nt + tid) * VE + e;
-        const key_t k = c < end ? score_key((float)v[i].v[e], c) : 0;
-        if (k < last && k > best) best = k;
-      }
-    best = wave_max_key(best);
-    const key_t worst = __shfl(list, top - 1, 64);
-    if (best <= worst) break;
-    list_insert(list, best, lane);
-    last = best;
+    for (int e = 0; e < VE; ++e) {
+      const int c = c0 + (i * nt + tid) * VE + e;
+      const key_t k = c < end ? score_key((float)v[i].v[e], c) : 0;
+      if (k < last && k > best) best = k;
+    }
+  return best;
+}
+// The wave's best entries of a chunk, taken in descending order: into an empty
+// list one lane after the other, into a list while they beat its last.
+template <class T, int V>
+__device__ __forceinline__ void score_top(const Vec16<T> (&v)[V], int c0, int nt, int tid, int end,
+                                          int top, bool empty, key_t& list, int lane) {
+  key_t mine = score_best(v, c0, nt, tid, end, ~(key_t)0);
+  const auto next = [&](key_t best) {
+    // only the lane that held it looks for its next one
+    if (mine == best) mine = score_best(v, c0, nt, tid, end, best);
+  };
+  if (empty) {
+    for (int i = 0; i < top; ++i) {
+      const key_t best = wave_max_key(mine);
+      if (best == 0) break;
+      if (lane == i) list = best;
+      next(best);
+    }
+  } else {
+    while (true) {
+      const key_t best = wave_max_key(mine);
+      if (best <= __shfl(list, top - 1, 64)) break;
+      list_insert(list, best, lane);
+      next(best);
+    }
   }
 }
 
@@ -190,7 +208,7 @@ __global__ __launch_bounds__(256) void score_row_kernel(const T* __restrict__ x,
   r.s = lanes_sum<L>(s);
   r.t = lanes_sum<L>(t);
   key_t list = 0;
-  if constexpr (TOP) score_best(v, 0, L, lane, end, top, list, lane);
+  if constexpr (TOP) score_top(v, 0, L, lane, end, top, true, list, lane);
   if (row < rows) score_finish(r, xr, row, vocab, tokens, tok64, list, TOP ? top : 0, out, lane);
 }
 
@@ -228,7 +246,7 @@ __global__ __launch_bounds__(256) void score_forward_kernel(
     acc.t = (acc.t + acc.s * d0) * r0 + t;
     acc.s = acc.s * r0 + s;
     acc.m = m;
-    if constexpr (TOP) score_best(v, c0, NT, tid, end, top, list, lane);
+    if constexpr (TOP) score_top(v, c0, NT, tid, end, top, c0 == beg, list, lane);
   }
   acc = score_join_lanes<64>(acc);
   __shared__ ScoreSum sums[4];

@@ -34,14 +34,15 @@ def test_layer_norm_limits():
     assert norm(width=(1 << 20) + 1) == N.FM_E_UNSUPPORTED
     assert norm(rows=0, x=None, y=None) == N.FM_OK  # nothing to do, nothing launched
     assert N.lib.fm_layer_norm_backward_workspace(4, 0, N.FM_F32) == N.FM_E_INVAL
-    for rows, width in ((1, 1), (5, 1000), (100000, 1024), (100000, 30000)):
+    assert N.lib.fm_layer_norm_backward_workspace(16, 1024, N.FM_BF16) == 0  # one workgroup
+    for rows, width in ((500, 1), (50, 1000), (100000, 1024), (100000, 30000)):
         parts = N.lib.fm_layer_norm_backward_workspace(rows, width, N.FM_BF16) / (8 * width)
         assert parts == int(parts) and 1 <= parts <= 1024
 
 
 @pytest.mark.parametrize("kw", [
     dict(rows=-1), dict(width=0), dict(dtype=N.FM_I16), dict(dtype=N.FM_F16, pdtype=N.FM_BF16), dict(dy=None),
-    dict(x=None), dict(mean=None), dict(rstd=None), dict(dx=None), dict(ws=None), dict(ws=P + 4), dict(dw=None),
+    dict(x=None), dict(mean=None), dict(rstd=None), dict(dx=None), dict(ws=None, rows=5000), dict(ws=P + 4, rows=5000), dict(dw=None),
     dict(w=None), dict(stride=-1), dict(dx=P + 2)])
 def test_layer_norm_backward_refuses(kw):
     assert norm_back(**kw) == N.FM_E_INVAL
