@@ -7,10 +7,15 @@
 //   delta_i = do_i.o_i,  dq_i = scale sum ds_ij k_j,  dk_j = scale sum ds_ij q_i,
 //   dtable[b][head] = sum of ds_ij over the pairs of bucket b
 //
-// Matrix products run on 32x32x16 MFMAs (float32: eight 32x32x2 ones, which
-// take the same fragments).  Lane l = 32 h + n of a fragment holds row (or
-// column) n and the 8 contraction indices of half h.  A result's lane holds
-// column n and rows 8 (r / 4) + 4 h + r % 4 for its 16 registers r.
+// Matrix products run on 32x32x16 MFMAs.  Lane l = 32 h + n of a fragment holds
+// row (or column) n and the 8 contraction indices of half h.  A result's lane
+// holds column n and rows 8 (r / 4) + 4 h + r % 4 for its 16 registers r.
+//
+// float32 values are taken apart into three bfloat16 ones, x = a + b + c exactly
+// (8 significant bits each, rounded to nearest, so that the rests have either
+// sign), and a product is the six terms a a', a b', b a', a c', c a', b b' with
+// float32 sums; what is left out, b c' + c b' + c c', is at most 2^-25 of x x'.
+// Six bfloat16 products of 8 passes take the place of eight float32 ones of 16.
 //
 // Probabilities never pass through LDS: their product with the next operand
 // contracts over the result's rows, in whatever order, as long as the other
@@ -29,41 +34,112 @@ typedef float acc4 __attribute__((ext_vector_type(4)));
 typedef short short4v __attribute__((ext_vector_type(4)));
 
 template <class T>
-struct FragOf {
+struct RawOf {
   typedef T type __attribute__((ext_vector_type(8)));
 };
 template <class T>
+using Raw = typename RawOf<T>::type;  // eight values as they are in memory
+struct Frag3 {
+  Raw<bf16_t> a, b, c;
+};
+template <class T>
+struct FragOf {
+  typedef Raw<T> type;
+  typedef T lds;  // element of an LDS tile
+  static constexpr int planes = 1;
+};
+template <>
+struct FragOf<float> {
+  typedef Frag3 type;
+  typedef bf16_t lds;
+  static constexpr int planes = 3;
+};
+template <class T>
 using Frag = typename FragOf<T>::type;
+template <class T>
+using Lds = typename FragOf<T>::lds;
 
-__device__ __forceinline__ acc16 mma32(Frag<bf16_t> a, Frag<bf16_t> b, acc16 c) {
+// N float32 values as three times N bfloat16 ones.  An infinity stays one.
+template <int N, bool INF>
+__device__ __forceinline__ void take_apart(const float (&x)[N], bf16_t (&a)[N], bf16_t (&b)[N],
+                                           bf16_t (&c)[N]) {
+  typedef float fN __attribute__((ext_vector_type(N)));
+  typedef bf16_t bN __attribute__((ext_vector_type(N)));
+  fN v, r;
+#pragma unroll
+  for (int e = 0; e < N; ++e) v[e] = x[e];
+  const bN va = __builtin_convertvector(v, bN);
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const float w = (float)va[e];
+    r[e] = INF && __builtin_isinf(w) ? 0.f : v[e] - w;
+  }
+  const bN vb = __builtin_convertvector(r, bN);
+#pragma unroll
+  for (int e = 0; e < N; ++e) r[e] -= (float)vb[e];
+  const bN vc = __builtin_convertvector(r, bN);
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    a[e] = va[e];
+    b[e] = vb[e];
+    c[e] = vc[e];
+  }
+}
+template <bool INF>
+__device__ __forceinline__ Frag3 take_apart(const Raw<float>& x) {
+  float v[8];
+  bf16_t a[8], b[8], c[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = x[e];
+  take_apart<8, INF>(v, a, b, c);
+  Frag3 f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    f.a[e] = a[e];
+    f.b[e] = b[e];
+    f.c[e] = c[e];
+  }
+  return f;
+}
+__device__ __forceinline__ Raw<bf16_t> to_frag(Raw<bf16_t> x) { return x; }
+__device__ __forceinline__ Raw<f16_t> to_frag(Raw<f16_t> x) { return x; }
+__device__ __forceinline__ Frag3 to_frag(Raw<float> x) { return take_apart<true>(x); }
+
+__device__ __forceinline__ acc16 mma32(Raw<bf16_t> a, Raw<bf16_t> b, acc16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
-__device__ __forceinline__ acc16 mma32(Frag<f16_t> a, Frag<f16_t> b, acc16 c) {
+__device__ __forceinline__ acc16 mma32(Raw<f16_t> a, Raw<f16_t> b, acc16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
-__device__ __forceinline__ acc16 mma32(Frag<float> a, Frag<float> b, acc16 c) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
-  return c;
+__device__ __forceinline__ acc16 mma32(const Frag3& x, const Frag3& y, acc16 c) {
+  c = mma32(x.b, y.b, c);
+  c = mma32(x.c, y.a, c);
+  c = mma32(x.a, y.c, c);
+  c = mma32(x.b, y.a, c);
+  c = mma32(x.a, y.b, c);
+  return mma32(x.a, y.a, c);
 }
-// 16x16x32 (float32: eight 16x16x4): lane 16 g + n holds row n and the 8
-// contraction indices of quarter g; a result's lane column n, rows 4 g + r.
-__device__ __forceinline__ acc4 mma16(Frag<bf16_t> a, Frag<bf16_t> b, acc4 c) {
+// 16x16x32: lane 16 g + n holds row n and the 8 contraction indices of quarter
+// g; a result's lane column n, rows 4 g + r.
+__device__ __forceinline__ acc4 mma16(Raw<bf16_t> a, Raw<bf16_t> b, acc4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
-__device__ __forceinline__ acc4 mma16(Frag<f16_t> a, Frag<f16_t> b, acc4 c) {
+__device__ __forceinline__ acc4 mma16(Raw<f16_t> a, Raw<f16_t> b, acc4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
-__device__ __forceinline__ acc4 mma16(Frag<float> a, Frag<float> b, acc4 c) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
-  return c;
+__device__ __forceinline__ acc4 mma16(const Frag3& x, const Frag3& y, acc4 c) {
+  c = mma16(x.b, y.b, c);
+  c = mma16(x.c, y.a, c);
+  c = mma16(x.a, y.c, c);
+  c = mma16(x.b, y.a, c);
+  c = mma16(x.a, y.b, c);
+  return mma16(x.a, y.a, c);
 }
 
 // Eight contiguous elements of a row in memory, of which `have` exist.
 template <class T>
-__device__ __forceinline__ Frag<T> load_frag(const T* p, int have) {
-  Frag<T> f;
+__device__ __forceinline__ Raw<T> load_raw(const T* p, int have) {
+  Raw<T> f;
   if (have >= 8) {
     __builtin_memcpy(&f, p, sizeof(f));
   } else {
@@ -74,57 +150,89 @@ __device__ __forceinline__ Frag<T> load_frag(const T* p, int have) {
 }
 
 // Row-major LDS tile: 16 bytes of padding per row spread the rows over the
-// banks.
+// banks.  float32: three planes of 32 rows.
 template <class T, int DP>
 struct Tile {
-  static constexpr int ld = DP + 16 / (int)sizeof(T);
-  static constexpr int chunks = DP * (int)sizeof(T) / 16;  // 16-byte groups per row
+  static constexpr int ld = DP + 8;
+  static constexpr int plane = 32 * ld;
+  static constexpr int chunks = DP * (int)sizeof(T) / 16;  // 16-byte groups of a row in memory
+  static constexpr int size(int rows) { return FragOf<T>::planes * rows * ld; }
 };
 
 // Fragment of row n (a lane's own), contraction indices 16 s + 8 h ..: one
-// 16-byte read (two for float32).
+// 16-byte read.
 template <class T, int DP>
-__device__ __forceinline__ Frag<T> tile_rows(const T* tile, int row, int s, int h) {
-  return *(const Frag<T>*)(tile + row * Tile<T, DP>::ld + 16 * s + 8 * h);
+__device__ __forceinline__ Frag<T> tile_rows(const Lds<T>* tile, int row, int s, int h) {
+  const Lds<T>* p = tile + row * Tile<T, DP>::ld + 16 * s + 8 * h;
+  if constexpr (sizeof(T) == 4)
+    return {*(const Raw<bf16_t>*)p, *(const Raw<bf16_t>*)(p + Tile<T, DP>::plane),
+            *(const Raw<bf16_t>*)(p + 2 * Tile<T, DP>::plane)};
+  else
+    return *(const Frag<T>*)p;
 }
 
-// Fragment of column d0 + l % 32, contraction over rows r0 + 4 h + 0..3 and
-// r0 + 8 + 4 h + 0..3.
+// Four rows of a column each, twice: `p` and `step` elements further.
 __device__ __forceinline__ short4v lds_read_tr(const void* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) short4v*)p);
 }
+template <class E>
+__device__ __forceinline__ Raw<E> lds_columns(const E* p, int step) {
+  typedef short short8v __attribute__((ext_vector_type(8)));
+  const short4v lo = lds_read_tr(p), hi = lds_read_tr(p + step);
+  const short8v both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  return __builtin_bit_cast(Raw<E>, both);
+}
+template <class T>
+__device__ __forceinline__ Frag<T> lds_columns_of(const Lds<T>* p, int step, int plane) {
+  if constexpr (sizeof(T) == 4)
+    return {lds_columns(p, step), lds_columns(p + plane, step), lds_columns(p + 2 * plane, step)};
+  else
+    return lds_columns(p, step);
+}
+// Fragment of column d0 + l % 32, contraction over rows r0 + 4 h + 0..3 and
+// r0 + 8 + 4 h + 0..3: a group of 16 lanes reads 4 rows of 16 columns, 8 bytes
+// each, and gets them transposed, lane i the 4 rows of column i.
 template <class T, int DP>
-__device__ __forceinline__ Frag<T> tile_cols(const T* tile, int r0, int d0, int lane) {
+__device__ __forceinline__ Frag<T> tile_cols(const Lds<T>* tile, int r0, int d0, int lane) {
   constexpr int ld = Tile<T, DP>::ld;
-  Frag<T> f;
-  if constexpr (sizeof(T) == 2) {
-    // a group of 16 lanes reads 4 rows of 16 columns, 8 bytes each, and gets
-    // them transposed: lane i the 4 rows of column i
-    const int g = lane >> 4, i = lane & 15;
-    const T* p = tile + (r0 + 4 * (g >> 1) + (i >> 2)) * ld + d0 + 16 * (g & 1) + 4 * (i & 3);
-    const short4v lo = lds_read_tr(p), hi = lds_read_tr(p + 8 * ld);
-    typedef short short8v __attribute__((ext_vector_type(8)));
-    const short8v both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    f = __builtin_bit_cast(Frag<T>, both);
-  } else {
-    const T* p = tile + (r0 + 4 * (lane >> 5)) * ld + d0 + (lane & 31);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      f[e] = p[e * ld];
-      f[4 + e] = p[(8 + e) * ld];
-    }
-  }
-  return f;
+  const int g = lane >> 4, i = lane & 15;
+  return lds_columns_of<T>(tile + (r0 + 4 * (g >> 1) + (i >> 2)) * ld + d0 + 16 * (g & 1) + 4 * (i & 3),
+                           8 * ld, Tile<T, DP>::plane);
 }
 
+// Eight float32 values as a fragment.
+template <class T>
+__device__ __forceinline__ Frag<T> round_frag(const Raw<float>& v) {
+  if constexpr (sizeof(T) == 4)
+    return take_apart<false>(v);
+  else
+    return __builtin_convertvector(v, Raw<T>);
+}
 // Registers 8 c .. 8 c + 7 of a result as the fragment of contraction step c.
 template <class T>
 __device__ __forceinline__ Frag<T> acc_frag(const acc16& a, int c) {
-  typedef float f8 __attribute__((ext_vector_type(8)));
-  f8 v;
+  Raw<float> v;
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = a[8 * c + e];
-  return __builtin_convertvector(v, Frag<T>);
+  return round_frag<T>(v);
+}
+
+// 16 bytes of a row in memory into its place in a tile.
+template <class T, int DP>
+__device__ __forceinline__ void tile_put(Lds<T>* tile, int row, int col, const Vec16<T>& v) {
+  Lds<T>* p = tile + row * Tile<T, DP>::ld + col;
+  if constexpr (sizeof(T) == 4) {
+    struct Four {
+      bf16_t v[4];
+    };
+    Four a, b, c;
+    take_apart<4, true>(v.v, a.v, b.v, c.v);
+    *(Four*)__builtin_assume_aligned(p, 8) = a;
+    *(Four*)__builtin_assume_aligned(p + Tile<T, DP>::plane, 8) = b;
+    *(Four*)__builtin_assume_aligned(p + 2 * Tile<T, DP>::plane, 8) = c;
+  } else {
+    *(Vec16<T>*)__builtin_assume_aligned(p, 16) = v;
+  }
 }
 
 // A tile of ROWS rows on its way from memory to LDS.  Rows from `valid` on and
@@ -162,11 +270,12 @@ struct TileLoad {
     for (int i = 0; i < n; ++i)
       v[i] = __builtin_amdgcn_raw_buffer_load_b128(r, at[even ? 0 : i], even ? i * step : 0, 0);
   }
-  __device__ __forceinline__ void store(T* tile, int tid) const {
+  __device__ __forceinline__ void store(Lds<T>* tile, int tid) const {
 #pragma unroll
     for (int i = 0; i < n; ++i) {
       const int c = i * NT + tid, row = c / ch, col = (c - row * ch) * ve;
-      if (ROWS * ch % NT == 0 || row < ROWS) *(u4*)(tile + row * Tile<T, DP>::ld + col) = v[i];
+      if (ROWS * ch % NT == 0 || row < ROWS)
+        tile_put<T, DP>(tile, row, col, __builtin_bit_cast(Vec16<T>, v[i]));
     }
   }
 };
@@ -186,12 +295,12 @@ struct TileLoad<T, DP, ROWS, NT, false> {
     valid = valid_;
     dim = dim_;
   }
-  __device__ __forceinline__ void store(T* tile, int tid) const {
+  __device__ __forceinline__ void store(Lds<T>* tile, int tid) const {
 #pragma unroll 1
     for (int c = tid; c < ROWS * ch; c += NT) {
       const int row = c / ch, col = (c - row * ch) * ve;
-      *(Vec16<T>*)__builtin_assume_aligned(tile + row * Tile<T, DP>::ld + col, 16) =
-          load16_part(base + row * stride + col, row < valid ? dim - col : 0, (T)0.f);
+      tile_put<T, DP>(tile, row, col,
+                      load16_part(base + row * stride + col, row < valid ? dim - col : 0, (T)0.f));
     }
   }
 };

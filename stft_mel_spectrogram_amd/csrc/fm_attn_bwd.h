@@ -52,9 +52,14 @@ constexpr int kDiagScratch = 32 + 16 * kDiagRow;
 template <class T, int DP, bool VEC>
 constexpr int kDqWaves = sizeof(T) == 2 && DP == 64 && VEC && !kIsF16<T> ? 3 : attn_waves<T, DP>();
 
+// Tiles of keys and of values in LDS: one computed on and one arriving, but a
+// single one where two would leave no room for the widest bias window.
+template <class T, int DP>
+constexpr int kDqTiles = sizeof(T) == 4 && DP == 128 ? 1 : 2;
+
 template <class T, int DP>
 constexpr size_t attn_dq_lds(int far, bool table) {
-  return 4 * kDqStep * Tile<T, DP>::ld * sizeof(T) +
+  return 2 * kDqTiles<T, DP> * Tile<T, DP>::size(kDqStep) * sizeof(Lds<T>) +
          (table ? (4 * kDiagScratch + 2 * kAttnThreads) * sizeof(float) : 0) +
          bias_window(far) * sizeof(float) * (table ? 5 : 1) + 8 * sizeof(float);
 }
@@ -85,11 +90,12 @@ __device__ __forceinline__ float tile_diagonals(float* scratch, const acc16& s, 
 
 template <class T, int DP, bool TABLE, bool VEC>
 __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_kernel(const AttnArgs a) {
-  constexpr int BK = kDqStep, NS = BK / 32, LD = Tile<T, DP>::ld, KS = DP / 16, DT = DP / 32;
+  constexpr int BK = kDqStep, NS = BK / 32, TS = Tile<T, DP>::size(BK), KS = DP / 16, DT = DP / 32;
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  T* kt = (T*)smem;
-  T* vt = kt + 2 * BK * LD;
-  float* diag = (float*)(vt + 2 * BK * LD);  // [4][kDiagScratch]
+  Lds<T>* kt = (Lds<T>*)smem;
+  constexpr int TILES = kDqTiles<T, DP>;
+  Lds<T>* vt = kt + TILES * TS;
+  float* diag = (float*)(vt + TILES * TS);  // [4][kDiagScratch]
   float* bias = diag + (TABLE ? 4 * kDiagScratch : 0);
   const int win = bias_window(a.far);
   float* ends = bias + win;      // [4][2]
@@ -127,13 +133,13 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       const int d = 16 * s + 8 * h, have = real ? a.dim - d : 0;
-      qf[s] = load_frag(qp + d, have);
-      gf[s] = load_frag(gp + d, have);
-      const Frag<T> of = load_frag((const T*)a.o + off + d, have);
+      qf[s] = to_frag(load_raw(qp + d, have));
+      const Raw<T> gr = load_raw(gp + d, have), of = load_raw((const T*)a.o + off + d, have);
+      gf[s] = to_frag(gr);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        delta = fmaf((float)gf[s][e], (float)of[e], delta);
-        amax = fmaxf(amax, fabsf((float)gf[s][e]));
+        delta = fmaf((float)gr[e], (float)of[e], delta);
+        amax = fmaxf(amax, fabsf((float)gr[e]));
       }
     }
     delta = halves_sum(delta);
@@ -197,15 +203,15 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
   float* mysums = sums + wave * win;
   float* mydiag = diag + wave * kDiagScratch;
   int buf = 0;
-  for (int j0 = 0; j0 < k_end; j0 += BK, buf ^= 1) {
+  for (int j0 = 0; j0 < k_end; j0 += BK, buf ^= TILES - 1) {
     const bool more = j0 + BK < k_end;
     if (more) {
       kl.load(kp + (int64_t)(j0 + BK) * a.ks[2], a.ks[2], k_end - j0 - BK, a.dim, tid);
       vl.load(vp + (int64_t)(j0 + BK) * a.vs[2], a.vs[2], k_end - j0 - BK, a.dim, tid);
     }
     if (!idle && j0 < wave_end) {
-      const T* ktb = kt + buf * BK * LD;
-      const T* vtb = vt + buf * BK * LD;
+      const Lds<T>* ktb = kt + buf * TS;
+      const Lds<T>* vtb = vt + buf * TS;
 #pragma unroll
       for (int u = 0; u < NS; ++u) {
         const int dist = j0 + 32 * u - first - q0;
@@ -270,9 +276,10 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
         }
       }
     }
+    if (TILES == 1) __syncthreads();
     if (more) {
-      kl.store(kt + (buf ^ 1) * BK * LD, tid);
-      vl.store(vt + (buf ^ 1) * BK * LD, tid);
+      kl.store(kt + (buf ^ (TILES - 1)) * TS, tid);
+      vl.store(vt + (buf ^ (TILES - 1)) * TS, tid);
     }
     __syncthreads();
   }
@@ -379,23 +386,28 @@ __global__ __launch_bounds__(1024) void attn_table_buckets_kernel(const AttnArgs
 
 template <class T, int DP>
 constexpr size_t attn_dkv_lds(int far) {
-  return 4 * attn_step<T>() * Tile<T, DP>::ld * sizeof(T) + 4 * attn_step<T>() * sizeof(float) +
+  return 4 * Tile<T, DP>::size(attn_step<T>()) * sizeof(Lds<T>) + 4 * attn_step<T>() * sizeof(float) +
          bias_window(far) * sizeof(float);
 }
 
 template <class T, int DP, bool VEC>
 __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 2 : 1)) void attn_dkv_kernel(const AttnArgs a) {
-  constexpr int BQ = attn_step<T>(), NS = BQ / 32, LD = Tile<T, DP>::ld, KS = DP / 16, DT = DP / 32;
+  constexpr int BQ = attn_step<T>(), NS = BQ / 32, TS = Tile<T, DP>::size(BQ), KS = DP / 16, DT = DP / 32;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   // float32 fragments of 128 columns leave no registers for the next tile, and
   // neither do loads of odd rows
   constexpr bool AHEAD = VEC && !(sizeof(T) == 4 && DP == 128);
-  T* qt = (T*)smem;
-  T* gt = qt + 2 * BQ * LD;
+  // float32's three-part fragments leave none for operands read ahead
+  constexpr bool STAGED = sizeof(T) == 2;
+  Lds<T>* qt = (Lds<T>*)smem;
+  Lds<T>* gt = qt + 2 * TS;
   // -lse in units of the product and -delta start the accumulators: exp2 of the
-  // scaled scores then is p, and dp comes out less delta
-  float* neg_lse = (float*)(gt + 2 * BQ * LD);  // [2][BQ]
-  float* neg_delta = neg_lse + 2 * BQ;          // [2][BQ]
+  // scaled scores then is p, and dp comes out less delta.  In float32 the sums
+  // would be rounded at lse's size instead of the scores': there it is -lse in
+  // base 2, added after.
+  constexpr bool LSE_LATE = sizeof(T) == 4;
+  float* neg_lse = (float*)(gt + 2 * TS);  // [2][BQ]
+  float* neg_delta = neg_lse + 2 * BQ;     // [2][BQ]
   float* bias = neg_delta + 2 * BQ;
 
   const int tid = threadIdx.x, wave = wave_index(), lane = tid & 63, n = lane & 31, h = lane >> 5;
@@ -413,8 +425,8 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       const int d = 16 * s + 8 * h, have = j < len ? a.dim - d : 0;
-      kf[s] = load_frag(kp + d, have);
-      vf[s] = load_frag(vp + d, have);
+      kf[s] = to_frag(load_raw(kp + d, have));
+      vf[s] = to_frag(load_raw(vp + d, have));
     }
   }
   acc16 dk[DT], dv[DT];
@@ -458,13 +470,13 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
       if (tid < BQ) {
         const bool in = i0 + tid < i_end;
         const float v = in ? a.lse[row0 + i0 + tid] : -INFINITY;
-        l_next = v == -INFINITY ? v : fmaf(v, -kLog2e, kProbShift<T>) * inv_c;
+        l_next = v == -INFINITY ? v : fmaf(v, -kLog2e, kProbShift<T>) * (LSE_LATE ? 1.f : inv_c);
         d_next = in ? -a.delta[row0 + i0 + tid] : 0.f;
       }
     };
     const auto put = [&](int buf) __attribute__((always_inline)) {
-      ql.store(qt + buf * BQ * LD, tid);
-      gl.store(gt + buf * BQ * LD, tid);
+      ql.store(qt + buf * TS, tid);
+      gl.store(gt + buf * TS, tid);
       if (tid < BQ) {
         neg_lse[buf * BQ + tid] = l_next;
         neg_delta[buf * BQ + tid] = d_next;
@@ -481,14 +493,14 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
       const bool more = i0 + BQ < i_end;
       if (AHEAD && more) fetch(i0 + BQ);
       if (jw < len && !(a.causal && i0 + BQ - 1 + first < jw)) {
-        const T* qtb = qt + buf * BQ * LD;
-        const T* gtb = gt + buf * BQ * LD;
+        const Lds<T>* qtb = qt + buf * TS;
+        const Lds<T>* gtb = gt + buf * TS;
         acc16 s[NS], ds[NS];
         float far_bias[NS];
 #pragma unroll
         for (int u = 0; u < NS; ++u) {
           const int dist = jw - first - i0 - 32 * u;
-          s[u] = acc_rows(neg_lse + buf * BQ + 32 * u, h);
+          s[u] = LSE_LATE ? acc_zero() : acc_rows(neg_lse + buf * BQ + 32 * u, h);
           if (tile_before(dist, a.far) || tile_behind(dist, a.far)) {
             far_bias[u] = dist < 0 ? lo : hi;
           } else {
@@ -498,29 +510,41 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
         }
         // Products in stages, each reading the next one's operands: queries and
         // gradients by rows, then by columns.
-        Frag<T> rows[2][KS];
-        const auto read_rows = [&](const T* tile, int u, Frag<T>(&f)[KS]) __attribute__((always_inline)) {
+        if constexpr (STAGED) {
+          Frag<T> rows[2][KS];
+          const auto read_rows = [&](const Lds<T>* tile, int u, Frag<T>(&f)[KS]) __attribute__((always_inline)) {
 #pragma unroll
-          for (int x = 0; x < KS; ++x) f[x] = tile_rows<T, DP>(tile, 32 * u + n, x, h);
-        };
-        read_rows(qtb, 0, rows[0]);
-        ds[0] = acc_rows(neg_delta + buf * BQ, h);
-        stage();
-#pragma unroll
-        for (int u = 0; u < NS; ++u) {
-          read_rows(gtb, u, rows[1]);
+            for (int x = 0; x < KS; ++x) f[x] = tile_rows<T, DP>(tile, 32 * u + n, x, h);
+          };
+          read_rows(qtb, 0, rows[0]);
+          ds[0] = acc_rows(neg_delta + buf * BQ, h);
           stage();
 #pragma unroll
-          for (int x = 0; x < KS; ++x) s[u] = mma32(rows[0][x], kf[x], s[u]);
-          stage();
-          if (u + 1 < NS) {
-            read_rows(qtb, u + 1, rows[0]);
-            ds[u + 1] = acc_rows(neg_delta + buf * BQ + 32 * (u + 1), h);
+          for (int u = 0; u < NS; ++u) {
+            read_rows(gtb, u, rows[1]);
+            stage();
+#pragma unroll
+            for (int x = 0; x < KS; ++x) s[u] = mma32(rows[0][x], kf[x], s[u]);
+            stage();
+            if (u + 1 < NS) {
+              read_rows(qtb, u + 1, rows[0]);
+              ds[u + 1] = acc_rows(neg_delta + buf * BQ + 32 * (u + 1), h);
+            }
+            stage();
+#pragma unroll
+            for (int x = 0; x < KS; ++x) ds[u] = mma32(rows[1][x], vf[x], ds[u]);
+            stage();
           }
-          stage();
+        } else {
 #pragma unroll
-          for (int x = 0; x < KS; ++x) ds[u] = mma32(rows[1][x], vf[x], ds[u]);
-          stage();
+          for (int u = 0; u < NS; ++u) {
+            ds[u] = acc_rows(neg_delta + buf * BQ + 32 * u, h);
+#pragma unroll
+            for (int x = 0; x < KS; ++x) {
+              s[u] = mma32(tile_rows<T, DP>(qtb, 32 * u + n, x, h), kf[x], s[u]);
+              ds[u] = mma32(tile_rows<T, DP>(gtb, 32 * u + n, x, h), vf[x], ds[u]);
+            }
+          }
         }
         if (jw + 32 > len || (a.causal && jw + 31 - first > i0)) {
 #pragma unroll
@@ -530,19 +554,14 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
               s[u][r] = i0 + 32 * u + 8 * (r / 4) + 4 * h + r % 4 >= need ? s[u][r] : -INFINITY;
         }
         // step t: rows 16 t .. 16 t + 15 of the tile
-        Frag<T> cols[2][2 * DT], p[2], f[2];
-        const auto read_cols = [&](int t, Frag<T>(&c)[2 * DT]) __attribute__((always_inline)) {
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            c[d] = tile_cols<T, DP>(gtb, 16 * t, 32 * d, lane);
-            c[DT + d] = tile_cols<T, DP>(qtb, 16 * t, 32 * d, lane);
-          }
-        };
+        Frag<T> p[2], f[2];
         const auto scores = [&](int t) __attribute__((always_inline)) {
           const int u = t >> 1, x = t & 1;
+          acc16 late;
+          if constexpr (LSE_LATE) late = acc_rows(neg_lse + buf * BQ + 32 * u, h);
 #pragma unroll
           for (int r = 8 * x; r < 8 * x + 8; ++r) {
-            s[u][r] = __builtin_amdgcn_exp2f(fmaf(s[u][r], c, far_bias[u]));
+            s[u][r] = __builtin_amdgcn_exp2f(fmaf(s[u][r], c, LSE_LATE ? far_bias[u] + late[r] : far_bias[u]));
             if constexpr (kIsF16<T>)
               ds[u][r] *= s[u][r] * back;
             else
@@ -551,22 +570,42 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
           p[t & 1] = acc_frag<T>(s[u], x);
           f[t & 1] = acc_frag<T>(ds[u], x);
         };
-        read_cols(0, cols[0]);
-        stage();
-        scores(0);
-        stage();
+        if constexpr (STAGED) {
+          Frag<T> cols[2][2 * DT];
+          const auto read_cols = [&](int t, Frag<T>(&c)[2 * DT]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int t = 0; t < 2 * NS; ++t) {
-          if (t + 1 < 2 * NS) read_cols(t + 1, cols[(t + 1) & 1]);
+            for (int d = 0; d < DT; ++d) {
+              c[d] = tile_cols<T, DP>(gtb, 16 * t, 32 * d, lane);
+              c[DT + d] = tile_cols<T, DP>(qtb, 16 * t, 32 * d, lane);
+            }
+          };
+          read_cols(0, cols[0]);
           stage();
-          if (t + 1 < 2 * NS) scores(t + 1);
+          scores(0);
+          stage();
 #pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            dv[d] = mma32(cols[t & 1][d], p[t & 1], dv[d]);
-            dk[d] = mma32(cols[t & 1][DT + d], f[t & 1], dk[d]);
+          for (int t = 0; t < 2 * NS; ++t) {
+            if (t + 1 < 2 * NS) read_cols(t + 1, cols[(t + 1) & 1]);
+            stage();
+            if (t + 1 < 2 * NS) scores(t + 1);
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+              dv[d] = mma32(cols[t & 1][d], p[t & 1], dv[d]);
+              dk[d] = mma32(cols[t & 1][DT + d], f[t & 1], dk[d]);
+            }
+            if constexpr (sizeof(T) == 2) alternate<2 * DT, 32 / (2 * DT)>();
+            stage();
           }
-          if constexpr (sizeof(T) == 2) alternate<2 * DT, 32 / (2 * DT)>();
-          stage();
+        } else {
+#pragma unroll
+          for (int t = 0; t < 2 * NS; ++t) {
+            scores(t);
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+              dv[d] = mma32(tile_cols<T, DP>(gtb, 16 * t, 32 * d, lane), p[t & 1], dv[d]);
+              dk[d] = mma32(tile_cols<T, DP>(qtb, 16 * t, 32 * d, lane), f[t & 1], dk[d]);
+            }
+          }
         }
       }
       if (!AHEAD && more) fetch(i0 + BQ);

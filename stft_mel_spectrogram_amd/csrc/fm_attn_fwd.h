@@ -15,7 +15,7 @@ constexpr int attn_keys() { return sizeof(T) == 2 ? 64 : 32; }
 
 template <class T, int DP>
 constexpr size_t attn_forward_lds(int far) {
-  return 4 * attn_keys<T>() * Tile<T, DP>::ld * sizeof(T) + bias_window(far) * sizeof(float);
+  return 4 * Tile<T, DP>::size(attn_keys<T>()) * sizeof(Lds<T>) + bias_window(far) * sizeof(float);
 }
 
 // The transposed scores s' = K q' have queries as columns, so that a lane
@@ -23,11 +23,11 @@ constexpr size_t attn_forward_lds(int far) {
 // next product's right operand as they stand: o' = V' p'.
 template <class T, int DP, bool SPLIT, bool VEC>
 __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 4 : attn_waves<T, DP>())) void attn_forward_kernel(const AttnArgs a) {
-  constexpr int BK = attn_keys<T>(), NS = BK / 32, LD = Tile<T, DP>::ld, KS = DP / 16, DT = DP / 32;
+  constexpr int BK = attn_keys<T>(), NS = BK / 32, TS = Tile<T, DP>::size(BK), KS = DP / 16, DT = DP / 32;
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  T* kt = (T*)smem;              // [2][BK][LD]
-  T* vt = kt + 2 * BK * LD;      // [2][BK][LD]
-  float* bias = (float*)(vt + 2 * BK * LD);
+  Lds<T>* kt = (Lds<T>*)smem;  // [2][TS]
+  Lds<T>* vt = kt + 2 * TS;    // [2][TS]
+  float* bias = (float*)(vt + 2 * TS);
 
   const int tid = threadIdx.x, wave = wave_index(), lane = tid & 63, n = lane & 31, h = lane >> 5;
   const int blocks = (a.q_len + kAttnQueries - 1) / kAttnQueries;
@@ -59,7 +59,7 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
   const T* qp = (const T*)a.q + b * a.qs[0] + head * a.qs[1] + i * a.qs[2];
 #pragma unroll
   for (int s = 0; s < KS; ++s)
-    qf[s] = load_frag(qp + 16 * s + 8 * h, i < a.q_len ? a.dim - 16 * s - 8 * h : 0);
+    qf[s] = to_frag(load_raw(qp + 16 * s + 8 * h, i < a.q_len ? a.dim - 16 * s - 8 * h : 0));
   fill_bias<T>(a, head, bias, tid, kAttnThreads);
   const float c = a.scale * kLog2e;
   const float lo = as_scalar(bias_of<T>(a, head, -a.far) * kLog2e);
@@ -88,8 +88,8 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
       vl.load(vp + (int64_t)(j0 + BK) * a.vs[2], a.vs[2], k_end - j0 - BK, a.dim, tid);
     }
     if (!idle && j0 < wave_end) {
-      const T* ktb = kt + buf * BK * LD;
-      const T* vtb = vt + buf * BK * LD;
+      const Lds<T>* ktb = kt + buf * TS;
+      const Lds<T>* vtb = vt + buf * TS;
       acc16 s[NS];
       float far_bias[NS];  // of a tile that lies outside the window, in base 2
       // the two tiles' products in turn: one that continues the last one's
@@ -177,8 +177,8 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
         }
     }
     if (more) {
-      kl.store(kt + (buf ^ 1) * BK * LD, tid);
-      vl.store(vt + (buf ^ 1) * BK * LD, tid);
+      kl.store(kt + (buf ^ 1) * TS, tid);
+      vl.store(vt + (buf ^ 1) * TS, tid);
     }
     __syncthreads();
   }
@@ -233,7 +233,7 @@ inline int attn_token_bias(const AttnArgs& a) {
 template <class T, int DP>
 constexpr size_t attn_token_lds(int bias) {
   constexpr int nw = attn_token_waves(sizeof(T), DP);
-  constexpr size_t tiles = nw * kTokenKeys * Tile<T, DP>::ld * sizeof(T);
+  constexpr size_t tiles = nw * Tile<T, DP>::size(kTokenKeys) * sizeof(Lds<T>);
   constexpr size_t join = nw * 16 * (DP + 2) * sizeof(float);
   return (tiles > join ? tiles : join) + bias;
 }
@@ -244,7 +244,7 @@ __global__ __launch_bounds__((attn_token_waves(sizeof(T), DP) * 64)) void attn_t
   constexpr int LD = Tile<T, DP>::ld, KS = DP / 32, DT = DP / 16;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const int tid = threadIdx.x, wave = wave_index(), lane = tid & 63, n = lane & 15, g = lane >> 4;
-  T* vt = (T*)smem + wave * kTokenKeys * LD;
+  Lds<T>* vt = (Lds<T>*)smem + wave * Tile<T, DP>::size(kTokenKeys);
   const int group = a.heads / a.kv_heads, rows = group * a.q_len;
   const int b = blockIdx.x / a.kv_heads, kvh = blockIdx.x % a.kv_heads;
   const int head = kvh * group + n / a.q_len, i = n % a.q_len;
@@ -260,7 +260,7 @@ __global__ __launch_bounds__((attn_token_waves(sizeof(T), DP) * 64)) void attn_t
   const T* vp = (const T*)a.v + b * a.vs[0] + kvh * a.vs[1];
 
   const float c = a.scale * kLog2e;
-  Frag<T> kf[2][KS];
+  Raw<T> kf[2][KS];
   TileLoad<T, DP, kTokenKeys, 64, VEC> vl;
   vl.init(a.vs[2], a.dim, lane);
   const auto fetch = [&](int j) __attribute__((always_inline)) {
@@ -269,7 +269,7 @@ __global__ __launch_bounds__((attn_token_waves(sizeof(T), DP) * 64)) void attn_t
       const int key = j + 16 * u + n;
       const T* p = kp + (int64_t)key * a.ks[2] + 8 * g;
 #pragma unroll
-      for (int s = 0; s < KS; ++s) kf[u][s] = load_frag(p + 32 * s, key < k_end ? a.dim - 32 * s - 8 * g : 0);
+      for (int s = 0; s < KS; ++s) kf[u][s] = load_raw(p + 32 * s, key < k_end ? a.dim - 32 * s - 8 * g : 0);
     }
     vl.load(vp + (int64_t)j * a.vs[2], a.vs[2], k_end - j, a.dim, lane);
   };
@@ -278,7 +278,7 @@ __global__ __launch_bounds__((attn_token_waves(sizeof(T), DP) * 64)) void attn_t
   Frag<T> qf[KS];
   const T* qp = (const T*)a.q + b * a.qs[0] + (real ? head : 0) * a.qs[1] + i * a.qs[2];
 #pragma unroll
-  for (int s = 0; s < KS; ++s) qf[s] = load_frag(qp + 32 * s + 8 * g, real ? a.dim - 32 * s - 8 * g : 0);
+  for (int s = 0; s < KS; ++s) qf[s] = to_frag(load_raw(qp + 32 * s + 8 * g, real ? a.dim - 32 * s - 8 * g : 0));
   // the bias in units of the product: [group][2 far + 1]
   const int dists = 2 * a.far + 1;
   const bool table = (int64_t)dists * group * 4 <= kTokenBias;
@@ -322,7 +322,7 @@ __global__ __launch_bounds__((attn_token_waves(sizeof(T), DP) * 64)) void attn_t
           s[u][r] = real ? bias_at(j0 + 16 * u + 4 * g + r - pos) : 0.f;
       }
 #pragma unroll
-      for (int x = 0; x < KS; ++x) s[u] = mma16(kf[u][x], qf[x], s[u]);
+      for (int x = 0; x < KS; ++x) s[u] = mma16(to_frag(kf[u][x]), qf[x], s[u]);
     }
     const int j = j0;
     if (j0 + NW * kTokenKeys < k_end) fetch(j0 + NW * kTokenKeys);
@@ -347,8 +347,7 @@ __global__ __launch_bounds__((attn_token_waves(sizeof(T), DP) * 64)) void attn_t
     const float mc = m == -INFINITY ? 0.f : m * c;
     Frag<T> p;
     {
-      typedef float f8 __attribute__((ext_vector_type(8)));
-      f8 e;
+      Raw<float> e;
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -356,28 +355,14 @@ __global__ __launch_bounds__((attn_token_waves(sizeof(T), DP) * 64)) void attn_t
           e[4 * u + r] = __builtin_amdgcn_exp2f(fmaf(s[u][r], c, -mc));
           l += e[4 * u + r];
         }
-      p = __builtin_convertvector(e, Frag<T>);
+      p = round_frag<T>(e);
     }
     // contraction over rows 4 g + 0..3 and 16 + 4 g + 0..3 of the tile
 #pragma unroll
-    for (int d = 0; d < DT; ++d) {
-      Frag<T> vf;
-      if constexpr (sizeof(T) == 2) {
-        const T* q = vt + (4 * g + (n >> 2)) * LD + 16 * d + 4 * (n & 3);
-        const short4v x = lds_read_tr(q), y = lds_read_tr(q + 16 * LD);
-        typedef short short8v __attribute__((ext_vector_type(8)));
-        const short8v both = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-        vf = __builtin_bit_cast(Frag<T>, both);
-      } else {
-        const T* q = vt + 4 * g * LD + 16 * d + n;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          vf[e] = q[e * LD];
-          vf[4 + e] = q[(16 + e) * LD];
-        }
-      }
-      o[d] = mma16(vf, p, o[d]);
-    }
+    for (int d = 0; d < DT; ++d)
+      o[d] = mma16(lds_columns_of<T>(vt + (4 * g + (n >> 2)) * LD + 16 * d + 4 * (n & 3), 16 * LD,
+                                     Tile<T, DP>::plane),
+                   p, o[d]);
   }
   l += __shfl_xor(l, 16, 64);
   l = halves_sum(l);
