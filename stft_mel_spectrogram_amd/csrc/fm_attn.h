@@ -149,6 +149,37 @@ __device__ __forceinline__ Raw<T> load_raw(const T* p, int have) {
   return f;
 }
 
+// Rows of a matrix [.., dim] in memory, for fragments of eight elements: VEC
+// (whole, aligned 16-byte groups, see attn_groups) without a branch, by buffer
+// loads whose offsets lie past the range where nothing is.  A branch per
+// fragment makes the kernels' prologues long: mostly skipped code, but fetched.
+template <class T, bool VEC>
+struct Rows {
+  const T* base;
+  int64_t stride;
+  int count, dim;  // rows that exist
+  __device__ __forceinline__ Raw<T> at(int row, int d) const {
+    if constexpr (VEC) {
+      typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+      const __amdgpu_buffer_rsrc_t r =
+          __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, 0x7ffffff0, 0x00020000);
+      struct Parts {
+        u4 v[sizeof(Raw<T>) / 16];
+      } p;
+#pragma unroll
+      for (int k = 0; k < (int)(sizeof(Raw<T>) / 16); ++k) {
+        const int e = d + k * Vec16<T>::n;
+        const uint32_t off = (uint32_t)((row * stride + e) * sizeof(T));
+        p.v[k] = __builtin_amdgcn_raw_buffer_load_b128(
+            r, row >= 0 && row < count && e < dim ? off : 0x7ffffff0u, 0, 0);
+      }
+      return __builtin_bit_cast(Raw<T>, p);
+    } else {
+      return load_raw(base + row * stride + d, row >= 0 && row < count ? dim - d : 0);
+    }
+  }
+};
+
 // Row-major LDS tile: 16 bytes of padding per row spread the rows over the
 // banks.  float32: three planes of 32 rows.
 template <class T, int DP>
@@ -317,12 +348,15 @@ constexpr int attn_waves() { return sizeof(T) == 2 || DP == 64 ? 2 : 1; }
 // 32x32 tile that reaches inside +-far (kBiasPad more on either side); tiles
 // beyond take an end value.
 template <class T>
-__device__ __forceinline__ float bias_of(const AttnArgs& a, int head, int d) {
-  const int i = d < -a.far ? 0 : d > a.far ? 2 * a.far : d + a.far;
-  const int b = a.map[i];
+__device__ __forceinline__ float bias_of_bucket(const AttnArgs& a, int head, int b) {
   if (b < 0 || b >= a.num_buckets) return 0.f;  // a distance without a bucket
   const int64_t at = (int64_t)b * a.heads + head;
   return a.table32 ? ((const float*)a.table)[at] : (float)((const T*)a.table)[at];
+}
+template <class T>
+__device__ __forceinline__ float bias_of(const AttnArgs& a, int head, int d) {
+  const int i = d < -a.far ? 0 : d > a.far ? 2 * a.far : d + a.far;
+  return bias_of_bucket<T>(a, head, a.map[i]);
 }
 
 __device__ __forceinline__ int clamp_int(int v, int lo, int hi) {
@@ -378,11 +412,26 @@ __device__ __forceinline__ acc16 acc_zero() {
   return a;
 }
 
+// Fills the window; a thread's map entries are on their way together, and then
+// its table entries.
 template <class T>
 __device__ __forceinline__ void fill_bias(const AttnArgs& a, int head, float* bias, int tid, int nt) {
   const float inv = 1.f / a.scale;
-  for (int i = tid; i < bias_window(a.far); i += nt)
-    bias[i] = bias_of<T>(a, head, i - a.far - kBiasPad) * inv;
+  const int win = bias_window(a.far);
+  for (int i0 = tid; i0 < win; i0 += 4 * nt) {
+    int b[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + k * nt;
+      b[k] = i < win ? a.map[clamp_int(i - kBiasPad, 0, 2 * a.far)] : -1;
+    }
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = bias_of_bucket<T>(a, head, b[k]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i0 + k * nt < win) bias[i0 + k * nt] = v[k] * inv;
+  }
 }
 
 // Which unit (entry, key head) and which of its blocks a workgroup takes.
@@ -447,14 +496,35 @@ __device__ __forceinline__ void alternate() {
   }
 }
 
-// Stores 4 consecutive elements of a result column's rows.
-template <class T>
+// N steps that each use an operand from LDS.  float32's six terms last as long
+// as a read takes: there each step's operand is read in the step before.
+template <class T, int N, class Read, class Use>
+__device__ __forceinline__ void steps(const Read& read, const Use& use) {
+  if constexpr (sizeof(T) == 4) {
+    Frag<T> f[2];
+    f[0] = read(0);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i + 1 < N) f[(i + 1) & 1] = read(i + 1);
+      stage();
+      use(i, f[i & 1]);
+      stage();
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) use(i, read(i));
+  }
+}
+
+// Stores 4 consecutive elements of a result column's rows (VEC: all of them
+// exist).
+template <class T, bool VEC>
 __device__ __forceinline__ void store4(T* p, float a, float b, float c, float d, int have) {
   typedef T t4 __attribute__((ext_vector_type(4)));
   typedef float f4 __attribute__((ext_vector_type(4)));
   const f4 v = {a, b, c, d};
   const t4 r = __builtin_convertvector(v, t4);
-  if (have >= 4) {
+  if (VEC || have >= 4) {
     __builtin_memcpy(p, &r, sizeof(r));
   } else {
 #pragma unroll

@@ -127,14 +127,16 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
   Frag<T> qf[KS], gf[KS];
   float delta = 0.f, amax = 0.f;
   {
-    const T* qp = (const T*)a.q + b * a.qs[0] + head * a.qs[1] + i * a.qs[2];
-    const T* gp = (const T*)a.d_o + b * a.dos[0] + head * a.dos[1] + i * a.dos[2];
-    const int64_t off = b * a.os[0] + head * a.os[1] + i * a.os[2];
+    const int qw = qb * kAttnQueries, count = a.q_len - qw;  // the workgroup's first query
+    const Rows<T, VEC> qr = {(const T*)a.q + b * a.qs[0] + head * a.qs[1] + qw * a.qs[2], a.qs[2], count, a.dim};
+    const Rows<T, VEC> dr = {(const T*)a.d_o + b * a.dos[0] + head * a.dos[1] + qw * a.dos[2], a.dos[2], count,
+                             a.dim};
+    const Rows<T, VEC> rr = {(const T*)a.o + b * a.os[0] + head * a.os[1] + qw * a.os[2], a.os[2], count, a.dim};
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-      const int d = 16 * s + 8 * h, have = real ? a.dim - d : 0;
-      qf[s] = to_frag(load_raw(qp + d, have));
-      const Raw<T> gr = load_raw(gp + d, have), of = load_raw((const T*)a.o + off + d, have);
+      const int d = 16 * s + 8 * h;
+      qf[s] = to_frag(qr.at(i - qw, d));
+      const Raw<T> gr = dr.at(i - qw, d), of = rr.at(i - qw, d);
       gf[s] = to_frag(gr);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -154,8 +156,6 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
   }
   const float unit = kIsF16<T> ? unit_scale(amax) : 1.f;
   fill_bias<T>(a, head, bias, tid, kAttnThreads);
-  const float lo = as_scalar(bias_of<T>(a, head, -a.far) * kLog2e);
-  const float hi = as_scalar(bias_of<T>(a, head, a.far) * kLog2e);
   if constexpr (TABLE) {
     for (int t = tid; t < 4 * win; t += kAttnThreads) sums[t] = 0.f;
     for (int t = tid; t < 4 * kDiagScratch; t += kAttnThreads) diag[t] = 0.f;
@@ -165,6 +165,7 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
   __syncthreads();
 
   const float c = a.scale * kLog2e;
+  const float lo = as_scalar(bias[0] * c), hi = as_scalar(bias[win - 1] * c);
   const int mine = a.causal ? min(len, first + i + 1) : len;
   const int least = a.causal ? min(len, first + q0 + 1) : len;
   const int wave_end = a.causal ? min(k_end, first + q0 + 32) : k_end;
@@ -226,11 +227,15 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
           s = mma32(k0, qf[0], bias_start_keys(bias, a.far, dist, h, n));
           far_bias = 0.f;
         }
-#pragma unroll
-        for (int x = 1; x < KS; ++x) s = mma32(tile_rows<T, DP>(ktb, 32 * u + n, x, h), qf[x], s);
         acc16 dp = acc_zero();
-#pragma unroll
-        for (int x = 0; x < KS; ++x) dp = mma32(tile_rows<T, DP>(vtb, 32 * u + n, x, h), gf[x], dp);
+        steps<T, 2 * KS - 1>(
+            [&](int t) { return tile_rows<T, DP>(t < KS - 1 ? ktb : vtb, 32 * u + n, (t + 1) % KS, h); },
+            [&](int t, const Frag<T>& f) {
+              if (t < KS - 1)
+                s = mma32(f, qf[t + 1], s);
+              else
+                dp = mma32(f, gf[(t + 1) % KS], dp);
+            });
         if (j0 + 32 * u + 32 > least) {
 #pragma unroll
           for (int r = 0; r < 16; ++r)
@@ -269,10 +274,9 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const Frag<T> f = acc_frag<T>(s, x);
-#pragma unroll
-          for (int d = 0; d < DT; ++d)
-            dq[d] = mma32(tile_cols<T, DP>(ktb, 32 * u + 16 * x, 32 * d, lane), f, dq[d]);
+          const Frag<T> ds = acc_frag<T>(s, x);
+          steps<T, DT>([&](int d) { return tile_cols<T, DP>(ktb, 32 * u + 16 * x, 32 * d, lane); },
+                       [&](int d, const Frag<T>& f) { dq[d] = mma32(f, ds, dq[d]); });
         }
       }
     }
@@ -295,7 +299,7 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
       for (int y = 0; y < 4; ++y) {
         const int at_d = 32 * d + 8 * y + 4 * he;
         if (at_d < a.dim)
-          store4(out + at_d, dq[d][4 * y] * f, dq[d][4 * y + 1] * f, dq[d][4 * y + 2] * f,
+          store4<T, VEC>(out + at_d, dq[d][4 * y] * f, dq[d][4 * y + 1] * f, dq[d][4 * y + 2] * f,
                  dq[d][4 * y + 3] * f, a.dim - at_d);
       }
   }
@@ -358,16 +362,30 @@ __global__ __launch_bounds__(1024) void attn_table_distances_kernel(const AttnAr
 }
 
 // ... and by bucket, one head per workgroup: the threads beyond one per bucket
-// take further shares of the distances.
+// take further shares of the distances.  Up to kTableRows partials (entries
+// times query blocks) the sums by distance are formed here too, which saves a
+// launch.
+constexpr int kTableRows = 64;
 template <class W>
 __global__ __launch_bounds__(1024) void attn_table_buckets_kernel(const AttnArgs a) {
   __shared__ float dist[bias_window(kAttnMaxFar)];
   __shared__ int bucket[bias_window(kAttnMaxFar)];
   __shared__ float red[1024];
   const int win = bias_window(a.far), head = blockIdx.x, tid = threadIdx.x;
+  const int blocks = (a.q_len + kAttnQueries - 1) / kAttnQueries, rows = a.batch * blocks;
   for (int t = tid; t < win; t += 1024) {
-    dist[t] = a.table_dist[(int64_t)head * win + t];
     bucket[t] = a.map[clamp_int(t - kBiasPad, 0, 2 * a.far)];
+    float s = 0.f;
+    if (rows > kTableRows) {
+      s = a.table_dist[(int64_t)head * win + t];
+    } else {
+#pragma unroll 8
+      for (int p = 0; p < rows; ++p) {
+        const int b = p / blocks, qb = p - b * blocks;
+        s += a.table_part[((int64_t)(b * a.heads + head) * blocks + qb) * win + t];
+      }
+    }
+    dist[t] = s;
   }
   __syncthreads();
   const int shares = 1024 / a.num_buckets, k = tid % a.num_buckets, share = tid / a.num_buckets;
@@ -420,13 +438,14 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
 
   Frag<T> kf[KS], vf[KS];
   {
-    const T* kp = (const T*)a.k + b * a.ks[0] + kvh * a.ks[1] + j * a.ks[2];
-    const T* vp = (const T*)a.v + b * a.vs[0] + kvh * a.vs[1] + j * a.vs[2];
+    const Rows<T, VEC> kr = {(const T*)a.k + b * a.ks[0] + kvh * a.ks[1] + j_wg * a.ks[2], a.ks[2], len - j_wg,
+                             a.dim};
+    const Rows<T, VEC> vr = {(const T*)a.v + b * a.vs[0] + kvh * a.vs[1] + j_wg * a.vs[2], a.vs[2], len - j_wg,
+                             a.dim};
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-      const int d = 16 * s + 8 * h, have = j < len ? a.dim - d : 0;
-      kf[s] = to_frag(load_raw(kp + d, have));
-      vf[s] = to_frag(load_raw(vp + d, have));
+      kf[s] = to_frag(kr.at(j - j_wg, 16 * s + 8 * h));
+      vf[s] = to_frag(vr.at(j - j_wg, 16 * s + 8 * h));
     }
   }
   acc16 dk[DT], dv[DT];
@@ -484,10 +503,9 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
     };
     fetch(i_beg);
     fill_bias<T>(a, head, bias, tid, kAttnThreads);
-    const float lo = as_scalar(bias_of<T>(a, head, -a.far) * kLog2e);
-    const float hi = as_scalar(bias_of<T>(a, head, a.far) * kLog2e);
     put(0);
     __syncthreads();
+    const float lo = as_scalar(bias[0] * c), hi = as_scalar(bias[bias_window(a.far) - 1] * c);
     int buf = 0;
     for (int i0 = i_beg; i0 < i_end; i0 += BQ, buf ^= 1) {
       const bool more = i0 + BQ < i_end;
@@ -539,11 +557,14 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
 #pragma unroll
           for (int u = 0; u < NS; ++u) {
             ds[u] = acc_rows(neg_delta + buf * BQ + 32 * u, h);
-#pragma unroll
-            for (int x = 0; x < KS; ++x) {
-              s[u] = mma32(tile_rows<T, DP>(qtb, 32 * u + n, x, h), kf[x], s[u]);
-              ds[u] = mma32(tile_rows<T, DP>(gtb, 32 * u + n, x, h), vf[x], ds[u]);
-            }
+            steps<T, 2 * KS>(
+                [&](int t) { return tile_rows<T, DP>(t & 1 ? gtb : qtb, 32 * u + n, t >> 1, h); },
+                [&](int t, const Frag<T>& f) {
+                  if (t & 1)
+                    ds[u] = mma32(f, vf[t >> 1], ds[u]);
+                  else
+                    s[u] = mma32(f, kf[t >> 1], s[u]);
+                });
           }
         }
         if (jw + 32 > len || (a.causal && jw + 31 - first > i0)) {
@@ -600,11 +621,14 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
 #pragma unroll
           for (int t = 0; t < 2 * NS; ++t) {
             scores(t);
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-              dv[d] = mma32(tile_cols<T, DP>(gtb, 16 * t, 32 * d, lane), p[t & 1], dv[d]);
-              dk[d] = mma32(tile_cols<T, DP>(qtb, 16 * t, 32 * d, lane), f[t & 1], dk[d]);
-            }
+            steps<T, 2 * DT>(
+                [&](int i) { return tile_cols<T, DP>(i & 1 ? qtb : gtb, 16 * t, 32 * (i >> 1), lane); },
+                [&](int i, const Frag<T>& c) {
+                  if (i & 1)
+                    dk[i >> 1] = mma32(c, f[t & 1], dk[i >> 1]);
+                  else
+                    dv[i >> 1] = mma32(c, p[t & 1], dv[i >> 1]);
+                });
           }
         }
       }
@@ -623,9 +647,9 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
     for (int y = 0; y < 4; ++y) {
       const int at_d = 32 * d + 8 * y + 4 * h;
       if (at_d < a.dim) {
-        store4(ok + at_d, dk[d][4 * y] * fk, dk[d][4 * y + 1] * fk, dk[d][4 * y + 2] * fk,
+        store4<T, VEC>(ok + at_d, dk[d][4 * y] * fk, dk[d][4 * y + 1] * fk, dk[d][4 * y + 2] * fk,
                dk[d][4 * y + 3] * fk, a.dim - at_d);
-        store4(ov + at_d, dv[d][4 * y] * fv, dv[d][4 * y + 1] * fv, dv[d][4 * y + 2] * fv,
+        store4<T, VEC>(ov + at_d, dv[d][4 * y] * fv, dv[d][4 * y + 1] * fv, dv[d][4 * y + 2] * fv,
                dv[d][4 * y + 3] * fv, a.dim - at_d);
       }
     }
@@ -660,7 +684,7 @@ int attn_backward_t(const AttnArgs& a, void* stream) {
   int st = FM_OK;
   if (a.batch > 0) {
     const bool vec = attn_groups(a.q, a.qs, a.dim, sizeof(T)) && attn_groups(a.k, a.ks, a.dim, sizeof(T)) &&
-                     attn_groups(a.v, a.vs, a.dim, sizeof(T)) && attn_groups(a.d_o, a.dos, a.dim, sizeof(T));
+                     attn_groups(a.v, a.vs, a.dim, sizeof(T)) && attn_groups(a.d_o, a.dos, a.dim, sizeof(T)) && attn_groups(a.o, a.os, a.dim, sizeof(T));
     const auto go = [&](auto narrow, auto wide, auto widest) {
       return a.dim <= 64 ? narrow(a, stream) : a.dim <= 96 ? wide(a, stream) : widest(a, stream);
     };
@@ -670,9 +694,11 @@ int attn_backward_t(const AttnArgs& a, void* stream) {
                   attn_backward_dim<T, 128, false>);
   }
   if (st != FM_OK || !a.d_table) return st;
-  st = launch("attention backward (distances)", attn_table_distances_kernel<T>,
-              dim3((unsigned)(bias_window(a.far) + 63) / 64, (unsigned)a.heads), dim3(1024), 0, stream, a);
-  if (st != FM_OK) return st;
+  if ((int64_t)a.batch * attn_query_blocks(a) > kTableRows) {
+    st = launch("attention backward (distances)", attn_table_distances_kernel<T>,
+                dim3((unsigned)(bias_window(a.far) + 63) / 64, (unsigned)a.heads), dim3(1024), 0, stream, a);
+    if (st != FM_OK) return st;
+  }
   return launch("attention backward (buckets)",
                 a.table32 ? attn_table_buckets_kernel<float> : attn_table_buckets_kernel<T>,
                 dim3((unsigned)a.heads), dim3(1024), 0, stream, a);

@@ -8,10 +8,10 @@
 namespace fm {
 
 constexpr int kAttnThreads = 256;
-// Keys per LDS tile: two 32-key steps for 16-bit types, one for float32,
-// whose tile of 64 x 128 would leave room for one workgroup per CU.
+// Keys per LDS tile.  32 and 64 take the same time (8 x 16 heads x 1501, 64
+// columns: 87 us); 32 leave the registers and the LDS for four waves per SIMD.
 template <class T>
-constexpr int attn_keys() { return sizeof(T) == 2 ? 64 : 32; }
+constexpr int attn_keys() { return 32; }
 
 template <class T, int DP>
 constexpr size_t attn_forward_lds(int far) {
@@ -56,17 +56,17 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
   kl.load(kp + k_beg * a.ks[2], a.ks[2], k_end - k_beg, a.dim, tid);
   vl.load(vp + k_beg * a.vs[2], a.vs[2], k_end - k_beg, a.dim, tid);
   Frag<T> qf[KS];
-  const T* qp = (const T*)a.q + b * a.qs[0] + head * a.qs[1] + i * a.qs[2];
+  const int qw = qb * kAttnQueries;  // the workgroup's first query
+  const Rows<T, VEC> qr = {(const T*)a.q + b * a.qs[0] + head * a.qs[1] + qw * a.qs[2], a.qs[2],
+                           a.q_len - qw, a.dim};
 #pragma unroll
-  for (int s = 0; s < KS; ++s)
-    qf[s] = to_frag(load_raw(qp + 16 * s + 8 * h, i < a.q_len ? a.dim - 16 * s - 8 * h : 0));
+  for (int s = 0; s < KS; ++s) qf[s] = to_frag(qr.at(i - qw, 16 * s + 8 * h));
   fill_bias<T>(a, head, bias, tid, kAttnThreads);
   const float c = a.scale * kLog2e;
-  const float lo = as_scalar(bias_of<T>(a, head, -a.far) * kLog2e);
-  const float hi = as_scalar(bias_of<T>(a, head, a.far) * kLog2e);
   kl.store(kt, tid);
   vl.store(vt, tid);
   __syncthreads();
+  const float lo = as_scalar(bias[0] * c), hi = as_scalar(bias[bias_window(a.far) - 1] * c);
 
   acc16 o[DT];
 #pragma unroll
@@ -92,35 +92,20 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
       const Lds<T>* vtb = vt + buf * TS;
       acc16 s[NS];
       float far_bias[NS];  // of a tile that lies outside the window, in base 2
-      // the two tiles' products in turn: one that continues the last one's
-      // accumulator waits for all of its passes
-      Frag<T> k0[NS];
-      bool near = false;
 #pragma unroll
       for (int u = 0; u < NS; ++u) {
         const int dist = j0 + 32 * u - first - q0;
-        k0[u] = tile_rows<T, DP>(ktb, 32 * u + n, 0, h);
-        const bool far = tile_before(dist, a.far) || tile_behind(dist, a.far);
-        far_bias[u] = far ? (dist < 0 ? lo : hi) : 0.f;
-        near |= !far;
-      }
-      if (near) {
-#pragma unroll
-        for (int u = 0; u < NS; ++u) {
-          const int dist = j0 + 32 * u - first - q0;
-          if (tile_before(dist, a.far) || tile_behind(dist, a.far))
-            s[u] = mma32(k0[u], qf[0], acc_zero());
-          else
-            s[u] = mma32(k0[u], qf[0], bias_start_keys(bias, a.far, dist, h, n));
+        const Frag<T> k0 = tile_rows<T, DP>(ktb, 32 * u + n, 0, h);
+        if (tile_before(dist, a.far) || tile_behind(dist, a.far)) {
+          s[u] = mma32(k0, qf[0], acc_zero());
+          far_bias[u] = dist < 0 ? lo : hi;
+        } else {
+          s[u] = mma32(k0, qf[0], bias_start_keys(bias, a.far, dist, h, n));
+          far_bias[u] = 0.f;
         }
-      } else {
-#pragma unroll
-        for (int u = 0; u < NS; ++u) s[u] = mma32(k0[u], qf[0], acc_zero());
+        steps<T, KS - 1>([&](int t) { return tile_rows<T, DP>(ktb, 32 * u + n, 1 + t, h); },
+                         [&](int t, const Frag<T>& f) { s[u] = mma32(f, qf[1 + t], s[u]); });
       }
-#pragma unroll
-      for (int x = 1; x < KS; ++x)
-#pragma unroll
-        for (int u = 0; u < NS; ++u) s[u] = mma32(tile_rows<T, DP>(ktb, 32 * u + n, x, h), qf[x], s[u]);
 #pragma unroll
       for (int u = 0; u < NS; ++u) {
         if (j0 + 32 * u + 32 > least) {
@@ -165,16 +150,13 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
       }
       l += sum;
 #pragma unroll
-      for (int u = 0; u < NS; ++u)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          // rounded to the element type for the product: half a step of each
-          // probability, as the result's own rounding; the sum l is not
-          const Frag<T> p = acc_frag<T>(s[u], x);
-#pragma unroll
-          for (int d = 0; d < DT; ++d)
-            o[d] = mma32(tile_cols<T, DP>(vtb, 32 * u + 16 * x, 32 * d, lane), p, o[d]);
-        }
+      for (int t = 0; t < 2 * NS; ++t) {
+        // rounded to the element type for the product: half a step of each
+        // probability, as the result's own rounding; the sum l is not
+        const Frag<T> p = acc_frag<T>(s[t / 2], t & 1);
+        steps<T, DT>([&](int d) { return tile_cols<T, DP>(vtb, 16 * t, 32 * d, lane); },
+                     [&](int d, const Frag<T>& f) { o[d] = mma32(f, p, o[d]); });
+      }
     }
     if (more) {
       kl.store(kt + (buf ^ 1) * TS, tid);
@@ -184,34 +166,35 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
   }
 
   l = halves_sum(l);
-  if (i >= a.q_len) return;
+  const int ie = afresh(q0 + n), he = afresh(lane >> 5);
+  if (ie >= a.q_len) return;
   const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-  const int64_t row = (int64_t)(b * a.heads + head) * a.q_len + i;
+  const int64_t row = (int64_t)(b * a.heads + head) * a.q_len + ie;
   const float lse = l != l ? l : m == -INFINITY ? -INFINITY : fmaf(m, kLn2, logf(l));
   if constexpr (SPLIT) {
     const int64_t rows = (int64_t)a.batch * a.heads * a.q_len;
-    if (h == 0) a.part_lse[blockIdx.y * rows + row] = lse;
+    if (he == 0) a.part_lse[blockIdx.y * rows + row] = lse;
     float* po = a.part_o + (blockIdx.y * rows + row) * a.dim;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        const int at_d = 32 * d + 8 * y + 4 * h;
+        const int at_d = 32 * d + 8 * y + 4 * he;
         if (at_d < a.dim)
-          store4(po + at_d, o[d][4 * y] * inv, o[d][4 * y + 1] * inv, o[d][4 * y + 2] * inv,
+          store4<float, VEC>(po + at_d, o[d][4 * y] * inv, o[d][4 * y + 1] * inv, o[d][4 * y + 2] * inv,
                  o[d][4 * y + 3] * inv, a.dim - at_d);
       }
   } else {
-    if (a.lse && h == 0) a.lse[row] = lse;
-    const int64_t off = b * a.os[0] + head * a.os[1] + i * a.os[2];
+    if (a.lse && he == 0) a.lse[row] = lse;
+    const int64_t off = b * a.os[0] + head * a.os[1] + ie * a.os[2];
     T* op = (T*)a.o + off;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        const int at_d = 32 * d + 8 * y + 4 * h;
+        const int at_d = 32 * d + 8 * y + 4 * he;
         if (at_d < a.dim)
-          store4(op + at_d, o[d][4 * y] * inv, o[d][4 * y + 1] * inv, o[d][4 * y + 2] * inv,
+          store4<T, VEC>(op + at_d, o[d][4 * y] * inv, o[d][4 * y + 1] * inv, o[d][4 * y + 2] * inv,
                  o[d][4 * y + 3] * inv, a.dim - at_d);
       }
   }
@@ -264,13 +247,11 @@ __global__ __launch_bounds__((attn_token_waves(sizeof(T), DP) * 64)) void attn_t
   TileLoad<T, DP, kTokenKeys, 64, VEC> vl;
   vl.init(a.vs[2], a.dim, lane);
   const auto fetch = [&](int j) __attribute__((always_inline)) {
+    const Rows<T, VEC> kr = {kp + (int64_t)j * a.ks[2], a.ks[2], k_end - j, a.dim};
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int key = j + 16 * u + n;
-      const T* p = kp + (int64_t)key * a.ks[2] + 8 * g;
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int s = 0; s < KS; ++s) kf[u][s] = load_raw(p + 32 * s, key < k_end ? a.dim - 32 * s - 8 * g : 0);
-    }
+      for (int s = 0; s < KS; ++s) kf[u][s] = kr.at(16 * u + n, 32 * s + 8 * g);
     vl.load(vp + (int64_t)j * a.vs[2], a.vs[2], k_end - j, a.dim, lane);
   };
   int j0 = k_beg + wave * kTokenKeys;
@@ -488,7 +469,8 @@ int attn_forward_dim(const AttnArgs& a, void* stream) {
 
 template <class T>
 int attn_forward_t(const AttnArgs& a, void* stream) {
-  const bool vec = attn_groups(a.k, a.ks, a.dim, sizeof(T)) && attn_groups(a.v, a.vs, a.dim, sizeof(T));
+  const bool vec = attn_groups(a.q, a.qs, a.dim, sizeof(T)) && attn_groups(a.k, a.ks, a.dim, sizeof(T)) &&
+                   attn_groups(a.v, a.vs, a.dim, sizeof(T));
   const auto go = [&](auto narrow, auto wide, auto widest) {
     return a.dim <= 64 ? narrow(a, stream) : a.dim <= 96 ? wide(a, stream) : widest(a, stream);
   };

@@ -255,13 +255,13 @@ inline AttnBackwardSpace attn_backward_space(const AttnArgs& a, bool f16) {
   return s;
 }
 
-// Whether rows are whole, aligned 16-byte groups and a tile of them lies
-// within a buffer load's reach (64 rows, 31-bit byte offsets).
+// Whether rows are whole, aligned 16-byte groups and a block of them lies
+// within a buffer load's reach (128 rows, 31-bit byte offsets).
 inline bool attn_groups(const void* p, const int64_t* stride, int dim, int size) {
   const int n = 16 / size;
   return dim % n == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride[0] % n == 0 &&
          stride[1] % n == 0 && stride[2] % n == 0 &&
-         (63 * stride[2] + dim) * size < 0x7fff0000;
+         (127 * stride[2] + dim) * size < 0x7fff0000;
 }
 
 int attn_forward_f32(const AttnArgs& a, void* stream);
