@@ -20,7 +20,8 @@
 namespace fm {
 
 // Sum over the LPR lanes that hold a row: within a wave by lane exchange, over
-// several waves through LDS (`red`, one slot set per call site).
+// several waves through LDS (`red`; successive calls take two slot sets in turn,
+// so that one barrier each does).
 template <int LPR>
 __device__ __forceinline__ float2 row_sum2(float2 v, float2* red) {
   constexpr int L = LPR < 64 ? LPR : 64;
@@ -36,7 +37,6 @@ __device__ __forceinline__ float2 row_sum2(float2 v, float2* red) {
       v.x += red[w].x;
       v.y += red[w].y;
     }
-    __syncthreads();
   }
   return v;
 }
@@ -47,13 +47,14 @@ __device__ __forceinline__ float row_sum(float v, float2* red) {
 }
 
 template <class T, class W, int LPR, int VPL>
-__global__ __launch_bounds__(kNormThreads) void norm_forward_kernel(
+__global__ __launch_bounds__(norm_threads(LPR)) void norm_forward_kernel(
     const T* __restrict__ x, int64_t x_stride, const W* __restrict__ w, const W* __restrict__ b,
     T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int width,
     float eps) {
   constexpr int VE = Vec16<T>::n;
-  constexpr int RPB = kNormThreads / LPR;
-  __shared__ float2 red[LPR > 64 ? LPR / 64 : 1];
+  constexpr int RPB = norm_threads(LPR) / LPR;
+  constexpr int SLOTS = LPR > 64 ? LPR / 64 : 0;
+  __shared__ float2 red[2 * SLOTS + 1];
   const int lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
   // divided, not multiplied by 1 / n: a constant row has exactly that mean
   const float n = (float)width;
@@ -96,7 +97,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_forward_kernel(
         q = fmaf(d, d, q);
       }
     }
-    const float rs = 1.f / sqrtf(row_sum<LPR>(q, red) / n + eps);
+    const float rs = 1.f / sqrtf(row_sum<LPR>(q, red + SLOTS) / n + eps);
     if (lane == 0 && row < rows) {
       if (mean) mean[row] = mu;
       if (rstd) rstd[row] = rs;
@@ -119,15 +120,17 @@ __global__ __launch_bounds__(kNormThreads) void norm_forward_kernel(
 // PARTS: also add up dw and db (part: one row of [dw | db], 2 * width floats,
 // per workgroup; a single workgroup writes dw and db themselves).
 template <class T, class W, int LPR, int VPL, bool PARTS>
-__global__ __launch_bounds__(kNormThreads) void norm_backward_kernel(
+__global__ __launch_bounds__(norm_threads(LPR)) void norm_backward_kernel(
     const T* __restrict__ dy, int64_t dy_stride, const T* __restrict__ x, int64_t x_stride,
     const W* __restrict__ w, const float* __restrict__ mean, const float* __restrict__ rstd,
     T* __restrict__ dx, float* __restrict__ part, W* __restrict__ dw, W* __restrict__ db,
     int64_t rows, int width) {
   constexpr int VE = Vec16<T>::n;
-  constexpr int NT = kNormThreads;
+  constexpr int NT = norm_threads(LPR);
   constexpr int RPB = NT / LPR;
-  __shared__ float2 red[LPR > 64 ? LPR / 64 : 1];
+  constexpr int SLOTS = LPR > 64 ? LPR / 64 : 0;
+  __shared__ float2 red[2 * SLOTS + 1];
+  bool odd = false;
   const int lane = threadIdx.x % LPR;
   const int sub = threadIdx.x / LPR;
   const float inv_n = 1.f / (float)width;
@@ -172,7 +175,8 @@ __global__ __launch_bounds__(kNormThreads) void norm_backward_kernel(
           ab[i * VE + e] += d;
         }
       }
-    s = row_sum2<LPR>(s, red);
+    s = row_sum2<LPR>(s, red + (odd ? SLOTS : 0));
+    odd = !odd;
     const float m1 = s.x * inv_n, m2 = s.y * inv_n;
     T* dr = dx + row * width;
 #pragma unroll
@@ -242,7 +246,7 @@ __global__ __launch_bounds__(kNormWide) void norm_forward_wide_kernel(
     T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int width,
     float eps) {
   constexpr int VE = Vec16<T>::n;
-  __shared__ float2 red[kNormWide / 64];
+  __shared__ float2 red[2 * kNormWide / 64];
   const int64_t row = blockIdx.x;
   const T* xr = x + row * x_stride;
   T* yr = y + row * width;
@@ -265,7 +269,7 @@ __global__ __launch_bounds__(kNormWide) void norm_forward_wide_kernel(
       q = fmaf(d, d, q);
     }
   }
-  const float rs = 1.f / sqrtf(row_sum<kNormWide>(q, red) / n + eps);
+  const float rs = 1.f / sqrtf(row_sum<kNormWide>(q, red + kNormWide / 64) / n + eps);
   if (threadIdx.x == 0) {
     if (mean) mean[row] = mu;
     if (rstd) rstd[row] = rs;
@@ -290,7 +294,7 @@ __global__ __launch_bounds__(kNormWide) void norm_backward_wide_kernel(
     const W* __restrict__ w, const float* __restrict__ mean, const float* __restrict__ rstd,
     T* __restrict__ dx, int64_t rows, int width) {
   constexpr int VE = Vec16<T>::n;
-  __shared__ float2 red[kNormWide / 64];
+  __shared__ float2 red[2 * kNormWide / 64];
   const int64_t row = blockIdx.x;
   const T* xr = x + row * x_stride;
   const T* gr = dy + row * dy_stride;
@@ -389,12 +393,12 @@ int norm_forward_t(const NormForward& a) {
   constexpr int VE = Vec16<T>::n;
   const NormShape s = norm_shape(a.width, VE);
 #define FM_NORM_FWD(L, V)                                                                     \
-  if constexpr (V * VE <= 32)                                                                 \
+  if constexpr (V * VE <= norm_most(L))                                                                 \
     if (s.lpr == L && s.vpl == V) {                                                           \
-      const int64_t need = (a.rows + kNormThreads / L - 1) / (kNormThreads / L);              \
+      const int64_t need = (a.rows + norm_rows(L) - 1) / norm_rows(L);                        \
       return launch("layer norm forward", norm_forward_kernel<T, W, L, V>,                    \
                     dim3((unsigned)(need < kNormBlocks ? need : kNormBlocks)),                \
-                    dim3(kNormThreads), 0, a.stream, (const T*)a.x, a.x_stride,               \
+                    dim3(norm_threads(L)), 0, a.stream, (const T*)a.x, a.x_stride,            \
                     (const W*)a.weight, (const W*)a.bias, (T*)a.y, a.mean, a.rstd, a.rows,    \
                     a.width, a.eps);                                                          \
     }
@@ -419,12 +423,12 @@ int norm_backward_t(const NormBackward& a) {
                   dim3(kNormWide), 0, a.stream, (const T*)a.dy, a.dy_stride, (const T*)a.x,
                   a.x_stride, (const W*)a.weight, a.mean, a.rstd, (T*)a.dx, a.rows, a.width);
 #define FM_NORM_BWD(L, V)                                                                      \
-  if constexpr (V * VE <= 32)                                                                  \
+  if constexpr (V * VE <= norm_most(L))                                                                  \
     if (s.lpr == L && s.vpl == V)                                                              \
       st = launch("layer norm backward",                                                       \
                   want ? norm_backward_kernel<T, W, L, V, true>                                \
                        : norm_backward_kernel<T, W, L, V, false>,                              \
-                  dim3((unsigned)parts), dim3(kNormThreads), 0, a.stream, (const T*)a.dy,      \
+                  dim3((unsigned)parts), dim3(norm_threads(L)), 0, a.stream, (const T*)a.dy,   \
                   a.dy_stride, (const T*)a.x, a.x_stride, (const W*)a.weight, a.mean, a.rstd,  \
                   (T*)a.dx, part, (W*)a.dw, (W*)a.db, a.rows, a.width);
     FM_NORM_SHAPES(FM_NORM_BWD)

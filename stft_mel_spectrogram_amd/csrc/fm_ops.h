@@ -45,10 +45,15 @@ constexpr int kNormMaxWidth = 1 << 20;
 constexpr int kNormThreads = 256;
 constexpr int kNormBlocks = 2048;  // workgroups that walk over rows: 8 per CU
 
-// Lane layout of a width: lanes per row and 16-byte groups per lane, at most
-// 32 elements per lane, so that the backward's two sums per column fit beside
-// the row.  Wider rows do not stay in registers: {1024, 0}, sweeps that read
-// the row again from the cache.
+// Lane layout of a width: lanes per row and 16-byte groups per lane.  At most 16
+// elements per lane, and at most 8 in workgroups of 512 and 1024 threads, so that
+// the backward's two sums per column fit beside the row with four waves per SIMD.
+// Few lanes with more groups suit short rows (us, backward: 24008 x 128 f32, 16
+// lanes of 2 groups 12.3, 64 lanes of 1 14.3; 96064 x 1024 bf16, 64 lanes of 2
+// groups 130, 256 lanes of 1 197), more lanes long ones (24016 x 4096 bf16: 512
+// lanes of 1 group 136, 256 lanes of 2 150; 12008 x 8192: 1024 of 1 130, 256 of 4
+// 200).  Rows beyond 1024 lanes do not stay in registers: {1024, 0}, sweeps that
+// read the row again from the cache.
 struct NormShape {
   int lpr, vpl;
 };
@@ -59,31 +64,40 @@ inline NormShape norm_shape(int width, int ve) {
   if (nvec <= 64) return {64, 1};
   if (nvec <= 128) return {64, 2};
   if (nvec <= 256) return {256, 1};
-  if (nvec <= 512) return {256, 2};
-  if (nvec <= 1024) return {256, 4};
-  if (nvec <= 2048 && ve == 4) return {256, 8};
+  if (nvec <= 512) return {512, 1};
+  if (nvec <= 1024) return {1024, 1};
+  if (nvec <= 2048 && ve == 4) return {1024, 2};
   return {1024, 0};
 }
-#define FM_NORM_SHAPES(X) X(16, 1) X(16, 2) X(64, 1) X(64, 2) X(256, 1) X(256, 2) X(256, 4) X(256, 8)
+#define FM_NORM_SHAPES(X) X(16, 1) X(16, 2) X(64, 1) X(64, 2) X(256, 1) X(512, 1) X(1024, 1) X(1024, 2)
+// Threads of a workgroup and the rows it holds at a time.
+constexpr int norm_threads(int lpr) { return lpr > kNormThreads ? lpr : kNormThreads; }
+constexpr int norm_most(int lpr) { return lpr > 256 ? 8 : 16; }  // elements of a lane
+constexpr int norm_rows(int lpr) { return norm_threads(lpr) / lpr; }
 
 // Whether one workgroup of the backward takes all rows: four passes over its
-// rows cost less than the second launch (64 x 122: 29 us of host time against
-// ...).
+// rows take about as long on the GPU as two launches (us: 16 x 122 f32 3.5
+// against 5.2, 64 x 122 5.9 against 5.5, 16 x 1024 bf16 9.1 against 7.2), and a
+// call 5 us less on the host (14.5 against 19.3).
 inline bool norm_single(int64_t rows, int width, int ve) {
   const NormShape s = norm_shape(width, ve);
-  return s.vpl > 0 && rows > 0 && rows <= 4 * (kNormThreads / s.lpr);
+  return s.vpl > 0 && rows > 0 && rows <= 4 * norm_rows(s.lpr);
 }
-// Partial rows (workgroups of the backward): enough to fill the chip several
-// times over, few enough that their sum stays small.
+// Partial rows (workgroups of the backward, which walk over the rows): as many
+// as the chip holds at once, 1024 threads per compute unit (24016 x 4096 bf16:
+// 136 us, 150 with twice as many; 48032 x 2048: 135, 198 with half).  Fewer for few
+// rows, 8 per partial row while that leaves one workgroup per unit, since a
+// partial row's sums cost as much traffic as three rows (1000 x 2048: 12 us, 25
+// with a partial row per row).
 inline int norm_parts(int64_t rows, int width, int ve) {
   const NormShape s = norm_shape(width, ve);
   if (norm_single(rows, width, ve)) return 1;
-  const int rpb = s.vpl > 0 ? kNormThreads / s.lpr : 1;
+  const int rpb = s.vpl > 0 ? norm_rows(s.lpr) : 1;
   const int64_t need = (rows + rpb - 1) / rpb;
-  const int64_t most = s.vpl > 0 ? 1024 : 64;
+  int64_t most = s.vpl == 0 ? 64 : 1024 * kNormThreads / norm_threads(s.lpr);
+  if (s.vpl > 0 && rows / 8 < most) most = rows / 8 < 256 ? 256 : rows / 8;
   return (int)(need < most ? need : most);
 }
-
 
 // One translation unit per element type; w32: float32 parameters.
 int norm_forward_f32(const NormForward& a);
