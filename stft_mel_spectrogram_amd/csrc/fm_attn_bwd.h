@@ -364,8 +364,9 @@ __global__ __launch_bounds__(1024) void attn_table_distances_kernel(const AttnAr
 // ... and by bucket, one head per workgroup: the threads beyond one per bucket
 // take further shares of the distances.  Up to kTableRows partials (entries
 // times query blocks) the sums by distance are formed here too, which saves a
-// launch.
-constexpr int kTableRows = 64;
+// launch (whole backward, us: 1 partial 41.1, with both launches 43.0; 12: 88.0
+// and 88.4; 32: 74.0 and 72.4; 64: 101 and 95).
+constexpr int kTableRows = 16;
 template <class W>
 __global__ __launch_bounds__(1024) void attn_table_buckets_kernel(const AttnArgs a) {
   __shared__ float dist[bias_window(kAttnMaxFar)];

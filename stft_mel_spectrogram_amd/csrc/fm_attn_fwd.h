@@ -10,12 +10,11 @@ namespace fm {
 constexpr int kAttnThreads = 256;
 // Keys per LDS tile.  32 and 64 take the same time (8 x 16 heads x 1501, 64
 // columns: 87 us); 32 leave the registers and the LDS for four waves per SIMD.
-template <class T>
-constexpr int attn_keys() { return 32; }
+constexpr int kAttnKeys = 32;
 
 template <class T, int DP>
 constexpr size_t attn_forward_lds(int far) {
-  return 4 * Tile<T, DP>::size(attn_keys<T>()) * sizeof(Lds<T>) + bias_window(far) * sizeof(float);
+  return 4 * Tile<T, DP>::size(kAttnKeys) * sizeof(Lds<T>) + bias_window(far) * sizeof(float);
 }
 
 // The transposed scores s' = K q' have queries as columns, so that a lane
@@ -23,7 +22,7 @@ constexpr size_t attn_forward_lds(int far) {
 // next product's right operand as they stand: o' = V' p'.
 template <class T, int DP, bool SPLIT, bool VEC>
 __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 4 : attn_waves<T, DP>())) void attn_forward_kernel(const AttnArgs a) {
-  constexpr int BK = attn_keys<T>(), NS = BK / 32, TS = Tile<T, DP>::size(BK), KS = DP / 16, DT = DP / 32;
+  constexpr int BK = kAttnKeys, NS = BK / 32, TS = Tile<T, DP>::size(BK), KS = DP / 16, DT = DP / 32;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   Lds<T>* kt = (Lds<T>*)smem;  // [2][TS]
   Lds<T>* vt = kt + 2 * TS;    // [2][TS]

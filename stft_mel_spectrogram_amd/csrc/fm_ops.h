@@ -145,10 +145,13 @@ struct ScoreBackward {
 constexpr int kScoreMaxTop = 64;  // one kept entry per lane of a wave
 
 // Work split of a call: lanes of a row (256: a workgroup per row segment), 16-
-// byte groups of a lane, segments and their length.  Top alternatives need a
-// whole wave per row.  Long rows take segments of one chunk of 4 groups per
-// lane while the rows alone give fewer than 1024 workgroups, of one group where
-// even those leave compute units idle (8 x 50001, 5 alternatives: ...).
+// byte groups of a lane, segments and their length.  Short rows lie in 16 lanes
+// (24008 x 129 f32: 4.5 us, in a whole wave 8.3), with top alternatives in a wave.
+// Long rows take segments while there are fewer rows than compute units, up to 1024
+// workgroups (128 x 32000, 5 alternatives: 17 us, unsegmented 30; 64 x 32000
+// without: 5.9 and 7.2; 512 rows: 12.1 and 11.0), of one chunk of 4 groups per
+// lane, or of one group where those leave units idle (8 x 50001, 5 alternatives:
+// 11.0 us, of 4 groups 16.3, unsegmented 37.7; without: 5.0, 5.9 and 10.9).
 struct ScoreSplit {
   int lanes, vecs, segs, seg_len;
 };
@@ -165,7 +168,7 @@ inline ScoreSplit score_split(int64_t rows, int vocab, int ve, int top) {
     chunk = 256 * ve;
     chunks = (vocab + chunk - 1) / chunk;
   }
-  int64_t segs = rows > 0 ? (1024 + rows - 1) / rows : 1;
+  int64_t segs = rows > 0 && rows < 256 ? (1024 + rows - 1) / rows : 1;
   if (segs > chunks) segs = chunks;
   if (segs < 1) segs = 1;
   const int per = (chunks + (int)segs - 1) / (int)segs;
@@ -220,8 +223,10 @@ constexpr int kAttnMaxSplits = 512; // key ranges of a forward call
 constexpr int kAttnQueries = 128;   // queries of a workgroup
 constexpr int kAttnTokenRows = 16;  // query rows of the single-token kernel
 
-// Query rows that share a key head: a few of them take the single-token
-// kernel, whose waves divide the keys instead of the queries.
+// Query rows that share a key head: as many as one 16-column fragment holds take
+// the single-token kernel, whose waves divide the keys instead of the queries
+// (8 x 16 heads against 1501 keys, bf16, us: 1 row 12.2, the other kernel 18.9;
+// 16 rows 13.8 and 20.0).
 inline bool attn_token_kernel(const AttnArgs& a) {
   return (int64_t)a.q_len * (a.heads / a.kv_heads) <= kAttnTokenRows;
 }
@@ -230,19 +235,25 @@ inline bool attn_token_kernel(const AttnArgs& a) {
 constexpr int attn_token_waves(int size, int dp) {
   return size == 2 ? (dp == 64 ? 16 : 8) : (dp == 64 ? 8 : 4);
 }
-// Key ranges a forward call is cut into while its workgroups alone do not
-// fill the chip (256 compute units): two workgroups per unit; at least 2048
-// keys each for the single-token kernel (shorter ranges cost more in the join
-// than they gain: ...), 512 for the other.
+// Key ranges a forward call is cut into while its workgroups alone do not fill
+// the chip (256 compute units), us in bf16 at 64 columns, a call's GPU time:
+// Single tokens: one of their large workgroups per unit (2 x 8 key heads, 20000
+// keys: 20.8, with two 23.8), of 512 keys, one round of 16 waves (1 x 8, 8000: 12.3;
+// ranges of 2048 keys 17.2, none 39.4).  Where the workgroups reach a third of the
+// units they draw the whole memory rate without a join (8 x 16, 8000: 40.3, two
+// ranges 44.5), and a short call's join costs more on the host than it gains
+// (8 x 16, 1501: 12.7; 1 x 1, 1501: 11.6 and 14.6 with the host's part, 11.5 and
+// 19.5 with ranges).
+// Others: two workgroups per unit, of 256 keys (1 x 8 heads, 101 queries, 4000
+// keys: 15.0; ranges of 512 17.3, none 70.2), from 1024 keys on (1 x 8, 600
+// queries, 600 keys: 15.3, with ranges 17.7; 1 x 16, 400, 1000: 21.9 and 21.3).
 inline int attn_splits(const AttnArgs& a) {
   const bool token = attn_token_kernel(a);
   const int64_t wgs = token ? (int64_t)a.batch * a.kv_heads
                             : (int64_t)a.batch * a.heads * ((a.q_len + kAttnQueries - 1) / kAttnQueries);
-  if (wgs == 0) return 1;
-  int64_t s = 512 / wgs;
-  const int64_t least = token ? 2048 : 512, most = (a.k_len + least - 1) / least;
-  if (s > most) s = most;
-  return s < 1 ? 1 : (int)s;
+  if (wgs == 0 || wgs > (token ? 85 : 256) || a.k_len < (token ? 2048 : 1024)) return 1;
+  const int64_t fill = (token ? 256 : 512) / wgs, most = a.k_len / (token ? 512 : 256);
+  return (int)(fill < most ? fill : most);
 }
 inline int64_t attn_round16(int64_t n) { return (n + 15) / 16 * 16; }
 inline int64_t attn_rows(const AttnArgs& a) { return (int64_t)a.batch * a.heads * a.q_len; }
