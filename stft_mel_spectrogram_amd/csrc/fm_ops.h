@@ -147,11 +147,13 @@ constexpr int kScoreMaxTop = 64;  // one kept entry per lane of a wave
 // Work split of a call: lanes of a row (256: a workgroup per row segment), 16-
 // byte groups of a lane, segments and their length.  Short rows lie in 16 lanes
 // (24008 x 129 f32: 4.5 us, in a whole wave 8.3), with top alternatives in a wave.
-// Long rows take segments while there are fewer rows than compute units, up to 1024
-// workgroups (128 x 32000, 5 alternatives: 17 us, unsegmented 30; 64 x 32000
-// without: 5.9 and 7.2; 512 rows: 12.1 and 11.0), of one chunk of 4 groups per
-// lane, or of one group where those leave units idle (8 x 50001, 5 alternatives:
-// 11.0 us, of 4 groups 16.3, unsegmented 37.7; without: 5.0, 5.9 and 10.9).
+// Long rows take segments while their workgroups fit on the chip at once, 5 per
+// compute unit: of one chunk of 4 groups per lane below 256 rows (128 x 32000, 5
+// alternatives: 13 us, unsegmented 30; 64 x 32000 without: 5.9 and 7.2), of 4
+// chunks for more rows (300 x 131072, 20 alternatives: 43 us, unsegmented 58; 512 x
+// 32000 of one chunk 11.8, unsegmented 10.9).  Chunks of one group per lane where
+// the others leave units idle (8 x 50001, 5 alternatives: 10 us, of 4 groups 16,
+// unsegmented 38; without: 5.0, 5.9 and 10.9).
 struct ScoreSplit {
   int lanes, vecs, segs, seg_len;
 };
@@ -168,8 +170,9 @@ inline ScoreSplit score_split(int64_t rows, int vocab, int ve, int top) {
     chunk = 256 * ve;
     chunks = (vocab + chunk - 1) / chunk;
   }
-  int64_t segs = rows > 0 && rows < 256 ? (1024 + rows - 1) / rows : 1;
-  if (segs > chunks) segs = chunks;
+  int64_t segs = rows > 0 ? 1280 / rows : 1;
+  const int most = rows < 256 ? chunks : chunks / 4;
+  if (segs > most) segs = most;
   if (segs < 1) segs = 1;
   const int per = (chunks + (int)segs - 1) / (int)segs;
   return {256, vecs, (chunks + per - 1) / per, per * chunk};

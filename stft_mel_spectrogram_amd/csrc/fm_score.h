@@ -12,11 +12,12 @@
 // add nothing to the entropy; NaN anywhere in a row makes its results NaN.
 // A row of -inf only has lp = -inf, H = 0 and a zero gradient.
 //
-// Top alternatives: a wave keeps its best `top` entries as 64-bit keys
-// (value in an ordered integer, then the complement of the index, so that
-// ties go to the lower index), one per lane in descending order; a chunk's
-// entries are taken in descending order while they beat the last one kept (the
-// wave's best by rotations of lanes, the next one looked for by its lane alone).
+// Top alternatives: entries are 64-bit keys (value in an ordered integer, then
+// the complement of the index, so that ties go to the lower index).  A wave
+// collects candidates in LDS: of its first chunk those that reach a value which
+// at least `top` of its lanes' maxima reach, of later ones those that beat the
+// last one kept.  From time to time each candidate counts the larger ones, which
+// is its place in the sorted list; the first `top` stay.
 //
 // Memory bound.  A row that 16 or 64 lanes hold in registers is read once, its
 // maximum taken first.  Longer rows go through 4 waves chunk by chunk (8 waves
@@ -43,20 +44,82 @@ __device__ __forceinline__ float key_value(key_t k) {
 }
 __device__ __forceinline__ int key_index(key_t k) { return (int)~(uint32_t)k; }
 
-// The largest key of the wave: the largest value, then among its holders the
-// largest rest (the lowest index).
-__device__ __forceinline__ key_t wave_max_key(key_t k) {
-  const uint32_t hi = wave_umax((uint32_t)(k >> 32));
-  const uint32_t lo = wave_umax((uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
-  return (key_t)hi << 32 | lo;
-}
+// The candidates of a wave for the `top` largest keys.
+struct TopKeys {
+  static constexpr int kRoom = 128;
+  static constexpr int kSize = kRoom + 4;  // keys of LDS
+  key_t* buf;
+  int top, lane;
+  int count = 0;
+  key_t last = 0;                // the least key kept, once there are `top`
+  float bar = -INFINITY;         // entries below it need not be looked at
 
-// Inserts `k` (the same in every lane) into the wave's descending list.
-__device__ __forceinline__ void list_insert(key_t& list, key_t k, int lane) {
-  const key_t up = __shfl_up(list, 1, 64);
-  const bool below = list < k;
-  const bool above_too = lane > 0 && up < k;
-  list = below ? (above_too ? up : k) : list;
+  // stores of the wave's lanes are seen by its reads
+  __device__ __forceinline__ void settle() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+  // Sorts what there is and keeps the first `top`.
+  __device__ __forceinline__ void prune() {
+    if (lane < 4) buf[count + lane] = 0;
+    settle();
+    const key_t a = lane < count ? buf[lane] : 0, b = 64 + lane < count ? buf[64 + lane] : 0;
+    int ra = 0, rb = 0;
+    for (int i = 0; i < count; i += 4) {
+      key_t k[4];
+      __builtin_memcpy(k, buf + i, sizeof(k));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        ra += k[j] > a;
+        rb += k[j] > b;
+      }
+    }
+    settle();
+    if (a != 0 && ra < top) buf[ra] = a;
+    if (b != 0 && rb < top) buf[rb] = b;
+    settle();
+    if (count < top) return;
+    count = top;
+    last = buf[top - 1];
+    // later entries have higher indices: they have to be larger
+    const uint32_t hi = (uint32_t)(last >> 32) + 1;
+    bar = key_value((key_t)hi << 32);
+  }
+  __device__ __forceinline__ void push(bool real, key_t key) {
+    const bool in = real && key > last;
+    const uint64_t who = __ballot(in);
+    if (who == 0) return;
+    const int at = count + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32),
+                                                     __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+    if (in) buf[at] = key;
+    count += __popcll(who);
+    if (count > kRoom - 64) prune();
+  }
+  __device__ __forceinline__ key_t listed() {
+    prune();
+    return lane < count ? buf[lane] : 0;
+  }
+};
+
+// A value (as the upper half of a key) that at least `top` of the wave's values
+// reach, and few more.
+__device__ __forceinline__ uint32_t top_bound(uint32_t o, int top) {
+  uint32_t most = wave_umax(o), lo = ~wave_umax(~o);
+  if (top == 1) return most;
+  uint32_t span = most - lo;  // fewer than `top` reach lo + span + 1
+  while (span > 0) {
+    const uint32_t step = span / 2 + 1;
+    const int n = __popcll(__ballot(o >= lo + step));
+    if (n >= top) {
+      lo += step;
+      span -= step;
+      if (n <= top + top / 4 + 2) break;
+    } else {
+      span = step - 1;
+    }
+  }
+  return lo;
 }
 
 // m = max x, s = sum exp2(y), t = sum exp2(y) y of a set of entries, y = (x - m)
@@ -140,48 +203,36 @@ __device__ __forceinline__ float score_max(const Vec16<T> (&v)[V]) {
   return m;
 }
 
-// This lane's best entry of a chunk below `last` (group i starts at c0 + (i * nt
-// + tid) * VE).
+// A chunk's entries into the candidates (group i starts at c0 + (i * nt + tid) *
+// VE), m the lane's largest: marked by a bit each where they pass the bar, then
+// read again, every lane's first one, second one, ... at a time.
 template <class T, int V>
-__device__ __forceinline__ key_t score_best(const Vec16<T> (&v)[V], int c0, int nt, int tid, int end,
-                                            key_t last) {
+__device__ __forceinline__ void score_top(const Vec16<T> (&v)[V], const T* xr, float m, int c0, int nt,
+                                          int tid, int end, TopKeys& keys) {
   constexpr int VE = Vec16<T>::n;
-  key_t best = 0;
+  if (keys.count == 0) {
+    keys.bar = key_value((key_t)top_bound((uint32_t)(score_key(m, 0) >> 32), keys.top) << 32);
+  } else if (__ballot(!(m < keys.bar)) == 0) {
+    return;
+  }
+  uint32_t marks = 0;
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
-    for (int e = 0; e < VE; ++e) {
-      const int c = c0 + (i * nt + tid) * VE + e;
-      const key_t k = c < end ? score_key((float)v[i].v[e], c) : 0;
-      if (k < last && k > best) best = k;
-    }
-  return best;
-}
-// The wave's best entries of a chunk, taken in descending order: into an empty
-// list one lane after the other, into a list while they beat its last.
-template <class T, int V>
-__device__ __forceinline__ void score_top(const Vec16<T> (&v)[V], int c0, int nt, int tid, int end,
-                                          int top, bool empty, key_t& list, int lane) {
-  key_t mine = score_best(v, c0, nt, tid, end, ~(key_t)0);
-  const auto next = [&](key_t best) {
-    // only the lane that held it looks for its next one
-    if (mine == best) mine = score_best(v, c0, nt, tid, end, best);
-  };
-  if (empty) {
-    for (int i = 0; i < top; ++i) {
-      const key_t best = wave_max_key(mine);
-      if (best == 0) break;
-      if (lane == i) list = best;
-      next(best);
-    }
-  } else {
-    while (true) {
-      const key_t best = wave_max_key(mine);
-      if (best <= __shfl(list, top - 1, 64)) break;
-      list_insert(list, best, lane);
-      next(best);
-    }
+    for (int e = 0; e < VE; ++e)
+      marks |= !((float)v[i].v[e] < keys.bar) ? 1u << (i * VE + e) : 0u;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int have = end - (c0 + (i * nt + tid) * VE);
+    if (have < VE) marks &= ~(((1u << VE) - (1u << (have > 0 ? have : 0))) << (i * VE));
   }
+  while (__ballot(marks != 0)) {
+    const int j = marks ? __builtin_ctz(marks) : 0;
+    const int c = c0 + (j / VE * nt + tid) * VE + j % VE;
+    keys.push(marks != 0, marks ? score_key((float)xr[c], c) : 0);
+    marks &= marks - 1;
+  }
+  if (keys.last == 0 ? keys.count >= keys.top : keys.count >= keys.top + 16) keys.prune();
 }
 
 // Rows that L lanes hold, V groups each.
@@ -202,13 +253,19 @@ __global__ __launch_bounds__(256) void score_row_kernel(const T* __restrict__ x,
     v[i] = load16_part(xr + c, end - c, (T)-INFINITY);
   }
   ScoreSum r;
-  r.m = lanes_max<L>(score_max(v));
+  const float most = score_max(v);
+  r.m = lanes_max<L>(most);
   float s = 0.f, t = 0.f;
   score_add(v, r.m == -INFINITY ? 0.f : r.m, s, t);
   r.s = lanes_sum<L>(s);
   r.t = lanes_sum<L>(t);
   key_t list = 0;
-  if constexpr (TOP) score_top(v, 0, L, lane, end, top, true, list, lane);
+  if constexpr (TOP) {
+    __shared__ __attribute__((aligned(16))) key_t buf[256 / L][TopKeys::kSize];
+    TopKeys keys = {buf[threadIdx.x / L], top, lane};
+    score_top(v, xr, most, 0, L, lane, end, keys);
+    list = keys.listed();
+  }
   if (row < rows) score_finish(r, xr, row, vocab, tokens, tok64, list, TOP ? top : 0, out, lane);
 }
 
@@ -230,7 +287,8 @@ __global__ __launch_bounds__(256) void score_forward_kernel(
   const int end = beg + seg_len < vocab ? beg + seg_len : vocab;
 
   ScoreSum acc = {-INFINITY, 0.f, 0.f};
-  key_t list = 0;
+  __shared__ __attribute__((aligned(16))) key_t buf[TOP ? 4 : 1][TopKeys::kSize];
+  TopKeys keys = {buf[TOP ? wave : 0], top, lane};
   for (int c0 = beg; c0 < end; c0 += CH) {
     Vec16<T> v[V];
 #pragma unroll
@@ -238,7 +296,8 @@ __global__ __launch_bounds__(256) void score_forward_kernel(
       const int c = c0 + (i * NT + tid) * VE;
       v[i] = load16_part(xr + c, end - c, (T)-INFINITY);
     }
-    const float m = fmaxf(acc.m, score_max(v));
+    const float most = score_max(v);
+    const float m = fmaxf(acc.m, most);
     const float d0 = score_shift(acc.m, m);
     const float r0 = __builtin_amdgcn_exp2f(d0);
     float s = 0.f, t = 0.f;
@@ -246,25 +305,22 @@ __global__ __launch_bounds__(256) void score_forward_kernel(
     acc.t = (acc.t + acc.s * d0) * r0 + t;
     acc.s = acc.s * r0 + s;
     acc.m = m;
-    if constexpr (TOP) score_top(v, c0, NT, tid, end, top, c0 == beg, list, lane);
+    if constexpr (TOP) score_top(v, xr, most, c0, NT, tid, end, keys);
   }
   acc = score_join_lanes<64>(acc);
   __shared__ ScoreSum sums[4];
-  __shared__ key_t keys[TOP ? 256 : 1];
+  __shared__ key_t lists[TOP ? 256 : 1];
   if (lane == 0) sums[wave] = acc;
-  if constexpr (TOP) keys[tid] = lane < top ? list : 0;
+  if constexpr (TOP) lists[tid] = keys.listed();
   __syncthreads();
   if (wave != 0) return;
   acc = sums[0];
 #pragma unroll
   for (int w = 1; w < 4; ++w) acc = score_join(acc, sums[w]);
+  key_t list = 0;
   if constexpr (TOP) {
-    for (int w = 1; w < 4; ++w)
-      for (int i = 0; i < top; ++i) {
-        const key_t k = keys[w * 64 + i];
-        if (k <= __shfl(list, top - 1, 64)) break;
-        list_insert(list, k, lane);
-      }
+    for (int w = 1; w < 4; ++w) keys.push(lists[w * 64 + lane] != 0, lists[w * 64 + lane]);
+    list = keys.listed();
   }
   if (segs == 1) {
     score_finish(acc, xr, row, vocab, tokens, tok64, list, TOP ? top : 0, out, lane);
@@ -294,17 +350,24 @@ __global__ __launch_bounds__(64) void score_join_kernel(
   acc = score_join_lanes<64>(acc);
   key_t list = 0;
   if (top > 0) {
-    const int64_t n = (int64_t)segs * top;
-    const key_t* keys = part_keys + row * n;
-    for (int64_t i0 = 0; i0 < n; i0 += 64) {
-      key_t mine = i0 + lane < n ? keys[i0 + lane] : 0;
-      while (true) {
-        const key_t best = wave_max_key(mine);
-        if (best <= __shfl(list, top - 1, 64)) break;
-        list_insert(list, best, lane);
-        if (mine == best) mine = 0;
-      }
+    __shared__ __attribute__((aligned(16))) key_t buf[TopKeys::kSize];
+    TopKeys keys = {buf, top, lane};
+    const int n = segs * top;
+    const key_t* from = part_keys + row * n;
+    uint32_t first = 0;  // the segments' best
+    for (int s = lane; s < segs; s += 64) {
+      const uint32_t hi = (uint32_t)(from[s * top] >> 32);
+      first = hi > first ? hi : first;
     }
+    const key_t least = (key_t)top_bound(first, top) << 32;
+    for (int i0 = 0; i0 < n; i0 += 256) {
+      key_t k[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) k[j] = i0 + 64 * j + lane < n ? from[i0 + 64 * j + lane] : 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) keys.push(k[j] != 0 && k[j] >= least, k[j]);
+    }
+    list = keys.listed();
   }
   score_finish(acc, x + row * x_stride, row, vocab, tokens, tok64, list, top, out, lane);
 }
