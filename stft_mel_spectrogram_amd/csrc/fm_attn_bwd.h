@@ -11,7 +11,6 @@
 namespace fm {
 
 constexpr int kAttnThreads = 256;
-constexpr int kAttnBlockKeys = 128;  // keys of a dk, dv workgroup
 template <class T>
 constexpr bool kIsF16 = false;
 template <>
@@ -475,8 +474,14 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
   // row i of the tile at i0 sees this lane's key if i >= need
   const int need = j >= len ? a.q_len : a.causal ? max(j - first, 0) : 0;
 
-  for (int gi = 0; gi < group; ++gi) {
-    const int head = kvh * group + gi;
+  // this workgroup's share of the query tiles, head after head
+  const int tiles = max(i_end - i_beg + BQ - 1, 0) / BQ, per = (group * tiles + a.dkv_splits - 1) / a.dkv_splits;
+  const int t_end = min(((int)blockIdx.y + 1) * per, group * tiles);
+  for (int t_head = blockIdx.y * per; t_head < t_end;) {
+    const int gi = t_head / tiles, head = kvh * group + gi;
+    const int i_first = i_beg + (t_head - gi * tiles) * BQ;
+    t_head = min(t_end, (gi + 1) * tiles);
+    const int i_last = min(i_end, i_beg + (t_head - gi * tiles) * BQ);
     const T* qp = (const T*)a.q + b * a.qs[0] + head * a.qs[1];
     const T* gp = (const T*)a.d_o + b * a.dos[0] + head * a.dos[1];
     const int64_t row0 = (int64_t)(b * a.heads + head) * a.q_len;
@@ -502,14 +507,14 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
         neg_delta[buf * BQ + tid] = d_next;
       }
     };
-    fetch(i_beg);
+    fetch(i_first);
     fill_bias<T>(a, head, bias, tid, kAttnThreads);
     put(0);
     __syncthreads();
     const float lo = as_scalar(bias[0] * c), hi = as_scalar(bias[bias_window(a.far) - 1] * c);
     int buf = 0;
-    for (int i0 = i_beg; i0 < i_end; i0 += BQ, buf ^= 1) {
-      const bool more = i0 + BQ < i_end;
+    for (int i0 = i_first; i0 < i_last; i0 += BQ, buf ^= 1) {
+      const bool more = i0 + BQ < i_last;
       if (AHEAD && more) fetch(i0 + BQ);
       if (jw < len && !(a.causal && i0 + BQ - 1 + first < jw)) {
         const Lds<T>* qtb = qt + buf * TS;
@@ -640,6 +645,23 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
   }
   if (j >= a.k_len) return;
   const float fk = a.scale / unit, fv = __builtin_amdgcn_exp2f(-kProbShift<T>);
+  if (a.dkv_splits > 1) {
+    const int64_t unit_of = (int64_t)blockIdx.y * a.batch * a.kv_heads + at.unit;
+    float* pk = a.part_dkv + (unit_of * a.k_len + j) * 2 * a.dim;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int at_d = 32 * d + 8 * y + 4 * h;
+        if (at_d < a.dim) {
+          store4<float, VEC>(pk + at_d, dk[d][4 * y] * fk, dk[d][4 * y + 1] * fk, dk[d][4 * y + 2] * fk,
+                             dk[d][4 * y + 3] * fk, a.dim - at_d);
+          store4<float, VEC>(pk + a.dim + at_d, dv[d][4 * y] * fv, dv[d][4 * y + 1] * fv, dv[d][4 * y + 2] * fv,
+                             dv[d][4 * y + 3] * fv, a.dim - at_d);
+        }
+      }
+    return;
+  }
   T* ok = (T*)a.dk + b * a.dks[0] + kvh * a.dks[1] + j * a.dks[2];
   T* ov = (T*)a.dv + b * a.dvs[0] + kvh * a.dvs[1] + j * a.dvs[2];
 #pragma unroll
@@ -654,6 +676,27 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
                dv[d][4 * y + 3] * fv, a.dim - at_d);
       }
     }
+}
+
+// Adds up the shares in order: a thread per column of [dk | dv], 256 / cols rows
+// of keys per workgroup.
+template <class T>
+__global__ __launch_bounds__(kAttnThreads) void attn_dkv_join_kernel(const AttnArgs a) {
+  const int cols = a.dim <= 32 ? 64 : a.dim <= 64 ? 128 : 256;
+  const int64_t rows = (int64_t)a.batch * a.kv_heads * a.k_len;
+  const int64_t row = (int64_t)blockIdx.x * (kAttnThreads / cols) + threadIdx.x / cols;
+  const int c = threadIdx.x & (cols - 1);
+  if (row >= rows || c >= 2 * a.dim) return;
+  const float* p = a.part_dkv + row * 2 * a.dim + c;
+  const int64_t step = rows * 2 * a.dim;
+  float s = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < a.dkv_splits; ++i) s += p[i * step];
+  const int64_t unit = row / a.k_len, b = unit / a.kv_heads, kvh = unit - b * a.kv_heads, j = row - unit * a.k_len;
+  if (c < a.dim)
+    ((T*)a.dk)[b * a.dks[0] + kvh * a.dks[1] + j * a.dks[2] + c] = (T)s;
+  else
+    ((T*)a.dv)[b * a.dvs[0] + kvh * a.dvs[1] + j * a.dvs[2] + c - a.dim] = (T)s;
 }
 
 template <class T, int DP, bool VEC>
@@ -672,11 +715,18 @@ int attn_backward_dim(const AttnArgs& a, void* stream) {
                           dim3(kAttnThreads), attn_dq_lds<T, DP>(a.far, table), stream, a);
     if (st != FM_OK) return st;
   }
-  if (a.k_len > 0)
-    return launch("attention backward (dk, dv)", attn_dkv_kernel<T, DP, VEC>,
-                  dim3(place_grid((int64_t)a.batch * a.kv_heads,
-                                  (a.k_len + kAttnBlockKeys - 1) / kAttnBlockKeys)),
-                  dim3(kAttnThreads), attn_dkv_lds<T, DP>(a.far), stream, a);
+  if (a.k_len > 0) {
+    const int st = launch("attention backward (dk, dv)", attn_dkv_kernel<T, DP, VEC>,
+                          dim3(place_grid((int64_t)a.batch * a.kv_heads,
+                                          (a.k_len + kAttnBlockKeys - 1) / kAttnBlockKeys),
+                               (unsigned)a.dkv_splits),
+                          dim3(kAttnThreads), attn_dkv_lds<T, DP>(a.far), stream, a);
+    if (st != FM_OK || a.dkv_splits == 1) return st;
+    const int per = kAttnThreads / (a.dim <= 32 ? 64 : a.dim <= 64 ? 128 : 256);
+    return launch("attention backward (join)", attn_dkv_join_kernel<T>,
+                  dim3((unsigned)(((int64_t)a.batch * a.kv_heads * a.k_len + per - 1) / per)),
+                  dim3(kAttnThreads), 0, stream, a);
+  }
   return FM_OK;
 }
 

@@ -440,6 +440,46 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(const AttnArgs 
   }
 }
 
+// Few ranges: a row per wave, its weights in the lanes, a lane per column (2 x 4
+// heads, 1777 queries, 4 ranges: 4 us, by whole workgroups 16).
+constexpr int kAttnFewRanges = 16;
+template <class T>
+__global__ __launch_bounds__(kAttnThreads) void attn_join_rows_kernel(const AttnArgs a) {
+  const int64_t rows = (int64_t)a.batch * a.heads * a.q_len;
+  const int64_t row = (int64_t)blockIdx.x * (kAttnThreads / 64) + wave_index();
+  if (row >= rows) return;
+  const int lane = threadIdx.x & 63;
+  const float* p = a.part_o + row * a.dim + lane;
+  const int64_t step = rows * a.dim;
+  const bool one = lane < a.dim, two = lane + 64 < a.dim;
+  const float v = lane < a.splits ? a.part_lse[lane * rows + row] : -INFINITY;
+  const float m = lanes_max<64>(v);
+  const float ms = m == -INFINITY ? 0.f : m;
+  // a NaN weight makes the sum NaN, and with it the row
+  const float w = __builtin_amdgcn_exp2f((v - ms) * kLog2e), sum = lanes_sum<64>(w);
+  float o = 0.f, o2 = 0.f;
+  for (int s = 0; s < a.splits; s += 4) {
+    float x[4], y[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool in = s + k < a.splits;
+      x[k] = in && one ? p[(s + k) * step] : 0.f;
+      y[k] = in && two ? p[(s + k) * step + 64] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float f = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), s + k));
+      o = fmaf(f, x[k], o);
+      o2 = fmaf(f, y[k], o2);
+    }
+  }
+  const int64_t bh = row / a.q_len, i = row - bh * a.q_len;
+  T* to = (T*)a.o + bh / a.heads * a.os[0] + bh % a.heads * a.os[1] + i * a.os[2] + lane;
+  if (one) to[0] = (T)(sum == 0.f ? 0.f : o / sum);
+  if (two) to[64] = (T)(sum == 0.f ? 0.f : o2 / sum);
+  if (a.lse && lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : ms + logf(sum);
+}
+
 template <class T, int DP, bool VEC>
 int attn_forward_dim(const AttnArgs& a, void* stream) {
   if (attn_token_kernel(a)) {
@@ -478,6 +518,9 @@ int attn_forward_t(const AttnArgs& a, void* stream) {
                      : go(attn_forward_dim<T, 64, false>, attn_forward_dim<T, 96, false>,
                           attn_forward_dim<T, 128, false>);
   if (st != FM_OK || a.splits == 1) return st;
+  if (a.splits <= kAttnFewRanges)
+    return launch("attention (join)", attn_join_rows_kernel<T>, dim3((unsigned)((attn_rows(a) + 3) / 4)),
+                  dim3(kAttnThreads), 0, stream, a);
   return launch("attention (join)", attn_join_kernel<T>, dim3((unsigned)attn_rows(a)), dim3(kAttnThreads),
                 0, stream, a);
 }

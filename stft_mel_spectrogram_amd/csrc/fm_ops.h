@@ -213,6 +213,8 @@ struct AttnArgs {
   float* amax;        // [batch, heads, q_len], float16 only
   float* table_part;  // [batch * heads * query blocks, distances of the window]
   float* table_dist;  // [heads, distances of the window]
+  float* part_dkv;    // [dkv_splits, batch, kv_heads, k_len, 2, dim]
+  int dkv_splits;
   // forward over key ranges
   float* part_o;    // [splits, batch, heads, q_len, dim]
   float* part_lse;  // [splits, batch, heads, q_len]
@@ -270,8 +272,25 @@ inline int64_t attn_forward_workspace(const AttnArgs& a) {
 // Distances of the bias window: +-(far + 63), see fm_attn.h.
 constexpr int kBiasPad = 63;
 constexpr int bias_window(int far) { return 2 * (far + kBiasPad) + 1; }
+constexpr int kAttnBlockKeys = 128;  // keys of a dk, dv workgroup
+// Shares of the queries (of all heads of a group, in order) that workgroups of the
+// dk, dv kernel take of a key block, while the blocks alone leave compute units
+// idle; a second launch adds them up.  Shares of at least 4 tiles of 64 queries,
+// 16 where there are blocks for a quarter of the units, since the sums are as much
+// traffic per block then as they save (whole backward, us: 2 x 4 heads on 1, 1777
+// queries, 28 blocks, 18 shares 109, unshared 268; 5 x 16 on 4, 202, f32, 40 blocks,
+// 4 shares 66 and 131; 3 x 8 on 4, 1098, 128 columns, 108 blocks, 2 shares 130 and
+// 165; 2 x 8 on 8, 1000, 128 blocks, unshared 68, 4 shares 74).
+inline int attn_dkv_splits(const AttnArgs& a) {
+  const int64_t wgs = (int64_t)a.batch * a.kv_heads * ((a.k_len + kAttnBlockKeys - 1) / kAttnBlockKeys);
+  if (wgs == 0 || wgs > 256) return 1;
+  const int64_t tiles = (int64_t)(a.heads / a.kv_heads) * ((a.q_len + 63) / 64);
+  const int64_t fill = 512 / wgs, most = tiles / (wgs <= 64 ? 4 : 16);
+  const int64_t s = fill < most ? fill : most;
+  return s < 1 ? 1 : (int)s;
+}
 struct AttnBackwardSpace {
-  int64_t amax, part, dist, total;  // byte offsets; delta at 0
+  int64_t amax, part, dist, dkv, total;  // byte offsets; delta at 0
 };
 inline AttnBackwardSpace attn_backward_space(const AttnArgs& a, bool f16) {
   const int64_t rows = attn_round16(4 * attn_rows(a));
@@ -279,7 +298,9 @@ inline AttnBackwardSpace attn_backward_space(const AttnArgs& a, bool f16) {
   s.amax = rows;
   s.part = rows * (f16 ? 2 : 1);
   s.dist = s.part + attn_round16(4 * (int64_t)a.batch * a.heads * attn_query_blocks(a) * bias_window(a.far));
-  s.total = s.dist + attn_round16(4 * (int64_t)a.heads * bias_window(a.far));
+  s.dkv = s.dist + attn_round16(4 * (int64_t)a.heads * bias_window(a.far));
+  const int splits = attn_dkv_splits(a);
+  s.total = s.dkv + (splits == 1 ? 0 : 8 * (int64_t)splits * a.batch * a.kv_heads * a.k_len * a.dim);
   return s;
 }
 
