@@ -199,11 +199,12 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
   }
 }
 
-// Few query rows per key head (rows = heads of the group x queries, at most
-// 16): one 16-column fragment holds them all; the waves take 32 keys each in
-// turn, straight from memory, and join at the end.  Memory bound: keys are the
-// left operand as they lie in memory, values pass through a wave's own LDS
-// tile to be read by columns.
+// Few queries: the rows of a key head (heads of the group x queries) go into
+// 16-column fragments, one per workgroup; its waves take 32 keys each in turn,
+// straight from memory, and join at the end.  Memory bound: keys are the left
+// operand as they lie in memory, values pass through a wave's own LDS tile to be
+// read by columns.  The fragments of a key range follow each other on one XCD, so
+// that the second one finds the keys in its L2.
 constexpr int kTokenKeys = 32;
 // The group's bias windows are kept in LDS where they take at most this much;
 // larger ones are looked up in memory by the few tiles that need them.
@@ -228,14 +229,21 @@ __global__ __launch_bounds__((attn_token_waves(sizeof(T), DP) * 64)) void attn_t
   const int tid = threadIdx.x, wave = wave_index(), lane = tid & 63, n = lane & 15, g = lane >> 4;
   Lds<T>* vt = (Lds<T>*)smem + wave * Tile<T, DP>::size(kTokenKeys);
   const int group = a.heads / a.kv_heads, rows = group * a.q_len;
-  const int b = blockIdx.x / a.kv_heads, kvh = blockIdx.x % a.kv_heads;
-  const int head = kvh * group + n / a.q_len, i = n % a.q_len;
-  const bool real = n < rows;
+  const int units = a.batch * a.kv_heads;
+  const Place at = place_of(units * a.splits, (rows + 15) / 16, blockIdx.x);
+  if (at.none) return;
+  const int range = at.unit / units, unit = at.unit - range * units;
+  const int b = unit / a.kv_heads, kvh = unit - b * a.kv_heads;
+  // this lane's column: a head of the group and a query
+  const int row0 = 16 * at.block, mine_at = row0 + n;
+  const bool real = mine_at < rows;
+  const int member = real ? mine_at / a.q_len : 0, i = real ? mine_at - member * a.q_len : 0;
+  const int head = kvh * group + member;
   const int len = key_count(a, b), first = position_of_first(a, b);
   int k_beg = 0, k_end = a.causal ? clamp_int(first + a.q_len, 0, len) : len;
   if constexpr (SPLIT) {
     const int per = ((k_end + a.splits - 1) / a.splits + kTokenKeys - 1) / kTokenKeys * kTokenKeys;
-    k_beg = min((int)blockIdx.y * per, k_end);
+    k_beg = min(range * per, k_end);
     k_end = min(k_beg + per, k_end);
   }
   const T* kp = (const T*)a.k + b * a.ks[0] + kvh * a.ks[1];
@@ -256,7 +264,7 @@ __global__ __launch_bounds__((attn_token_waves(sizeof(T), DP) * 64)) void attn_t
   int j0 = k_beg + wave * kTokenKeys;
   if (j0 < k_end) fetch(j0);
   Frag<T> qf[KS];
-  const T* qp = (const T*)a.q + b * a.qs[0] + (real ? head : 0) * a.qs[1] + i * a.qs[2];
+  const T* qp = (const T*)a.q + b * a.qs[0] + head * a.qs[1] + i * a.qs[2];
 #pragma unroll
   for (int s = 0; s < KS; ++s) qf[s] = to_frag(load_raw(qp + 32 * s + 8 * g, real ? a.dim - 32 * s - 8 * g : 0));
   // the bias in units of the product: [group][2 far + 1]
@@ -272,7 +280,7 @@ __global__ __launch_bounds__((attn_token_waves(sizeof(T), DP) * 64)) void attn_t
     __syncthreads();
   }
   const auto bias_at = [&](int d) {
-    return table ? bias[n / a.q_len * dists + clamp_int(d + a.far, 0, dists - 1)]
+    return table ? bias[member * dists + clamp_int(d + a.far, 0, dists - 1)]
                  : bias_of<T>(a, head, d) * inv_scale;
   };
   const float lo = real ? bias_at(-a.far) : 0.f, hi = real ? bias_at(a.far) : 0.f;
@@ -306,7 +314,7 @@ __global__ __launch_bounds__((attn_token_waves(sizeof(T), DP) * 64)) void attn_t
     }
     const int j = j0;
     if (j0 + NW * kTokenKeys < k_end) fetch(j0 + NW * kTokenKeys);
-    if (j + kTokenKeys > least || rows < 16) {
+    if (j + kTokenKeys > least || rows < row0 + 16) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -361,7 +369,7 @@ __global__ __launch_bounds__((attn_token_waves(sizeof(T), DP) * 64)) void attn_t
     jw[DP + 1] = l;
   }
   __syncthreads();
-  for (int t = tid; t < rows * DP; t += NT) {
+  for (int t = tid; t < min(rows - row0, 16) * DP; t += NT) {
     const int r = t / DP, d = t - r * DP;
     if (d >= a.dim) continue;
     float mm = -INFINITY;
@@ -378,12 +386,12 @@ __global__ __launch_bounds__((attn_token_waves(sizeof(T), DP) * 64)) void attn_t
     }
     const float out = sum == 0.f ? 0.f : val / sum;
     const float lse = sum != sum ? sum : mm == -INFINITY ? -INFINITY : fmaf(mm, a.scale, logf(sum));
-    const int hd = kvh * group + r / a.q_len, qi = r % a.q_len;
+    const int hd = kvh * group + (row0 + r) / a.q_len, qi = (row0 + r) % a.q_len;
     const int64_t row = (int64_t)(b * a.heads + hd) * a.q_len + qi;
     if constexpr (SPLIT) {
       const int64_t all = (int64_t)a.batch * a.heads * a.q_len;
-      a.part_o[(blockIdx.y * all + row) * a.dim + d] = out;
-      if (d == 0) a.part_lse[blockIdx.y * all + row] = lse;
+      a.part_o[(range * all + row) * a.dim + d] = out;
+      if (d == 0) a.part_lse[range * all + row] = lse;
     } else {
       const int64_t off = b * a.os[0] + hd * a.os[1] + qi * a.os[2] + d;
       ((T*)a.o)[off] = (T)out;
@@ -487,10 +495,11 @@ int attn_forward_dim(const AttnArgs& a, void* stream) {
         lds_opt_in(attn_token_kernel<T, DP, false, VEC>, attn_token_lds<T, DP>(kTokenBias)) |
         lds_opt_in(attn_token_kernel<T, DP, true, VEC>, attn_token_lds<T, DP>(kTokenBias));
     if (opted != FM_OK) return set_error(FM_E_HIP, "attention: LDS size refused");
-    return launch("attention of single tokens",
+    return launch("attention of few queries",
                   a.splits > 1 ? attn_token_kernel<T, DP, true, VEC>
                                : attn_token_kernel<T, DP, false, VEC>,
-                  dim3((unsigned)(a.batch * a.kv_heads), (unsigned)a.splits), dim3(64 * attn_token_waves(sizeof(T), DP)),
+                  dim3(place_grid((int64_t)a.batch * a.kv_heads * a.splits, attn_token_blocks(a))),
+                  dim3(64 * attn_token_waves(sizeof(T), DP)),
                   attn_token_lds<T, DP>(attn_token_bias(a)), stream, a);
   }
   static const int opted =

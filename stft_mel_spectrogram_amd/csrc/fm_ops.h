@@ -226,23 +226,25 @@ constexpr int kAttnMaxFar = 1024;
 constexpr int kAttnMaxBuckets = 1024;
 constexpr int kAttnMaxSplits = 512; // key ranges of a forward call
 constexpr int kAttnQueries = 128;   // queries of a workgroup
-constexpr int kAttnTokenRows = 16;  // query rows of the single-token kernel
 
-// Query rows that share a key head: as many as one 16-column fragment holds take
-// the single-token kernel, whose waves divide the keys instead of the queries
-// (8 x 16 heads against 1501 keys, bf16, us: 1 row 12.2, the other kernel 18.9;
-// 16 rows 13.8 and 20.0).
-inline bool attn_token_kernel(const AttnArgs& a) {
-  return (int64_t)a.q_len * (a.heads / a.kv_heads) <= kAttnTokenRows;
+// Few queries against a cache take a kernel of their own, whose waves divide the
+// keys instead of the queries (bf16 at 64 columns, us: 8 x 16 heads, 1501 keys, 1
+// query 13, the other kernel 19; 32 queries 14.3 and 18.3, 48 queries 25.9 and
+// 20.3; 6 x 4 heads on 1, 7 queries, 68001 keys 30 and 102).  Short rows do not
+// make up for its join of the waves (8 x 16, 32 queries, 128 keys: 9.6 and 6.0; 300
+// keys, 1 query: 7.1 and 8.7).
+inline bool attn_token_kernel(const AttnArgs& a) { return a.q_len <= 32 && a.k_len > 256; }
+inline int64_t attn_token_blocks(const AttnArgs& a) {
+  return ((int64_t)a.q_len * (a.heads / a.kv_heads) + 15) / 16;
 }
-// Waves of a single-token workgroup: as many as its registers and LDS let one
-// compute unit hold, since they join without a second launch.
+// Waves of its workgroups: as many as its registers and LDS let one compute unit
+// hold, since they join without a second launch.
 constexpr int attn_token_waves(int size, int dp) {
   return size == 2 ? (dp == 64 ? 16 : 8) : (dp == 64 ? 8 : 4);
 }
 // Key ranges a forward call is cut into while its workgroups alone do not fill
 // the chip (256 compute units), us in bf16 at 64 columns, a call's GPU time:
-// Single tokens: one of their large workgroups per unit (2 x 8 key heads, 20000
+// Few queries: one of their large workgroups per unit (2 x 8 key heads, 20000
 // keys: 20.8, with two 23.8), of 512 keys, one round of 16 waves (1 x 8, 8000: 12.3;
 // ranges of 2048 keys 17.2, none 39.4).  Where the workgroups reach a third of the
 // units they draw the whole memory rate without a join (8 x 16, 8000: 40.3, two
@@ -254,7 +256,7 @@ constexpr int attn_token_waves(int size, int dp) {
 // queries, 600 keys: 15.3, with ranges 17.7; 1 x 16, 400, 1000: 21.9 and 21.3).
 inline int attn_splits(const AttnArgs& a) {
   const bool token = attn_token_kernel(a);
-  const int64_t wgs = token ? (int64_t)a.batch * a.kv_heads
+  const int64_t wgs = token ? (int64_t)a.batch * a.kv_heads * attn_token_blocks(a)
                             : (int64_t)a.batch * a.heads * ((a.q_len + kAttnQueries - 1) / kAttnQueries);
   if (wgs == 0 || wgs > (token ? 85 : 256) || a.k_len < (token ? 2048 : 1024)) return 1;
   const int64_t fill = (token ? 256 : 512) / wgs, most = a.k_len / (token ? 512 : 256);
