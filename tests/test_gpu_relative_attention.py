@@ -383,3 +383,43 @@ def test_relative_buckets():
     from stft_mel_spectrogram_amd import relative_buckets
     b = relative_buckets(32, 128)
     assert b.dtype == torch.int32 and b.is_cuda and b.numel() == 257
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("h,hk,tq,tk,d", [
+    (4, 1, 7, 2500, 40),   # 28 rows of a key head, key ranges
+    (2, 2, 32, 300, 64),   # the most queries, no ranges
+    (6, 2, 11, 257, 128),  # the fewest keys, three fragments with a short last one
+    (3, 3, 17, 2048, 33),  # odd rows
+    (8, 1, 1, 2100, 96),
+])
+def test_few_queries_against_a_cache(h, hk, tq, tk, d, dtype):
+    q, k, v, table, m, do = make(2, h, hk, tq, tk, d, dtype, seed=tk + d, layout="bhtd", far=40)
+    lengths = torch.tensor([tk, tk // 3], device="cuda", dtype=torch.int32)
+    offset = torch.tensor([tk - tq, tk // 3 - tq], device="cuda", dtype=torch.int32)
+    run_case(q, k, v, table, m, do, causal=True, lengths=lengths, offset=offset, backward=False)
+    run_case(q, k, v, table, m, do, lengths=lengths, offset=offset, backward=False)
+    # an entry without keys, one whose queries lie before every key
+    lengths[1], offset[0] = 0, -tq
+    run_case(q, k, v, table, m, do, causal=True, lengths=lengths, offset=offset, backward=False)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("h,hk,t,d", [(4, 1, 300, 40), (6, 2, 517, 64), (8, 1, 140, 128), (2, 2, 530, 33)])
+def test_shares_of_queries(h, hk, t, d, dtype):
+    """Few key blocks: dk and dv from several workgroups each."""
+    q, k, v, table, m, do = make(2, h, hk, t, t, d, dtype, seed=t)
+    lengths = torch.tensor([t, t // 2 + 3], device="cuda", dtype=torch.int32)
+    for causal in (False, True):
+        run_case(q, k, v, table, m, do, causal=causal, lengths=lengths)
+    lengths[0] = 0
+    run_case(q, k, v, table, m, do, lengths=lengths)
+
+
+@pytest.mark.parametrize("tk", [1024, 1500, 5000])
+def test_ranges_of_many_queries(tk):
+    q, k, v, table, m, do = make(2, 2, 2, 150, tk, 72, "bf16", seed=tk)
+    lengths = torch.tensor([tk, 3], device="cuda", dtype=torch.int32)
+    run_case(q, k, v, table, m, do, lengths=lengths, backward=False)
+    lengths[1] = 0
+    run_case(q, k, v, table, m, do, causal=True, lengths=lengths, offset=tk - 150, backward=False)

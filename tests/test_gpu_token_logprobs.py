@@ -287,3 +287,25 @@ def test_another_stream_and_graph_replays():
         torch.cuda.synchronize()
         for a, e in zip((*gr, gdx), (*er, edx)):
             assert torch.equal(a, e)
+
+
+@pytest.mark.parametrize("rows,vocab,top", [(300, 70001, 20), (260, 40000, 3), (9, 2048, 64), (40, 1025, 17)])
+def test_top_of_many_rows(rows, vocab, top):
+    """Segments of several chunks, lists of every length."""
+    x, tok = inputs(rows, vocab, torch.float16, rows)
+    run_case(x, tok, top)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab", [200, 9000, 70000])
+def test_top_of_ordered_and_tied_rows(vocab, dtype):
+    """Rising rows replace every entry kept, falling rows none; ties are cut at
+    the last place by the index."""
+    up = torch.linspace(-4, 4, vocab, device="cuda").to(DT[dtype])
+    steps = (torch.arange(vocab, device="cuda") // 37 % 5).to(DT[dtype])
+    few = torch.full((vocab,), -math.inf, device="cuda", dtype=DT[dtype])
+    few[[3, vocab // 2, vocab - 1]] = 1.0
+    x = torch.stack([up, up.flip(0), steps, few])
+    tok = torch.tensor([0, 5, 7, 3], device="cuda")
+    for top in (1, 20, 64):
+        run_case(x, tok, top)
