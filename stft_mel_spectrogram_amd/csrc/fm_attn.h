@@ -370,11 +370,16 @@ __device__ __forceinline__ int position_of_first(const AttnArgs& a, int b) {
   return clamp_int(o, -(1 << 30), 1 << 30);
 }
 
-// A 32x32 tile's place against the window, dist = first key - first query's
-// position: all of it at or beyond -far or far (one bias for every pair), or
-// not (the window's values start the accumulators).
-__device__ __forceinline__ bool tile_before(int dist, int far) { return dist + 31 <= -far; }
-__device__ __forceinline__ bool tile_behind(int dist, int far) { return dist - 31 >= far; }
+// The distances up to `left` share the first bucket of the map and those from
+// `right` on its last (the ends may be wide buckets: 32 of them up to distance
+// 128 leave 91 to 128 to the last).  A 32x32 tile, dist = first key - first
+// query's position, that lies in one of them has one bias for every pair; in the
+// others the window's values start the accumulators.
+struct Reach {
+  int left, right;
+};
+__device__ __forceinline__ bool tile_before(int dist, Reach r) { return dist + 31 <= r.left; }
+__device__ __forceinline__ bool tile_behind(int dist, Reach r) { return dist - 31 >= r.right; }
 // Rows keys, columns queries: rows 8 (r / 4) + 4 h + r % 4, column n have
 // distance dist + row - n.
 __device__ __forceinline__ acc16 bias_start_keys(const float* bias, int far, int dist, int h, int n) {
@@ -413,25 +418,43 @@ __device__ __forceinline__ acc16 acc_zero() {
 }
 
 // Fills the window; a thread's map entries are on their way together, and then
-// its table entries.
-template <class T>
-__device__ __forceinline__ void fill_bias(const AttnArgs& a, int head, float* bias, int tid, int nt) {
+// its table entries.  `ends` gets each wave's part of the map's reach (2 values).
+template <class T, bool REACH = true>
+__device__ __forceinline__ void fill_bias(const AttnArgs& a, int head, float* bias, float* ends, int tid, int nt) {
   const float inv = 1.f / a.scale;
-  const int win = bias_window(a.far);
+  const int win = bias_window(a.far), first = a.map[0], last = a.map[2 * a.far];
+  float below = -0x1p29f, above = -0x1p29f;  // the farthest distances of other buckets, below negated
   for (int i0 = tid; i0 < win; i0 += 4 * nt) {
     int b[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int i = i0 + k * nt;
-      b[k] = i < win ? a.map[clamp_int(i - kBiasPad, 0, 2 * a.far)] : -1;
-    }
+    for (int k = 0; k < 4; ++k) b[k] = a.map[clamp_int(min(i0 + k * nt, win - 1) - kBiasPad, 0, 2 * a.far)];
     float v[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = bias_of_bucket<T>(a, head, b[k]);
+    for (int k = 0; k < 4; ++k) {
+      const float d = (float)(min(i0 + k * nt, win - 1) - a.far - kBiasPad);
+      v[k] = bias_of_bucket<T>(a, head, b[k]);
+      if constexpr (REACH) {
+        below = fmaxf(below, b[k] != first ? -d : below);
+        above = fmaxf(above, b[k] != last ? d : above);
+      }
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (i0 + k * nt < win) bias[i0 + k * nt] = v[k] * inv;
   }
+  if constexpr (!REACH) return;
+  below = lanes_max<64>(below);
+  above = lanes_max<64>(above);
+  if ((tid & 63) == 0) {
+    ends[2 * (tid >> 6)] = below;
+    ends[2 * (tid >> 6) + 1] = above;
+  }
+}
+// From the four waves' parts, after a barrier.
+__device__ __forceinline__ Reach reach_of(const float* ends) {
+  const float below = fmaxf(fmaxf(ends[0], ends[2]), fmaxf(ends[4], ends[6]));
+  const float above = fmaxf(fmaxf(ends[1], ends[3]), fmaxf(ends[5], ends[7]));
+  return {__builtin_amdgcn_readfirstlane(-(int)below - 1), __builtin_amdgcn_readfirstlane((int)above + 1)};
 }
 
 // Which unit (entry, key head) and which of its blocks a workgroup takes.

@@ -154,7 +154,7 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
     if (kIsF16<T> && h == 0) a.amax[row] = amax;
   }
   const float unit = kIsF16<T> ? unit_scale(amax) : 1.f;
-  fill_bias<T>(a, head, bias, tid, kAttnThreads);
+  fill_bias<T>(a, head, bias, ends, tid, kAttnThreads);
   if constexpr (TABLE) {
     for (int t = tid; t < 4 * win; t += kAttnThreads) sums[t] = 0.f;
     for (int t = tid; t < 4 * kDiagScratch; t += kAttnThreads) diag[t] = 0.f;
@@ -165,6 +165,7 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
 
   const float c = a.scale * kLog2e;
   const float lo = as_scalar(bias[0] * c), hi = as_scalar(bias[win - 1] * c);
+  const Reach reach = reach_of(ends);
   const int mine = a.causal ? min(len, first + i + 1) : len;
   const int least = a.causal ? min(len, first + q0 + 1) : len;
   const int wave_end = a.causal ? min(k_end, first + q0 + 32) : k_end;
@@ -174,14 +175,14 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
     // themselves.  Their few probabilities are large, and so would be the error
     // that the rounding of o leaves in delta.
     const int dist = -first - q0;
-    const bool far = tile_before(dist, a.far) || tile_behind(dist, a.far);
+    const bool is_before = tile_before(dist, reach), far = is_before || tile_behind(dist, reach);
     acc16 s = far ? acc_zero() : bias_start_keys(bias, a.far, dist, h, n), dp = acc_zero();
 #pragma unroll
     for (int x = 0; x < KS; ++x) {
       s = mma32(tile_rows<T, DP>(kt, n, x, h), qf[x], s);
       dp = mma32(tile_rows<T, DP>(vt, n, x, h), gf[x], dp);
     }
-    const float t = (far ? (dist < 0 ? lo : hi) : 0.f) - lse2;
+    const float t = (far ? (is_before ? lo : hi) : 0.f) - lse2;
     float sum = 0.f;
 #pragma unroll
     for (int r = 0; r < 16; ++r)
@@ -215,13 +216,13 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
 #pragma unroll
       for (int u = 0; u < NS; ++u) {
         const int dist = j0 + 32 * u - first - q0;
-        const bool is_before = tile_before(dist, a.far), is_behind = tile_behind(dist, a.far);
+        const bool is_before = tile_before(dist, reach), is_behind = tile_behind(dist, reach);
         const Frag<T> k0 = tile_rows<T, DP>(ktb, 32 * u + n, 0, h);
         acc16 s;
         float far_bias;
         if (is_before || is_behind) {
           s = mma32(k0, qf[0], acc_zero());
-          far_bias = dist < 0 ? lo : hi;
+          far_bias = is_before ? lo : hi;
         } else {
           s = mma32(k0, qf[0], bias_start_keys(bias, a.far, dist, h, n));
           far_bias = 0.f;
@@ -323,7 +324,7 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
       ends[2 * wave + 1] = right;
     }
     __syncthreads();
-    // the window's first and last distances lie beyond +-far like the far tiles
+    // the window's first and last distances have the buckets of the far tiles
     float* out = a.table_part + ((int64_t)(b * a.heads + head) * blocks + qb) * win;
     for (int t = tid; t < win; t += kAttnThreads) {
       float v = 0.f;
@@ -404,8 +405,8 @@ __global__ __launch_bounds__(1024) void attn_table_buckets_kernel(const AttnArgs
 
 template <class T, int DP>
 constexpr size_t attn_dkv_lds(int far) {
-  return 4 * Tile<T, DP>::size(attn_step<T>()) * sizeof(Lds<T>) + 4 * attn_step<T>() * sizeof(float) +
-         bias_window(far) * sizeof(float);
+  return 4 * Tile<T, DP>::size(attn_step<T>()) * sizeof(Lds<T>) +
+         (4 * attn_step<T>() + 8 + bias_window(far)) * sizeof(float);
 }
 
 template <class T, int DP, bool VEC>
@@ -417,6 +418,8 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
   constexpr bool AHEAD = VEC && !(sizeof(T) == 4 && DP == 128);
   // float32's three-part fragments leave none for operands read ahead
   constexpr bool STAGED = sizeof(T) == 2;
+  // nor for the map's reach, which is +-far at least
+  constexpr bool REACH = sizeof(T) == 2;
   Lds<T>* qt = (Lds<T>*)smem;
   Lds<T>* gt = qt + 2 * TS;
   // -lse in units of the product and -delta start the accumulators: exp2 of the
@@ -426,7 +429,8 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
   constexpr bool LSE_LATE = sizeof(T) == 4;
   float* neg_lse = (float*)(gt + 2 * TS);  // [2][BQ]
   float* neg_delta = neg_lse + 2 * BQ;     // [2][BQ]
-  float* bias = neg_delta + 2 * BQ;
+  float* ends = neg_delta + 2 * BQ;  // [4][2]
+  float* bias = ends + 8;
 
   const int tid = threadIdx.x, wave = wave_index(), lane = tid & 63, n = lane & 31, h = lane >> 5;
   const int blocks = (a.k_len + kAttnBlockKeys - 1) / kAttnBlockKeys;
@@ -508,10 +512,11 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
       }
     };
     fetch(i_first);
-    fill_bias<T>(a, head, bias, tid, kAttnThreads);
+    fill_bias<T, REACH>(a, head, bias, ends, tid, kAttnThreads);
     put(0);
     __syncthreads();
     const float lo = as_scalar(bias[0] * c), hi = as_scalar(bias[bias_window(a.far) - 1] * c);
+    const Reach reach = REACH ? reach_of(ends) : Reach{-a.far, a.far};
     int buf = 0;
     for (int i0 = i_first; i0 < i_last; i0 += BQ, buf ^= 1) {
       const bool more = i0 + BQ < i_last;
@@ -525,8 +530,9 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
         for (int u = 0; u < NS; ++u) {
           const int dist = jw - first - i0 - 32 * u;
           s[u] = LSE_LATE ? acc_zero() : acc_rows(neg_lse + buf * BQ + 32 * u, h);
-          if (tile_before(dist, a.far) || tile_behind(dist, a.far)) {
-            far_bias[u] = dist < 0 ? lo : hi;
+          const bool is_before = tile_before(dist, reach);
+          if (is_before || tile_behind(dist, reach)) {
+            far_bias[u] = is_before ? lo : hi;
           } else {
             s[u] += bias_start_queries(bias, a.far, dist, h, n);
             far_bias[u] = 0.f;

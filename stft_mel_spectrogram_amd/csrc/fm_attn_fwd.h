@@ -14,7 +14,7 @@ constexpr int kAttnKeys = 32;
 
 template <class T, int DP>
 constexpr size_t attn_forward_lds(int far) {
-  return 4 * Tile<T, DP>::size(kAttnKeys) * sizeof(Lds<T>) + bias_window(far) * sizeof(float);
+  return 4 * Tile<T, DP>::size(kAttnKeys) * sizeof(Lds<T>) + (bias_window(far) + 8) * sizeof(float);
 }
 
 // The transposed scores s' = K q' have queries as columns, so that a lane
@@ -26,7 +26,8 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
   extern __shared__ __attribute__((aligned(16))) char smem[];
   Lds<T>* kt = (Lds<T>*)smem;  // [2][TS]
   Lds<T>* vt = kt + 2 * TS;    // [2][TS]
-  float* bias = (float*)(vt + 2 * TS);
+  float* ends = (float*)(vt + 2 * TS);  // [4][2]
+  float* bias = ends + 8;
 
   const int tid = threadIdx.x, wave = wave_index(), lane = tid & 63, n = lane & 31, h = lane >> 5;
   const int blocks = (a.q_len + kAttnQueries - 1) / kAttnQueries;
@@ -60,12 +61,13 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
                            a.q_len - qw, a.dim};
 #pragma unroll
   for (int s = 0; s < KS; ++s) qf[s] = to_frag(qr.at(i - qw, 16 * s + 8 * h));
-  fill_bias<T>(a, head, bias, tid, kAttnThreads);
+  fill_bias<T>(a, head, bias, ends, tid, kAttnThreads);
   const float c = a.scale * kLog2e;
   kl.store(kt, tid);
   vl.store(vt, tid);
   __syncthreads();
   const float lo = as_scalar(bias[0] * c), hi = as_scalar(bias[bias_window(a.far) - 1] * c);
+  const Reach reach = reach_of(ends);
 
   acc16 o[DT];
 #pragma unroll
@@ -95,9 +97,10 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
       for (int u = 0; u < NS; ++u) {
         const int dist = j0 + 32 * u - first - q0;
         const Frag<T> k0 = tile_rows<T, DP>(ktb, 32 * u + n, 0, h);
-        if (tile_before(dist, a.far) || tile_behind(dist, a.far)) {
+        const bool is_before = tile_before(dist, reach);
+        if (is_before || tile_behind(dist, reach)) {
           s[u] = mma32(k0, qf[0], acc_zero());
-          far_bias[u] = dist < 0 ? lo : hi;
+          far_bias[u] = is_before ? lo : hi;
         } else {
           s[u] = mma32(k0, qf[0], bias_start_keys(bias, a.far, dist, h, n));
           far_bias[u] = 0.f;
