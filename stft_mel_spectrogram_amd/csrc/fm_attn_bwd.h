@@ -352,6 +352,7 @@ __global__ __launch_bounds__(1024) void attn_table_distances_kernel(const AttnAr
   const int t = blockIdx.x * 64 + lane;
   float s = 0.f;
   if (t < win)
+#pragma unroll 4
     for (int p = set; p < a.batch * blocks; p += 16) {
       const int b = p / blocks, qb = p - b * blocks;
       s += a.table_part[((int64_t)(b * a.heads + head) * blocks + qb) * win + t];
@@ -374,13 +375,13 @@ __global__ __launch_bounds__(1024) void attn_table_distances_kernel(const AttnAr
 constexpr int kTableRows = 16;
 template <class W>
 __global__ __launch_bounds__(1024) void attn_table_buckets_kernel(const AttnArgs a) {
-  __shared__ float dist[bias_window(kAttnMaxFar)];
-  __shared__ int bucket[bias_window(kAttnMaxFar)];
+  constexpr int AHEAD = 8;  // LDS reads on their way at a time
+  __shared__ float2 dist[bias_window(kAttnMaxFar) + AHEAD];  // sum, bucket
   __shared__ float red[1024];
   const int win = bias_window(a.far), head = blockIdx.x, tid = threadIdx.x;
   const int blocks = (a.q_len + kAttnQueries - 1) / kAttnQueries, rows = a.batch * blocks;
   for (int t = tid; t < win; t += 1024) {
-    bucket[t] = a.map[clamp_int(t - kBiasPad, 0, 2 * a.far)];
+    const int bucket = a.map[clamp_int(t - kBiasPad, 0, 2 * a.far)];
     float s = 0.f;
     if (rows > kTableRows) {
       s = a.table_dist[(int64_t)head * win + t];
@@ -391,18 +392,26 @@ __global__ __launch_bounds__(1024) void attn_table_buckets_kernel(const AttnArgs
         s += a.table_part[((int64_t)(b * a.heads + head) * blocks + qb) * win + t];
       }
     }
-    dist[t] = s;
+    dist[t] = make_float2(s, __int_as_float(bucket));
   }
   __syncthreads();
   const int shares = 1024 / a.num_buckets, k = tid % a.num_buckets, share = tid / a.num_buckets;
   const int per = (win + shares - 1) / shares;
   float s = 0.f;
   if (share < shares)
-    for (int t = share * per; t < min((share + 1) * per, win); ++t) s += bucket[t] == k ? dist[t] : 0.f;
+    for (int t = share * per; t < min((share + 1) * per, win); t += AHEAD) {
+      float2 x[AHEAD];
+#pragma unroll
+      for (int e = 0; e < AHEAD; ++e) x[e] = dist[t + e];
+#pragma unroll
+      for (int e = 0; e < AHEAD; ++e)
+        s += t + e < min((share + 1) * per, win) && __float_as_int(x[e].y) == k ? x[e].x : 0.f;
+    }
   red[tid] = s;
   __syncthreads();
   if (tid < a.num_buckets) {
     float v = 0.f;
+#pragma unroll 8
     for (int x = 0; x < shares; ++x) v += red[x * a.num_buckets + tid];
     ((W*)a.d_table)[(int64_t)tid * a.heads + head] = (W)v;
   }
