@@ -96,6 +96,7 @@ int attention_args(const fm_attention_args* p, bool backward, AttnArgs& a) {
   a.q_len = static_cast<int>(p->q_len);
   a.k_len = static_cast<int>(p->k_len);
   a.dim = static_cast<int>(p->head_dim);
+  a.size = elem_size(p->dtype);
   a.scale = static_cast<float>(p->scale);
   for (int i = 0; i < 3; ++i) {
     a.qs[i] = p->q_stride[i];

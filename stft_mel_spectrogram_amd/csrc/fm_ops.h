@@ -198,6 +198,7 @@ struct AttnArgs {
   int query_offset_value;
   int far, num_buckets, table32, causal;
   int batch, heads, kv_heads, q_len, k_len, dim;
+  int size;  // bytes of an element
   float scale;
   int64_t qs[3], ks[3], vs[3], os[3];
   void* o;
@@ -282,12 +283,19 @@ constexpr int kAttnBlockKeys = 128;  // keys of a dk, dv workgroup
 // traffic per block then as they save (whole backward, us: 2 x 4 heads on 1, 1777
 // queries, 28 blocks, 18 shares 109, unshared 268; 5 x 16 on 4, 202, f32, 40 blocks,
 // 4 shares 66 and 131; 3 x 8 on 4, 1098, 128 columns, 108 blocks, 2 shares 130 and
-// 165; 2 x 8 on 8, 1000, 128 blocks, unshared 68, 4 shares 74).
+// 165; 2 x 8 on 8, 1000, 128 blocks, unshared 68, 4 shares 74).  float32, whose
+// tiles of 32 queries take as long as two of those and whose workgroups have a
+// compute unit to themselves: single tiles below 48 blocks (1 x 8, 101 queries, 96
+// columns: 4 shares 46, unshared 55; 1 x 8, 500: 8 shares 77, 2 shares 87, 16 shares
+// 89), else 8 (8 x 8, 101, 64 blocks: unshared 44, 4 shares 46).
 inline int attn_dkv_splits(const AttnArgs& a) {
   const int64_t wgs = (int64_t)a.batch * a.kv_heads * ((a.k_len + kAttnBlockKeys - 1) / kAttnBlockKeys);
   if (wgs == 0 || wgs > 256) return 1;
-  const int64_t tiles = (int64_t)(a.heads / a.kv_heads) * ((a.q_len + 63) / 64);
-  const int64_t fill = 512 / wgs, most = tiles / (wgs <= 64 ? 4 : 16);
+  const bool f32 = a.size == 4;
+  const int rows = f32 ? 32 : 64;
+  const int64_t tiles = (int64_t)(a.heads / a.kv_heads) * ((a.q_len + rows - 1) / rows);
+  const int64_t least = f32 ? (wgs <= 48 ? 1 : 8) : wgs <= 64 ? 4 : 16;
+  const int64_t fill = (f32 ? 256 : 512) / wgs, most = tiles / least;
   const int64_t s = fill < most ? fill : most;
   return s < 1 ? 1 : (int)s;
 }
