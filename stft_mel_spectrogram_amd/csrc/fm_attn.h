@@ -481,6 +481,10 @@ inline unsigned place_grid(int64_t units, int64_t blocks) {
   return (unsigned)(place_by_xcd(units) ? (units + 7) / 8 * 8 * blocks : units * blocks);
 }
 
+__device__ __forceinline__ int64_t attn_row_count(const AttnArgs& a) {
+  return (int64_t)a.batch * a.heads * a.q_len;
+}
+
 // The wave of a thread as a scalar: what depends on it alone then branches
 // without touching the lane mask.
 __device__ __forceinline__ int wave_index() {

@@ -52,9 +52,11 @@ inline constexpr float kProbShift<f16_t> = 8.f;
 constexpr int kDiagRow = 68;  // 32 keys, 36 zeros (at least 31 on either side)
 constexpr int kDiagScratch = 32 + 16 * kDiagRow;
 
-// float16's scale takes the registers that a third wave would need.
-template <class T, int DP, bool VEC>
-constexpr int kDqWaves = sizeof(T) == 2 && DP == 64 && VEC && !kIsF16<T> ? 3 : attn_waves<T, DP>();
+// float16's scale takes the registers that a third wave would need, and so do the
+// ranges of the keys, whose workgroups have a compute unit to themselves.
+template <class T, int DP, bool VEC, bool RANGES>
+constexpr int kDqWaves =
+    sizeof(T) == 2 && DP == 64 && VEC && !RANGES && !kIsF16<T> ? 3 : attn_waves<T, DP>();
 
 // Tiles of keys and of values in LDS: one computed on and one arriving, but a
 // single one where two would leave no room for the widest bias window.
@@ -92,8 +94,8 @@ __device__ __forceinline__ float tile_diagonals(float* scratch, const acc16& s, 
   return sum;
 }
 
-template <class T, int DP, bool TABLE, bool VEC>
-__global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_kernel(const AttnArgs a) {
+template <class T, int DP, bool TABLE, bool VEC, bool RANGES>
+__global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC, RANGES>)) void attn_dq_kernel(const AttnArgs a) {
   constexpr int BK = kDqStep, NS = BK / 32, TS = Tile<T, DP>::size(BK), KS = DP / 16, DT = DP / 32;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   Lds<T>* kt = (Lds<T>*)smem;
@@ -118,15 +120,22 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
   const bool real = i < a.q_len;
   const int len = key_count(a, b), first = position_of_first(a, b);
   const int q_end = min((qb + 1) * kAttnQueries, a.q_len);
-  const int k_end = a.causal ? clamp_int(first + q_end, 0, len) : len;
+  // this workgroup's range of the keys
+  const int all_end = a.causal ? clamp_int(first + q_end, 0, len) : len, range = RANGES ? blockIdx.y : 0;
+  int k_beg = 0, k_end = all_end;
+  if constexpr (RANGES) {
+    const int per = ((len + a.dq_splits - 1) / a.dq_splits + BK - 1) / BK * BK;
+    k_beg = min(range * per, all_end);
+    k_end = min(k_beg + per, all_end);
+  }
 
   const T* kp = (const T*)a.k + b * a.ks[0] + kvh * a.ks[1];
   const T* vp = (const T*)a.v + b * a.vs[0] + kvh * a.vs[1];
   TileLoad<T, DP, BK, kAttnThreads, VEC> kl, vl;
   kl.init(a.ks[2], a.dim, tid);
   vl.init(a.vs[2], a.dim, tid);
-  kl.load(kp, a.ks[2], k_end, a.dim, tid);
-  vl.load(vp, a.vs[2], k_end, a.dim, tid);
+  kl.load(kp + k_beg * a.ks[2], a.ks[2], k_end - k_beg, a.dim, tid);
+  vl.load(vp + k_beg * a.vs[2], a.vs[2], k_end - k_beg, a.dim, tid);
   const int64_t row = (int64_t)(b * a.heads + head) * a.q_len + i;
   Frag<T> qf[KS], gf[KS];
   float delta = 0.f, amax = 0.f;
@@ -156,7 +165,7 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
   if (real) {
     const float v = a.lse[row];
     if (v != -INFINITY) lse2 = v * kLog2e;
-    if (kIsF16<T> && h == 0) a.amax[row] = amax;
+    if (kIsF16<T> && h == 0 && range == 0) a.amax[row] = amax;
   }
   const float unit = kIsF16<T> ? unit_scale(amax) : 1.f;
   fill_bias<T>(a, head, bias, ends, tid, kAttnThreads);
@@ -175,7 +184,7 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
   const int least = a.causal ? min(len, first + q0 + 1) : len;
   const int wave_end = a.causal ? min(k_end, first + q0 + 32) : k_end;
   const bool idle = q0 >= a.q_len;
-  if (!idle && wave_end <= 32) {
+  if (!idle && range == 0 && (a.causal ? min(all_end, first + q0 + 32) : all_end) <= 32) {
     // All keys of these queries lie in the first tile: delta from p and dp
     // themselves.  Their few probabilities are large, and so would be the error
     // that the rounding of o leaves in delta.
@@ -209,7 +218,7 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
   float* mysums = sums + wave * win;
   float* mydiag = diag + wave * kDiagScratch;
   int buf = 0;
-  for (int j0 = 0; j0 < k_end; j0 += BK, buf ^= TILES - 1) {
+  for (int j0 = k_beg; j0 < k_end; j0 += BK, buf ^= TILES - 1) {
     const bool more = j0 + BK < k_end;
     if (more) {
       kl.load(kp + (int64_t)(j0 + BK) * a.ks[2], a.ks[2], k_end - j0 - BK, a.dim, tid);
@@ -295,15 +304,21 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
 
   const int ie = afresh(q0 + n), he = afresh(lane >> 5);
   if (ie < a.q_len) {
-    if (he == 0) a.delta[(int64_t)(b * a.heads + head) * a.q_len + ie] = delta;
+    const int64_t at_row = (int64_t)(b * a.heads + head) * a.q_len + ie;
+    if (he == 0 && range == 0) a.delta[at_row] = delta;
     const float f = a.scale / unit;
+    float* part = a.part_dq + (range * attn_row_count(a) + at_row) * a.dim;
     T* out = (T*)a.dq + b * a.dqs[0] + head * a.dqs[1] + ie * a.dqs[2];
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         const int at_d = 32 * d + 8 * y + 4 * he;
-        if (at_d < a.dim)
+        if (at_d >= a.dim) continue;
+        if constexpr (RANGES)
+          store4<float, VEC>(part + at_d, dq[d][4 * y] * f, dq[d][4 * y + 1] * f, dq[d][4 * y + 2] * f,
+                             dq[d][4 * y + 3] * f, a.dim - at_d);
+        else
           store4<T, VEC>(out + at_d, dq[d][4 * y] * f, dq[d][4 * y + 1] * f, dq[d][4 * y + 2] * f,
                  dq[d][4 * y + 3] * f, a.dim - at_d);
       }
@@ -314,13 +329,24 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
     // much times a pair's p is in each ds.  The far sides hold most of a long
     // row's probability in one bucket each, where these errors would add up;
     // there they are taken out.
-    const float off = halves_sum(all);
+    float off = halves_sum(all);
     float left = far_ds, left_p = far_p, right = 0.f, right_p = 0.f;
     if (put_away) {
       right = far_ds;
       right_p = far_p;
       left = before[tid];
       left_p = before[kAttnThreads + tid];
+    }
+    if constexpr (RANGES) {
+      // the whole row's is known to the join only
+      const float lp = halves_sum(left_p), rp = halves_sum(right_p);
+      if (ie < a.q_len && he == 0) {
+        float* r = a.part_row + (range * attn_row_count(a) + (int64_t)(b * a.heads + head) * a.q_len + ie) * 3;
+        r[0] = off;
+        r[1] = lp;
+        r[2] = rp;
+      }
+      off = 0.f;
     }
     left = lanes_sum<64>(fmaf(-off, left_p, left));
     right = lanes_sum<64>(fmaf(-off, right_p, right));
@@ -330,7 +356,7 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
     }
     __syncthreads();
     // the window's first and last distances have the buckets of the far tiles
-    float* out = a.table_part + ((int64_t)(b * a.heads + head) * blocks + qb) * win;
+    float* out = a.table_part + (((int64_t)(b * a.heads + head) * blocks + qb) * (RANGES ? a.dq_splits : 1) + range) * win;
     for (int t = tid; t < win; t += kAttnThreads) {
       float v = 0.f;
 #pragma unroll
@@ -342,12 +368,59 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC>)) void attn_dq_
   }
 }
 
+constexpr int kDqJoinRows = 8;  // of a workgroup
+// Joins the key ranges of a query block: dq, and the correction of the bias
+// table's end buckets (see above) with the rows' whole sums.
+template <class T>
+__global__ __launch_bounds__(kAttnThreads) void attn_dq_join_kernel(const AttnArgs a) {
+  __shared__ float red[4][2];
+  const int blocks = (a.q_len + kAttnQueries - 1) / kAttnQueries, tid = threadIdx.x;
+  const int64_t bh = blockIdx.x / blocks, rows = attn_row_count(a);
+  const int qb = blockIdx.x - (int)bh * blocks, i0 = qb * kAttnQueries, have = min(kAttnQueries, a.q_len - i0);
+  const int64_t b = bh / a.heads, head = bh - b * a.heads, row0 = bh * a.q_len + i0, step = rows * a.dim;
+  const float* p = a.part_dq + row0 * a.dim;
+  T* out = (T*)a.dq + b * a.dqs[0] + head * a.dqs[1];
+  const int t_end = min((int)(blockIdx.y + 1) * kDqJoinRows, have) * a.dim;
+  for (int t = blockIdx.y * kDqJoinRows * a.dim + tid; t < t_end; t += kAttnThreads) {
+    float s = 0.f;
+#pragma unroll 8
+    for (int r = 0; r < a.dq_splits; ++r) s += p[r * step + t];
+    const int i = t / a.dim;
+    out[(i0 + i) * a.dqs[2] + t - i * a.dim] = (T)s;
+  }
+  if (!a.d_table || blockIdx.y > 0) return;
+  float left = 0.f, right = 0.f;
+  if (tid < have) {
+    float off = 0.f, lp = 0.f, rp = 0.f;
+    for (int r = 0; r < a.dq_splits; ++r) {
+      const float* x = a.part_row + (r * rows + row0 + tid) * 3;
+      off += x[0];
+      lp += x[1];
+      rp += x[2];
+    }
+    left = -off * lp;
+    right = -off * rp;
+  }
+  left = lanes_sum<64>(left);
+  right = lanes_sum<64>(right);
+  if ((tid & 63) == 0) {
+    red[tid >> 6][0] = left;
+    red[tid >> 6][1] = right;
+  }
+  __syncthreads();
+  if (tid < 2) {
+    const int win = bias_window(a.far);
+    float* at = a.table_part + (bh * blocks + qb) * a.dq_splits * win + (tid ? win - 1 : 0);
+    *at += (red[0][tid] + red[1][tid]) + (red[2][tid] + red[3][tid]);
+  }
+}
+
 // Sums over entries and query blocks: by distance, 64 distances of a head per
 // workgroup, 16 interleaved sets of partials.
 template <class T>
 __global__ __launch_bounds__(1024) void attn_table_distances_kernel(const AttnArgs a) {
   __shared__ float red[16][64];
-  const int win = bias_window(a.far), blocks = (a.q_len + kAttnQueries - 1) / kAttnQueries;
+  const int win = bias_window(a.far), blocks = (a.q_len + kAttnQueries - 1) / kAttnQueries * a.dq_splits;
   const int lane = threadIdx.x & 63, set = threadIdx.x >> 6, head = blockIdx.y;
   const int t = blockIdx.x * 64 + lane;
   float s = 0.f;
@@ -379,7 +452,7 @@ __global__ __launch_bounds__(1024) void attn_table_buckets_kernel(const AttnArgs
   __shared__ float2 dist[bias_window(kAttnMaxFar) + AHEAD];  // sum, bucket
   __shared__ float red[1024];
   const int win = bias_window(a.far), head = blockIdx.x, tid = threadIdx.x;
-  const int blocks = (a.q_len + kAttnQueries - 1) / kAttnQueries, rows = a.batch * blocks;
+  const int blocks = (a.q_len + kAttnQueries - 1) / kAttnQueries * a.dq_splits, rows = a.batch * blocks;
   for (int t = tid; t < win; t += 1024) {
     const int bucket = a.map[clamp_int(t - kBiasPad, 0, 2 * a.far)];
     float s = 0.f;
@@ -722,18 +795,30 @@ __global__ __launch_bounds__(kAttnThreads) void attn_dkv_join_kernel(const AttnA
 template <class T, int DP, bool VEC>
 int attn_backward_dim(const AttnArgs& a, void* stream) {
   static const int opted =
-      lds_opt_in(attn_dq_kernel<T, DP, false, VEC>, attn_dq_lds<T, DP>(kAttnMaxFar, false)) |
-      lds_opt_in(attn_dq_kernel<T, DP, true, VEC>, attn_dq_lds<T, DP>(kAttnMaxFar, true)) |
+      lds_opt_in(attn_dq_kernel<T, DP, false, VEC, false>, attn_dq_lds<T, DP>(kAttnMaxFar, false)) |
+      lds_opt_in(attn_dq_kernel<T, DP, true, VEC, false>, attn_dq_lds<T, DP>(kAttnMaxFar, true)) |
+      lds_opt_in(attn_dq_kernel<T, DP, false, VEC, true>, attn_dq_lds<T, DP>(kAttnMaxFar, false)) |
+      lds_opt_in(attn_dq_kernel<T, DP, true, VEC, true>, attn_dq_lds<T, DP>(kAttnMaxFar, true)) |
       lds_opt_in(attn_dkv_kernel<T, DP, VEC>, attn_dkv_lds<T, DP>(kAttnMaxFar));
   if (opted != FM_OK) return set_error(FM_E_HIP, "attention backward: LDS size refused");
   const bool table = a.d_table != nullptr;
   if (a.q_len > 0) {
     const int st = launch("attention backward (dq)",
-                          table ? attn_dq_kernel<T, DP, true, VEC> : attn_dq_kernel<T, DP, false, VEC>,
+                          a.dq_splits > 1 ? (table ? attn_dq_kernel<T, DP, true, VEC, true>
+                                                   : attn_dq_kernel<T, DP, false, VEC, true>)
+                                          : (table ? attn_dq_kernel<T, DP, true, VEC, false>
+                                                   : attn_dq_kernel<T, DP, false, VEC, false>),
                           dim3(place_grid((int64_t)a.batch * a.kv_heads,
-                                          (int64_t)attn_query_blocks(a) * (a.heads / a.kv_heads))),
+                                          (int64_t)attn_query_blocks(a) * (a.heads / a.kv_heads)),
+                               (unsigned)a.dq_splits),
                           dim3(kAttnThreads), attn_dq_lds<T, DP>(a.far, table), stream, a);
     if (st != FM_OK) return st;
+    if (a.dq_splits > 1) {
+      const int st2 = launch("attention backward (dq join)", attn_dq_join_kernel<T>,
+                             dim3((unsigned)(a.batch * a.heads * attn_query_blocks(a)), kAttnQueries / kDqJoinRows),
+                             dim3(kAttnThreads), 0, stream, a);
+      if (st2 != FM_OK) return st2;
+    }
   }
   if (a.k_len > 0) {
     const int st = launch("attention backward (dk, dv)", attn_dkv_kernel<T, DP, VEC>,
@@ -765,7 +850,7 @@ int attn_backward_t(const AttnArgs& a, void* stream) {
                   attn_backward_dim<T, 128, false>);
   }
   if (st != FM_OK || !a.d_table) return st;
-  if ((int64_t)a.batch * attn_query_blocks(a) > kTableRows) {
+  if ((int64_t)a.batch * attn_query_blocks(a) * a.dq_splits > kTableRows) {
     st = launch("attention backward (distances)", attn_table_distances_kernel<T>,
                 dim3((unsigned)(bias_window(a.far) + 63) / 64, (unsigned)a.heads), dim3(1024), 0, stream, a);
     if (st != FM_OK) return st;

@@ -309,6 +309,9 @@ int fm_attention_backward(const fm_attention_args* args, void* workspace, void* 
   a.table_dist = reinterpret_cast<float*>(base + w.dist);
   a.part_dkv = reinterpret_cast<float*>(base + w.dkv);
   a.dkv_splits = fm::attn_dkv_splits(a);
+  a.part_dq = reinterpret_cast<float*>(base + w.dq);
+  a.part_row = reinterpret_cast<float*>(base + w.row);
+  a.dq_splits = fm::attn_dq_splits(a);
   if (args->dtype == FM_F32) return fm::attn_backward_f32(a, stream);
   return args->dtype == FM_F16 ? fm::attn_backward_f16(a, stream) : fm::attn_backward_bf16(a, stream);
 } catch (...) {

@@ -212,10 +212,12 @@ struct AttnArgs {
   void* d_table;
   float* delta;       // [batch, heads, q_len]
   float* amax;        // [batch, heads, q_len], float16 only
-  float* table_part;  // [batch * heads * query blocks, distances of the window]
+  float* table_part;  // [batch * heads * query blocks * dq_splits, distances of the window]
   float* table_dist;  // [heads, distances of the window]
   float* part_dkv;    // [dkv_splits, batch, kv_heads, k_len, 2, dim]
-  int dkv_splits;
+  float* part_dq;     // [dq_splits, batch, heads, q_len, dim]
+  float* part_row;    // [dq_splits, batch, heads, q_len, 3]
+  int dkv_splits, dq_splits;
   // forward over key ranges
   float* part_o;    // [splits, batch, heads, q_len, dim]
   float* part_lse;  // [splits, batch, heads, q_len]
@@ -299,18 +301,35 @@ inline int attn_dkv_splits(const AttnArgs& a) {
   const int64_t s = fill < most ? fill : most;
   return s < 1 ? 1 : (int)s;
 }
+// Ranges of the keys that workgroups of the dq kernel take while the query blocks
+// alone leave compute units idle, of at least 8 tiles of 32 keys (float32, whose
+// tiles take longer: 4); a second launch joins them.  Whole backward, us, against
+// one range: 1 x 1 head, 2295, 80 columns, f32 causal 98 and 289; 1 x 2, 825, 128, f32
+// 93 and 177 (with 8 tiles 109); 1 x 1, 2139, 128, f16 75 and 129 (with 4 tiles 83);
+// 1 x 8, 1501, 64, bf16, 96 blocks 80 and 87; 2 x 8, 1000, 128 blocks 69 and 67.
+inline int attn_dq_splits(const AttnArgs& a) {
+  const int64_t wgs = (int64_t)a.batch * a.heads * attn_query_blocks(a);
+  if (wgs == 0 || wgs > 128) return 1;
+  const int64_t fill = 256 / wgs, most = a.k_len / (a.size == 4 ? 128 : 256);
+  const int64_t s = fill < most ? fill : most;
+  return s < 1 ? 1 : (int)s;
+}
 struct AttnBackwardSpace {
-  int64_t amax, part, dist, dkv, total;  // byte offsets; delta at 0
+  int64_t amax, part, dist, dkv, dq, row, total;  // byte offsets; delta at 0
 };
 inline AttnBackwardSpace attn_backward_space(const AttnArgs& a, bool f16) {
   const int64_t rows = attn_round16(4 * attn_rows(a));
   AttnBackwardSpace s;
   s.amax = rows;
   s.part = rows * (f16 ? 2 : 1);
-  s.dist = s.part + attn_round16(4 * (int64_t)a.batch * a.heads * attn_query_blocks(a) * bias_window(a.far));
+  const int splits = attn_dkv_splits(a), ranges = attn_dq_splits(a);
+  s.dist = s.part +
+           attn_round16(4 * (int64_t)a.batch * a.heads * attn_query_blocks(a) * ranges * bias_window(a.far));
   s.dkv = s.dist + attn_round16(4 * (int64_t)a.heads * bias_window(a.far));
-  const int splits = attn_dkv_splits(a);
-  s.total = s.dkv + (splits == 1 ? 0 : 8 * (int64_t)splits * a.batch * a.kv_heads * a.k_len * a.dim);
+  s.dq = s.dkv +
+         (splits == 1 ? 0 : attn_round16(8 * (int64_t)splits * a.batch * a.kv_heads * a.k_len * a.dim));
+  s.row = s.dq + (ranges == 1 ? 0 : attn_round16(4 * ranges * attn_rows(a) * a.dim));
+  s.total = s.row + (ranges == 1 ? 0 : 12 * ranges * attn_rows(a));
   return s;
 }
 

@@ -42,8 +42,13 @@ int attn_backward(const AttnArgs& a, bool f16) {
   fill(a.delta, attn_rows(a));
   if (f16) fill(a.amax, attn_rows(a));
   if (a.d_table) {
-    fill(a.table_part, int64_t(a.batch) * a.heads * attn_query_blocks(a) * bias_window(a.far));
+    fill(a.table_part, int64_t(a.batch) * a.heads * attn_query_blocks(a) * a.dq_splits * bias_window(a.far));
     fill(a.table_dist, int64_t(a.heads) * bias_window(a.far));
+  }
+  if (a.dq_splits < 1) return set_error(FM_E_HIP, "no ranges");
+  if (a.dq_splits > 1) {
+    fill(a.part_dq, a.dq_splits * attn_rows(a) * a.dim);
+    fill(a.part_row, a.dq_splits * attn_rows(a) * 3);
   }
   if (a.dkv_splits < 1) return set_error(FM_E_HIP, "no shares");
   if (a.dkv_splits > 1) fill(a.part_dkv, int64_t(a.dkv_splits) * a.batch * a.kv_heads * a.k_len * 2 * a.dim);

@@ -423,3 +423,15 @@ def test_ranges_of_many_queries(tk):
     run_case(q, k, v, table, m, do, lengths=lengths, backward=False)
     lengths[1] = 0
     run_case(q, k, v, table, m, do, causal=True, lengths=lengths, offset=tk - 150, backward=False)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("h,hk,t,d,far", [(2, 1, 1030, 64, 60), (1, 1, 515, 40, 20), (3, 3, 777, 33, 300), (2, 2, 900, 128, 20)])
+def test_ranges_of_keys_in_the_backward(h, hk, t, d, far, dtype):
+    """Few query blocks: dq and the bias table's gradient from several key ranges."""
+    q, k, v, table, m, do = make(2, h, hk, t, t, d, dtype, seed=t, far=far)
+    lengths = torch.tensor([t, t // 3], device="cuda", dtype=torch.int32)
+    for causal in (False, True):
+        run_case(q, k, v, table, m, do, causal=causal, lengths=lengths)
+    lengths[0] = 0
+    run_case(q, k, v, table, m, do, lengths=lengths)
