@@ -282,14 +282,14 @@ constexpr int kAttnBlockKeys = 128;  // keys of a dk, dv workgroup
 // dk, dv kernel take of a key block, while the blocks alone leave compute units
 // idle; a second launch adds them up.  Shares of at least 4 tiles of 64 queries,
 // 16 where there are blocks for a quarter of the units, since the sums are as much
-// traffic per block then as they save (whole backward, us: 2 x 4 heads on 1, 1777
-// queries, 28 blocks, 18 shares 109, unshared 268; 5 x 16 on 4, 202, f32, 40 blocks,
-// 4 shares 66 and 131; 3 x 8 on 4, 1098, 128 columns, 108 blocks, 2 shares 130 and
-// 165; 2 x 8 on 8, 1000, 128 blocks, unshared 68, 4 shares 74).  float32, whose
-// tiles of 32 queries take as long as two of those and whose workgroups have a
-// compute unit to themselves: single tiles below 48 blocks (1 x 8, 101 queries, 96
-// columns: 4 shares 46, unshared 55; 1 x 8, 500: 8 shares 77, 2 shares 87, 16 shares
-// 89), else 8 (8 x 8, 101, 64 blocks: unshared 44, 4 shares 46).
+// traffic per block then as they save.  Whole backward with dq in one range, us: 2
+// x 4 heads on 1, 1777 queries, 28 blocks, 18 shares 109, unshared 268; 3 x 8 on 4,
+// 1098, 128 columns, 108 blocks, 2 shares 130 and 165; 2 x 8 on 8, 1000, 128 blocks,
+// unshared 68, 4 shares 74.  float32, whose tiles of 32 queries take as long as two
+// of those and whose workgroups have a compute unit to themselves: single tiles
+// below 48 blocks (1 x 8, 101 queries, 96 columns: 4 shares 46, unshared 55; 5 x 16
+// on 4, 202, 40 blocks, 6 shares 62, unshared 131; 1 x 8, 500: 8 shares 77, 2 shares
+// 87, 16 shares 89), else 8 (8 x 8, 101, 64 blocks: unshared 44, 4 shares 46).
 inline int attn_dkv_splits(const AttnArgs& a) {
   const int64_t wgs = (int64_t)a.batch * a.kv_heads * ((a.k_len + kAttnBlockKeys - 1) / kAttnBlockKeys);
   if (wgs == 0 || wgs > 256) return 1;
