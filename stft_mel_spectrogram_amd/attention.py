@@ -177,9 +177,9 @@ def relative_attention(q, k, v, table, buckets, *, scale=None, causal: bool = Fa
     distances as relative_buckets makes it; scale defaults to head_dim ** -0.5;
     key_lengths: int32 [batch] or None; query_offset: the position of each
     entry's first query, an int or int32 [batch] (for new tokens against a
-    cache: the cache length before them).  A few query rows per key head take
-    a kernel that divides the keys, so one token against a long cache runs on
-    the whole GPU.
+    cache: the cache length before them).  Few queries against a longer cache
+    take a kernel that divides the keys, so one token against a long cache runs
+    on the whole GPU.
     """
     if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad
                                        for t in (q, k, v, table)):
