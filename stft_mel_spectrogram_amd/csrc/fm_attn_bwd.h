@@ -28,14 +28,22 @@ template <class T>
 constexpr int attn_step() { return sizeof(T) == 2 && !kIsF16<T> ? 64 : 32; }
 constexpr int kDqStep = 32;
 
-// float16 has no room for small gradients: ds is scaled by the power of two
-// that brings the largest |do| into [1, 2), so that ds stays within a few
-// powers of two of v's size, and the scale is taken out at the end.  The
-// other types have float32's exponents.
-__device__ __forceinline__ float unit_scale(float amax) {
-  const int e = clamp_int((int)(__float_as_uint(amax) >> 23) & 255, 1, 253);
-  return amax == 0.f ? 1.f : __uint_as_float((uint32_t)(254 - e) << 23);
+// float16 has no room for gradients of any size: ds is scaled by powers of two,
+// which are taken out at the end.  The other types have float32's exponents.
+//
+// dk, dv: one scale per key j (a lane's column), from |ds| <= |do_i| |v_j| +
+// |delta_i| with the largest norm and delta of the group's queries: below 2^15
+// whatever the values are, and with random ones (a bound 10 times too wide at 128
+// columns) normal numbers down to probabilities of 2^-25.  The largest |do| alone
+// does not bound ds, which holds a sum over the columns.
+// dq: a scale per query (a lane's column again), lowered with the sums so far when
+// a tile's largest |ds| leaves 2^15 behind; it then has room for 2^3 more.
+__device__ __forceinline__ float scale_to(float size, int top) {
+  // the power of two that brings size into [2^top, 2^(top + 1))
+  const int e = clamp_int((int)(__float_as_uint(size) >> 23) & 255, top, 255);
+  return __uint_as_float((uint32_t)(254 + top - e) << 23);
 }
+constexpr float kDqUnit = 0x1p100f;  // of a row without any ds yet
 // float16 probabilities are scaled too: 2^8 p is a normal number from p =
 // 2.4e-7 on.
 template <class T>
@@ -138,7 +146,7 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC, RANGES>)) void 
   vl.load(vp + k_beg * a.vs[2], a.vs[2], k_end - k_beg, a.dim, tid);
   const int64_t row = (int64_t)(b * a.heads + head) * a.q_len + i;
   Frag<T> qf[KS], gf[KS];
-  float delta = 0.f, amax = 0.f;
+  float delta = 0.f, size = 0.f;
   {
     const int qw = qb * kAttnQueries, count = a.q_len - qw;  // the workgroup's first query
     const Rows<T, VEC> qr = {(const T*)a.q + b * a.qs[0] + head * a.qs[1] + qw * a.qs[2], a.qs[2], count, a.dim};
@@ -154,20 +162,20 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC, RANGES>)) void 
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         delta = fmaf((float)gr[e], (float)of[e], delta);
-        amax = fmaxf(amax, fabsf((float)gr[e]));
+        if constexpr (kIsF16<T>) size = fmaf((float)gr[e], (float)gr[e], size);
       }
     }
     delta = halves_sum(delta);
-    amax = halves_max(amax);
+    if constexpr (kIsF16<T>) size = halves_sum(size);
   }
   // empty rows and rows past the end: every probability is 0
   float lse2 = INFINITY;
   if (real) {
     const float v = a.lse[row];
     if (v != -INFINITY) lse2 = v * kLog2e;
-    if (kIsF16<T> && h == 0 && range == 0) a.amax[row] = amax;
+    if (kIsF16<T> && h == 0 && range == 0) a.amax[row] = sqrtf(size);
   }
-  const float unit = kIsF16<T> ? unit_scale(amax) : 1.f;
+  float unit = kIsF16<T> ? kDqUnit : 1.f;
   fill_bias<T>(a, head, bias, ends, tid, kAttnThreads);
   if constexpr (TABLE) {
     for (int t = tid; t < 4 * win; t += kAttnThreads) sums[t] = 0.f;
@@ -283,6 +291,19 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC, RANGES>)) void 
           }
         }
         if constexpr (kIsF16<T>) {
+          float most = 0.f;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) most = fmaxf(most, fabsf(s[r]));
+          most = halves_max(most);
+          const bool lower = most * unit > 0x1p15f;
+          if (__any(lower)) {
+            const float to = lower ? scale_to(most, 11) : unit, f = to / unit;
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+              for (int r = 0; r < 16; ++r) dq[d][r] *= f;
+            unit = to;
+          }
 #pragma unroll
           for (int r = 0; r < 16; ++r) s[r] *= unit;
         }
@@ -550,14 +571,26 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
   const int i_end = j_wg < len ? a.q_len : 0;
   float unit = 1.f;
   if constexpr (kIsF16<T>) {
-    // one scale for every query of the sums: the group's largest |do|
-    float m = 0.f;
-    const float* am = a.amax + (int64_t)(b * a.heads + kvh * group) * a.q_len;
-    for (int64_t t = tid; t < (int64_t)group * a.q_len; t += kAttnThreads) m = fmaxf(m, am[t]);
-    m = lanes_max<64>(m);
-    if (lane == 0) neg_lse[wave] = m;
+    float g = 0.f, t_most = 0.f, v = 0.f;
+    const int64_t row0 = (int64_t)(b * a.heads + kvh * group) * a.q_len;
+    for (int64_t t = tid; t < (int64_t)group * a.q_len; t += kAttnThreads) {
+      g = fmaxf(g, a.amax[row0 + t]);
+      t_most = fmaxf(t_most, fabsf(a.delta[row0 + t]));
+    }
+    g = lanes_max<64>(g);
+    t_most = lanes_max<64>(t_most);
+    if (lane == 0) {
+      neg_lse[wave] = g;
+      neg_delta[wave] = t_most;
+    }
     __syncthreads();
-    unit = unit_scale(fmaxf(fmaxf(neg_lse[0], neg_lse[1]), fmaxf(neg_lse[2], neg_lse[3])));
+    g = fmaxf(fmaxf(neg_lse[0], neg_lse[1]), fmaxf(neg_lse[2], neg_lse[3]));
+    t_most = fmaxf(fmaxf(neg_delta[0], neg_delta[1]), fmaxf(neg_delta[2], neg_delta[3]));
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v = fmaf((float)vf[s][e], (float)vf[s][e], v);
+    unit = scale_to(fmaf(g, sqrtf(halves_sum(v)), t_most), 14);
     __syncthreads();
   }
   const float c = a.scale * kLog2e, inv_c = 1.f / c;

@@ -211,7 +211,7 @@ struct AttnArgs {
   void* dv;
   void* d_table;
   float* delta;       // [batch, heads, q_len]
-  float* amax;        // [batch, heads, q_len], float16 only
+  float* amax;        // [batch, heads, q_len] norm of a row of do, float16 only
   float* table_part;  // [batch * heads * query blocks * dq_splits, distances of the window]
   float* table_dist;  // [heads, distances of the window]
   float* part_dkv;    // [dkv_splits, batch, kv_heads, k_len, 2, dim]
