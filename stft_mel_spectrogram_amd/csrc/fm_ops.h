@@ -177,6 +177,11 @@ inline ScoreSplit score_split(int64_t rows, int vocab, int ve, int top) {
   const int per = (chunks + (int)segs - 1) / (int)segs;
   return {256, vecs, (chunks + per - 1) / per, per * chunk};
 }
+// Where a segment ends.  The last ones may reach past the row by up to segs - 1
+// chunks: beg + seg_len alone would leave int near the longest vocabularies.
+constexpr int score_segment_end(int beg, int seg_len, int vocab) {
+  return vocab - beg < seg_len ? vocab : beg + seg_len;
+}
 inline int64_t score_part_bytes(int64_t rows, int segs) {
   return (rows * segs * 3 * (int64_t)sizeof(float) + 15) / 16 * 16;
 }

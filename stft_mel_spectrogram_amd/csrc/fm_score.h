@@ -286,7 +286,7 @@ __global__ __launch_bounds__(256) void score_forward_kernel(
   const int seg = (int)(unit - row * segs);
   const T* xr = x + row * x_stride;
   const int beg = seg * seg_len;
-  const int end = beg + seg_len < vocab ? beg + seg_len : vocab;
+  const int end = score_segment_end(beg, seg_len, vocab);
 
   ScoreSum acc = {-INFINITY, 0.f, 0.f};
   __shared__ __attribute__((aligned(16))) key_t buf[TOP ? 4 : 1][TopKeys::kSize];
@@ -392,7 +392,7 @@ __global__ __launch_bounds__(256) void score_backward_kernel(
   const T* xr = x + row * x_stride;
   T* dr = dx + row * vocab;
   const int beg = seg * seg_len;
-  const int end = beg + seg_len < vocab ? beg + seg_len : vocab;
+  const int end = score_segment_end(beg, seg_len, vocab);
   Vec16<T> v[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
