@@ -12,6 +12,27 @@ constexpr int kAttnThreads = 256;
 // columns: 87 us); 32 leave the registers and the LDS for four waves per SIMD.
 constexpr int kAttnKeys = 32;
 
+// Probabilities are rounded to the element type for their product, and the sum
+// that divides them is not: in float16, 2^shift p is a normal number, rounded by
+// half a step of itself, for probabilities down to 2^(-14 - shift) of the row's
+// largest (a sink key of value 0 leaves the result to those). With a maximum that
+// is raised only by 2^slack, 2^(shift + slack) p has to stay below 2^16: beside a
+// slack of 2^4 shift 11, normal down to 17 nats (8 x 16 x 1501, 64 columns: 109.5 us;
+// slack 2^8, which leaves 7 and 14 nats, 108). The kernel for few queries raises at
+// once and takes 15.
+template <class T>
+constexpr float kSlack = 8.f;
+template <>
+inline constexpr float kSlack<f16_t> = 4.f;
+template <class T>
+constexpr float kShift = 0.f;
+template <>
+inline constexpr float kShift<f16_t> = 11.f;
+template <class T>
+constexpr float kTokenShift = 0.f;
+template <>
+inline constexpr float kTokenShift<f16_t> = 15.f;
+
 template <class T, int DP>
 constexpr size_t attn_forward_lds(int far) {
   return 4 * Tile<T, DP>::size(kAttnKeys) * sizeof(Lds<T>) + (bias_window(far) + 8) * sizeof(float);
@@ -77,7 +98,8 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
   for (int d = 0; d < DT; ++d)
 #pragma unroll
     for (int r = 0; r < 16; ++r) o[d][r] = 0.f;
-  // running maximum of the scores in base 2, its finite negative, and the sum
+  // running maximum of the scores in base 2, its finite negative (with the shift),
+  // and the sum
   float m = -INFINITY, neg = 0.f, l = 0.f;
   const int mine = a.causal ? min(len, first + i + 1) : len;   // keys this lane's query sees
   const int least = a.causal ? min(len, first + q0 + 1) : len; // of the wave's first query
@@ -128,9 +150,9 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
         mx = fmaxf(mx, fmaf(mu, c, far_bias[u]));
       }
       mx = halves_max(mx);
-      // a maximum raised by less than 2^8 leaves m as it is: every later
+      // a maximum raised by less than 2^kSlack leaves m as it is: every later
       // product with o and l waits for it
-      const bool raise = mx > m + 8.f;
+      const bool raise = mx > m + kSlack<T>;
       if (__any(raise)) {
         const float m2 = raise ? mx : m;
         // nothing seen yet: o and l are 0
@@ -141,7 +163,7 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
           for (int r = 0; r < 16; ++r) o[d][r] *= f;
         l *= f;
         m = m2;
-        neg = m == -INFINITY ? 0.f : -m;
+        neg = m == -INFINITY ? 0.f : kShift<T> - m;
       }
       float sum = 0.f;
 #pragma unroll
@@ -157,7 +179,8 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
 #pragma unroll
       for (int t = 0; t < 2 * NS; ++t) {
         // rounded to the element type for the product: half a step of each
-        // probability, as the result's own rounding; the sum l is not
+        // probability (in float16 while 2^kShift p is normal), as the result's own
+        // rounding; the sum l is not
         const Frag<T> p = acc_frag<T>(s[t / 2], t & 1);
         steps<T, DT>([&](int d) { return tile_cols<T, DP>(vtb, 16 * t, 32 * d, lane); },
                      [&](int d, const Frag<T>& f) { o[d] = mma32(f, p, o[d]); });
@@ -175,7 +198,7 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 
   if (ie >= a.q_len) return;
   const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
   const int64_t row = (int64_t)(b * a.heads + head) * a.q_len + ie;
-  const float lse = l != l ? l : m == -INFINITY ? -INFINITY : fmaf(m, kLn2, logf(l));
+  const float lse = l != l ? l : m == -INFINITY ? -INFINITY : fmaf(m - kShift<T>, kLn2, logf(l));
   if constexpr (SPLIT) {
     const int64_t rows = (int64_t)a.batch * a.heads * a.q_len;
     if (he == 0) a.part_lse[blockIdx.y * rows + row] = lse;
@@ -340,7 +363,7 @@ __global__ __launch_bounds__((attn_token_waves(sizeof(T), DP) * 64)) void attn_t
       l *= f;
       m = m2;
     }
-    const float mc = m == -INFINITY ? 0.f : m * c;
+    const float mc = m == -INFINITY ? 0.f : fmaf(m, c, -kTokenShift<T>);
     Frag<T> p;
     {
       Raw<float> e;
@@ -393,7 +416,7 @@ __global__ __launch_bounds__((attn_token_waves(sizeof(T), DP) * 64)) void attn_t
       val = fmaf(f, p[d], val);
     }
     const float out = sum == 0.f ? 0.f : val / sum;
-    const float lse = sum != sum ? sum : mm == -INFINITY ? -INFINITY : fmaf(mm, a.scale, logf(sum));
+    const float lse = sum != sum ? sum : mm == -INFINITY ? -INFINITY : fmaf(mm, a.scale, logf(sum) - kTokenShift<T> * kLn2);
     const int hd = kvh * group + (row0 + r) / a.q_len, qi = (row0 + r) % a.q_len;
     const int64_t row = (int64_t)(b * a.heads + hd) * a.q_len + qi;
     if constexpr (SPLIT) {

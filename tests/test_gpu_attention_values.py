@@ -60,3 +60,26 @@ def test_float16_overflow_of_two_keys():
     assert (dq.double().abs() <= 2.1 * h * 2 * ds * scale).all()  # ds of both cancel
     assert (dv.double() - 0.5e-3).abs().max() <= 3.1 * h * 0.5e-3
     assert torch.isfinite(dt).all()
+
+
+def sink_case(tq, tk, d, nats, at, seed):
+    """A key of value 0 whose score is `nats` above all others', which lie close together."""
+    q, k, v, table, m, do = plain.make(1, 2, 2, tq, tk, d, "f16", seed=seed, layout="bhtd")
+    table = torch.zeros_like(table)
+    q = q / 8
+    k = k / 4
+    q[..., 0], k[..., 0] = 4.0, 0.0
+    k[:, :, at] = 0
+    k[:, :, at, 0] = nats * d ** 0.5 / 4
+    v[:, :, at] = 0
+    return q, k, v, table, m, do
+
+
+@pytest.mark.parametrize("nats", [12, 14, 16, 17])
+@pytest.mark.parametrize("tq,tk,d", [(60, 310, 64), (150, 1500, 128), (1, 1501, 64), (7, 1501, 128),
+                                     (1, 5000, 40), (17, 2500, 33)])
+def test_float16_probabilities_beside_a_sink(tq, tk, d, nats):
+    """The general kernel and the cache kernel, each in one range and in several."""
+    for at in (0, tk - 1):
+        q, k, v, table, m, do = sink_case(tq, tk, d, nats, at, nats + tk)
+        plain.run_case(q, k, v, table, m, do, backward=False)
