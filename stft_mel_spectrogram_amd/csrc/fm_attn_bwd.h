@@ -44,12 +44,13 @@ __device__ __forceinline__ float scale_to(float size, int top) {
   return __uint_as_float((uint32_t)(254 + top - e) << 23);
 }
 constexpr float kDqUnit = 0x1p100f;  // of a row without any ds yet
-// float16 probabilities are scaled too: 2^8 p is a normal number from p =
-// 2.4e-7 on.
+// float16 probabilities are scaled too: at most 1, so that 2^15 p is in range, and a
+// normal number from p = 1.9e-9 on (dv of the keys beside one that takes nearly
+// all the probability).
 template <class T>
 constexpr float kProbShift = 0.f;
 template <>
-inline constexpr float kProbShift<f16_t> = 8.f;
+inline constexpr float kProbShift<f16_t> = 15.f;
 // Sums of ds by distance inside the window.  A 32x32 tile's 63 diagonals come
 // from a wave's scratch in LDS: 16 queries at a time are stored as rows of 32
 // keys with zeros between them, and lane t adds up diagonal t (key - query = t -

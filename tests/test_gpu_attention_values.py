@@ -83,3 +83,11 @@ def test_float16_probabilities_beside_a_sink(tq, tk, d, nats):
     for at in (0, tk - 1):
         q, k, v, table, m, do = sink_case(tq, tk, d, nats, at, nats + tk)
         plain.run_case(q, k, v, table, m, do, backward=False)
+
+
+@pytest.mark.parametrize("nats", [10, 13, 15])
+@pytest.mark.parametrize("tq,tk,d", [(60, 310, 64), (150, 700, 128), (200, 90, 40)])
+def test_float16_gradients_beside_a_sink(tq, tk, d, nats):
+    for at in (0, tk - 1):
+        q, k, v, table, m, do = sink_case(tq, tk, d, nats, at, nats + tk)
+        plain.run_case(q, k, v, table, m, do)
