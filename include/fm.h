@@ -426,7 +426,8 @@ int fm_token_logprobs_backward(const void* x, int64_t x_stride, const void* toke
  *                head h reads key head h / (heads / kv_heads); head_dim <= 128;
  *   scale        in [2^-60, 2^60];
  *   table        [num_buckets, heads] contiguous, table_dtype (dtype or
- *                FM_F32), num_buckets <= 1024;
+ *                FM_F32), num_buckets <= 1024; finite values beyond +-65536
+ *                count as +-65536, -inf hides a distance;
  *   bucket_map   [2 far + 1] int32, the bucket of each distance key - query
  *                from -far to far (<= 1024), farther ones taken at the ends; a
  *                distance with an entry outside [0, num_buckets) has no bias;

@@ -347,11 +347,18 @@ constexpr int attn_waves() { return sizeof(T) == 2 || DP == 64 ? 2 : 1; }
 // one multiplication scales both.  The window covers every distance of a
 // 32x32 tile that reaches inside +-far (kBiasPad more on either side); tiles
 // beyond take an end value.
+// Finite table values count as at most 2^16 either way (float16's whole range):
+// enough to hide a key beside any other, while the scores of a row whose keys all
+// have such a value, and its log sum exp, still hold the products' part in float32
+// (half a step there is 2^-8).  Larger ones, the masks of a type's lowest value,
+// would leave nothing of it, or float32's range by the factor 1 / scale or log2 e.
+constexpr float kBiasMost = 65536.f;
 template <class T>
 __device__ __forceinline__ float bias_of_bucket(const AttnArgs& a, int head, int b) {
   if (b < 0 || b >= a.num_buckets) return 0.f;  // a distance without a bucket
   const int64_t at = (int64_t)b * a.heads + head;
-  return a.table32 ? ((const float*)a.table)[at] : (float)((const T*)a.table)[at];
+  const float v = a.table32 ? ((const float*)a.table)[at] : (float)((const T*)a.table)[at];
+  return __builtin_isfinite(v) ? fminf(fmaxf(v, -kBiasMost), kBiasMost) : v;
 }
 template <class T>
 __device__ __forceinline__ float bias_of(const AttnArgs& a, int head, int d) {

@@ -69,7 +69,7 @@ int attention_args(const fm_attention_args* p, bool backward, AttnArgs& a) {
     return bad("attention: q_len and k_len must be in [0, 2^30)");
   if (p->head_dim < 1) return bad("attention: head_dim must be >= 1");
   if (p->head_dim > kAttnMaxDim) return set_error(FM_E_UNSUPPORTED, "attention: head_dim must be <= 128");
-  // its reciprocal times a bias or a log sum exp has to stay in float32's range
+  // its reciprocal times a bias (at most 2^16) or a log sum exp has to stay in float32's range
   if (!(p->scale >= 0x1p-60 && p->scale <= 0x1p60))
     return bad("attention: scale must be in [2^-60, 2^60]");
   if (p->far < 0 || p->num_buckets < 1) return bad("attention: far >= 0 and num_buckets >= 1 are wanted");

@@ -6,6 +6,7 @@ products, so that half a step (h) of each is relative for probabilities down to
 2^-25 of the row's largest and for score gradients down to 2^-24 of the largest
 that the row (dq) or the key (dk) can have.
 """
+import math
 
 import pytest
 
@@ -91,3 +92,55 @@ def test_float16_gradients_beside_a_sink(tq, tk, d, nats):
     for at in (0, tk - 1):
         q, k, v, table, m, do = sink_case(tq, tk, d, nats, at, nats + tk)
         plain.run_case(q, k, v, table, m, do)
+
+
+LIMIT = 65536.0
+
+
+@pytest.mark.parametrize("low", ["min", "max", -1e9, -65504.0, -1e4])
+@pytest.mark.parametrize("dtype,table_dtype", [("f32", "f32"), ("f16", "f32"), ("f16", "f16"), ("bf16", "bf16"),
+                                               ("bf16", "f32")])
+@pytest.mark.parametrize("tq,tk,d", [(70, 75, 64), (150, 1100, 40), (1, 400, 64), (7, 5000, 128), (1, 1, 8)])
+def test_rows_whose_keys_all_have_a_bias_of_the_lowest_value(tq, tk, d, dtype, table_dtype, low):
+    """Finite table values count as at most 2^16 either way, so a row of such keys alone is an
+    ordinary row.  Its scores are held in float32 at 2^16: in units of the product, 2^16 / scale,
+    every one of the D / 16 accumulations (six times as many in float32, up to four roundings each)
+    and the scaling round by half a step, 2^-8 in the scores, the log sum exp likewise."""
+    from stft_mel_spectrogram_amd import relative_attention_backward, relative_attention_forward
+    q, k, v, table, m, do = plain.make(1, 2, 2, tq, tk, d, dtype, seed=tk, far=20, buckets=12)
+    dt = plain.DT[table_dtype]
+    big = {"min": torch.finfo(dt).min, "max": torch.finfo(dt).max}.get(low, low)
+    if abs(big) > torch.finfo(dt).max:
+        pytest.skip("not a value of the type")
+    table = torch.full((12, 2), big, device="cuda").to(dt)
+    want = table.double().clamp(-LIMIT, LIMIT)
+    off = torch.zeros(1, device="cuda")
+    v = torch.ones_like(v)  # o is 1 whatever the probabilities are
+    o, stats = relative_attention_forward(q, k, v, table, m)
+    half = torch.finfo(q.dtype).eps / 2
+    # half a step of p and of o; float32 sums
+    assert ((o.double() - 1).abs() <= 2 * half + 2.0 ** -18).all()
+    lse = plain.reference(q, k, v, want, m, do, d ** -0.5, False, torch.full((1,), tk, device="cuda"), off)[2]
+    steps = (d + 15) // 16 * (24 if dtype == "f32" else 4) + 8
+    assert ((stats.double() - lse).abs() <= steps * 2.0 ** -8).all()
+    got = relative_attention_backward(do, q, k, v, table, m, o, stats)
+    assert all(torch.isfinite(g).all() for g in got)
+    # dv: probabilities within exp of the scores' and the log sum exp's error
+    dv = plain.reference(q, k, v, want, m, do, d ** -0.5, False, torch.full((1,), tk, device="cuda"), off)[4]["dv"]
+    p_tol = math.expm1(2 * steps * 2.0 ** -8) + 4 * half
+    size = plain.reference(q, k, v, want, m, do.abs(), d ** -0.5, False, torch.full((1,), tk, device="cuda"),
+                           off)[4]["dv"]
+    tiny = torch.finfo(q.dtype).smallest_normal
+    assert ((got[2].double() - dv).abs() <= p_tol * size + tiny).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("tq", [1, 60])
+def test_a_bias_of_the_lowest_value_still_hides_a_key_from_others(tq, dtype):
+    q, k, v, table, m, do = plain.make(1, 2, 2, tq, 600, 64, dtype, seed=5)
+    table[2] = torch.finfo(table.dtype).min
+    m[m.numel() // 2] = 0
+    from stft_mel_spectrogram_amd import relative_attention
+    hidden = table.clone()
+    hidden[2] = -math.inf
+    assert torch.equal(relative_attention(q, k, v, table, m), relative_attention(q, k, v, hidden, m))
