@@ -372,6 +372,8 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<T, DP, VEC, RANGES>)) void 
     }
     left = lanes_sum<64>(fmaf(-off, left_p, left));
     right = lanes_sum<64>(fmaf(-off, right_p, right));
+    // without any tile, other waves may still be reading the map's reach there
+    __syncthreads();
     if (lane == 0) {
       ends[2 * wave] = left;
       ends[2 * wave + 1] = right;
