@@ -89,16 +89,11 @@ __device__ __forceinline__ float tile_diagonals(float* scratch, const acc16& s, 
         *(float4*)(scratch + 32 + (n & 15) * kDiagRow + 8 * y + 4 * h) =
             make_float4(s[4 * y], s[4 * y + 1], s[4 * y + 2], s[4 * y + 3]);
     }
-    // the lanes' stores above are seen by the wave's reads below
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    wave_lds_fence();
     const float* p = scratch + 1 + 16 * half + lane;
 #pragma unroll
     for (int i = 0; i < 16; ++i) sum += p[(kDiagRow + 1) * i];
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    wave_lds_fence();
   }
   return sum;
 }

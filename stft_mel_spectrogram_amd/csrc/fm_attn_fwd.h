@@ -325,8 +325,10 @@ __global__ __launch_bounds__((attn_token_waves(sizeof(T), DP) * 64)) void attn_t
   float m = -INFINITY, l = 0.f;
 
   for (; j0 < k_end; j0 += NW * kTokenKeys) {
-    // the wave's own tile: its reads of the last round are done
+    // the wave's own tile, written by lanes for other lanes
+    wave_lds_fence();
     vl.store(vt, lane);
+    wave_lds_fence();
     acc4 s[2];
     const int dist = j0 - first;  // of key j0 to the first query
     const bool left = dist + kTokenKeys - 1 <= -a.far, right = dist - (a.q_len - 1) >= a.far;

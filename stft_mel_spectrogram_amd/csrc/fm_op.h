@@ -50,6 +50,14 @@ int lds_opt_in(K kernel, size_t bytes) {
              : FM_E_HIP;
 }
 
+// What the wave's lanes have stored in LDS is seen by its reads below, and what
+// they have read above is not yet overwritten.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // A 16-byte group of elements.  Loads and stores take any element-aligned
 // address: gfx950 runs with unaligned global access on, so one dwordx4
 // access serves rows of odd widths too.

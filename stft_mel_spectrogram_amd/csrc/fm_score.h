@@ -56,16 +56,10 @@ struct TopKeys {
   key_t last = 0;                // the least key kept, once there are `top`
   float bar = -INFINITY;         // entries below it need not be looked at
 
-  // stores of the wave's lanes are seen by its reads
-  __device__ __forceinline__ void settle() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-  }
   // Sorts what there is and keeps the first `top`.
   __device__ __forceinline__ void prune() {
     if (lane < 4) buf[count + lane] = 0;
-    settle();
+    wave_lds_fence();
     const key_t a = lane < count ? buf[lane] : 0, b = 64 + lane < count ? buf[64 + lane] : 0;
     int ra = 0, rb = 0;
     for (int i = 0; i < count; i += 4) {
@@ -77,10 +71,10 @@ struct TopKeys {
         rb += k[j] > b;
       }
     }
-    settle();
+    wave_lds_fence();
     if (a != 0 && ra < top) buf[ra] = a;
     if (b != 0 && rb < top) buf[rb] = b;
-    settle();
+    wave_lds_fence();
     if (count < top) return;
     count = top;
     last = buf[top - 1];

@@ -144,3 +144,19 @@ def test_a_bias_of_the_lowest_value_still_hides_a_key_from_others(tq, dtype):
     hidden = table.clone()
     hidden[2] = -math.inf
     assert torch.equal(relative_attention(q, k, v, table, m), relative_attention(q, k, v, hidden, m))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("tq", [1, 7])
+@pytest.mark.parametrize("tk", [300, 1500, 5000])
+def test_nan_past_the_lengths_of_a_cache(tk, tq, dtype):
+    """The kernel for few queries, in one range and in several."""
+    q, k, v, table, m, do = plain.make(2, 4, 2, tq, tk, 64, dtype, seed=tk, layout="bhtd")
+    ends = (tk - 37, tk // 3 + 1)
+    lengths = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    for how in (dict(lengths=lengths), dict(lengths=lengths, causal=True, offset=lengths - tq)):
+        clean = plain.run_case(q, k, v, table, m, do, backward=False, **how)
+        k2, v2 = k.clone(), v.clone()
+        for e, n in enumerate(ends):
+            k2[e, :, n:], v2[e, :, n:] = math.nan, math.inf
+        assert torch.equal(plain.run_case(q, k2, v2, table, m, do, backward=False, **how), clean)
