@@ -160,3 +160,22 @@ def test_nan_past_the_lengths_of_a_cache(tk, tq, dtype):
         for e, n in enumerate(ends):
             k2[e, :, n:], v2[e, :, n:] = math.nan, math.inf
         assert torch.equal(plain.run_case(q, k2, v2, table, m, do, backward=False, **how), clean)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("h,hk,t,d,far", [
+    (2, 2, 70, 40, 20), (4, 1, 300, 64, 60), (2, 2, 90, 33, 20), (2, 1, 140, 128, 300), (3, 3, 75, 96, 5),
+    # few query blocks: ranges of the keys
+    (2, 1, 1030, 64, 60), (1, 1, 515, 40, 20), (3, 3, 777, 33, 300), (2, 2, 900, 128, 20)])
+def test_gradients_without_the_tables(h, hk, t, d, far, dtype):
+    """A table that is not trained: dq from kernels of their own."""
+    from stft_mel_spectrogram_amd import relative_attention
+    q, k, v, table, m, do = plain.make(2, h, hk, t, t, d, dtype, seed=t, far=far)
+    for causal, second in ((False, t // 3), (True, t), (True, 0)):
+        lengths = torch.tensor([t, second], dtype=torch.int32, device="cuda")
+        leaves = [x.clone().requires_grad_(True) for x in (q, k, v)]
+        relative_attention(*leaves, table, m, causal=causal, key_lengths=lengths).backward(do)
+        grads, tols = plain.reference(q, k, v, table, m, do, d ** -0.5, causal, lengths,
+                                      torch.zeros(2, device="cuda"))[4:]
+        for leaf, name in zip(leaves, ("dq", "dk", "dv")):
+            plain.close(name, leaf.grad, grads[name], tols[name])
