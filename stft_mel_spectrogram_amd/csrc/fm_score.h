@@ -403,14 +403,22 @@ __global__ __launch_bounds__(256) void score_backward_kernel(
   if (g_top && !empty)
     for (int i = 0; i < top; ++i) all += g_top[row * top + i];
   const float ge = g_ent && !empty ? g_ent[row] : 0.f;
-  // -p (g_H (lp + H) + all) from y = lp in base 2 plus 64: the exponential then
-  // stays a normal number down to p = 2^-190, and 2^-64 goes into the factor
-  // (a gradient may lift what float32 holds as subnormal)
-  const float slope = -ge * kLn2 * 0x1p-64f;
-  const float base = -0x1p-64f * (all + (ge != 0.f ? ge * (ent[row] - 64.f * kLn2) : 0.f));
+  // -p (g_H (lp + H) + all), y = lp in base 2
+  const float slope = -ge * kLn2, base = -(all + (ge != 0.f ? ge * ent[row] : 0.f));
   const auto dense = [&](float xv) {
-    const float y = fmaf(xv - ls, kLog2e, 64.f);
-    return __builtin_amdgcn_exp2f(y) * fmaf(slope, fmaxf(y, -300.f), base);
+    const float y = (xv - ls) * kLog2e;
+    return __builtin_amdgcn_exp2f(y) * fmaf(slope, y, base);
+  };
+  // The exponential's results end at 2^-126, but a large gradient may lift smaller
+  // probabilities: these are computed 2^64 larger, down to 2^-190.  (For all entries
+  // the 64 in the argument would cost their last bits.)  Chunks without such an entry
+  // do without the distinction.
+  const float tiny = ls - 120.f * kLn2;  // well before 2^-126, as its own rounding goes
+  const auto dense_far = [&](float xv) {
+    const float y = (xv - ls) * kLog2e;
+    const bool small = y < -126.f;
+    const float p = __builtin_amdgcn_exp2f(small ? y + 64.f : y);
+    return p * fmaf(slope, fmaxf(y, -300.f), base) * (small ? 0x1p-64f : 1.f);
   };
   for (int c0 = beg; c0 < end; c0 += L * VE * V) {
     if (c0 > beg) {
@@ -420,13 +428,24 @@ __global__ __launch_bounds__(256) void score_backward_kernel(
         v[i] = load16_part(xr + c, end - c, (T)0.f);
       }
     }
+    float least = INFINITY;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = c0 + (i * L + tid) * VE;
+    for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int e = 0; e < VE; ++e) v[i].v[e] = (T)dense((float)v[i].v[e]);
-      store16_part(dr + c, v[i], end - c);
-    }
+      for (int e = 0; e < VE; ++e) least = fminf(least, (float)v[i].v[e]);
+    const auto put = [&](const auto& f) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = c0 + (i * L + tid) * VE;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) v[i].v[e] = (T)f((float)v[i].v[e]);
+        store16_part(dr + c, v[i], end - c);
+      }
+    };
+    if (__any(least < tiny))
+      put(dense_far);
+    else
+      put(dense);
     if constexpr (L < 256) break;
   }
   // The named tokens' entries, written again by the lane that wrote them
@@ -434,7 +453,7 @@ __global__ __launch_bounds__(256) void score_backward_kernel(
   // unrounded sum.
   const auto named = [&](int64_t j) {
     if (j < beg || j >= end || (int)(((j - beg) / VE) % L) != tid) return;
-    float d = dense((float)xr[j]);
+    float d = dense_far((float)xr[j]);
     if (tok == j) d += g;
     if (g_top)
       for (int i = 0; i < top; ++i)
