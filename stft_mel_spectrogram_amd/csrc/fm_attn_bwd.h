@@ -825,13 +825,15 @@ __global__ __launch_bounds__(kAttnThreads) void attn_dkv_join_kernel(const AttnA
 
 template <class T, int DP, bool VEC>
 int attn_backward_dim(const AttnArgs& a, void* stream) {
-  static const int opted =
-      lds_opt_in(attn_dq_kernel<T, DP, false, VEC, false>, attn_dq_lds<T, DP>(kAttnMaxFar, false)) |
-      lds_opt_in(attn_dq_kernel<T, DP, true, VEC, false>, attn_dq_lds<T, DP>(kAttnMaxFar, true)) |
-      lds_opt_in(attn_dq_kernel<T, DP, false, VEC, true>, attn_dq_lds<T, DP>(kAttnMaxFar, false)) |
-      lds_opt_in(attn_dq_kernel<T, DP, true, VEC, true>, attn_dq_lds<T, DP>(kAttnMaxFar, true)) |
-      lds_opt_in(attn_dkv_kernel<T, DP, VEC>, attn_dkv_lds<T, DP>(kAttnMaxFar));
-  if (opted != FM_OK) return set_error(FM_E_HIP, "attention backward: LDS size refused");
+  static DeviceOnce once;
+  const int opted = opted_in(once, [] {
+    return lds_opt_in(attn_dq_kernel<T, DP, false, VEC, false>, attn_dq_lds<T, DP>(kAttnMaxFar, false)) |
+           lds_opt_in(attn_dq_kernel<T, DP, true, VEC, false>, attn_dq_lds<T, DP>(kAttnMaxFar, true)) |
+           lds_opt_in(attn_dq_kernel<T, DP, false, VEC, true>, attn_dq_lds<T, DP>(kAttnMaxFar, false)) |
+           lds_opt_in(attn_dq_kernel<T, DP, true, VEC, true>, attn_dq_lds<T, DP>(kAttnMaxFar, true)) |
+           lds_opt_in(attn_dkv_kernel<T, DP, VEC>, attn_dkv_lds<T, DP>(kAttnMaxFar));
+  });
+  if (opted != FM_OK) return opted;
   const bool table = a.d_table != nullptr;
   if (a.q_len > 0) {
     const int st = launch("attention backward (dq)",

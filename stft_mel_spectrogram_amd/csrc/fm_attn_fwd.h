@@ -526,10 +526,12 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_rows_kernel(const Attn
 template <class T, int DP, bool VEC>
 int attn_forward_dim(const AttnArgs& a, void* stream) {
   if (attn_token_kernel(a)) {
-    static const int opted =
-        lds_opt_in(attn_token_kernel<T, DP, false, VEC>, attn_token_lds<T, DP>(kTokenBias)) |
-        lds_opt_in(attn_token_kernel<T, DP, true, VEC>, attn_token_lds<T, DP>(kTokenBias));
-    if (opted != FM_OK) return set_error(FM_E_HIP, "attention: LDS size refused");
+    static DeviceOnce once;
+    const int opted = opted_in(once, [] {
+      return lds_opt_in(attn_token_kernel<T, DP, false, VEC>, attn_token_lds<T, DP>(kTokenBias)) |
+             lds_opt_in(attn_token_kernel<T, DP, true, VEC>, attn_token_lds<T, DP>(kTokenBias));
+    });
+    if (opted != FM_OK) return opted;
     return launch("attention of few queries",
                   a.splits > 1 ? attn_token_kernel<T, DP, true, VEC>
                                : attn_token_kernel<T, DP, false, VEC>,
@@ -537,10 +539,12 @@ int attn_forward_dim(const AttnArgs& a, void* stream) {
                   dim3(64 * attn_token_waves(sizeof(T), DP)),
                   attn_token_lds<T, DP>(attn_token_bias(a)), stream, a);
   }
-  static const int opted =
-      lds_opt_in(attn_forward_kernel<T, DP, false, VEC>, attn_forward_lds<T, DP>(kAttnMaxFar)) |
-      lds_opt_in(attn_forward_kernel<T, DP, true, VEC>, attn_forward_lds<T, DP>(kAttnMaxFar));
-  if (opted != FM_OK) return set_error(FM_E_HIP, "attention: LDS size refused");
+  static DeviceOnce once;
+  const int opted = opted_in(once, [] {
+    return lds_opt_in(attn_forward_kernel<T, DP, false, VEC>, attn_forward_lds<T, DP>(kAttnMaxFar)) |
+           lds_opt_in(attn_forward_kernel<T, DP, true, VEC>, attn_forward_lds<T, DP>(kAttnMaxFar));
+  });
+  if (opted != FM_OK) return opted;
   return launch("attention",
                 a.splits > 1 ? attn_forward_kernel<T, DP, true, VEC>
                              : attn_forward_kernel<T, DP, false, VEC>,

@@ -40,7 +40,8 @@ typedef _Float16 f16_t;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Lets a kernel use `bytes` of dynamic LDS (over 64 KiB needs this).
+// Lets a kernel use `bytes` of dynamic LDS (over 64 KiB needs this) on the current
+// device.
 template <class K>
 int lds_opt_in(K kernel, size_t bytes) {
   return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
@@ -48,6 +49,13 @@ int lds_opt_in(K kernel, size_t bytes) {
                              static_cast<int>(bytes)) == hipSuccess
              ? FM_OK
              : FM_E_HIP;
+}
+// `opt_in()` of a set of kernels, once on each device that launches them.
+template <class F>
+int opted_in(DeviceOnce& once, F opt_in) {
+  int device = 0;
+  if (hipGetDevice(&device) != hipSuccess) return set_error(FM_E_HIP, "no current device");
+  return once(device, opt_in) == FM_OK ? FM_OK : set_error(FM_E_HIP, "attention: LDS size refused");
 }
 
 // What the wave's lanes have stored in LDS is seen by its reads below, and what

@@ -3,12 +3,30 @@
 // (fm_op_*.hip).  No HIP types, so that host-only builds can include it.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
 #include "fm_internal.h"
 
 namespace fm {
+
+// Work that each device needs once, such as a kernel's attributes.  What fails is
+// tried again by the next call; devices from 64 on do it every time.
+class DeviceOnce {
+ public:
+  template <class F>
+  int operator()(int device, F work) {
+    const uint64_t bit = device >= 0 && device < 64 ? uint64_t(1) << device : 0;
+    if (done_.load(std::memory_order_acquire) & bit) return FM_OK;
+    const int st = work();
+    if (st == FM_OK) done_.fetch_or(bit, std::memory_order_release);
+    return st;
+  }
+
+ private:
+  std::atomic<uint64_t> done_{0};
+};
 
 struct NormForward {
   const void* x;
