@@ -424,6 +424,8 @@ int fm_token_logprobs_backward(const void* x, int64_t x_stride, const void* toke
  *                head_dim]: strides in elements of (entry, head, time), >= 0,
  *                the last axis contiguous; heads a multiple of kv_heads, query
  *                head h reads key head h / (heads / kv_heads); head_dim <= 128;
+ *                batch * heads * (query blocks of 128) and batch * kv_heads *
+ *                (key blocks of 128) stay below about 2^24;
  *   scale        in [2^-60, 2^60];
  *   table        [num_buckets, heads] contiguous, table_dtype (dtype or
  *                FM_F32), num_buckets <= 1024; finite values beyond +-65536

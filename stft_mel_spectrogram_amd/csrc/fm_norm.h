@@ -406,9 +406,12 @@ int norm_forward_t(const NormForward& a) {
     }
   FM_NORM_SHAPES(FM_NORM_FWD)
 #undef FM_NORM_FWD
-  return launch("layer norm forward", norm_forward_wide_kernel<T, W>, dim3((unsigned)a.rows),
-                dim3(kNormWide), 0, a.stream, (const T*)a.x, a.x_stride, (const W*)a.weight,
-                (const W*)a.bias, (T*)a.y, a.mean, a.rstd, a.rows, a.width, a.eps);
+  return by_rows(a.rows, kGridThreads / kNormWide, [&](int64_t at, int64_t rows) {
+    return launch("layer norm forward", norm_forward_wide_kernel<T, W>, dim3((unsigned)rows),
+                  dim3(kNormWide), 0, a.stream, (const T*)a.x + at * a.x_stride, a.x_stride,
+                  (const W*)a.weight, (const W*)a.bias, (T*)a.y + at * a.width,
+                  a.mean ? a.mean + at : nullptr, a.rstd ? a.rstd + at : nullptr, rows, a.width, a.eps);
+  });
 }
 
 template <class T, class W>
@@ -421,9 +424,12 @@ int norm_backward_t(const NormBackward& a) {
   if (a.rows > 0) {
     int st = FM_OK;
     if (s.vpl == 0)
-      st = launch("layer norm backward", norm_backward_wide_kernel<T, W>, dim3((unsigned)a.rows),
-                  dim3(kNormWide), 0, a.stream, (const T*)a.dy, a.dy_stride, (const T*)a.x,
-                  a.x_stride, (const W*)a.weight, a.mean, a.rstd, (T*)a.dx, a.rows, a.width);
+      st = by_rows(a.rows, kGridThreads / kNormWide, [&](int64_t at, int64_t rows) {
+        return launch("layer norm backward", norm_backward_wide_kernel<T, W>, dim3((unsigned)rows),
+                      dim3(kNormWide), 0, a.stream, (const T*)a.dy + at * a.dy_stride, a.dy_stride,
+                      (const T*)a.x + at * a.x_stride, a.x_stride, (const W*)a.weight, a.mean + at,
+                      a.rstd + at, (T*)a.dx + at * a.width, rows, a.width);
+      });
 #define FM_NORM_BWD(L, V)                                                                      \
   if constexpr (V * VE <= norm_most(L))                                                                  \
     if (s.lpr == L && s.vpl == V)                                                              \

@@ -112,10 +112,7 @@ int attention_args(const fm_attention_args* p, bool backward, AttnArgs& a) {
       (backward && (!strides_fit(a.dos) || !strides_fit(a.dqs) || !strides_fit(a.dks) || !strides_fit(a.dvs))))
     return bad("attention: strides must be >= 0");
   // grids: query blocks x heads, key blocks x key heads, rows of the join
-  const int64_t q_units = (a.q_len + int64_t(127)) / 128 * a.batch * a.heads;
-  const int64_t k_units = (a.k_len + int64_t(127)) / 128 * a.batch * a.kv_heads;
-  if (q_units >= most || k_units >= most || attn_rows(a) >= most)
-    return bad("attention: too many rows for one launch");
+  if (!attn_fits_grids(a)) return bad("attention: too many rows for one launch");
   a.o = p->o;
   a.lse = p->lse;
   a.d_o = p->grad_o;

@@ -28,6 +28,19 @@ class DeviceOnce {
   std::atomic<uint64_t> done_{0};
 };
 
+// A grid may have fewer than 2^32 threads in a dimension.  Calls launch(first, count)
+// for consecutive ranges of at most `most` rows; kGridThreads over a row's threads is
+// such a number of rows.
+constexpr int64_t kGridThreads = int64_t(1) << 31;
+template <class F>
+int by_rows(int64_t rows, int64_t most, F launch) {
+  for (int64_t at = 0; at < rows; at += most) {
+    const int st = launch(at, rows - at < most ? rows - at : most);
+    if (st != FM_OK) return st;
+  }
+  return FM_OK;
+}
+
 struct NormForward {
   const void* x;
   int64_t x_stride;  // elements between rows
@@ -354,6 +367,20 @@ inline AttnBackwardSpace attn_backward_space(const AttnArgs& a, bool f16) {
   s.row = s.dq + (ranges == 1 ? 0 : attn_round16(4 * ranges * attn_rows(a) * a.dim));
   s.total = s.row + (ranges == 1 ? 0 : 12 * ranges * attn_rows(a));
   return s;
+}
+
+// Whether a call's grids stay below 2^32 threads (units rounded up to the 8 XCDs).
+inline bool attn_fits_grids(const AttnArgs& a) {
+  const auto fits = [](int64_t units, int64_t blocks, int threads) {
+    const int64_t most = (int64_t(1) << 32) / threads;
+    return units < most && blocks < most && units * blocks < most;
+  };
+  const int64_t units = (int64_t)a.batch * a.kv_heads + 7, group = a.heads / a.kv_heads;
+  const int64_t queries = (a.q_len + (int64_t)kAttnQueries - 1) / kAttnQueries;
+  const int64_t keys = (a.k_len + (int64_t)kAttnBlockKeys - 1) / kAttnBlockKeys;
+  const int dp = a.dim <= 64 ? 64 : a.dim <= 96 ? 96 : 128;
+  return fits(units, queries * group, 256) && fits(units, keys, 256) &&
+         (!attn_token_kernel(a) || fits(units, attn_token_blocks(a), 64 * attn_token_waves(a.size, dp)));
 }
 
 // Whether rows are whole, aligned 16-byte groups and a block of them lies

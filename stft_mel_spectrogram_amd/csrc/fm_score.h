@@ -469,41 +469,59 @@ __global__ __launch_bounds__(256) void score_backward_kernel(
 #define FM_SCORE_SHAPES(X) X(16, 1) X(16, 2) X(16, 4) X(64, 2) X(64, 4)
 #define FM_SCORE_TOP_SHAPES(X) X(64, 1) X(64, 2) X(64, 4)
 
+// The part of a call from row `at` on.
+inline const void* score_tokens(const void* tokens, int tok64, int64_t at) {
+  return (const char*)tokens + at * (tok64 ? 8 : 4);
+}
+template <class P>
+P* score_rows(P* p, int64_t at) {
+  return p ? p + at : nullptr;
+}
+
 template <class T>
 int score_forward_t(const ScoreForward& a) {
   const ScoreSplit p = score_split(a.rows, a.vocab, Vec16<T>::n, a.top);
-  ScoreOut out = {a.lp, a.ent, a.lse, a.top_ids, a.top_lp};
-#define FM_SCORE_ROW(L, V)                                                                        \
+  const auto out_at = [&](int64_t at) {
+    return ScoreOut{score_rows(a.lp, at), score_rows(a.ent, at), score_rows(a.lse, at),
+                    score_rows(a.top_ids, at * a.top), score_rows(a.top_lp, at * a.top)};
+  };
+#define FM_SCORE_ROW(L, V, TOP)                                                                    \
   if (p.lanes == L && p.vecs == V)                                                                \
-    return launch("token log probabilities", score_row_kernel<T, L, V, false>,                    \
-                  dim3((unsigned)((a.rows + 256 / L - 1) / (256 / L))), dim3(256), 0, a.stream,   \
-                  (const T*)a.x, a.x_stride, a.tokens, a.tok64, out, a.rows, a.vocab, a.top);
-#define FM_SCORE_TOP_ROW(L, V)                                                                    \
-  if (p.lanes == L && p.vecs == V)                                                                \
-    return launch("token log probabilities", score_row_kernel<T, L, V, true>,                     \
-                  dim3((unsigned)((a.rows + 256 / L - 1) / (256 / L))), dim3(256), 0, a.stream,   \
-                  (const T*)a.x, a.x_stride, a.tokens, a.tok64, out, a.rows, a.vocab, a.top);
+    return by_rows(a.rows, kGridThreads / L, [&](int64_t at, int64_t rows) {                      \
+      return launch("token log probabilities", score_row_kernel<T, L, V, TOP>,                    \
+                    dim3((unsigned)((rows + 256 / L - 1) / (256 / L))), dim3(256), 0, a.stream,   \
+                    (const T*)a.x + at * a.x_stride, a.x_stride,                                  \
+                    score_tokens(a.tokens, a.tok64, at), a.tok64, out_at(at), rows, a.vocab,      \
+                    a.top);                                                                       \
+    });
+#define FM_SCORE_PLAIN_ROW(L, V) FM_SCORE_ROW(L, V, false)
+#define FM_SCORE_TOP_ROW(L, V) FM_SCORE_ROW(L, V, true)
   if (a.top == 0) {
-    FM_SCORE_SHAPES(FM_SCORE_ROW)
+    FM_SCORE_SHAPES(FM_SCORE_PLAIN_ROW)
   } else {
     FM_SCORE_TOP_SHAPES(FM_SCORE_TOP_ROW)
   }
-#undef FM_SCORE_ROW
+#undef FM_SCORE_PLAIN_ROW
 #undef FM_SCORE_TOP_ROW
+#undef FM_SCORE_ROW
   float* part = (float*)a.workspace;
   key_t* keys = (key_t*)((char*)a.workspace + score_part_bytes(a.rows, p.segs));
   const auto go = [&](auto kernel) {
-    return launch("token log probabilities", kernel, dim3((unsigned)(a.rows * p.segs)), dim3(256), 0,
-                  a.stream, (const T*)a.x, a.x_stride, a.tokens, a.tok64, out, part, keys, a.vocab,
-                  a.top, p.seg_len, p.segs);
+    return by_rows(a.rows, kGridThreads / 256 / p.segs, [&](int64_t at, int64_t rows) {
+      return launch("token log probabilities", kernel, dim3((unsigned)(rows * p.segs)), dim3(256), 0,
+                    a.stream, (const T*)a.x + at * a.x_stride, a.x_stride,
+                    score_tokens(a.tokens, a.tok64, at), a.tok64, out_at(at), part + at * p.segs * 3,
+                    keys + at * p.segs * a.top, a.vocab, a.top, p.seg_len, p.segs);
+    });
   };
   const int st = p.vecs == 1 ? (a.top ? go(score_forward_kernel<T, 1, true>)
                                       : go(score_forward_kernel<T, 1, false>))
                              : (a.top ? go(score_forward_kernel<T, 4, true>)
                                       : go(score_forward_kernel<T, 4, false>));
   if (st != FM_OK || p.segs == 1) return st;
+  // few rows: more than one segment each
   return launch("token log probabilities (join)", score_join_kernel<T>, dim3((unsigned)a.rows),
-                dim3(64), 0, a.stream, (const T*)a.x, a.x_stride, a.tokens, a.tok64, out, part, keys,
+                dim3(64), 0, a.stream, (const T*)a.x, a.x_stride, a.tokens, a.tok64, out_at(0), part, keys,
                 a.vocab, a.top, p.segs);
 }
 
@@ -512,11 +530,15 @@ int score_backward_t(const ScoreBackward& a) {
   const ScoreSplit p = score_split(a.rows, a.vocab, Vec16<T>::n, 0);
 #define FM_SCORE_BWD(L, V)                                                                        \
   if (p.lanes == L && (L < 256 ? p.vecs == V : true))                                             \
-    return launch("token log probabilities backward", score_backward_kernel<T, L, V>,             \
-                  dim3((unsigned)((a.rows * p.segs + 256 / L - 1) / (256 / L))), dim3(256), 0,    \
-                  a.stream, (const T*)a.x, a.x_stride, a.tokens, a.tok64, a.lse, a.ent, a.g_lp,   \
-                  a.g_ent, a.top_ids, a.g_top, (T*)a.dx, a.rows, a.vocab, a.top, p.seg_len,       \
-                  p.segs);
+    return by_rows(a.rows, kGridThreads / L / p.segs, [&](int64_t at, int64_t rows) {             \
+      return launch("token log probabilities backward", score_backward_kernel<T, L, V>,           \
+                    dim3((unsigned)((rows * p.segs + 256 / L - 1) / (256 / L))), dim3(256), 0,    \
+                    a.stream, (const T*)a.x + at * a.x_stride, a.x_stride,                        \
+                    score_tokens(a.tokens, a.tok64, at), a.tok64, a.lse + at,                     \
+                    score_rows(a.ent, at), score_rows(a.g_lp, at), score_rows(a.g_ent, at),       \
+                    score_rows(a.top_ids, at * a.top), score_rows(a.g_top, at * a.top),           \
+                    (T*)a.dx + at * a.vocab, rows, a.vocab, a.top, p.seg_len, p.segs);            \
+    });
   FM_SCORE_SHAPES(FM_SCORE_BWD)
   FM_SCORE_BWD(256, 4)
 #undef FM_SCORE_BWD

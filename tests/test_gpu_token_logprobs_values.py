@@ -88,3 +88,32 @@ def test_the_largest_vocabulary():
     # the other gradients are subnormal in float16
     tail = dx[0, vocab - 20000:vocab - 1].double()
     assert ((tail + g * math.exp(-want)).abs() <= 2.0 ** -25 + 2 * tol * g * math.exp(-want)).all()
+
+
+def test_more_rows_than_one_launch_takes():
+    """2^26 rows of 64 lanes are 2^32 threads, more than a grid may have."""
+    from stft_mel_spectrogram_amd import token_logprobs
+    rows = (1 << 26) + 5
+    x = torch.zeros(rows, 2, dtype=torch.float16, device="cuda")
+    x[:, 1] = 1.0
+    x[rows - 3:] = torch.tensor([3.0, 0.0], device="cuda")
+    tok = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    r = token_logprobs(x, tok, 1)
+    assert bool((r.top_ids[:rows - 3] == 1).all()) and bool((r.top_ids[rows - 3:] == 0).all())
+    want = -math.log1p(math.e)
+    assert bool(((r.logprobs[:rows - 3] - want).abs() <= 1e-6).all())
+    assert bool(((r.logprobs[rows - 3:] + math.log1p(math.exp(-3.0))).abs() <= 1e-6).all())
+
+
+def test_more_rows_than_one_gradient_launch_takes():
+    """2^28 rows of 16 lanes."""
+    from stft_mel_spectrogram_amd import token_logprobs_backward
+    rows = (1 << 28) + 5
+    x = torch.zeros(rows, 2, dtype=torch.float16, device="cuda")
+    tok = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    tok[rows - 3:] = 1
+    lse = torch.full((rows,), math.log(2.0), device="cuda")
+    g = torch.ones(rows, device="cuda")
+    dx = token_logprobs_backward(x, tok, lse, lse, g)
+    assert bool((dx[:rows - 3, 0] == 0.5).all()) and bool((dx[:rows - 3, 1] == -0.5).all())
+    assert dx[rows - 3:].tolist() == [[-0.5, 0.5]] * 3
