@@ -3,16 +3,27 @@ a strided tensor, the launch on a tensor's device and torch's current stream."""
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _native as N
 
 DTYPES = {torch.float32: N.FM_F32, torch.float16: N.FM_F16, torch.bfloat16: N.FM_BF16}
 
 
+def _no_tangent(x: torch.Tensor, name: str) -> None:
+    """The operators have no forward-mode derivative: a dual number's tangent
+    would be lost without a word."""
+    if forward_ad.unpack_dual(x).tangent is not None:
+        raise NotImplementedError(f"{name} carries a forward-mode tangent, which the operators do not "
+                                  "propagate")
+
+
 def dtype_code(x: torch.Tensor, name: str) -> int:
     """The library's code of x's element type; x must be a GPU tensor."""
     if not isinstance(x, torch.Tensor):
         raise ValueError(f"{name} must be a tensor, got {type(x).__name__}")
+    if forward_ad._current_level >= 0:
+        _no_tangent(x, name)
     if not x.is_cuda:
         raise ValueError(f"{name} must be on a GPU, got {x.device}")
     code = DTYPES.get(x.dtype)
@@ -54,6 +65,8 @@ def same_device(x: torch.Tensor, **others) -> None:
             continue
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} must be a tensor, got {type(t).__name__}")
+        if forward_ad._current_level >= 0:
+            _no_tangent(t, name)
         if t.get_device() != dev:
             raise ValueError(f"{name} must be on {x.device}, got {t.device}")
 
