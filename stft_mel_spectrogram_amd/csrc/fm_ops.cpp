@@ -55,8 +55,9 @@ bool strides_fit(const int64_t* s) {
   return true;
 }
 
-// Checks what forward and backward share and translates the public struct.
-int attention_args(const fm_attention_args* p, bool backward, AttnArgs& a) {
+// Checks what every call shares (a workspace's size depends on no more) and
+// translates the public struct.
+int attention_args(const fm_attention_args* p, AttnArgs& a) {
   if (!p) return bad("attention: args must not be NULL");
   if (!elem_size(p->dtype)) return bad("attention: dtype must be FM_F32, FM_F16 or FM_BF16");
   if (p->table_dtype != p->dtype && p->table_dtype != FM_F32)
@@ -108,9 +109,6 @@ int attention_args(const fm_attention_args* p, bool backward, AttnArgs& a) {
     a.dks[i] = p->grad_k_stride[i];
     a.dvs[i] = p->grad_v_stride[i];
   }
-  if (!strides_fit(a.qs) || !strides_fit(a.ks) || !strides_fit(a.vs) || !strides_fit(a.os) ||
-      (backward && (!strides_fit(a.dos) || !strides_fit(a.dqs) || !strides_fit(a.dks) || !strides_fit(a.dvs))))
-    return bad("attention: strides must be >= 0");
   // grids: query blocks x heads, key blocks x key heads, rows of the join
   if (!attn_fits_grids(a)) return bad("attention: too many rows for one launch");
   a.o = p->o;
@@ -124,8 +122,11 @@ int attention_args(const fm_attention_args* p, bool backward, AttnArgs& a) {
   return FM_OK;
 }
 
-// The pointers of a call: what it reads must exist, elements aligned.
-int attention_pointers(const AttnArgs& a, int dtype) {
+// The strides and pointers of a call: what it reads must exist, elements aligned.
+int attention_pointers(const AttnArgs& a, int dtype, bool backward) {
+  if (!strides_fit(a.qs) || !strides_fit(a.ks) || !strides_fit(a.vs) || !strides_fit(a.os) ||
+      (backward && (!strides_fit(a.dos) || !strides_fit(a.dqs) || !strides_fit(a.dks) || !strides_fit(a.dvs))))
+    return bad("attention: strides must be >= 0");
   if (!a.table || !a.map) return bad("attention: table and bucket_map must not be NULL");
   const int es = elem_size(dtype);
   const bool q = attn_rows(a) > 0, k = q && a.k_len > 0;
@@ -264,7 +265,7 @@ int fm_token_logprobs_backward(const void* x, int64_t x_stride, const void* toke
 
 int64_t fm_attention_workspace(const fm_attention_args* args, int backward) try {
   fm::AttnArgs a;
-  if (int st = fm::attention_args(args, backward != 0, a)) return st;
+  if (int st = fm::attention_args(args, a)) return st;
   return backward ? fm::attn_backward_space(a, args->dtype == FM_F16).total
                   : fm::attn_forward_workspace(a);
 } catch (...) {
@@ -273,8 +274,8 @@ int64_t fm_attention_workspace(const fm_attention_args* args, int backward) try 
 
 int fm_attention_forward(const fm_attention_args* args, void* workspace, void* stream) try {
   fm::AttnArgs a;
-  if (int st = fm::attention_args(args, false, a)) return st;
-  if (int st = fm::attention_pointers(a, args->dtype)) return st;
+  if (int st = fm::attention_args(args, a)) return st;
+  if (int st = fm::attention_pointers(a, args->dtype, false)) return st;
   if (fm::attn_rows(a) == 0) return FM_OK;
   if (a.splits > 1) {
     if (!workspace || !fm::aligned(workspace, 16))
@@ -290,8 +291,8 @@ int fm_attention_forward(const fm_attention_args* args, void* workspace, void* s
 
 int fm_attention_backward(const fm_attention_args* args, void* workspace, void* stream) try {
   fm::AttnArgs a;
-  if (int st = fm::attention_args(args, true, a)) return st;
-  if (int st = fm::attention_pointers(a, args->dtype)) return st;
+  if (int st = fm::attention_args(args, a)) return st;
+  if (int st = fm::attention_pointers(a, args->dtype, true)) return st;
   const bool rows = fm::attn_rows(a) > 0;
   if (rows && (!a.lse || !a.d_o || !a.dq)) return bad("attention: lse, grad_o and grad_q must not be NULL");
   if (a.batch > 0 && a.k_len > 0 && (!a.k || !a.v || !a.dk || !a.dv))
