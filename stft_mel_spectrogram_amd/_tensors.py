@@ -58,10 +58,12 @@ def rows_of(x: torch.Tensor, name: str):
     return rows, width, width if stride is None else stride
 
 
-def same_device(x: torch.Tensor, **others) -> None:
+def same_device(x: torch.Tensor, optional: tuple = (), **others) -> None:
+    """Checks that the others are tensors on x's device; those named in
+    `optional` may be None."""
     dev = x.get_device()
     for name, t in others.items():
-        if t is None:
+        if t is None and name in optional:
             continue
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} must be a tensor, got {type(t).__name__}")

@@ -76,8 +76,8 @@ class _Call:
             offset = query_offset
         else:
             offset_value = int(query_offset)
-        T.same_device(q, k=k, v=v, table=table, buckets=buckets, key_lengths=key_lengths,
-                      query_offset=offset)
+        T.same_device(q, ("key_lengths", "query_offset"), k=k, v=v, table=table, buckets=buckets,
+                      key_lengths=key_lengths, query_offset=offset)
         shape, kshape = q.shape, k.shape
         if len(shape) != 4 or len(kshape) != 4 or v.dim() != 4:
             raise ValueError("q, k and v must be [batch, heads, time, head_dim]")

@@ -19,7 +19,7 @@ def _check(x, weight, bias):
     rows, width, stride = T.rows_of(x, "x")
     pcode = code
     if weight is not None:
-        T.same_device(x, weight=weight, bias=bias)
+        T.same_device(x, ("bias",), weight=weight, bias=bias)
         pcode = T.dtype_code(weight, "weight")
         if pcode not in (code, N.FM_F32):
             raise TypeError(f"weight must be {x.dtype} or float32, got {weight.dtype}")

@@ -72,10 +72,11 @@ def token_logprobs_backward(logits, tokens, lse, entropy, grad_logprobs=None, gr
     """The logits' gradient of sum(grad_logprobs * logprobs) + sum(grad_entropy
     * entropy) + sum(grad_top_logprobs * top_logprobs); float32 gradients, None
     where there is none."""
-    top_k = 0 if top_ids is None else top_ids.shape[-1]
+    top_k = top_ids.shape[-1] if isinstance(top_ids, torch.Tensor) and top_ids.dim() else 0
     code, rows, vocab, stride, bits, top_k = _check(logits, tokens, top_k)
     lead = logits.shape[:-1]
-    T.same_device(logits, lse=lse, entropy=entropy, grad_logprobs=grad_logprobs,
+    T.same_device(logits, ("entropy", "grad_logprobs", "grad_entropy", "top_ids", "grad_top_logprobs"),
+                  lse=lse, entropy=entropy, grad_logprobs=grad_logprobs,
                   grad_entropy=grad_entropy, top_ids=top_ids, grad_top_logprobs=grad_top_logprobs)
     for name, t in (("lse", lse), ("entropy", entropy), ("grad_logprobs", grad_logprobs),
                     ("grad_entropy", grad_entropy)):
