@@ -75,6 +75,8 @@ def token_logprobs_backward(logits, tokens, lse, entropy, grad_logprobs=None, gr
     top_k = top_ids.shape[-1] if isinstance(top_ids, torch.Tensor) and top_ids.dim() else 0
     code, rows, vocab, stride, bits, top_k = _check(logits, tokens, top_k)
     lead = logits.shape[:-1]
+    if grad_entropy is not None and entropy is None:
+        raise ValueError("grad_entropy needs entropy")
     T.same_device(logits, ("entropy", "grad_logprobs", "grad_entropy", "top_ids", "grad_top_logprobs"),
                   lse=lse, entropy=entropy, grad_logprobs=grad_logprobs,
                   grad_entropy=grad_entropy, top_ids=top_ids, grad_top_logprobs=grad_top_logprobs)

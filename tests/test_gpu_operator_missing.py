@@ -19,7 +19,7 @@ def refuses(fn, args, optional, **kw):
             fn(*with_none, **kw)
             continue
         for bad in (None, 3.0):
-            with pytest.raises(ValueError, match="must be a tensor"):
+            with pytest.raises(ValueError):
                 fn(*(bad if j == i else a for j, a in enumerate(args)), **kw)
 
 
