@@ -411,6 +411,24 @@ int fm_token_logprobs_backward(const void* x, int64_t x_stride, const void* toke
                                int dtype, void* stream);
 
 /*
+ * fm_token_logprobs_strided, fm_token_logprobs_backward_strided -- the same for
+ * logits whose rows lie in groups, such as all but the last position of every
+ * entry: x_stride elements from row to row of a group of x_inner rows, x_outer
+ * elements from group to group.  x_inner 0: all rows at x_stride.  Everything
+ * else is contiguous as above.
+ */
+int fm_token_logprobs_strided(const void* x, int64_t x_stride, int64_t x_inner, int64_t x_outer,
+                              const void* tokens, int token_bits, float* lp, float* ent, float* lse,
+                              int64_t* top_ids, float* top_lp, void* workspace, int64_t rows,
+                              int64_t vocab, int top, int dtype, void* stream);
+int fm_token_logprobs_backward_strided(const void* x, int64_t x_stride, int64_t x_inner,
+                                       int64_t x_outer, const void* tokens, int token_bits,
+                                       const float* lse, const float* ent, const float* g_lp,
+                                       const float* g_ent, const int64_t* top_ids, const float* g_top,
+                                       void* dx, int64_t rows, int64_t vocab, int top, int dtype,
+                                       void* stream);
+
+/*
  * fm_attention_args -- attention with a learned relative position bias:
  *
  *   s[i, j] = scale * q[i].k[j] + table[bucket_map[far + clamp(j - pos(i), -far, far)]][head]

@@ -112,6 +112,9 @@ def _load() -> ctypes.CDLL:
         "fm_token_logprobs_workspace": (I64, [I64, I64, I, I]),
         "fm_token_logprobs": (I, [P, I64, P, I, P, P, P, P, P, P, I64, I64, I, I, P]),
         "fm_token_logprobs_backward": (I, [P, I64, P, I, P, P, P, P, P, P, P, I64, I64, I, I, P]),
+        "fm_token_logprobs_strided": (I, [P, I64, I64, I64, P, I, P, P, P, P, P, P, I64, I64, I, I, P]),
+        "fm_token_logprobs_backward_strided": (I, [P, I64, I64, I64, P, I, P, P, P, P, P, P, P, I64, I64, I, I,
+                                                   P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)

@@ -58,16 +58,41 @@ def rows_of(x: torch.Tensor, name: str):
     return rows, width, width if stride is None else stride
 
 
+def grouped_rows_of(x: torch.Tensor, name: str):
+    """(rows, width, elements between rows) of x's last axis, and (rows of a
+    group, elements between groups) besides where its rows lie at two strides."""
+    if x.is_contiguous() or x.dim() < 3 or x.numel() == 0:
+        return rows_of(x, name)
+    width = x.shape[-1]
+    if width > 1 and x.stride(-1) != 1:
+        raise ValueError(f"{name}'s last axis must be contiguous")
+    groups = []  # (rows, stride), the last axis's first
+    for size, st in zip(reversed(x.shape[:-1]), reversed(x.stride()[:-1])):
+        if size == 1:
+            continue
+        if groups and st == groups[-1][1] * groups[-1][0]:
+            groups[-1] = (groups[-1][0] * size, groups[-1][1])
+        else:
+            groups.append((size, st))
+    if len(groups) > 2:
+        raise ValueError(f"{name}'s leading axes must lie at one or two strides (make it contiguous)")
+    rows = x.numel() // width
+    if len(groups) < 2:
+        return rows, width, groups[0][1] if groups else width
+    return rows, width, groups[0][1], groups[0][0], groups[1][1]
+
+
 def same_device(x: torch.Tensor, optional: tuple = (), **others) -> None:
     """Checks that the others are tensors on x's device; those named in
     `optional` may be None."""
     dev = x.get_device()
+    duals = forward_ad._current_level >= 0
     for name, t in others.items():
         if t is None and name in optional:
             continue
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} must be a tensor, got {type(t).__name__}")
-        if forward_ad._current_level >= 0:
+        if duals:
             _no_tangent(t, name)
         if t.get_device() != dev:
             raise ValueError(f"{name} must be on {x.device}, got {t.device}")

@@ -49,6 +49,13 @@ int check_scores(int64_t rows, int64_t vocab, int top, int dtype) {
   return FM_OK;
 }
 
+int check_score_strides(int64_t rows, int64_t stride, int64_t inner, int64_t outer) {
+  if (rows > 1 && stride < 0) return bad("token log probabilities: x_stride must be >= 0");
+  if (inner < 0 || inner >= int64_t(1) << 31 || (inner > 0 && outer < 0))
+    return bad("token log probabilities: x_inner must be in [0, 2^31) and x_outer >= 0");
+  return FM_OK;
+}
+
 bool strides_fit(const int64_t* s) {
   for (int i = 0; i < 3; ++i)
     if (s[i] < 0) return false;
@@ -212,10 +219,10 @@ int64_t fm_token_logprobs_workspace(int64_t rows, int64_t vocab, int top, int dt
   return FM_E_NOMEM;
 }
 
-int fm_token_logprobs(const void* x, int64_t x_stride, const void* tokens, int token_bits,
-                      float* lp, float* ent, float* lse, int64_t* top_ids, float* top_lp,
-                      void* workspace, int64_t rows, int64_t vocab, int top, int dtype,
-                      void* stream) try {
+int fm_token_logprobs_strided(const void* x, int64_t x_stride, int64_t x_inner, int64_t x_outer,
+                              const void* tokens, int token_bits, float* lp, float* ent, float* lse,
+                              int64_t* top_ids, float* top_lp, void* workspace, int64_t rows,
+                              int64_t vocab, int top, int dtype, void* stream) try {
   if (int st = fm::check_scores(rows, vocab, top, dtype)) return st;
   if (token_bits != 64 && token_bits != 32)
     return bad("token log probabilities: token_bits must be 32 or 64");
@@ -223,25 +230,26 @@ int fm_token_logprobs(const void* x, int64_t x_stride, const void* tokens, int t
   if (!x || !tokens) return bad("token log probabilities: x and tokens must not be NULL");
   if (top > 0 && (!top_ids || !top_lp))
     return bad("token log probabilities: top_ids and top_lp must not be NULL");
-  if (rows > 1 && x_stride < 0) return bad("token log probabilities: x_stride must be >= 0");
+  if (int st = fm::check_score_strides(rows, x_stride, x_inner, x_outer)) return st;
   if (!fm::aligned(x, fm::elem_size(dtype)) || !fm::aligned(tokens, token_bits / 8))
     return bad("token log probabilities: misaligned pointer");
   if (fm::score_workspace(rows, static_cast<int>(vocab), top, fm::vec_elems(dtype)) > 0 &&
       (!workspace || !fm::aligned(workspace, 16)))
     return bad("token log probabilities: the workspace must be 16-byte aligned device memory");
-  const fm::ScoreForward a = {x,      x_stride,  tokens, token_bits == 64, lp,  ent,   lse, top_ids,
-                              top_lp, workspace, rows,   static_cast<int>(vocab), top, stream};
+  const fm::ScoreForward a = {x, x_stride, x_inner, x_outer, tokens, token_bits == 64, lp, ent, lse, top_ids,
+                              top_lp, workspace, rows, static_cast<int>(vocab), top, stream};
   if (dtype == FM_F32) return fm::score_forward_f32(a);
   return dtype == FM_F16 ? fm::score_forward_f16(a) : fm::score_forward_bf16(a);
 } catch (...) {
   return FM_E_NOMEM;
 }
 
-int fm_token_logprobs_backward(const void* x, int64_t x_stride, const void* tokens,
-                               int token_bits, const float* lse, const float* ent,
-                               const float* g_lp, const float* g_ent, const int64_t* top_ids,
-                               const float* g_top, void* dx, int64_t rows, int64_t vocab, int top,
-                               int dtype, void* stream) try {
+int fm_token_logprobs_backward_strided(const void* x, int64_t x_stride, int64_t x_inner,
+                                       int64_t x_outer, const void* tokens, int token_bits,
+                                       const float* lse, const float* ent, const float* g_lp,
+                                       const float* g_ent, const int64_t* top_ids, const float* g_top,
+                                       void* dx, int64_t rows, int64_t vocab, int top, int dtype,
+                                       void* stream) try {
   if (int st = fm::check_scores(rows, vocab, top, dtype)) return st;
   if (token_bits != 64 && token_bits != 32)
     return bad("token log probabilities: token_bits must be 32 or 64");
@@ -250,17 +258,34 @@ int fm_token_logprobs_backward(const void* x, int64_t x_stride, const void* toke
     return bad("token log probabilities: x, tokens, lse and dx must not be NULL");
   if (g_ent && !ent) return bad("token log probabilities: g_ent needs ent");
   if (g_top && (!top_ids || top < 1)) return bad("token log probabilities: g_top needs top_ids");
-  if (rows > 1 && x_stride < 0) return bad("token log probabilities: x_stride must be >= 0");
+  if (int st = fm::check_score_strides(rows, x_stride, x_inner, x_outer)) return st;
   const int es = fm::elem_size(dtype);
   if (!fm::aligned(x, es) || !fm::aligned(dx, es) || !fm::aligned(tokens, token_bits / 8))
     return bad("token log probabilities: misaligned pointer");
-  const fm::ScoreBackward a = {x,    x_stride, tokens,  token_bits == 64, lse, ent,
-                               g_lp, g_ent,    top_ids, g_top,            dx,  rows,
-                               static_cast<int>(vocab), top, stream};
+  const fm::ScoreBackward a = {x,   x_stride, x_inner, x_outer, tokens, token_bits == 64,
+                               lse, ent,      g_lp,    g_ent,   top_ids, g_top,
+                               dx,  rows,     static_cast<int>(vocab), top, stream};
   if (dtype == FM_F32) return fm::score_backward_f32(a);
   return dtype == FM_F16 ? fm::score_backward_f16(a) : fm::score_backward_bf16(a);
 } catch (...) {
   return FM_E_NOMEM;
+}
+
+int fm_token_logprobs(const void* x, int64_t x_stride, const void* tokens, int token_bits,
+                      float* lp, float* ent, float* lse, int64_t* top_ids, float* top_lp,
+                      void* workspace, int64_t rows, int64_t vocab, int top, int dtype,
+                      void* stream) {
+  return fm_token_logprobs_strided(x, x_stride, 0, 0, tokens, token_bits, lp, ent, lse, top_ids, top_lp,
+                                   workspace, rows, vocab, top, dtype, stream);
+}
+
+int fm_token_logprobs_backward(const void* x, int64_t x_stride, const void* tokens,
+                               int token_bits, const float* lse, const float* ent,
+                               const float* g_lp, const float* g_ent, const int64_t* top_ids,
+                               const float* g_top, void* dx, int64_t rows, int64_t vocab, int top,
+                               int dtype, void* stream) {
+  return fm_token_logprobs_backward_strided(x, x_stride, 0, 0, tokens, token_bits, lse, ent, g_lp, g_ent,
+                                            top_ids, g_top, dx, rows, vocab, top, dtype, stream);
 }
 
 int64_t fm_attention_workspace(const fm_attention_args* args, int backward) try {

@@ -140,7 +140,9 @@ int norm_backward_bf16(const NormBackward& a, bool w32);
 
 struct ScoreForward {
   const void* x;
-  int64_t x_stride;
+  int64_t x_stride;  // elements between rows
+  int64_t x_inner;   // 0, or rows of a group at that stride and
+  int64_t x_outer;   // the elements between groups
   const void* tokens;
   int tok64;
   float* lp;
@@ -158,6 +160,8 @@ struct ScoreForward {
 struct ScoreBackward {
   const void* x;
   int64_t x_stride;
+  int64_t x_inner;
+  int64_t x_outer;
   const void* tokens;
   int tok64;
   const float* lse;

@@ -136,6 +136,25 @@ __device__ __forceinline__ ScoreSum score_join(ScoreSum a, ScoreSum b) {
   return {m, a.s * ra + b.s * rb, (a.t + a.s * da) * ra + (b.t + b.s * db) * rb};
 }
 
+// Where a row's logits lie: rows at one stride, or groups of `inner` rows at one
+// and the groups at another (a slice of positions out of every entry).
+template <class T>
+struct ScoreIn {
+  const T* x;
+  int64_t stride, outer, first;  // row 0 of this launch is row `first`
+  uint32_t inner;
+  __device__ __forceinline__ const T* row(int64_t r) const {
+    r += first;
+    if (inner == 0) return x + r * stride;
+    const uint32_t g = (uint32_t)r / inner;
+    return x + g * outer + (int64_t)((uint32_t)r - g * inner) * stride;
+  }
+};
+template <class T, class A>
+ScoreIn<T> score_in(const A& a, int64_t first) {
+  return {(const T*)a.x, a.x_stride, a.x_outer, first, (uint32_t)a.x_inner};
+}
+
 struct ScoreOut {
   float* lp;
   float* ent;
@@ -233,14 +252,14 @@ __device__ __forceinline__ void score_top(const Vec16<T> (&v)[V], const T* xr, f
 
 // Rows that L lanes hold, V groups each.
 template <class T, int L, int V, bool TOP>
-__global__ __launch_bounds__(256) void score_row_kernel(const T* __restrict__ x, int64_t x_stride,
+__global__ __launch_bounds__(256) void score_row_kernel(const ScoreIn<T> x,
                                                         const void* __restrict__ tokens, int tok64,
                                                         ScoreOut out, int64_t rows, int vocab,
                                                         int top) {
   constexpr int VE = Vec16<T>::n;
   const int lane = threadIdx.x % L;
   const int64_t row = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
-  const T* xr = x + row * x_stride;
+  const T* __restrict__ xr = x.row(row);
   const int end = row < rows ? vocab : 0;
   Vec16<T> v[V];
 #pragma unroll
@@ -269,7 +288,7 @@ __global__ __launch_bounds__(256) void score_row_kernel(const T* __restrict__ x,
 // the keys of each.
 template <class T, int V, bool TOP>
 __global__ __launch_bounds__(256) void score_forward_kernel(
-    const T* __restrict__ x, int64_t x_stride, const void* __restrict__ tokens, int tok64,
+    const ScoreIn<T> x, const void* __restrict__ tokens, int tok64,
     ScoreOut out, float* __restrict__ part, key_t* __restrict__ part_keys, int vocab, int top,
     int seg_len, int segs) {
   constexpr int VE = Vec16<T>::n;
@@ -278,7 +297,7 @@ __global__ __launch_bounds__(256) void score_forward_kernel(
   const int64_t unit = blockIdx.x;
   const int64_t row = unit / segs;
   const int seg = (int)(unit - row * segs);
-  const T* xr = x + row * x_stride;
+  const T* __restrict__ xr = x.row(row);
   const int beg = seg * seg_len;
   const int end = score_segment_end(beg, seg_len, vocab);
 
@@ -333,7 +352,7 @@ __global__ __launch_bounds__(256) void score_forward_kernel(
 // One wave per row: joins the segments in order.
 template <class T>
 __global__ __launch_bounds__(64) void score_join_kernel(
-    const T* __restrict__ x, int64_t x_stride, const void* __restrict__ tokens, int tok64,
+    const ScoreIn<T> x, const void* __restrict__ tokens, int tok64,
     ScoreOut out, const float* __restrict__ part, const key_t* __restrict__ part_keys, int vocab,
     int top, int segs) {
   const int lane = threadIdx.x;
@@ -365,14 +384,14 @@ __global__ __launch_bounds__(64) void score_join_kernel(
     }
     list = keys.listed();
   }
-  score_finish(acc, x + row * x_stride, row, vocab, tokens, tok64, list, top, out, lane);
+  score_finish(acc, x.row(row), row, vocab, tokens, tok64, list, top, out, lane);
 }
 
 // dx of one row segment (L = 256), or of whole rows that L < 256 lanes hold
 // with V groups each; see the formula above.
 template <class T, int L, int V>
 __global__ __launch_bounds__(256) void score_backward_kernel(
-    const T* __restrict__ x, int64_t x_stride, const void* __restrict__ tokens, int tok64,
+    const ScoreIn<T> x, const void* __restrict__ tokens, int tok64,
     const float* __restrict__ lse_, const float* __restrict__ ent, const float* __restrict__ g_lp,
     const float* __restrict__ g_ent, const int64_t* __restrict__ top_ids,
     const float* __restrict__ g_top, T* __restrict__ dx, int64_t rows, int vocab, int top,
@@ -383,7 +402,7 @@ __global__ __launch_bounds__(256) void score_backward_kernel(
   const int64_t row = L == 256 ? unit / segs : unit;
   const int seg = L == 256 ? (int)(unit - row * segs) : 0;
   if (row >= rows) return;
-  const T* xr = x + row * x_stride;
+  const T* __restrict__ xr = x.row(row);
   T* dr = dx + row * vocab;
   const int beg = seg * seg_len;
   const int end = score_segment_end(beg, seg_len, vocab);
@@ -490,7 +509,7 @@ int score_forward_t(const ScoreForward& a) {
     return by_rows(a.rows, kGridThreads / L, [&](int64_t at, int64_t rows) {                      \
       return launch("token log probabilities", score_row_kernel<T, L, V, TOP>,                    \
                     dim3((unsigned)((rows + 256 / L - 1) / (256 / L))), dim3(256), 0, a.stream,   \
-                    (const T*)a.x + at * a.x_stride, a.x_stride,                                  \
+                    score_in<T>(a, at),                                  \
                     score_tokens(a.tokens, a.tok64, at), a.tok64, out_at(at), rows, a.vocab,      \
                     a.top);                                                                       \
     });
@@ -509,7 +528,7 @@ int score_forward_t(const ScoreForward& a) {
   const auto go = [&](auto kernel) {
     return by_rows(a.rows, kGridThreads / 256 / p.segs, [&](int64_t at, int64_t rows) {
       return launch("token log probabilities", kernel, dim3((unsigned)(rows * p.segs)), dim3(256), 0,
-                    a.stream, (const T*)a.x + at * a.x_stride, a.x_stride,
+                    a.stream, score_in<T>(a, at),
                     score_tokens(a.tokens, a.tok64, at), a.tok64, out_at(at), part + at * p.segs * 3,
                     keys + at * p.segs * a.top, a.vocab, a.top, p.seg_len, p.segs);
     });
@@ -521,7 +540,7 @@ int score_forward_t(const ScoreForward& a) {
   if (st != FM_OK || p.segs == 1) return st;
   // few rows: more than one segment each
   return launch("token log probabilities (join)", score_join_kernel<T>, dim3((unsigned)a.rows),
-                dim3(64), 0, a.stream, (const T*)a.x, a.x_stride, a.tokens, a.tok64, out_at(0), part, keys,
+                dim3(64), 0, a.stream, score_in<T>(a, 0), a.tokens, a.tok64, out_at(0), part, keys,
                 a.vocab, a.top, p.segs);
 }
 
@@ -533,7 +552,7 @@ int score_backward_t(const ScoreBackward& a) {
     return by_rows(a.rows, kGridThreads / L / p.segs, [&](int64_t at, int64_t rows) {             \
       return launch("token log probabilities backward", score_backward_kernel<T, L, V>,           \
                     dim3((unsigned)((rows * p.segs + 256 / L - 1) / (256 / L))), dim3(256), 0,    \
-                    a.stream, (const T*)a.x + at * a.x_stride, a.x_stride,                        \
+                    a.stream, score_in<T>(a, at),                        \
                     score_tokens(a.tokens, a.tok64, at), a.tok64, a.lse + at,                     \
                     score_rows(a.ent, at), score_rows(a.g_lp, at), score_rows(a.g_ent, at),       \
                     score_rows(a.top_ids, at * a.top), score_rows(a.g_top, at * a.top),           \

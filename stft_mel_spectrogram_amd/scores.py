@@ -1,12 +1,12 @@
 """Log probabilities of given tokens, with entropy and top alternatives.
 
 One pass over the logits [..., vocab] (float32, float16 or bfloat16, rows at
-one stride) gives, per row, the token's log probability, the entropy of the
-softmax and the best entries in descending order, ties to the lower index; all
-in float32.  A negative token asks for nothing (log probability 0, no
-gradient), one past the vocabulary gives NaN.  Entries of -inf have
-probability 0; a row of only -inf has log probability -inf, entropy 0 and a
-zero gradient.
+one or two strides: logits[:, :-1] beside tokens[:, 1:] is read as it lies)
+gives, per row, the token's log probability, the entropy of the softmax and the
+best entries in descending order, ties to the lower index; all in float32.  A
+negative token asks for nothing (log probability 0, no gradient), one past the
+vocabulary gives NaN.  Entries of -inf have probability 0; a row of only -inf
+has log probability -inf, entropy 0 and a zero gradient.
 """
 from __future__ import annotations
 
@@ -23,20 +23,22 @@ TokenLogprobs = collections.namedtuple("TokenLogprobs",
 
 def _check(logits, tokens, top_k):
     code = T.dtype_code(logits, "logits")
-    rows, vocab, stride = T.rows_of(logits, "logits")
+    rows, vocab, *at = T.rows_of(logits, "logits") if logits.is_contiguous() else T.grouped_rows_of(logits, "logits")
     T.same_device(logits, tokens=tokens)
     if tokens.dtype not in (torch.int64, torch.int32):
         raise TypeError(f"tokens must be int64 or int32, got {tokens.dtype}")
-    if tokens.shape != logits.shape[:-1] or not tokens.is_contiguous():
-        raise ValueError(f"tokens must be a contiguous tensor of shape {tuple(logits.shape[:-1])}")
+    if tokens.shape != logits.shape[:-1]:
+        raise ValueError(f"tokens must be a tensor of shape {tuple(logits.shape[:-1])}")
     top_k = int(top_k)
     if not 0 <= top_k <= min(64, vocab):
         raise ValueError(f"top_k must be in 0 .. {min(64, vocab)}, got {top_k}")
-    return code, rows, vocab, stride, 64 if tokens.dtype == torch.int64 else 32, top_k
+    if not tokens.is_contiguous():
+        tokens = tokens.contiguous()
+    return code, rows, vocab, at, tokens, 64 if tokens.dtype == torch.int64 else 32, top_k
 
 
 def _forward(logits, tokens, top_k, need_lse):
-    code, rows, vocab, stride, bits, top_k = _check(logits, tokens, top_k)
+    code, rows, vocab, at, tokens, bits, top_k = _check(logits, tokens, top_k)
     lead = logits.shape[:-1]
     lp = logits.new_empty(lead, dtype=torch.float32)
     ent = torch.empty_like(lp)
@@ -46,9 +48,9 @@ def _forward(logits, tokens, top_k, need_lse):
         tops = logits.new_empty((*lead, top_k), dtype=torch.float32)
         ids = logits.new_empty((*lead, top_k), dtype=torch.int64)
     ws = T.workspace(logits, N.lib.fm_token_logprobs_workspace(rows, vocab, top_k, code))
-    T.call(logits, N.lib.fm_token_logprobs, logits.data_ptr(), stride, tokens.data_ptr(), bits,
-           lp.data_ptr(), ent.data_ptr(), T.ptr(lse), T.ptr(ids), T.ptr(tops), T.ptr(ws), rows,
-           vocab, top_k, code)
+    fn = N.lib.fm_token_logprobs if len(at) == 1 else N.lib.fm_token_logprobs_strided
+    T.call(logits, fn, logits.data_ptr(), *at, tokens.data_ptr(), bits, lp.data_ptr(), ent.data_ptr(),
+           T.ptr(lse), T.ptr(ids), T.ptr(tops), T.ptr(ws), rows, vocab, top_k, code)
     return TokenLogprobs(lp, ent, ids, tops), lse
 
 
@@ -73,7 +75,7 @@ def token_logprobs_backward(logits, tokens, lse, entropy, grad_logprobs=None, gr
     * entropy) + sum(grad_top_logprobs * top_logprobs); float32 gradients, None
     where there is none."""
     top_k = top_ids.shape[-1] if isinstance(top_ids, torch.Tensor) and top_ids.dim() else 0
-    code, rows, vocab, stride, bits, top_k = _check(logits, tokens, top_k)
+    code, rows, vocab, at, tokens, bits, top_k = _check(logits, tokens, top_k)
     lead = logits.shape[:-1]
     if grad_entropy is not None and entropy is None:
         raise ValueError("grad_entropy needs entropy")
@@ -91,9 +93,10 @@ def token_logprobs_backward(logits, tokens, lse, entropy, grad_logprobs=None, gr
                                 or tuple(top_ids.shape) != (*lead, top_k)):
         raise ValueError(f"top_ids must be a contiguous int64 tensor of shape {(*lead, top_k)}")
     dx = logits.new_empty(logits.shape)
-    T.call(logits, N.lib.fm_token_logprobs_backward, logits.data_ptr(), stride, tokens.data_ptr(),
-           bits, lse.data_ptr(), T.ptr(entropy), T.ptr(grad_logprobs), T.ptr(grad_entropy),
-           T.ptr(top_ids), T.ptr(grad_top_logprobs), dx.data_ptr(), rows, vocab, top_k, code)
+    fn = N.lib.fm_token_logprobs_backward if len(at) == 1 else N.lib.fm_token_logprobs_backward_strided
+    T.call(logits, fn, logits.data_ptr(), *at, tokens.data_ptr(), bits, lse.data_ptr(), T.ptr(entropy),
+           T.ptr(grad_logprobs), T.ptr(grad_entropy), T.ptr(top_ids), T.ptr(grad_top_logprobs), dx.data_ptr(),
+           rows, vocab, top_k, code)
     return dx
 
 

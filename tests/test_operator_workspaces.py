@@ -1,4 +1,4 @@
-"""Sizes of the operators' workspaces, on the CPU."""
+"""Sizes of the operators' workspaces, and refusals of strides, on the CPU."""
 import ctypes
 
 import pytest
@@ -25,3 +25,16 @@ def test_attention_workspace_does_not_look_at_pointers_and_strides(backward):
     assert size(**{f: -(1 << 40) for f in fields}) == want
     assert size(**{f: 1 for f in ("q", "k", "v", "table", "bucket_map", "o", "lse", "grad_o", "grad_q")}) == want
     assert size(scale=0.0) == N.FM_E_INVAL
+
+
+@pytest.mark.parametrize("kw", [dict(inner=-1), dict(inner=1 << 31), dict(inner=2, outer=-8), dict(inner=2, stride=-8),
+                                dict(inner=0, stride=-8)])
+def test_strided_scores_refuse(kw):
+    P = 1 << 20  # an address that must not be touched
+    a = dict(stride=100, inner=2, outer=400)
+    a.update(kw)
+    at = (P, a["stride"], a["inner"], a["outer"], P, 64)
+    assert N.lib.fm_token_logprobs_strided(*at, P, P, P, P, P, P, 4, 100, 5, N.FM_F32, None) == N.FM_E_INVAL
+    assert b"token log probabilities" in N.lib.fm_last_error()
+    assert N.lib.fm_token_logprobs_backward_strided(*at, P, P, P, P, P, P, P, 4, 100, 5, N.FM_F32,
+                                                    None) == N.FM_E_INVAL
