@@ -436,7 +436,9 @@ int fm_token_logprobs_backward_strided(const void* x, int64_t x_stride, int64_t 
  *
  * over the keys j < key_lengths[entry], and j <= pos(i) if causal.  A query
  * without any key gives o = 0, lse = -inf and zero gradients; keys and values
- * at or past key_lengths are not read (NaN there does no harm).
+ * at or past key_lengths are not read (NaN there does no harm).  Below
+ * key_lengths they have to be finite for a causal query too: the keys after it
+ * have a probability of 0, which times an infinity or NaN of a value is NaN.
  *   dtype        of q, k, v, o and their gradients;
  *   q, o [batch, heads, q_len, head_dim], k, v [batch, kv_heads, k_len,
  *                head_dim]: strides in elements of (entry, head, time), >= 0,

@@ -9,7 +9,9 @@ are shared evenly) with any strides whose last axis is contiguous, so a slice
 of a fused projection or a cache can be passed as it lies.  Scores, softmax
 statistics and sums are float32; probabilities and score gradients are
 rounded to the element type for their matrix products.  A query without any
-key gives zeros and zero gradients.  Finite table values beyond +-65536 count as
+key gives zeros and zero gradients.  Keys at or past key_lengths are not read;
+those that causal hides have to be finite (their probability is 0, which times
+an infinity or NaN is NaN).  Finite table values beyond +-65536 count as
 +-65536, so a bucket of the type's lowest value hides its keys from queries that
 see others, and leaves queries without others an ordinary softmax; one of -inf
 hides them always.

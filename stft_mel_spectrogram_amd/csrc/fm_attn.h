@@ -14,7 +14,7 @@
 // float32 values are taken apart into three bfloat16 ones, x = a + b + c exactly
 // (8 significant bits each, rounded to nearest, so that the rests have either
 // sign), and a product is the six terms a a', a b', b a', a c', c a', b b' with
-// float32 sums; what is left out, b c' + c b' + c c', is at most 2^-25 of x x'.
+// float32 sums; what is left out, b c' + c b' + c c', is at most 2^-24 of x x'.
 // Six bfloat16 products of 8 passes take the place of eight float32 ones of 16.
 //
 // Probabilities never pass through LDS: their product with the next operand
