@@ -41,9 +41,9 @@ constexpr size_t attn_forward_lds(int far) {
 // The transposed scores s' = K q' have queries as columns, so that a lane
 // keeps one query's running maximum and sum, and the probabilities are the
 // next product's right operand as they stand: o' = V' p'.  8 x 16 heads x 1501, 64
-// columns, bf16: 88 us, 655 TFLOP/s; the matrix units are busy 35% of the time,
-// exponentials and the rest of the softmax keep the vector units busy beside and
-// between them (without exponentials 60 us, without fetches and barriers 74).
+// columns, bf16: 88 us, 655 TFLOP/s; bound by the vector units, busy 69% of the time
+// with about 100 instructions per tile and wave, 16 of them exponentials (without
+// those 60 us, without fetches and barriers 74), the matrix units 35%.
 template <class T, int DP, bool SPLIT, bool VEC>
 __global__ __launch_bounds__(kAttnThreads, (sizeof(T) == 2 && DP == 64 && VEC ? 4 : attn_waves<T, DP>())) void attn_forward_kernel(const AttnArgs a) {
   constexpr int BK = kAttnKeys, NS = BK / 32, TS = Tile<T, DP>::size(BK), KS = DP / 16, DT = DP / 32;

@@ -24,7 +24,7 @@
 // per SIMD hide the loads better than a chunk fetched ahead: 75 us against 80 at
 // 4096 x 32000 bf16); few of them are cut into segments, one workgroup each,
 // whose partial results a second launch joins.  4096 x 32000 bf16: forward 73 us
-// (3.6 TB/s), with 5 and 20 alternatives 74 and 92, backward 120 (4.4 TB/s); 24008 x
+// (3.6 TB/s), with 5 and 20 alternatives 74 and 92, backward 115 (4.6 TB/s); 24008 x
 // 129 f32: 5.4 and 8.3 us.
 #pragma once
 
