@@ -63,6 +63,22 @@ def test_float16_overflow_of_two_keys():
     assert torch.isfinite(dt).all()
 
 
+@pytest.mark.parametrize("h,hk,d", [(2, 2, 64), (4, 1, 40), (1, 1, 128)])
+@pytest.mark.parametrize("one,others", [(2e3, 2e-3), (2e-2, 2e3)])
+def test_float16_gradients_of_very_different_rows(h, hk, d, one, others):
+    """A query whose gradient is 10^6 times the others' (or a 10^5th) and that sees one key only:
+    the other keys' gradients come from the other queries alone."""
+    q, k, v, table, m, do = plain.make(1, h, hk, 900, 900, d, "f16", seed=d, layout="bhtd")
+    table = torch.zeros_like(table)
+    at, key = 645, 30
+    q[..., 0], q[:, :, at] = 0, 0
+    k[..., 0] = 0
+    q[:, :, at, 0], k[:, :, key, 0] = 20.0, 2.5 * d ** 0.5  # 50 nats
+    sizes = torch.full((900, 1), others, device="cuda")
+    sizes[at] = one
+    plain.run_case(q, k, v, table, m, (do.float() * sizes).half())
+
+
 def sink_case(tq, tk, d, nats, at, seed):
     """A key of value 0 whose score is `nats` above all others', which lie close together."""
     q, k, v, table, m, do = plain.make(1, 2, 2, tq, tk, d, "f16", seed=seed, layout="bhtd")
