@@ -59,6 +59,8 @@ extern "C" {
 #define FM_I16 1
 #define FM_F16 2
 #define FM_BF16 3 /* operators below only (layer norm, attention, scores)    */
+#define FM_E4M3 4 /* 8-bit outputs of fm_rms_norm_quantized                  */
+#define FM_I8 5
 
 /* normalized: STFT normalisation folded into the window (flashmel/filters.py
  * make_window): none, divide by sqrt(sum of the squared window), or divide
@@ -490,6 +492,180 @@ int fm_attention_forward(const fm_attention_args* args, void* workspace, void* s
 
 /* Gradients of sum(grad_o * o); o and lse as the forward wrote them. */
 int fm_attention_backward(const fm_attention_args* args, void* workspace, void* stream);
+
+/*
+ * fm_recurrence_args -- a gated linear recurrence over time, per channel:
+ *
+ *   a = sigmoid(forget[t]), h[t] = a h[t - 1] + (1 - a) x[t], y[t] = h[t] silu(gate[t])
+ *
+ * from h[-1] = state.  forget of +inf keeps the state, -inf replaces it by x.
+ * Without a gate y = h.  Frames at or past lengths[entry] are not part of the
+ * sequence: NaN there does no harm, y and the gradients are 0 there and the
+ * state stays as it was after the last frame before.
+ *   dtype        of x, forget, gate, y and their gradients; states are float32;
+ *   x, forget, gate, grad_y [batch, time, channels]: strides in elements of
+ *                (entry, time), >= 0, channels contiguous; gate NULL: none;
+ *   y, grad_x, grad_forget, grad_gate [batch, time, channels] contiguous;
+ *   state, last_state, grad_last, grad_state [batch, channels]: state NULL is
+ *                0, and last_state may be the same memory; grad_last NULL is 0,
+ *                grad_state NULL is not wanted;
+ *   lengths      [batch] int32 (clamped to [0, time]) or NULL: time;
+ *   saved        [batch, (time + 63) / 64, channels] float32, the state before
+ *                every 64th frame: written by the forward (NULL: not wanted),
+ *                read by the backward;
+ * backward: grad_y and grad_last in; grad_x, grad_forget, grad_gate (with a
+ *                gate) and grad_state out; y and last_state are not looked at.
+ * batch, time < 2^30; batch * (blocks of 16 channels) < 2^23.
+ */
+typedef struct fm_recurrence_args {
+  int dtype, reserved;
+  int64_t batch, time, channels;
+  const void* x;
+  const void* forget;
+  const void* gate;
+  const float* state;
+  const int32_t* lengths;
+  void* y;
+  float* last_state;
+  float* saved;
+  const void* grad_y;
+  const float* grad_last;
+  void* grad_x;
+  void* grad_forget;
+  void* grad_gate;
+  float* grad_state;
+  int64_t x_stride[2], forget_stride[2], gate_stride[2], grad_y_stride[2];
+} fm_recurrence_args;
+
+/* Bytes of the workspace of fm_gated_recurrence_forward (backward 0) or
+ * _backward (1); pointers and strides are not looked at. */
+int64_t fm_gated_recurrence_workspace(const fm_recurrence_args* args, int backward);
+
+/* y, last_state (and saved if not NULL). */
+int fm_gated_recurrence_forward(const fm_recurrence_args* args, void* workspace, void* stream);
+
+/* Gradients of sum(grad_y * y) + sum(grad_last * last_state). */
+int fm_gated_recurrence_backward(const fm_recurrence_args* args, void* workspace, void* stream);
+
+/*
+ * fm_rms_norm_forward -- y = s / sqrt(mean(s^2) + eps) * weight over the last
+ * axis, s = x, or with a residual s = x + residual rounded to the rows' type.
+ *   x, residual [rows, width], strides in elements from row to row, elements of
+ *   a row contiguous; y [rows, width] contiguous, same type; sum [rows, width]
+ *   contiguous takes s where there is a residual (NULL otherwise) and may be the
+ *   residual's own memory if that is contiguous; weight [width] of type
+ *   param_dtype (dtype or FM_F32) or NULL; rstd [rows] float32 or NULL (the
+ *   backward needs it).  0 <= rows < 2^31, 1 <= width <= 2^20, eps >= 0.
+ */
+int fm_rms_norm_forward(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                        const void* weight, void* y, void* sum, float* rstd, int64_t rows, int64_t width,
+                        double eps, int dtype, int param_dtype, void* stream);
+
+/*
+ * fm_rms_norm_quantized -- the same with an output in 8 bits: scale [rows]
+ * float32 is the row's largest |y| over 448 (out_dtype FM_E4M3) or 127 (FM_I8),
+ * 1 for a row of zeros, at least 2^-126; q [rows, width] is y / scale rounded to
+ * nearest from the unrounded y.  A NaN in a row makes its scale NaN.
+ */
+int fm_rms_norm_quantized(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                          const void* weight, void* q, float* scale, void* sum, int64_t rows, int64_t width,
+                          double eps, int dtype, int param_dtype, int out_dtype, void* stream);
+
+/* Bytes of fm_rms_norm_backward's workspace. */
+int64_t fm_rms_norm_backward_workspace(int64_t rows, int64_t width, int dtype);
+
+/*
+ * fm_rms_norm_backward -- gradients of sum(dy * y) + sum(grad_sum * s), s (`sum`)
+ * and rstd from the forward (s = x without a residual).  dx [rows, width]
+ * contiguous is the gradient of x and of the residual alike; grad_sum may be
+ * NULL; dw [width] of type param_dtype, NULL leaves it out (workspace unused).
+ */
+int fm_rms_norm_backward(const void* dy, int64_t dy_stride, const void* sum, int64_t sum_stride,
+                         const void* grad_sum, int64_t grad_sum_stride, const void* weight, const float* rstd,
+                         void* dx, void* dw, void* workspace, int64_t rows, int64_t width, int dtype,
+                         int param_dtype, void* stream);
+
+/*
+ * fm_distill -- how far logits x [rows, vocab] are from a teacher of whom each
+ * row's `top` best tokens ids [rows, top] int64 and log probabilities lps
+ * [rows, top] float32 are known (1 <= top <= 64):
+ *
+ *   loss = T^2 sum_k q_k (log q_k - lp[ids_k]),  lp = log_softmax(x / T),
+ *   q = softmax(lps / T) over the row's tokens,  T the temperature;
+ *
+ * with rest != 0 (T has to be 1) q = exp(lps), and the mass that the teacher
+ * leaves, r = max(0, 1 - sum q), stands against the student's for all tokens
+ * that are not named: + r (log r - log sum of p over those).
+ * An entry with a negative id is none (rows with fewer); a row without any has
+ * loss 0 and no gradient; an id >= vocab gives NaN and takes no part in the
+ * gradient.  The same id twice counts twice.  Teacher entries of -inf have
+ * q = 0.  A student that gives a named token no probability (-inf) has loss inf;
+ * one that leaves nothing for the others has no rest term.  A row of -inf only
+ * has a zero gradient.  NaN or +inf in a row stays in its row.
+ *   x: x_stride elements from row to row, or groups of x_inner rows at x_stride
+ *   and the groups at x_outer (x_inner 0: none); loss [rows] float32; stats
+ *   [rows, 4] float32 or NULL: what the backward needs (the largest x and the log
+ *   of the sum of exp((x - largest) / T), both also over the tokens that are not
+ *   named).  T in [2^-10, 2^10]; vocab <
+ *   2^31 - 65536, rows * (row segments) < 2^31.
+ */
+int64_t fm_distill_workspace(int64_t rows, int64_t vocab, int dtype);
+int fm_distill(const void* x, int64_t x_stride, int64_t x_inner, int64_t x_outer, const int64_t* ids,
+               const float* lps, float* loss, float* stats, void* workspace, int64_t rows, int64_t vocab, int top,
+               double temperature, int rest, int dtype, void* stream);
+
+/*
+ * fm_distill_backward -- dx [rows, vocab] contiguous, the gradient of
+ * sum(grad_loss * loss) with respect to x: T grad (p - q) and, with the rest,
+ * the others' p (1 - r / their sum) grad.  stats from the forward.
+ */
+int fm_distill_backward(const void* x, int64_t x_stride, int64_t x_inner, int64_t x_outer, const int64_t* ids,
+                        const float* lps, const float* stats, const float* grad_loss, void* dx, int64_t rows,
+                        int64_t vocab, int top, double temperature, int rest, int dtype, void* stream);
+
+/*
+ * fm_adjust_args -- logits before a token is chosen from them; per row and token
+ *
+ *   x = x > 0 ? x / repetition : x * repetition    if the token is in the history
+ *   x = x - frequency * count - presence * (count > 0)
+ *   x = x + the sum of the token's biases, in their order
+ *   x = -inf                                       if its bit of `allowed` is 0
+ *
+ * in float32, rounded once.  count is how often the token is in the history from
+ * prompt_lengths[row] on (0 without).
+ *   x [rows, vocab]: x_stride elements from row to row; out [rows, vocab]
+ *   contiguous, same type, may be x's own memory if that is contiguous;
+ *   history [rows, history_len] of history_bits (32 or 64) wide integers,
+ *   history_stride from row to row; history_lengths, prompt_lengths [rows] int32
+ *   (clamped to [0, history_len]) or NULL: history_len, 0.  Tokens outside
+ *   [0, vocab) are none;
+ *   repetition, frequency, presence [rows] float32 or NULL: the *_value for all
+ *   rows (repetition > 0);
+ *   bias_ids [rows, biases] int64, bias [rows, biases] float32, contiguous; ids
+ *   outside [0, vocab) are none; the same one twice counts twice;
+ *   allowed: rows of (vocab + 31) / 32 words of 32 bits, lowest first,
+ *   allowed_stride words from row to row (0: one for all rows), or NULL.
+ * rows < 2^31, vocab < 2^31 - 65536, rows * (row segments) < 2^23.
+ */
+typedef struct fm_adjust_args {
+  int dtype, history_bits;
+  int64_t rows, vocab, history_len, biases;
+  int64_t x_stride, history_stride, allowed_stride;
+  double repetition_value, frequency_value, presence_value;
+  const void* x;
+  void* out;
+  const void* history;
+  const int32_t* history_lengths;
+  const int32_t* prompt_lengths;
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  const int64_t* bias_ids;
+  const float* bias;
+  const int32_t* allowed;
+} fm_adjust_args;
+
+int fm_adjust_logits(const fm_adjust_args* args, void* stream);
 
 #ifdef __cplusplus
 }

@@ -26,6 +26,8 @@ FM_F32 = 0
 FM_I16 = 1
 FM_F16 = 2
 FM_BF16 = 3
+FM_E4M3 = 4
+FM_I8 = 5
 FM_FWD_SPLIT = 0
 FM_FWD_PAIRED = 1
 FM_FWD_LARGE = 2
@@ -75,6 +77,28 @@ class AttentionArgs(ctypes.Structure):
                  for axis in ("entry", "head", "time")])
 
 
+class RecurrenceArgs(ctypes.Structure):
+    """fm_recurrence_args of include/fm.h (its stride arrays field by field)."""
+    _fields_ = ([(n, ctypes.c_int) for n in ("dtype", "reserved")] +
+                [(n, ctypes.c_int64) for n in ("batch", "time", "channels")] +
+                [(n, ctypes.c_void_p) for n in ("x", "forget", "gate", "state", "lengths", "y", "last_state",
+                                                 "saved", "grad_y", "grad_last", "grad_x", "grad_forget",
+                                                 "grad_gate", "grad_state")] +
+                [(f"{t}_stride_{axis}", ctypes.c_int64) for t in ("x", "forget", "gate", "grad_y")
+                 for axis in ("entry", "time")])
+
+
+class AdjustArgs(ctypes.Structure):
+    """fm_adjust_args of include/fm.h."""
+    _fields_ = ([(n, ctypes.c_int) for n in ("dtype", "history_bits")] +
+                [(n, ctypes.c_int64) for n in ("rows", "vocab", "history_len", "biases", "x_stride",
+                                                "history_stride", "allowed_stride")] +
+                [(n, ctypes.c_double) for n in ("repetition_value", "frequency_value", "presence_value")] +
+                [(n, ctypes.c_void_p) for n in ("x", "out", "history", "history_lengths", "prompt_lengths",
+                                                 "repetition", "frequency", "presence", "bias_ids", "bias",
+                                                 "allowed")])
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
@@ -115,6 +139,19 @@ def _load() -> ctypes.CDLL:
         "fm_token_logprobs_strided": (I, [P, I64, I64, I64, P, I, P, P, P, P, P, P, I64, I64, I, I, P]),
         "fm_token_logprobs_backward_strided": (I, [P, I64, I64, I64, P, I, P, P, P, P, P, P, P, I64, I64, I, I,
                                                    P]),
+    }
+    sigs |= {
+        "fm_gated_recurrence_workspace": (I64, [ctypes.POINTER(RecurrenceArgs), I]),
+        "fm_gated_recurrence_forward": (I, [ctypes.POINTER(RecurrenceArgs), P, P]),
+        "fm_gated_recurrence_backward": (I, [ctypes.POINTER(RecurrenceArgs), P, P]),
+        "fm_rms_norm_forward": (I, [P, I64, P, I64, P, P, P, P, I64, I64, D, I, I, P]),
+        "fm_rms_norm_quantized": (I, [P, I64, P, I64, P, P, P, P, I64, I64, D, I, I, I, P]),
+        "fm_rms_norm_backward_workspace": (I64, [I64, I64, I]),
+        "fm_rms_norm_backward": (I, [P, I64, P, I64, P, I64, P, P, P, P, P, I64, I64, I, I, P]),
+        "fm_distill_workspace": (I64, [I64, I64, I]),
+        "fm_distill": (I, [P, I64, I64, I64, P, P, P, P, P, I64, I64, I, D, I, I, P]),
+        "fm_distill_backward": (I, [P, I64, I64, I64, P, P, P, P, P, I64, I64, I, D, I, I, P]),
+        "fm_adjust_logits": (I, [ctypes.POINTER(AdjustArgs), P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)

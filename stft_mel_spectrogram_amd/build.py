@@ -21,7 +21,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfm.so")
-SOURCES = ["fm_api.cpp", "fm_ops.cpp", "fm_plan.cpp", "fm_launch.hip"]
+SOURCES = ["fm_api.cpp", "fm_ops.cpp", "fm_seq.cpp", "fm_logit.cpp", "fm_plan.cpp", "fm_launch.hip"]
 
 
 def sources() -> list:
