@@ -515,7 +515,8 @@ int fm_attention_backward(const fm_attention_args* args, void* workspace, void* 
  *                read by the backward;
  * backward: grad_y and grad_last in; grad_x, grad_forget, grad_gate (with a
  *                gate) and grad_state out; y and last_state are not looked at.
- * batch, time < 2^30; batch * (blocks of 16 channels) < 2^23.
+ * batch, time < 2^30, channels <= 2^20, batch * (blocks of 16 channels) < 2^23;
+ * frames of x, forget, gate and grad_y less than 8 MiB apart.
  */
 typedef struct fm_recurrence_args {
   int dtype, reserved;
@@ -645,7 +646,8 @@ int fm_distill_backward(const void* x, int64_t x_stride, int64_t x_inner, int64_
  *   outside [0, vocab) are none; the same one twice counts twice;
  *   allowed: rows of (vocab + 31) / 32 words of 32 bits, lowest first,
  *   allowed_stride words from row to row (0: one for all rows), or NULL.
- * rows < 2^31, vocab < 2^31 - 65536, rows * (row segments) < 2^23.
+ * rows < 2^31, vocab < 2^31 - 65536, rows * (row segments of 2048) < 2^22,
+ * history_len < 2^20, biases <= 1024.
  */
 typedef struct fm_adjust_args {
   int dtype, history_bits;

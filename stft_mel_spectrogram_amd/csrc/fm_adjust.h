@@ -4,14 +4,14 @@
 //   x = x > 0 ? x / rep : x rep (tokens seen), x -= freq count + pres [count > 0],
 //   x += sum of the token's biases, x = -inf where its bit is 0
 //
-// A workgroup takes a segment of a row: its logits go to registers while the
-// history is counted into LDS (whole numbers, so that the order of the atomics is
-// of no account: bit 0 says seen, the rest counts), then each lane works on its
-// own elements: one read and one write, in place too.  The segment's biases are
-// listed in order by one wave, and the first entry of each token writes their sum
-// into the slots that the counts have left.  Memory bound where the history is
-// short against the vocabulary; every segment reads the row's history again, from
-// the cache.
+// A workgroup of 512 lanes takes a segment of a row.  Its logits, the history and
+// the biases are asked for at once; the history is counted into a slot per token in
+// LDS while the logits are on their way (whole numbers, so that the order of the
+// atomics is of no account).  Before that the biases have left the number of their
+// token's first entry in its slot; where a token has several, that entry adds them up
+// in order.  Then each lane works on its own elements: one read, one write, in place
+// too.  Every segment reads the row's history and biases again, from the cache.
+// Memory bound.
 #pragma once
 
 #include "fm_logit.h"
@@ -19,154 +19,180 @@
 
 namespace fm {
 
+// A slot: bit 0 the token is in the history, 20 bits how often it counts, 11 bits
+// kAdjustMaxBiases less the number of its first bias entry.
+constexpr uint32_t kSlotOnce = 2, kSlotBias = 1u << 21;
+
 template <class T, int V>
-__global__ __launch_bounds__(256) void adjust_kernel(const AdjustArgs a) {
-  constexpr int VE = Vec16<T>::n, SEG = 256 * VE * V;
-  __shared__ __attribute__((aligned(16))) uint32_t count[SEG];
-  __shared__ int bias_id[kAdjustMaxBiases];
-  __shared__ float bias_val[kAdjustMaxBiases];
-  __shared__ int bias_n;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int64_t row = blockIdx.x / a.segs;
-  const int beg = (int)(blockIdx.x - row * a.segs) * SEG;
+__global__ __launch_bounds__(kAdjustThreads) void adjust_kernel(const AdjustArgs a) {
+  constexpr int VE = Vec16<T>::n, NT = kAdjustThreads, SEG = NT * VE * V;
+  constexpr int HIST = 8;                          // tokens of a lane at a time
+  constexpr int BIAS = kAdjustMaxBiases / NT;      // bias entries of a lane
+  extern __shared__ __attribute__((aligned(16))) uint32_t slots[];  // [SEG], ids and values of the biases
+  int* bias_id = (int*)slots + SEG;
+  float* bias_val = (float*)bias_id + a.biases;
+  __shared__ int again;  // a token has several biases
+  const int tid = threadIdx.x;
+  // the segments of a row on one XCD, whose L2 then holds its history: workgroups 8
+  // apart, for as many rows as are a multiple of 8
+  const unsigned b = blockIdx.x;
+  const bool spread = b >= (unsigned)(a.rows & ~(int64_t)7) * a.segs;
+  const unsigned at = spread ? b : b / 8;
+  const int64_t row = spread ? at / a.segs : at / a.segs * 8 + b % 8;
+  const int beg = (int)(at % a.segs) * SEG;
   const int n = a.vocab - beg < SEG ? a.vocab - beg : SEG;
   const T* x = (const T*)a.x + row * a.x_stride + beg;
   T* out = (T*)a.out + row * a.vocab + beg;
-  Vec16<T> raw[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = (i * 256 + tid) * VE;
-    raw[i] = load16_part(x + c, n - c, (T)0.f);
-  }
-  uint32_t bits[V];
-  if (a.allowed) {
-    const uint8_t* p = a.allowed + row * a.allowed_stride;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (i * 256 + tid) * VE;
-      bits[i] = c < n ? (uint32_t)p[(beg + c) >> 3] >> (VE == 4 ? c & 4 : 0) : 0u;
-    }
-  }
-  float v[V][VE];
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-#pragma unroll
-    for (int e = 0; e < VE; ++e) v[i][e] = (float)raw[i].v[e];
-
   int len = a.history_len;
   if (a.history_lengths && len > 0) {
     const int l = a.history_lengths[row];
     len = l < 0 ? 0 : l < len ? l : len;
   }
-  uint4* mine = (uint4*)count;  // group (i * 256 + tid): VE / 4 of these
-  const auto clear = [&]() {
+  const int prompt = a.prompt_lengths && len > 0 ? a.prompt_lengths[row] : 0;
+  const float rep = a.repetition ? a.repetition[row] : a.repetition_value;
+  const float freq = a.frequency ? a.frequency[row] : a.frequency_value;
+  const float pres = a.presence ? a.presence[row] : a.presence_value;
+  // tokens as slots of this segment, or -1
+  const auto slot = [&](int64_t id) {
+    const int64_t c = id - beg;
+    return c >= 0 && c < n ? (int)c : -1;
+  };
+  const char* h = (const char*)a.history + row * a.history_stride * (a.history64 ? 8 : 4);
+  int tok[HIST];
+  // all of them, so that no load waits for the row's length
+  const auto history = [&](int first) {
+#pragma unroll
+    for (int j = 0; j < HIST; ++j) {
+      const int k = first + j * NT + tid;
+      tok[j] = k >= a.history_len ? -1 : slot(a.history64 ? ((const int64_t*)h)[k] : ((const int32_t*)h)[k]);
+    }
+  };
+  const bool any = a.history_len > 0 || a.biases > 0;
+  uint4* mine = (uint4*)slots;  // of group i * NT + tid: VE / 4 of these
+  Vec16<T> raw[V];
+  uint32_t bits[V];
+  const auto logits = [&]() {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = (i * NT + tid) * VE;
+      raw[i] = load16_part(x + c, n - c, (T)0.f);
+    }
+    if (a.allowed) {
+      const uint8_t* p = a.allowed + row * a.allowed_stride;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = (i * NT + tid) * VE;
+        bits[i] = c < n ? (uint32_t)p[(beg + c) >> 3] >> (VE == 4 ? c & 4 : 0) : 0u;
+      }
+    }
+  };
+  if (any) {
+    if (a.history_len > 0) history(0);
+    int id[BIAS];
+#pragma unroll
+    for (int j = 0; j < BIAS; ++j) {
+      const int k = j * NT + tid;
+      id[j] = -1;
+      if (k < a.biases) {
+        id[j] = slot(a.bias_ids[row * a.biases + k]);
+        bias_id[k] = id[j];
+        bias_val[k] = a.bias[row * a.biases + k];
+      }
+    }
+    logits();
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int j = 0; j < VE / 4; ++j) mine[(i * 256 + tid) * (VE / 4) + j] = make_uint4(0, 0, 0, 0);
-  };
-  // the segment's biases, in their order, by the last wave
-  if (a.biases > 0 && tid >= 192) {
-    int m = 0;
-    for (int i = 0; i < a.biases; i += 64) {
-      const int k = i + lane;
-      int64_t id = -1;
-      float b = 0.f;
-      if (k < a.biases) {
-        id = a.bias_ids[row * a.biases + k];
-        b = a.bias[row * a.biases + k];
-      }
-      const bool in = id >= beg && id < (int64_t)beg + n;
-      const uint64_t who = __ballot(in);
-      const int at = m + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32),
-                                                   __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
-      if (in) {
-        bias_id[at] = (int)(id - beg);
-        bias_val[at] = b;
-      }
-      m += __popcll(who);
-    }
-    if (lane == 0) bias_n = m;
-  }
-  if (len > 0) {
-    clear();
+      for (int j = 0; j < VE / 4; ++j) mine[(i * NT + tid) * (VE / 4) + j] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) again = 0;
     __syncthreads();
-    int prompt = 0;
-    if (a.prompt_lengths) prompt = a.prompt_lengths[row];
-    const auto add = [&](int i, int64_t token) {
-      const int64_t c = token - beg;
-      if (c < 0 || c >= n) return;
-      if (i < prompt)
-        atomicOr(count + c, 1u);
-      else
-        atomicAdd(count + c, 2u);
-    };
-    const char* h = (const char*)a.history + row * a.history_stride * (a.history64 ? 8 : 4);
-    for (int i = tid; i < len; i += 1024) {
-      int64_t tok[4];
+    if (a.biases > 0) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = i + 256 * j;
-        tok[j] = k >= len ? -1 : a.history64 ? ((const int64_t*)h)[k] : ((const int32_t*)h)[k];
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) add(i + 256 * j, tok[j]);
+      for (int j = 0; j < BIAS; ++j)
+        if (id[j] >= 0) atomicMax(slots + id[j], (uint32_t)(kAdjustMaxBiases - (j * NT + tid)) * kSlotBias);
+      __syncthreads();
     }
-    __syncthreads();
-    const float rep = a.repetition ? a.repetition[row] : a.repetition_value;
-    const float freq = a.frequency ? a.frequency[row] : a.frequency_value;
-    const float pres = a.presence ? a.presence[row] : a.presence_value;
+    if (a.history_len > 0) {
+      for (int k = 0; k < len; k += HIST * NT) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      uint32_t k[VE];
-      uint32_t any = 0;
-      __builtin_memcpy(k, mine + (i * 256 + tid) * (VE / 4), sizeof(k));
-#pragma unroll
-      for (int e = 0; e < VE; ++e) any |= k[e];
-      if (any) {
-#pragma unroll
-        for (int e = 0; e < VE; ++e)
-          if (k[e]) {
-            const float s = v[i][e] > 0.f ? v[i][e] / rep : v[i][e] * rep;
-            v[i][e] = k[e] > 1u ? s - freq * (float)(k[e] >> 1) - pres : s;
+        for (int j = 0; j < HIST; ++j) {
+          const int at = k + j * NT + tid;
+          if (tok[j] >= 0 && at < len) {
+            if (at < prompt)
+              atomicOr(slots + tok[j], 1u);
+            else
+              atomicAdd(slots + tok[j], kSlotOnce);
           }
+        }
+        if (k + HIST * NT < len) history(k + HIST * NT);
       }
     }
-  }
-  if (a.biases > 0) {
-    clear();
+    if (a.biases > 0) {
+      // the others add to the slots' lower bits alone
+#pragma unroll
+      for (int j = 0; j < BIAS; ++j)
+        if (id[j] >= 0 && slots[id[j]] / kSlotBias != (uint32_t)(kAdjustMaxBiases - (j * NT + tid))) again = 1;
+    }
     __syncthreads();
-    const int m = bias_n;
-    if (m > 0) {
-      for (int k = tid; k < m; k += 256) {
-        const int id = bias_id[k];
-        float s = 0.f;
-        bool first = true;
-        for (int j = 0; j < m; ++j)
-          if (bias_id[j] == id) {
-            s += bias_val[j];
-            first &= j >= k;
+    if (a.biases > 0 && again) {
+      // a wave at a time looks for the entries of its lanes' tokens, 64 at a time
+      float s[BIAS];
+      bool first[BIAS];
+#pragma unroll
+      for (int j = 0; j < BIAS; ++j) {
+        const int k = j * NT + tid;
+        first[j] = id[j] >= 0 && slots[id[j]] / kSlotBias == (uint32_t)(kAdjustMaxBiases - k);
+        s[j] = 0.f;
+        for (uint64_t who = __ballot(first[j]); who; who &= who - 1) {
+          const int lead = __builtin_ctzll(who);
+          const int token = __builtin_amdgcn_readlane(id[j], lead);
+          float sum = 0.f;
+          for (int i = 0; i < a.biases; i += 64) {
+            const int at = i + (tid & 63);
+            const bool same = at < a.biases && bias_id[at] == token;
+            const float v = same ? bias_val[at] : 0.f;
+            for (uint64_t more = __ballot(same); more; more &= more - 1)
+              sum += __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), __builtin_ctzll(more)));
           }
-        if (first) count[id] = __float_as_uint(s);
+          if ((tid & 63) == lead) s[j] = sum;
+        }
       }
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float b[VE];
-        __builtin_memcpy(b, mine + (i * 256 + tid) * (VE / 4), sizeof(b));
-#pragma unroll
-        for (int e = 0; e < VE; ++e) v[i][e] += b[e];
-      }
+      for (int j = 0; j < BIAS; ++j)
+        if (first[j]) bias_val[j * NT + tid] = s[j];
+      __syncthreads();
     }
+  } else {
+    logits();
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c = (i * 256 + tid) * VE;
-    if (c < n) {
-      Vec16<T> o;
+    const int c = (i * NT + tid) * VE;
+    if (any) {
+      uint32_t k[VE], seen = 0;
+      __builtin_memcpy(k, mine + (i * NT + tid) * (VE / 4), sizeof(k));
 #pragma unroll
-      for (int e = 0; e < VE; ++e) o.v[e] = (T)(a.allowed && !(bits[i] >> e & 1u) ? -INFINITY : v[i][e]);
-      store16_part(out + c, o, n - c);
+      for (int e = 0; e < VE; ++e) seen |= k[e];
+      if (seen) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e)
+          if (k[e]) {
+            float v = (float)raw[i].v[e];
+            const uint32_t count = k[e] % kSlotBias / kSlotOnce, b = k[e] / kSlotBias;
+            if (k[e] % kSlotBias) v = v > 0.f ? v / rep : v * rep;
+            if (count) v = v - freq * (float)count - pres;
+            if (b) v += bias_val[kAdjustMaxBiases - b];
+            raw[i].v[e] = (T)v;
+          }
+      }
+    }
+    if (c < n) {
+      if (a.allowed) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) raw[i].v[e] = bits[i] >> e & 1u ? raw[i].v[e] : (T)-INFINITY;
+      }
+      store16_part(out + c, raw[i], n - c);
     }
   }
 }
@@ -176,9 +202,10 @@ int adjust_t(AdjustArgs a, void* stream) {
   constexpr int VE = Vec16<T>::n;
   a.segs = adjust_segments(a.rows, a.vocab, VE);
   const int vecs = adjust_vecs(a.rows, a.vocab, VE);
-  return launch("adjusted logits",
-                vecs == 1 ? adjust_kernel<T, 1> : vecs == 2 ? adjust_kernel<T, 2> : adjust_kernel<T, 4>,
-                dim3((unsigned)(a.rows * a.segs)), dim3(256), 0, stream, a);
+  const bool any = a.history_len > 0 || a.biases > 0;
+  const size_t lds = any ? 4 * (size_t)kAdjustThreads * VE * vecs + 8 * (size_t)a.biases : 0;
+  return launch("adjusted logits", vecs == 1 ? adjust_kernel<T, 1> : vecs == 2 ? adjust_kernel<T, 2> : adjust_kernel<T, 4>,
+                dim3((unsigned)(a.rows * a.segs)), dim3(kAdjustThreads), lds, stream, a);
 }
 
 }  // namespace fm

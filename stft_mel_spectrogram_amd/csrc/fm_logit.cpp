@@ -102,8 +102,9 @@ int fm_adjust_logits(const fm_adjust_args* p, void* stream) try {
   if (p->rows < 0 || p->rows >= int64_t(1) << 31) return bad("adjusted logits: rows must be in [0, 2^31)");
   if (p->vocab < 1 || p->vocab >= fm::kVocabMost)
     return bad("adjusted logits: vocab must be in [1, 2^31 - 65536)");
-  if (p->history_len < 0 || p->history_len > int64_t(1) << 30)
-    return bad("adjusted logits: history_len must be in [0, 2^30]");
+  if (p->history_len < 0) return bad("adjusted logits: history_len must be >= 0");
+  if (p->history_len >= fm::kAdjustMaxHistory)
+    return fm::set_error(FM_E_UNSUPPORTED, "adjusted logits: history_len must be < 2^20");
   if (p->history_bits != 64 && p->history_bits != 32) return bad("adjusted logits: history_bits must be 32 or 64");
   if (p->biases < 0) return bad("adjusted logits: biases must be >= 0");
   if (p->biases > fm::kAdjustMaxBiases)
@@ -116,7 +117,7 @@ int fm_adjust_logits(const fm_adjust_args* p, void* stream) try {
   a.rows = p->rows;
   a.vocab = static_cast<int>(p->vocab);
   a.segs = fm::adjust_segments(a.rows, a.vocab, 16 / es);
-  if (a.rows >= (int64_t(1) << 23) / a.segs) return bad("adjusted logits: too many rows for one launch");
+  if (a.rows >= (int64_t(1) << 22) / a.segs) return bad("adjusted logits: too many rows for one launch");
   if (a.rows == 0) return FM_OK;
   const bool history = p->history_len > 0;
   if (!p->x || !p->out) return bad("adjusted logits: x and out must not be NULL");

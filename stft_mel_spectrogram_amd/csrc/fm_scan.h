@@ -20,6 +20,8 @@
 // end instead; its lane stores only the channels that are its own.
 #pragma once
 
+#include <type_traits>
+
 #include "fm_op.h"
 #include "fm_seq.h"
 
@@ -65,26 +67,86 @@ struct ScanChannels {
   }
 };
 template <class T>
-__device__ __forceinline__ Quad<T> scan_load(const T* p, int channels) {
-  return load_group<T, kScanChannels>(p, channels, (T)0.f);
-}
-template <class T>
-__device__ __forceinline__ void scan_store(T* p, const Quad<T>& v, int own, int end) {
-  if (own == 0 && end == kScanChannels) {
-    __builtin_memcpy(p, &v, sizeof(v));
-  } else {
-#pragma unroll
-    for (int e = 0; e < kScanChannels; ++e)
-      if (e >= own && e < end) p[e] = v.v[e];
-  }
-}
-template <class T>
-__device__ __forceinline__ Quad<T> scan_pick(bool real, const Quad<T>& v, float other) {
+__device__ __forceinline__ Quad<T> scan_pick(bool real, const Quad<T>& v) {
   Quad<T> r;
 #pragma unroll
-  for (int e = 0; e < kScanChannels; ++e) r.v[e] = real ? v.v[e] : (T)other;
+  for (int e = 0; e < kScanChannels; ++e) r.v[e] = real ? v.v[e] : (T)0.f;
   return r;
 }
+
+// Four channels as loaded: whole words, which stay as they are while on their way
+// (as elements of 16 bits they would take a register each).
+template <class T>
+struct ScanRaw {
+  static constexpr int N = sizeof(T);
+  uint32_t w[N];
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (sizeof(T) == 4) {
+      return __uint_as_float(w[e]);
+    } else {
+      const uint32_t u = w[e / 2];
+      if constexpr (std::is_same<T, bf16_t>::value) {
+        return __uint_as_float(e % 2 ? u & 0xffff0000u : u << 16);
+      } else {
+        const uint16_t h = (uint16_t)(e % 2 ? u >> 16 : u);
+        T v;
+        __builtin_memcpy(&v, &h, sizeof(v));
+        return (float)v;
+      }
+    }
+  }
+  // What was made of the words is to be made again.
+  __device__ __forceinline__ void forget() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(w[i]));
+  }
+  // 0, or +inf, where the frame is not real
+  __device__ __forceinline__ void pick(bool real, bool inf) {
+    constexpr uint32_t kInf = sizeof(T) == 4 ? 0x7f800000u : std::is_same<T, bf16_t>::value ? 0x7f807f80u : 0x7c007c00u;
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = real ? w[i] : inf ? kInf : 0u;
+  }
+};
+
+// A lane's frames of a tensor, tile by tile: a uniform address that moves, and 32
+// bits of the lane's own.  TINY: fewer than four channels.
+template <class T, bool TINY>
+struct ScanRows {
+  T* tile;  // first frame of the tile
+  int64_t stride;
+  uint32_t own;  // elements to the lane's first frame and its channels
+  int have;
+  __device__ __forceinline__ ScanRows(const void* p, int64_t entry, int64_t entry_stride, int64_t time_stride, int t0,
+                                      int mine, int channel, int channels)
+      : tile((T*)p + entry * entry_stride + t0 * time_stride), stride(time_stride),
+        own((uint32_t)mine * (uint32_t)time_stride + (uint32_t)channel), have(channels - channel) {}
+  __device__ __forceinline__ void move(int frames) { tile += frames * stride; }
+  __device__ __forceinline__ ScanRaw<T> at(const T* p) const {
+    ScanRaw<T> r;
+    if constexpr (TINY) {
+      const Quad<T> q = load_group<T, kScanChannels>(p, have, (T)0.f);
+      __builtin_memcpy(&r, &q, sizeof(r));
+    } else {
+      __builtin_memcpy(&r, p, sizeof(r));
+    }
+    return r;
+  }
+  // the lane's frame r; where it is `past` frames after the last one, that one
+  __device__ __forceinline__ ScanRaw<T> load(int r) const { return at(tile + r * stride + own); }
+  __device__ __forceinline__ ScanRaw<T> load_last(int r, int past) const {
+    return at(tile + r * stride + ((int64_t)own - (past > 0 ? past : 0) * stride));
+  }
+  __device__ __forceinline__ void store(int r, const Quad<T>& v, const ScanChannels& ch, bool ragged) const {
+    T* p = tile + r * stride + own;
+    if (!TINY && !ragged) {
+      __builtin_memcpy(p, &v, sizeof(v));
+    } else {
+#pragma unroll
+      for (int e = 0; e < kScanChannels; ++e)
+        if (e >= ch.own && e < ch.end) p[e] = v.v[e];
+    }
+  }
+};
 
 // Workgroup -> (block of channels, time range, entry).  Blocks of 64-byte rows
 // that share a 128-byte line go to the same XCD: workgroups b and b + 8.
@@ -98,23 +160,26 @@ __device__ __forceinline__ int64_t scan_unit() {
 // What every scan kernel knows about its place.
 template <class T, int ROW, int R>
 struct ScanPlace {
-  static constexpr int VE = kScanChannels, LC = ROW / (int)(VE * sizeof(T)), K = LC * VE, SW = 64 / LC, SPAN = SW * R, TILE = kScanWaves * SPAN;
+  static constexpr int VE = kScanChannels, LC = ROW / (int)(VE * sizeof(T)), K = LC * VE, SW = 64 / LC, SPAN = SW * R;
+  static constexpr int NW = kScanWaves, TILE = NW * SPAN;
   int lane, wave, slot, time, len, entry, range, beg, end, c0;
   ScanChannels ch;
+  bool ragged;    // the block crosses the last channel
   int64_t part;   // of (entry, range 0) and this block's first channel
   int64_t pitch;  // from range to range
   // role of a lane in the carried sums: channel k of the block
   int k, kc;
   bool kown;
-  __device__ __forceinline__ ScanPlace(const ScanArgs& a, int ranges, int first_range)
+  __device__ __forceinline__ explicit ScanPlace(const ScanArgs& a)
       : lane(threadIdx.x & 63), wave(threadIdx.x >> 6), slot(lane / LC), time(a.time), ch(0, 1) {
     const int blocks = (a.channels + K - 1) / K;
     const int64_t unit = scan_unit<ROW>();
     const int64_t at = unit / blocks;
     const int blk = (int)(unit - at * blocks);
-    entry = (int)(at / ranges);
-    range = (int)(at - (int64_t)entry * ranges) + first_range;
+    entry = (int)(at / a.splits);
+    range = (int)(at - (int64_t)entry * a.splits);
     c0 = blk * K;
+    ragged = c0 + K > a.channels;
     ch = ScanChannels(c0 + lane % LC * VE, a.channels);
     len = time;
     if (a.lengths) {
@@ -134,11 +199,11 @@ struct ScanPlace {
   __device__ __forceinline__ int64_t state_at(const ScanArgs& a) const { return (int64_t)entry * a.channels + kc; }
 };
 
-// Joins ranges 0 .. n - 1 of `part` (A, U), from z = 0 on: 512 / K sets of lanes
+// Joins ranges 0 .. n - 1 of `part` (A, U), from z = 0 on: threads / K sets of lanes
 // a part of the list each.
 template <class P>
 __device__ __forceinline__ float scan_before(const P& p, const float* part, int n, float2* lds) {
-  constexpr int K = P::K, SETS = 64 * kScanWaves / K;
+  constexpr int K = P::K, SETS = 64 * P::NW / K;
   const int k = threadIdx.x % K, set = threadIdx.x / K;
   const int per = (n + SETS - 1) / SETS;
   const int lo = set * per, hi = lo + per < n ? lo + per : n;
@@ -198,19 +263,48 @@ __device__ __forceinline__ void scan_enter(int lane, const float (&A)[VE], const
 }
 
 // a, u (and silu(g)) of a lane's frames, the next tile's loads issued behind each.
-template <class T, int ROW, int R, bool GATE, bool WHOLE>
-__global__ __launch_bounds__(64 * kScanWaves) void scan_forward_kernel(const ScanArgs a) {
+// WHOLE: all ranges, writing y; otherwise the sums of all ranges but the last.
+template <class T, int ROW, int R, bool GATE, bool WHOLE, bool TINY>
+__global__ __launch_bounds__(64 * kScanWaves, (sizeof(T) == 2 && ROW == 128 ? 4 : 1)) void scan_forward_kernel(const ScanArgs a) {
   using P = ScanPlace<T, ROW, R>;
-  constexpr int VE = P::VE, LC = P::LC, K = P::K, NW = kScanWaves;
-  // WHOLE: all ranges, writing y; otherwise the sums of all ranges but the last
-  const P p(a, WHOLE ? a.splits : a.splits - 1, 0);
+  constexpr int VE = P::VE, LC = P::LC, K = P::K, NW = P::NW;
+  const P p(a);
+  if (!WHOLE && p.range == a.splits - 1) return;
   __shared__ float2 tot[2][NW][K];
   __shared__ __attribute__((aligned(16))) float cin[NW][K];
   __shared__ float2 sets[WHOLE ? 64 * NW : 1];
-  const T* x = (const T*)a.x + p.entry * a.xs[0] + p.ch.base;
-  const T* f = (const T*)a.f + p.entry * a.fs[0] + p.ch.base;
-  const T* g = GATE && WHOLE ? (const T*)a.g + p.entry * a.gs[0] + p.ch.base : nullptr;
-  T* y = WHOLE ? (T*)a.y + (int64_t)p.entry * a.time * a.channels + p.ch.base : nullptr;
+  const int mine = p.wave * P::SPAN + p.slot * R;
+  using Rows = ScanRows<T, TINY>;
+  int t0 = p.beg;
+  Rows x(a.x, p.entry, a.xs[0], a.xs[1], t0, mine, p.ch.base, a.channels);
+  Rows f(a.f, p.entry, a.fs[0], a.fs[1], t0, mine, p.ch.base, a.channels);
+  Rows g(a.g, p.entry, a.gs[0], a.gs[1], t0, mine, p.ch.base, a.channels);
+  Rows y(a.y, p.entry, (int64_t)a.time * a.channels, a.channels, t0, mine, p.ch.base, a.channels);
+
+  const int stop = p.len < p.end ? p.len : p.end;
+  ScanRaw<T> xv[R], fv[R], gv[R];
+  const auto load = [&](int r) {
+    xv[r] = x.load(r);
+    fv[r] = f.load(r);
+    if constexpr (GATE && WHOLE) gv[r] = g.load(r);
+  };
+  // of the tile at t, which may cross the end
+  const auto load_last = [&](int t, int r) {
+    const int past = t + mine + r - (stop - 1);
+    xv[r] = x.load_last(r, past);
+    fv[r] = f.load_last(r, past);
+    if constexpr (GATE && WHOLE) gv[r] = g.load_last(r, past);
+  };
+  const auto move = [&]() {
+    x.move(P::TILE);
+    f.move(P::TILE);
+    g.move(P::TILE);
+  };
+  if (t0 < stop) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) load_last(t0, r);
+  }
+  move();
 
   // in the role of channel k: the state before the tile, or the range's (A, U) so far
   float carry, carryA = 1.f;
@@ -225,23 +319,10 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_forward_kernel(const Sca
     carry = scan_before(p, a.part, p.range + 1, sets);
   }
 
-  const int stop = p.len < p.end ? p.len : p.end;
-  const int mine = p.wave * P::SPAN + p.slot * R;
-  Quad<T> xv[R], fv[R], gv[R];
-  const auto load = [&](int t0, int r) {
-    int t = t0 + mine + r;
-    t = t < stop ? t : stop - 1;
-    xv[r] = scan_load(x + t * a.xs[1], a.channels);
-    fv[r] = scan_load(f + t * a.fs[1], a.channels);
-    if constexpr (GATE && WHOLE) gv[r] = scan_load(g + t * a.gs[1], a.channels);
-  };
-  int t0 = p.beg;
-  if (t0 < stop) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) load(t0, r);
-  }
   int buf = 0;
-  for (; t0 < stop; t0 += P::TILE, buf ^= 1) {
+  // MORE: this tile and the next one are whole
+  const auto tile = [&](auto more) {
+    constexpr bool MORE = decltype(more)::value;
     float av[R][VE], uv[R][VE], gs[R][GATE && WHOLE ? VE : 1];
     float A[VE], U[VE];
 #pragma unroll
@@ -251,23 +332,34 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_forward_kernel(const Sca
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      // frames past the end keep the state: a = 1, u = 0
-      const bool real = t0 + mine + r < stop;
-      const Quad<T> xr = scan_pick(real, xv[r], 0.f), fr = scan_pick(real, fv[r], INFINITY);
+      if constexpr (!MORE) {
+        // frames past the end keep the state: a = 1, u = 0
+        const bool real = t0 + mine + r < stop;
+        xv[r].pick(real, false);
+        fv[r].pick(real, true);
+        if constexpr (GATE && WHOLE) gv[r].pick(real, false);
+      }
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
         float rest;
-        sigmoids<T>((float)fr.v[e], av[r][e], rest);
-        uv[r][e] = rest * (float)xr.v[e];
+        sigmoids<T>(fv[r].get(e), av[r][e], rest);
+        uv[r][e] = rest * xv[r].get(e);
         U[e] = fmaf(av[r][e], U[e], uv[r][e]);
         A[e] *= av[r][e];
         if constexpr (GATE && WHOLE) {
-          const float gg = (float)gv[r].v[e];
+          const float gg = gv[r].get(e);
           gs[r][e] = gg * __builtin_amdgcn_rcpf(1.f + exp_minus<T>(gg));
         }
       }
-      load(t0 + P::TILE, r);
+      if constexpr (MORE) load(r);
     }
+    if constexpr (!MORE) {
+      if (t0 + P::TILE < stop) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) load_last(t0 + P::TILE, r);
+      }
+    }
+    move();
     scan_slots<LC, VE, true>(p.lane, A, U);
     if (p.slot == P::SW - 1) {
 #pragma unroll
@@ -275,7 +367,7 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_forward_kernel(const Sca
     }
     __syncthreads();
     float before = 0.f;
-#pragma unroll
+#pragma unroll 2
     for (int w = 0; w < NW; ++w) {
       const float2 v = tot[buf][w][p.k];
       if (w == p.wave) before = carry;
@@ -303,22 +395,31 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_forward_kernel(const Sca
           h[e] = fmaf(av[r][e], h[e], uv[r][e]);
           float o = h[e];
           if constexpr (GATE) o *= gs[r][e];
-          out.v[e] = (T)(t < stop ? o : 0.f);
+          out.v[e] = (T)o;
         }
-        if (t < p.end) scan_store(y + (int64_t)t * a.channels, out, p.ch.own, p.ch.end);
+        if constexpr (MORE)
+          y.store(r, out, p.ch, p.ragged);
+        else if (t < p.end)
+          y.store(r, scan_pick(t < stop, out), p.ch, p.ragged);
       }
+      y.move(P::TILE);
     }
-  }
+    buf ^= 1;
+    t0 += P::TILE;
+  };
+  while (t0 + 2 * P::TILE <= stop) tile(std::true_type{});
+  while (t0 < stop) tile(std::false_type{});
   if constexpr (WHOLE) {
     // tiles past the length
     Quad<T> zero;
 #pragma unroll
     for (int e = 0; e < VE; ++e) zero.v[e] = (T)0.f;
-    for (; t0 < p.end; t0 += P::TILE)
+    for (; t0 < p.end; t0 += P::TILE) {
 #pragma unroll
       for (int r = 0; r < R; ++r)
-        if (t0 + mine + r < p.end)
-          scan_store(y + (int64_t)(t0 + mine + r) * a.channels, zero, p.ch.own, p.ch.end);
+        if (t0 + mine + r < p.end) y.store(r, zero, p.ch, p.ragged);
+      y.move(P::TILE);
+    }
     if (p.range == a.splits - 1 && p.wave == 0 && p.kown) a.last[p.state_at(a)] = carry;
   } else {
     if (p.wave == 0 && p.lane < K)
@@ -363,7 +464,14 @@ __global__ __launch_bounds__(64) void scan_step_kernel(const ScanArgs a) {
       }
       out.v[e] = (T)(t < len ? o : 0.f);
     }
-    scan_store(y + (int64_t)t * a.channels, out, 0, have < VE ? have : VE);
+    T* to = y + (int64_t)t * a.channels;
+    if (have >= VE) {
+      __builtin_memcpy(to, &out, sizeof(out));
+    } else {
+#pragma unroll
+      for (int e = 0; e < VE; ++e)
+        if (e < have) to[e] = out.v[e];
+    }
   }
   float* last = a.last + entry * a.channels + c;
 #pragma unroll
@@ -373,23 +481,51 @@ __global__ __launch_bounds__(64) void scan_step_kernel(const ScanArgs a) {
 
 // WHOLE: the gradients; otherwise the sums (A, m) of all ranges but the first.
 // Ranges count from the end of time.
-template <class T, int ROW, int R, bool GATE, bool WHOLE>
-__global__ __launch_bounds__(64 * kScanWaves) void scan_backward_kernel(const ScanArgs a) {
+template <class T, int ROW, int R, bool GATE, bool WHOLE, bool TINY>
+__global__ __launch_bounds__(64 * kScanWaves, (sizeof(T) == 2 && ROW == 128 ? 4 : 1)) void scan_backward_kernel(const ScanArgs a) {
   using P = ScanPlace<T, ROW, R>;
-  constexpr int VE = P::VE, LC = P::LC, K = P::K, NW = kScanWaves;
+  constexpr int VE = P::VE, LC = P::LC, K = P::K, NW = P::NW;
   static_assert(P::TILE % kScanSave == 0, "a tile starts where a state was kept");
-  const P p(a, WHOLE ? a.splits : a.splits - 1, WHOLE ? 0 : 1);
+  const P p(a);
+  if (!WHOLE && p.range == 0) return;
   const int back = a.splits - 1 - p.range;
   __shared__ float2 tot[2][NW][K];
   __shared__ float totm[2][NW][K];
   __shared__ __attribute__((aligned(16))) float cin[NW][2][K];
   __shared__ float2 sets[WHOLE ? 64 * NW : 1];
-  const T* x = (const T*)a.x + p.entry * a.xs[0] + p.ch.base;
-  const T* f = (const T*)a.f + p.entry * a.fs[0] + p.ch.base;
-  const T* g = GATE ? (const T*)a.g + p.entry * a.gs[0] + p.ch.base : nullptr;
-  const T* dy = (const T*)a.dy + p.entry * a.dys[0] + p.ch.base;
-  const int64_t out0 = (int64_t)p.entry * a.time * a.channels + p.ch.base;
-  const float* saved = a.saved + (int64_t)p.entry * ((a.time + kScanSave - 1) / kScanSave) * a.channels + p.kc;
+  const int mine = p.wave * P::SPAN + p.slot * R;
+  using Rows = ScanRows<T, TINY>;
+  const int stop = p.len < p.end ? p.len : p.end;
+  const int tiles = stop > p.beg ? (stop - p.beg + P::TILE - 1) / P::TILE : 0;
+  int t0 = p.beg + tiles * P::TILE;  // behind the last tile
+  const int64_t whole = (int64_t)a.time * a.channels;
+  Rows dx(a.dx, p.entry, whole, a.channels, t0, mine, p.ch.base, a.channels);
+  Rows df(a.df, p.entry, whole, a.channels, t0, mine, p.ch.base, a.channels);
+  Rows dg(a.dg, p.entry, whole, a.channels, t0, mine, p.ch.base, a.channels);
+  const auto put = [&](int r, const Quad<T>& ox, const Quad<T>& of, const Quad<T>& og) {
+    dx.store(r, ox, p.ch, p.ragged);
+    df.store(r, of, p.ch, p.ragged);
+    if constexpr (GATE) dg.store(r, og, p.ch, p.ragged);
+  };
+  const auto move_out = [&](int frames) {
+    dx.move(frames);
+    df.move(frames);
+    dg.move(frames);
+  };
+  if constexpr (WHOLE) {
+    // tiles past the length
+    Quad<T> zero;
+#pragma unroll
+    for (int e = 0; e < VE; ++e) zero.v[e] = (T)0.f;
+    int t = t0;
+    for (; t < p.end; t += P::TILE) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (t + mine + r < p.end) put(r, zero, zero, zero);
+      move_out(P::TILE);
+    }
+    move_out(t0 - t);
+  }
 
   // in the role of channel k: m behind the tile
   float carry, carryA = 1.f;
@@ -403,92 +539,105 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_backward_kernel(const Sc
     carry = scan_before(p, a.part, back + 1, sets);
   }
 
-  const int stop = p.len < p.end ? p.len : p.end;
-  const int tiles = stop > p.beg ? (stop - p.beg + P::TILE - 1) / P::TILE : 0;
-  const int mine = p.wave * P::SPAN + p.slot * R;
-  if constexpr (WHOLE) {
-    // tiles past the length
-    Quad<T> zero;
-#pragma unroll
-    for (int e = 0; e < VE; ++e) zero.v[e] = (T)0.f;
-    for (int t0 = p.beg + tiles * P::TILE; t0 < p.end; t0 += P::TILE)
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int t = t0 + mine + r;
-        if (t < p.end) {
-          const int64_t at = out0 + (int64_t)t * a.channels;
-          scan_store((T*)a.dx + at, zero, p.ch.own, p.ch.end);
-          scan_store((T*)a.df + at, zero, p.ch.own, p.ch.end);
-          if constexpr (GATE) scan_store((T*)a.dg + at, zero, p.ch.own, p.ch.end);
-        }
-      }
-  }
-
-  Quad<T> xv[R], fv[R], gv[R], dv[R];
+  t0 -= P::TILE;
+  move_out(-P::TILE);
+  Rows x(a.x, p.entry, a.xs[0], a.xs[1], t0, mine, p.ch.base, a.channels);
+  Rows f(a.f, p.entry, a.fs[0], a.fs[1], t0, mine, p.ch.base, a.channels);
+  Rows g(a.g, p.entry, a.gs[0], a.gs[1], t0, mine, p.ch.base, a.channels);
+  Rows dy(a.dy, p.entry, a.dys[0], a.dys[1], t0, mine, p.ch.base, a.channels);
+  const float* saved = a.saved + (int64_t)p.entry * ((a.time + kScanSave - 1) / kScanSave) * a.channels;
+  ScanRaw<T> xv[R], fv[R], gv[R], dv[R];
   float kept = 0.f;
-  const auto load = [&](int t0, int r) {
-    int t = t0 + mine + r;
-    t = t < stop ? t : stop - 1;
-    if constexpr (WHOLE) xv[r] = scan_load(x + t * a.xs[1], a.channels);
-    fv[r] = scan_load(f + t * a.fs[1], a.channels);
-    if constexpr (GATE) gv[r] = scan_load(g + t * a.gs[1], a.channels);
-    dv[r] = scan_load(dy + t * a.dys[1], a.channels);
+  const auto load = [&](int r) {
+    if constexpr (WHOLE) xv[r] = x.load(r);
+    fv[r] = f.load(r);
+    if constexpr (GATE) gv[r] = g.load(r);
+    dv[r] = dy.load(r);
   };
-  int t0 = p.beg + (tiles - 1) * P::TILE;
+  const auto move = [&]() {
+    x.move(-P::TILE);
+    f.move(-P::TILE);
+    g.move(-P::TILE);
+    dy.move(-P::TILE);
+  };
   if (tiles > 0) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) load(t0, r);
-    if constexpr (WHOLE) kept = saved[(int64_t)(t0 / kScanSave) * a.channels];
+    for (int r = 0; r < R; ++r) {
+      const int past = t0 + mine + r - (stop - 1);
+      if constexpr (WHOLE) xv[r] = x.load_last(r, past);
+      fv[r] = f.load_last(r, past);
+      if constexpr (GATE) gv[r] = g.load_last(r, past);
+      dv[r] = dy.load_last(r, past);
+    }
+    if constexpr (WHOLE) kept = (saved + (int64_t)(t0 / kScanSave) * a.channels)[(uint32_t)p.kc];
   }
+  move();
   int buf = 0;
-  for (int i = 0; i < tiles; ++i, t0 -= P::TILE, buf ^= 1) {
+  // FULL: all frames of this tile; only the first one may have fewer
+  const auto tile = [&](auto full) {
+    constexpr bool FULL = decltype(full)::value;
     float av[R][VE], rest[R][VE], ev[R][VE], gd[R][GATE ? VE : 1];
-    Quad<T> xr[R];
+    ScanRaw<T> xr[R];
     float A[VE], U[VE], B[VE], M[VE];
-    const int next = t0 - P::TILE > p.beg ? t0 - P::TILE : p.beg;
+    const float state = kept;
+    const bool more = t0 > p.beg;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const bool real = t0 + mine + r < stop;
-      if constexpr (WHOLE) xr[r] = scan_pick(real, xv[r], 0.f);
-      const Quad<T> fr = scan_pick(real, fv[r], INFINITY), dr = scan_pick(real, dv[r], 0.f);
-      Quad<T> gr;
-      if constexpr (GATE) gr = scan_pick(real, gv[r], 0.f);
+      if constexpr (!FULL) {
+        const bool real = t0 + mine + r < stop;
+        if constexpr (WHOLE) xv[r].pick(real, false);
+        fv[r].pick(real, true);
+        if constexpr (GATE) gv[r].pick(real, false);
+        dv[r].pick(real, false);
+      }
+      if constexpr (WHOLE) xr[r] = xv[r];
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
-        sigmoids<T>((float)fr.v[e], av[r][e], rest[r][e]);
-        const float d = (float)dr.v[e];
+        sigmoids<T>(fv[r].get(e), av[r][e], rest[r][e]);
+        const float d = dv[r].get(e);
         ev[r][e] = d;
         if constexpr (GATE) {
-          const float gg = (float)gr.v[e];
+          const float gg = gv[r].get(e);
           const float sg = __builtin_amdgcn_rcpf(1.f + exp_minus<T>(gg));
           const float sl = gg * sg;
           ev[r][e] = d * sl;
           gd[r][e] = d * fmaf(sl, 1.f - sg, sg);  // dy silu'(g)
         }
       }
-      load(next, r);
     }
-    const float state = kept;
-    if constexpr (WHOLE) kept = saved[(int64_t)(next / kScanSave) * a.channels];
+    if (more) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) load(r);
+      if constexpr (WHOLE) kept = (saved + (int64_t)((t0 - P::TILE) / kScanSave) * a.channels)[(uint32_t)p.kc];
+    }
+    move();
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
       A[e] = 1.f;
-      U[e] = M[e] = 0.f;
+      U[e] = 0.f;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        if constexpr (WHOLE) U[e] = fmaf(av[r][e], U[e], rest[r][e] * (float)xr[r].v[e]);
+        if constexpr (WHOLE) U[e] = fmaf(av[r][e], U[e], rest[r][e] * xr[r].get(e));
         A[e] *= av[r][e];
       }
       B[e] = A[e];
+    }
+    if constexpr (WHOLE) {
+      scan_slots<LC, VE, true>(p.lane, A, U);
+      if (p.slot == P::SW - 1) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) tot[buf][p.wave][p.lane % LC * VE + e] = make_float2(A[e], U[e]);
+      }
+      // one direction after the other: both at once take more registers than there are
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      M[e] = 0.f;
 #pragma unroll
       for (int r = R - 1; r >= 0; --r) M[e] = av[r][e] * (ev[r][e] + M[e]);
     }
-    if constexpr (WHOLE) scan_slots<LC, VE, true>(p.lane, A, U);
     scan_slots<LC, VE, false>(p.lane, B, M);
-    if (WHOLE && p.slot == P::SW - 1) {
-#pragma unroll
-      for (int e = 0; e < VE; ++e) tot[buf][p.wave][p.lane % LC * VE + e] = make_float2(A[e], U[e]);
-    }
     if (p.slot == 0) {
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
@@ -498,7 +647,7 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_backward_kernel(const Sc
     }
     __syncthreads();
     float behind = 0.f;
-#pragma unroll
+#pragma unroll 1
     for (int w = NW - 1; w >= 0; --w) {
       const float va = tot[buf][w][p.k].x;
       if (w == p.wave) behind = carry;
@@ -507,8 +656,8 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_backward_kernel(const Sc
     }
     if constexpr (WHOLE) {
       float before = state;
-#pragma unroll
-      for (int w = 0; w < NW - 1; ++w) {
+#pragma unroll 1
+      for (int w = 0; w < p.wave; ++w) {
         const float2 v = tot[buf][w][p.k];
         if (w < p.wave) before = fmaf(v.x, before, v.y);
       }
@@ -525,40 +674,47 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_backward_kernel(const Sc
 #pragma unroll
       for (int e = 0; e < VE; ++e) border[e] = cin[p.wave][1][p.lane % LC * VE + e];
       scan_enter<LC, VE, false>(p.lane, B, M, border, m);
+      // x is unpacked again rather than kept in registers since the first walk
+#pragma unroll
+      for (int r = 0; r < R; ++r) xr[r].forget();
+      // hs: h - x from here on, and dg in place of dy silu'(g)
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
-          h[e] = fmaf(av[r][e], h[e], rest[r][e] * (float)xr[r].v[e]);
-          hs[r][e] = h[e];
+          const float xe = xr[r].get(e);
+          h[e] = fmaf(av[r][e], h[e], rest[r][e] * xe);
+          hs[r][e] = h[e] - xe;
+          if constexpr (GATE) gd[r][e] *= h[e];
         }
 #pragma unroll
       for (int r = R - 1; r >= 0; --r) {
         const int t = t0 + mine + r;
-        Quad<T> dx, df, dg;
+        Quad<T> ox, of, og;
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
           const float d = ev[r][e] + m[e];
           const float u = rest[r][e] * d;
           m[e] = av[r][e] * d;
-          dx.v[e] = (T)u;
-          df.v[e] = (T)(u * (hs[r][e] - (float)xr[r].v[e]));
-          if constexpr (GATE) dg.v[e] = (T)(gd[r][e] * hs[r][e]);
+          ox.v[e] = (T)u;
+          of.v[e] = (T)(u * hs[r][e]);
+          if constexpr (GATE) og.v[e] = (T)gd[r][e];
         }
-        if (t >= stop) {
-          // rest is 0 there, but the state need not be finite
-#pragma unroll
-          for (int e = 0; e < VE; ++e) dx.v[e] = df.v[e] = dg.v[e] = (T)0.f;
-        }
-        if (t < p.end) {
-          const int64_t at = out0 + (int64_t)t * a.channels;
-          scan_store((T*)a.dx + at, dx, p.ch.own, p.ch.end);
-          scan_store((T*)a.df + at, df, p.ch.own, p.ch.end);
-          if constexpr (GATE) scan_store((T*)a.dg + at, dg, p.ch.own, p.ch.end);
+        if constexpr (FULL) {
+          put(r, ox, of, og);
+        } else if (t < p.end) {
+          // rest is 0 past the end, but the state need not be finite
+          const bool real = t < stop;
+          put(r, scan_pick(real, ox), scan_pick(real, of), GATE ? scan_pick(real, og) : ox);
         }
       }
+      move_out(-P::TILE);
     }
-  }
+    buf ^= 1;
+    t0 -= P::TILE;
+  };
+  if (tiles > 0 && t0 + P::TILE > stop) tile(std::false_type{});
+  while (t0 >= p.beg) tile(std::true_type{});
   if constexpr (WHOLE) {
     if (a.dstate && p.range == 0 && p.wave == 0 && p.kown) a.dstate[p.state_at(a)] = carry;
   } else {
@@ -578,20 +734,20 @@ int scan_forward_t(ScanArgs a, void* stream) {
   a.splits = s.splits;
   a.chunk = s.chunk;
   const int64_t units = a.batch * scan_blocks(a.channels, s.row, sizeof(T));
-  const auto go = [&](auto kernel, int ranges) {
-    return launch("gated recurrence", kernel, dim3((unsigned)(units * ranges)), dim3(64 * kScanWaves), 0, stream, a);
+  const auto go = [&](auto kernel) {
+    return launch("gated recurrence", kernel, dim3((unsigned)(units * s.splits)), dim3(64 * kScanWaves), 0, stream, a);
   };
-#define FM_SCAN_FWD(L, R)                                                                       \
-  if (s.row == L && s.frames == R) {                                                          \
-    if (s.splits > 1)                                                                           \
-      if (int st = go(scan_forward_kernel<T, L, R, false, false>, s.splits - 1)) return st;     \
-    return a.g ? go(scan_forward_kernel<T, L, R, true, true>, s.splits)                         \
-               : go(scan_forward_kernel<T, L, R, false, true>, s.splits);                       \
+#define FM_SCAN_FWD(L, R, TINY)                                                     \
+  if (s.row == L && s.frames == R && (a.channels < kScanChannels) == TINY) {        \
+    if (s.splits > 1)                                                               \
+      if (int st = go(scan_forward_kernel<T, L, R, false, false, TINY>)) return st; \
+    return a.g ? go(scan_forward_kernel<T, L, R, true, true, TINY>)                 \
+               : go(scan_forward_kernel<T, L, R, false, true, TINY>);               \
   }
-  FM_SCAN_FWD(128, 2)
-  FM_SCAN_FWD(128, 4)
-  FM_SCAN_FWD(64, 1)
-  FM_SCAN_FWD(64, 4)
+  FM_SCAN_FWD(128, 2, false)
+  FM_SCAN_FWD(128, 4, false)
+  FM_SCAN_FWD(64, 4, false)
+  FM_SCAN_FWD(64, 1, true)
 #undef FM_SCAN_FWD
   return set_error(FM_E_UNSUPPORTED, "gated recurrence: no kernel for this shape");
 }
@@ -602,22 +758,24 @@ int scan_backward_t(ScanArgs a, void* stream) {
   a.splits = s.splits;
   a.chunk = s.chunk;
   const int64_t units = a.batch * scan_blocks(a.channels, s.row, sizeof(T));
-  const auto go = [&](auto kernel, int ranges) {
-    return launch("gated recurrence backward", kernel, dim3((unsigned)(units * ranges)), dim3(64 * kScanWaves), 0,
+  const auto go = [&](auto kernel) {
+    return launch("gated recurrence backward", kernel, dim3((unsigned)(units * s.splits)), dim3(64 * kScanWaves), 0,
                   stream, a);
   };
-#define FM_SCAN_BWD(L, R)                                                                        \
-  if (s.row == L && s.frames == R) {                                                           \
-    if (s.splits > 1)                                                                            \
-      if (int st = a.g ? go(scan_backward_kernel<T, L, R, true, false>, s.splits - 1)            \
-                       : go(scan_backward_kernel<T, L, R, false, false>, s.splits - 1))          \
-        return st;                                                                               \
-    return a.g ? go(scan_backward_kernel<T, L, R, true, true>, s.splits)                         \
-               : go(scan_backward_kernel<T, L, R, false, true>, s.splits);                       \
+#define FM_SCAN_BWD(L, R, TINY)                                                 \
+  if (s.row == L && s.frames == R && (a.channels < kScanChannels) == TINY) {    \
+    if (s.splits > 1)                                                           \
+      if (int st = a.g ? go(scan_backward_kernel<T, L, R, true, false, TINY>)   \
+                       : go(scan_backward_kernel<T, L, R, false, false, TINY>)) \
+        return st;                                                              \
+    return a.g ? go(scan_backward_kernel<T, L, R, true, true, TINY>)            \
+               : go(scan_backward_kernel<T, L, R, false, true, TINY>);          \
   }
-  FM_SCAN_BWD(128, 2)
-  FM_SCAN_BWD(64, 1)
-  FM_SCAN_BWD(64, 2)
+  FM_SCAN_BWD(128, 2, false)
+  if constexpr (sizeof(T) == 4) {
+    FM_SCAN_BWD(64, 2, false)
+  }
+  FM_SCAN_BWD(64, 1, true)
 #undef FM_SCAN_BWD
   return set_error(FM_E_UNSUPPORTED, "gated recurrence: no kernel for this shape");
 }

@@ -18,8 +18,10 @@ int recurrence_args(const fm_recurrence_args* p, ScanArgs& a) {
   if (!p) return bad("gated recurrence: args must not be NULL");
   if (!elem_bytes(p->dtype)) return bad("gated recurrence: dtype must be FM_F32, FM_F16 or FM_BF16");
   const int64_t most = int64_t(1) << 30;
-  if (p->batch < 0 || p->batch >= most || p->time < 0 || p->time >= most || p->channels < 1 || p->channels >= most)
-    return bad("gated recurrence: batch and time must be in [0, 2^30), channels in [1, 2^30)");
+  if (p->batch < 0 || p->batch >= most || p->time < 0 || p->time >= most || p->channels < 1)
+    return bad("gated recurrence: batch and time must be in [0, 2^30), channels >= 1");
+  if (p->channels > kScanMaxChannels)
+    return set_error(FM_E_UNSUPPORTED, "gated recurrence: channels must be <= 2^20");
   a = ScanArgs{};
   a.batch = static_cast<int>(p->batch);
   a.time = static_cast<int>(p->time);
@@ -65,6 +67,9 @@ int recurrence_pointers(const ScanArgs& a, int dtype, bool backward) {
       (backward && !scan_strides_fit(a.dys)))
     return bad("gated recurrence: strides must be >= 0");
   const int es = elem_bytes(dtype);
+  if (a.xs[1] >= kScanMaxStride / es || a.fs[1] >= kScanMaxStride / es || (a.g && a.gs[1] >= kScanMaxStride / es) ||
+      (backward && a.dys[1] >= kScanMaxStride / es))
+    return set_error(FM_E_UNSUPPORTED, "gated recurrence: frames must be less than 8 MiB apart");
   if (!aligned_to(a.x, es) || !aligned_to(a.f, es) || !aligned_to(a.g, es) || !aligned_to(a.y, es) ||
       !aligned_to(a.dy, es) || !aligned_to(a.dx, es) || !aligned_to(a.df, es) || !aligned_to(a.dg, es) ||
       !aligned_to(a.state, 4) || !aligned_to(a.lengths, 4) || !aligned_to(a.last, 4) || !aligned_to(a.saved, 4) ||

@@ -34,29 +34,43 @@ struct ScanArgs {
 };
 
 constexpr int kScanSave = 64;   // frames between saved states
-constexpr int kScanWaves = 8;   // waves of a workgroup, one time range of a tile each
-
 // Bytes of a frame's row that a workgroup takes (four channels a lane), frames of
 // a lane, time ranges and their length.
 struct ScanSplit {
   int row, frames, splits, chunk;
 };
-// Frames of a tile: 8 waves, as many lanes of the same channels, frames of a lane.
+constexpr int kScanWaves = 8;  // waves of a workgroup, one time range of a tile each
+// Frames of a tile: waves, as many lanes of the same channels, frames of a lane.
 constexpr int scan_tile(int row, int frames, int size) { return kScanWaves * (64 * 4 * size / row) * frames; }
 inline int64_t scan_blocks(int channels, int row, int size) {
   const int n = row / size;
   return ((int64_t)channels + n - 1) / n;
 }
+// Whole 128-byte lines where that gives a workgroup per compute unit (forward,
+// 16 x 1501 x 2048 bf16: 83 us, 64-byte rows 100; backward 168 and 217), 64-byte rows
+// where those do for five eighths (8 x 1501 x 1024 bf16: 26 us, 128-byte rows 35, in
+// time ranges 32; 4 x 3000 x 1000 f32: 38, 39 and 52).
+// The backward of 16-bit frames, two of whose workgroups share a unit, takes time
+// ranges instead (50 us, 64-byte rows 55), and so does everything with fewer
+// channels: as many ranges as fill the chip, down to one tile each (1 x 1501 x 1024
+// bf16: forward 10, unsplit 21; backward 16 and 50; 1 x 100003 x 256 f16: 60 and 1230).
+// A first launch then reads x and forget (backward: forget, gate and grad_y) twice.
+// Four frames a lane forward (16 x 1501 x 2048: 83, 2 frames the same, 8 x 1501 x 1024: 26
+// and 28), two backward (four do not fit the registers), two for what one tile holds.
+// Fewer than four channels have kernels of their own, single frames.
 inline ScanSplit scan_split(int batch, int time, int channels, int size, bool backward) {
   ScanSplit p;
-  p.row = (int64_t)batch * scan_blocks(channels, 128, size) >= 256 ? 128 : 64;
-  const int least = p.row == 128 ? 2 : 1;
-  p.frames = time <= scan_tile(p.row, least, size) ? least : backward ? 2 : 4;
-  const int64_t units = batch * scan_blocks(channels, p.row, size);
+  const int64_t wide = (int64_t)batch * scan_blocks(channels, 128, size);
+  const int64_t narrow = (int64_t)batch * scan_blocks(channels, 64, size);
+  const bool tiny = channels < 4;
+  const bool brief = time <= scan_tile(128, 2, size);
+  p.row = tiny || (!brief && wide < 256 && narrow >= 160 && (!backward || size == 4)) ? 64 : 128;
+  p.frames = tiny ? 1 : backward || brief ? 2 : 4;
+  const int64_t units = p.row == 128 ? wide : narrow;
   const int tile = scan_tile(p.row, p.frames, size);
   const int64_t tiles = ((int64_t)time + tile - 1) / tile;
-  int64_t s = units > 0 ? 512 / units : 1;
-  if (s > tiles / 2) s = tiles / 2;
+  int64_t s = units > 0 && units < (p.row == 128 ? 256 : 160) ? 512 / units : 1;
+  if (s > tiles) s = tiles;
   if (s < 1) s = 1;
   const int64_t per = tiles > 0 ? (tiles + s - 1) / s : 1;
   p.splits = (int)(tiles > 0 ? (tiles + per - 1) / per : 1);
@@ -67,9 +81,13 @@ inline int64_t scan_workspace(int batch, int time, int channels, int size, bool 
   const ScanSplit p = scan_split(batch, time, channels, size, backward);
   return p.splits == 1 ? 0 : 8 * (int64_t)batch * p.splits * scan_blocks(channels, p.row, size) * (p.row / size);
 }
-// Few frames go one after another through threads that hold four channels.
-constexpr int kScanStepFrames = 8;
+// Few frames go one after another through threads that hold four channels (8 x 1 x
+// 1024 bf16: 3.2 us, tiles 4.0; 8 frames 7.2 and 4.1).
+constexpr int kScanStepFrames = 2;
 inline bool scan_steps(const ScanArgs& a) { return a.time <= kScanStepFrames && !a.saved; }
+// Bytes between frames below this stay in 32 bits over a tile (256 frames at most).
+constexpr int64_t kScanMaxStride = int64_t(1) << 23;
+constexpr int kScanMaxChannels = 1 << 20;
 
 int scan_forward_f32(const ScanArgs& a, void* stream);
 int scan_forward_f16(const ScanArgs& a, void* stream);

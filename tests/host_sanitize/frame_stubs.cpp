@@ -38,10 +38,10 @@ int distill(const DistillArgs& a, int ve) {
   return FM_OK;
 }
 int adjust(const AdjustArgs& a, int ve) {
-  const int64_t n = int64_t(256) * ve * adjust_vecs(a.rows, a.vocab, ve);
+  const int64_t n = int64_t(kAdjustThreads) * ve * adjust_vecs(a.rows, a.vocab, ve);
   if (a.segs != adjust_segments(a.rows, a.vocab, ve) || n * a.segs < a.vocab || n * (a.segs - 1) >= a.vocab)
     return set_error(FM_E_HIP, "segments do not cover the row");
-  return a.rows * a.segs * 256 < int64_t(1) << 31 ? FM_OK : set_error(FM_E_HIP, "grid");
+  return a.rows * a.segs * kAdjustThreads < int64_t(1) << 31 ? FM_OK : set_error(FM_E_HIP, "grid");
 }
 
 }  // namespace

@@ -32,7 +32,7 @@ def recurrence(backward=False, ws=P, **kw):
 @pytest.mark.parametrize("backward", [False, True])
 @pytest.mark.parametrize("kw", [
     dict(dtype=N.FM_I16), dict(dtype=9), dict(batch=-1), dict(batch=1 << 30), dict(time=-1), dict(time=1 << 30),
-    dict(channels=0), dict(channels=1 << 30), dict(batch=1 << 20, channels=1 << 20), dict(x=None), dict(forget=None),
+    dict(channels=0), dict(channels=-4), dict(batch=1 << 20, channels=1 << 20), dict(x=None), dict(forget=None),
     dict(x=P + 1), dict(gate=P + 1), dict(state=P + 2), dict(lengths=P + 1), dict(saved=P + 2), dict(ws=None),
     dict(ws=P + 8), dict(x_stride_time=-1), dict(forget_stride_entry=-40), dict(gate_stride_time=-1)])
 def test_recurrence_refuses(kw, backward):
@@ -46,6 +46,9 @@ def test_recurrence_ends():
     for kw in (dict(grad_y=None), dict(grad_x=None), dict(grad_forget=None), dict(grad_gate=None), dict(saved=None),
                dict(grad_y_stride_time=-1), dict(grad_x=P + 1), dict(grad_last=P + 1), dict(grad_state=P + 3)):
         assert recurrence(True, **kw) == N.FM_E_INVAL
+    for kw in (dict(channels=(1 << 20) + 1), dict(x_stride_time=1 << 22), dict(forget_stride_time=1 << 40)):
+        assert recurrence(False, **kw) == recurrence(True, **kw) == N.FM_E_UNSUPPORTED
+    assert recurrence(True, grad_y_stride_time=1 << 22) == N.FM_E_UNSUPPORTED
     assert recurrence(batch=0, ws=None, x=None, y=None) == N.FM_OK  # nothing to do, nothing launched
     assert N.lib.fm_gated_recurrence_forward(None, None, None) == N.FM_E_INVAL
     assert N.lib.fm_gated_recurrence_workspace(None, 0) == N.FM_E_INVAL
@@ -140,7 +143,7 @@ def test_distillation_ends():
 
 @pytest.mark.parametrize("kw", [
     dict(dtype=N.FM_I16), dict(rows=-1), dict(rows=1 << 31), dict(rows=1 << 22, vocab=1 << 20), dict(vocab=0),
-    dict(vocab=(1 << 31) - 65536), dict(history_len=-1), dict(history_len=(1 << 30) + 1), dict(history_bits=16),
+    dict(vocab=(1 << 31) - 65536), dict(history_len=-1), dict(history_bits=16),
     dict(biases=-1), dict(x=None), dict(out=None), dict(history=None), dict(bias=None), dict(bias_ids=None),
     dict(repetition=None, repetition_value=0.0), dict(repetition=None, repetition_value=-2.0),
     dict(repetition=None, repetition_value=math.nan), dict(frequency=None, frequency_value=math.inf),
@@ -160,7 +163,9 @@ def test_adjusted_logits_limits():
     base = dict(dtype=N.FM_F16, history_bits=64, rows=3, vocab=100, biases=1025, repetition_value=1.0, x=P, out=P,
                 bias=P, bias_ids=P)
     assert N.lib.fm_adjust_logits(fill(N.AdjustArgs(), base, {}), None) == N.FM_E_UNSUPPORTED
-    assert N.lib.fm_adjust_logits(fill(N.AdjustArgs(), base, dict(rows=0, biases=0, x=None)), None) == N.FM_OK
+    assert N.lib.fm_adjust_logits(fill(N.AdjustArgs(), base, dict(biases=0, history_len=1 << 20, history=P)),
+                                  None) == N.FM_E_UNSUPPORTED
+    assert N.lib.fm_adjust_logits(fill(N.AdjustArgs(), base, dict(history_len=0, rows=0, x=None)), None) == N.FM_OK
     assert N.lib.fm_adjust_logits(None, None) == N.FM_E_INVAL
 
 
