@@ -1,7 +1,7 @@
 // Logits before a token is chosen: penalties for tokens of the history, biases,
 // and a mask of allowed tokens.
 //
-//   x = x > 0 ? x / rep : x rep (tokens seen), x -= freq count + pres [count > 0],
+//   x = x > 0 ? x (1 / rep) : x rep (tokens seen), x -= freq count + pres [count > 0],
 //   x += sum of the token's biases, x = -inf where its bit is 0
 //
 // A workgroup of 512 lanes takes a segment of a row.  Its logits, the history and
@@ -26,7 +26,7 @@ constexpr uint32_t kSlotOnce = 2, kSlotBias = 1u << 21;
 template <class T, int V>
 __global__ __launch_bounds__(kAdjustThreads) void adjust_kernel(const AdjustArgs a) {
   constexpr int VE = Vec16<T>::n, NT = kAdjustThreads, SEG = NT * VE * V;
-  constexpr int HIST = 8;                          // tokens of a lane at a time
+  constexpr int HIST = V > 2 ? 4 : 8;                         // tokens of a lane at a time
   constexpr int BIAS = kAdjustMaxBiases / NT;      // bias entries of a lane
   extern __shared__ __attribute__((aligned(16))) uint32_t slots[];  // [SEG], ids and values of the biases
   int* bias_id = (int*)slots + SEG;
@@ -50,22 +50,34 @@ __global__ __launch_bounds__(kAdjustThreads) void adjust_kernel(const AdjustArgs
   }
   const int prompt = a.prompt_lengths && len > 0 ? a.prompt_lengths[row] : 0;
   const float rep = a.repetition ? a.repetition[row] : a.repetition_value;
+  const float over = 1.f / rep;  // one rounding more than a division, for a tenth of its instructions
   const float freq = a.frequency ? a.frequency[row] : a.frequency_value;
   const float pres = a.presence ? a.presence[row] : a.presence_value;
   // tokens as slots of this segment, or -1
-  const auto slot = [&](int64_t id) {
-    const int64_t c = id - beg;
-    return c >= 0 && c < n ? (int)c : -1;
+  const auto slot = [&](uint32_t lo, uint32_t hi) {
+    const uint32_t c = lo - (uint32_t)beg;
+    const bool in = (int)(hi == 0) & (int)(c < (uint32_t)n);
+    return in ? (int)c : -1;
   };
   const char* h = (const char*)a.history + row * a.history_stride * (a.history64 ? 8 : 4);
   int tok[HIST];
-  // all of them, so that no load waits for the row's length
+  // all of them, so that no load waits for the row's length, and without branches
   const auto history = [&](int first) {
-#pragma unroll
-    for (int j = 0; j < HIST; ++j) {
+    uint64_t id[HIST];
+    const auto at = [&](int j) {
       const int k = first + j * NT + tid;
-      tok[j] = k >= a.history_len ? -1 : slot(a.history64 ? ((const int64_t*)h)[k] : ((const int32_t*)h)[k]);
+      return k < a.history_len ? k : a.history_len - 1;
+    };
+    if (a.history64) {
+#pragma unroll
+      for (int j = 0; j < HIST; ++j) id[j] = ((const uint64_t*)h)[at(j)];
+    } else {
+      // (a negative one is past every vocabulary)
+#pragma unroll
+      for (int j = 0; j < HIST; ++j) id[j] = ((const uint32_t*)h)[at(j)];
     }
+#pragma unroll
+    for (int j = 0; j < HIST; ++j) tok[j] = slot((uint32_t)id[j], (uint32_t)(id[j] >> 32));
   };
   const bool any = a.history_len > 0 || a.biases > 0;
   uint4* mine = (uint4*)slots;  // of group i * NT + tid: VE / 4 of these
@@ -89,15 +101,18 @@ __global__ __launch_bounds__(kAdjustThreads) void adjust_kernel(const AdjustArgs
   if (any) {
     if (a.history_len > 0) history(0);
     int id[BIAS];
+    float val[BIAS];
+    if (a.biases > 0) {
+      uint64_t t[BIAS];
 #pragma unroll
-    for (int j = 0; j < BIAS; ++j) {
-      const int k = j * NT + tid;
-      id[j] = -1;
-      if (k < a.biases) {
-        id[j] = slot(a.bias_ids[row * a.biases + k]);
-        bias_id[k] = id[j];
-        bias_val[k] = a.bias[row * a.biases + k];
+      for (int j = 0; j < BIAS; ++j) {
+        const int k = j * NT + tid < a.biases ? j * NT + tid : a.biases - 1;
+        t[j] = ((const uint64_t*)a.bias_ids)[row * a.biases + k];
+        val[j] = a.bias[row * a.biases + k];
       }
+#pragma unroll
+      for (int j = 0; j < BIAS; ++j)
+        id[j] = j * NT + tid < a.biases ? slot((uint32_t)t[j], (uint32_t)(t[j] >> 32)) : -1;
     }
     logits();
 #pragma unroll
@@ -105,6 +120,14 @@ __global__ __launch_bounds__(kAdjustThreads) void adjust_kernel(const AdjustArgs
 #pragma unroll
       for (int j = 0; j < VE / 4; ++j) mine[(i * NT + tid) * (VE / 4) + j] = make_uint4(0, 0, 0, 0);
     if (tid == 0) again = 0;
+    if (a.biases > 0) {
+#pragma unroll
+      for (int j = 0; j < BIAS; ++j)
+        if (j * NT + tid < a.biases) {
+          bias_id[j * NT + tid] = id[j];
+          bias_val[j * NT + tid] = val[j];
+        }
+    }
     __syncthreads();
     if (a.biases > 0) {
 #pragma unroll
@@ -175,16 +198,22 @@ __global__ __launch_bounds__(kAdjustThreads) void adjust_kernel(const AdjustArgs
 #pragma unroll
       for (int e = 0; e < VE; ++e) seen |= k[e];
       if (seen) {
+        // without a branch per token: some lane of a wave takes nearly every one of them
+        float v[VE];
 #pragma unroll
-        for (int e = 0; e < VE; ++e)
-          if (k[e]) {
-            float v = (float)raw[i].v[e];
-            const uint32_t count = k[e] % kSlotBias / kSlotOnce, b = k[e] / kSlotBias;
-            if (k[e] % kSlotBias) v = v > 0.f ? v / rep : v * rep;
-            if (count) v = v - freq * (float)count - pres;
-            if (b) v += bias_val[kAdjustMaxBiases - b];
-            raw[i].v[e] = (T)v;
-          }
+        for (int e = 0; e < VE; ++e) {
+          const float r = (float)raw[i].v[e];
+          const uint32_t once = k[e] % kSlotBias, count = once / kSlotOnce;
+          const float w = once ? r * (r > 0.f ? over : rep) : r;
+          v[e] = count ? fmaf(-freq, (float)count, w) - pres : w;
+        }
+        if (seen >= kSlotBias) {
+#pragma unroll
+          for (int e = 0; e < VE; ++e)
+            if (k[e] >= kSlotBias) v[e] += bias_val[kAdjustMaxBiases - k[e] / kSlotBias];
+        }
+#pragma unroll
+        for (int e = 0; e < VE; ++e) raw[i].v[e] = k[e] ? (T)v[e] : raw[i].v[e];
       }
     }
     if (c < n) {
@@ -204,8 +233,13 @@ int adjust_t(AdjustArgs a, void* stream) {
   const int vecs = adjust_vecs(a.rows, a.vocab, VE);
   const bool any = a.history_len > 0 || a.biases > 0;
   const size_t lds = any ? 4 * (size_t)kAdjustThreads * VE * vecs + 8 * (size_t)a.biases : 0;
-  return launch("adjusted logits", vecs == 1 ? adjust_kernel<T, 1> : vecs == 2 ? adjust_kernel<T, 2> : adjust_kernel<T, 4>,
-                dim3((unsigned)(a.rows * a.segs)), dim3(kAdjustThreads), lds, stream, a);
+  const auto go = [&](auto kernel) {
+    return launch("adjusted logits", kernel, dim3((unsigned)(a.rows * a.segs)), dim3(kAdjustThreads), lds, stream, a);
+  };
+  if constexpr (sizeof(T) == 4) {
+    if (vecs == 4) return go(adjust_kernel<T, 4>);
+  }
+  return vecs == 1 ? go(adjust_kernel<T, 1>) : go(adjust_kernel<T, 2>);
 }
 
 }  // namespace fm

@@ -61,8 +61,8 @@ constexpr int kAdjustThreads = 512;
 
 // 16-byte groups of a lane: a workgroup takes a segment of a row, of 8192 tokens
 // while there are 512 of them, two per compute unit, since each reads the row's
-// history again (256 x 131072 f16, history 4000, 300 biases: 52 us, 4096 tokens 66,
-// 16384 66; 64 x 131072 f32: 24, 4096 tokens 26, 2048 30).
+// history again (256 x 131072 f16, history 4000, 300 biases, with an earlier counting
+// loop: 52 us, 4096 tokens 66, 16384 66; 64 x 131072 f32: 24, 4096 tokens 26, 2048 30).
 inline int adjust_vecs(int64_t rows, int vocab, int ve) {
   int v = 16 / ve;
   for (; v > 1; v /= 2) {

@@ -228,3 +228,16 @@ def test_captured():
         want = adjust_logits(s["x"], **kw)
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_segments_full_of_tokens(dtype):
+    """More touched tokens in a segment than are worked on as a list; results of
+    exactly 0 among them."""
+    s = inputs(2, 5000, 9000, 300, True, DT[dtype], 17)
+    s["history"] = torch.arange(9000, device="cuda").expand(2, 9000) % 4500
+    s["history_lengths"] = torch.tensor([9000, 3000], dtype=torch.int32, device="cuda")
+    run_case(s)
+    z = dict(s, x=torch.zeros_like(s["x"]), frequency=0.0, presence=0.0, bias_ids=None, bias=None, allowed=None)
+    assert (run_case(z) == 0).all()
+    assert (run_case(dict(z, history=s["history"][:, :40])) == 0).all()
