@@ -109,12 +109,27 @@ def contiguous_f32(t, shape, name: str) -> None:
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream() builds a Stream object first
+_current_device = torch._C._cuda_getDevice  # a tensor on the device is there: no initialisation to ask for
+
+
+def wants_grad(*tensors) -> bool:
+    """Whether a call on these is to be recorded."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                return True
+    return False
+
+
+def like(x: torch.Tensor) -> torch.Tensor:
+    """A contiguous tensor of x's shape and type."""
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
 
 
 def call(x: torch.Tensor, fn, *args) -> None:
     """fn(*args, stream) on x's device, on torch's current stream there."""
     dev = x.get_device()
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         st = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):

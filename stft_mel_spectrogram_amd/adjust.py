@@ -94,7 +94,7 @@ def adjust_logits(logits, history=None, history_lengths=None, *, prompt_lengths=
         if allowed.dim() == 1:
             a_stride = 0
     if out is None:
-        out = logits.new_empty(logits.shape)
+        out = T.like(logits)
     elif out.shape != logits.shape or out.dtype != logits.dtype or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous {logits.dtype} tensor of shape {tuple(logits.shape)}")
     a = N.AdjustArgs(code, bits, rows, vocab, length, biases, stride, h_stride, a_stride, rep_value, freq_value,

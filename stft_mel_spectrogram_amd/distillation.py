@@ -35,7 +35,11 @@ def _check(logits, ids, lps):
     if torch.is_grad_enabled() and lps.requires_grad:
         raise ValueError("teacher_logprobs has no gradient here: detach it")
     at = (*at, 0, 0) if len(at) == 1 else at
-    return code, rows, vocab, at, ids.contiguous(), lps.contiguous()
+    if not ids.is_contiguous():
+        ids = ids.contiguous()
+    if not lps.is_contiguous():
+        lps = lps.contiguous()
+    return code, rows, vocab, at, ids, lps
 
 
 def _forward(logits, ids, lps, temperature, rest, stats: bool):
@@ -55,7 +59,7 @@ def topk_distillation(logits, teacher_ids, teacher_logprobs, *, temperature: flo
     temperature in 2^-10 .. 2^10; rest=True counts the mass outside the named
     tokens too (temperature 1 only, teacher_logprobs as they are).
     """
-    if isinstance(logits, torch.Tensor) and logits.requires_grad and torch.is_grad_enabled():
+    if T.wants_grad(logits):
         return _TopkDistillation.apply(logits, teacher_ids, teacher_logprobs, temperature, rest)
     return _forward(logits, teacher_ids, teacher_logprobs, temperature, rest, False)[0]
 
@@ -74,7 +78,7 @@ def topk_distillation_backward(grad_loss, logits, teacher_ids, teacher_logprobs,
     T.same_device(logits, grad_loss=grad_loss, stats=stats)
     T.contiguous_f32(grad_loss, logits.shape[:-1], "grad_loss")
     T.contiguous_f32(stats, (*logits.shape[:-1], 4), "stats")
-    dx = logits.new_empty(logits.shape)
+    dx = T.like(logits)
     T.call(logits, N.lib.fm_distill_backward, logits.data_ptr(), *at, ids.data_ptr(), lps.data_ptr(),
            stats.data_ptr(), grad_loss.data_ptr(), dx.data_ptr(), rows, vocab, ids.shape[-1], float(temperature),
            1 if rest else 0, code)

@@ -68,7 +68,7 @@ class _Call:
               or out.device != x.device or not out.is_contiguous()):
             raise ValueError(f"out must be a contiguous {x.dtype} tensor of shape {tuple(self.shape)} on {x.device}")
         if out_state is None:
-            out_state = x.new_empty((b, c), dtype=torch.float32)
+            out_state = x.new_empty((b, c), dtype=torch.float32) if self.state is None else torch.empty_like(self.state)
         else:
             T.same_device(x, out_state=out_state)
             T.contiguous_f32(out_state, (b, c), "out_state")
@@ -76,7 +76,8 @@ class _Call:
         a = N.RecurrenceArgs(*self.head, out.data_ptr(), out_state.data_ptr(), T.ptr(saved), None, None, None, None,
                              None, None, *self.strides, 0, 0)
         ref = ctypes.byref(a)
-        ws = T.workspace(x, N.lib.fm_gated_recurrence_workspace(ref, 0))
+        # (one tile takes none)
+        ws = T.workspace(x, N.lib.fm_gated_recurrence_workspace(ref, 0)) if t > SAVED_FRAMES else None
         T.call(x, N.lib.fm_gated_recurrence_forward, ref, T.ptr(ws))
         return out, out_state, saved
 
@@ -108,8 +109,7 @@ def gated_recurrence(x, forget, gate=None, state=None, *, lengths=None, out=None
     None; out and out_state take the results (out_state may be state itself, for
     a program that goes on frame by frame).
     """
-    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad
-                                       for t in (x, forget, gate, state)):
+    if T.wants_grad(x, forget, gate, state):
         if out is not None or out_state is not None:
             raise ValueError("out= and out_state= are not supported for inputs that require grad")
         return _GatedRecurrence.apply(x, forget, gate, state, lengths)

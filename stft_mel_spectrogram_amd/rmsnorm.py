@@ -36,18 +36,18 @@ def _check(x, weight, residual):
     return code, pcode, rows, width, stride, r_stride
 
 
-def _result(x, out, dtype, name):
+def _result(x, out, name):
     if out is None:
-        return x.new_empty(x.shape, dtype=dtype)
-    if (not isinstance(out, torch.Tensor) or out.shape != x.shape or out.dtype != dtype or out.device != x.device
+        return T.like(x)
+    if (not isinstance(out, torch.Tensor) or out.shape != x.shape or out.dtype != x.dtype or out.device != x.device
             or not out.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(x.shape)} on {x.device}")
+        raise ValueError(f"{name} must be a contiguous {x.dtype} tensor of shape {tuple(x.shape)} on {x.device}")
     return out
 
 
 def _sum(x, residual, out_sum):
     if residual is not None:
-        return _result(x, out_sum, x.dtype, "out_sum")
+        return _result(x, out_sum, "out_sum")
     if out_sum is not None:
         raise ValueError("out_sum needs a residual")
     return None
@@ -55,7 +55,7 @@ def _sum(x, residual, out_sum):
 
 def _forward(x, weight, residual, eps, stats: bool, out=None, out_sum=None):
     code, pcode, rows, width, stride, r_stride = _check(x, weight, residual)
-    out = _result(x, out, x.dtype, "out")
+    out = _result(x, out, "out")
     total = _sum(x, residual, out_sum)
     rstd = x.new_empty(x.shape[:-1], dtype=torch.float32) if stats else None
     T.call(x, N.lib.fm_rms_norm_forward, x.data_ptr(), stride, T.ptr(residual), r_stride, T.ptr(weight),
@@ -66,8 +66,7 @@ def _forward(x, weight, residual, eps, stats: bool, out=None, out_sum=None):
 def rms_norm(x, weight=None, residual=None, eps: float = 1e-6, *, out=None, out_sum=None):
     """y, or (y, x + residual) with a residual; differentiable in all of them.
     out and out_sum take the results (out_sum may be the residual itself)."""
-    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad
-                                       for t in (x, weight, residual)):
+    if T.wants_grad(x, weight, residual):
         if out is not None or out_sum is not None:
             raise ValueError("out= and out_sum= are not supported for inputs that require grad")
         y, total = _RmsNorm.apply(x, weight, residual, eps)
@@ -98,7 +97,7 @@ def rms_norm_backward(grad_out, normed, weight, rstd, grad_sum=None, params: boo
             raise ValueError(f"{name} must be a {normed.dtype} tensor of shape {tuple(normed.shape)}")
         strides.append(T.rows_of(t, name)[2])
     T.contiguous_f32(rstd, normed.shape[:-1], "rstd")
-    dx = normed.new_empty(normed.shape)
+    dx = T.like(normed)
     dw = ws = None
     if weight is not None and params:
         dw = torch.empty_like(weight)
@@ -115,8 +114,7 @@ def rms_norm_quantized(x, weight=None, residual=None, eps: float = 1e-6, dtype=t
     largest |y| over 448 or 127.  Not differentiable."""
     if dtype not in _OUT8:
         raise TypeError(f"dtype must be torch.float8_e4m3fn or torch.int8, got {dtype}")
-    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad
-                                       for t in (x, weight, residual)):
+    if T.wants_grad(x, weight, residual):
         raise ValueError("rms_norm_quantized has no gradient: call it on detached tensors or under no_grad")
     code, pcode, rows, width, stride, r_stride = _check(x, weight, residual)
     total = _sum(x, residual, out_sum)
