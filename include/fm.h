@@ -58,7 +58,7 @@ extern "C" {
 #define FM_F32 0
 #define FM_I16 1
 #define FM_F16 2
-#define FM_BF16 3 /* operators below only (layer norm, attention, scores)    */
+#define FM_BF16 3 /* the models' operators below only                        */
 #define FM_E4M3 4 /* 8-bit outputs of fm_rms_norm_quantized                  */
 #define FM_I8 5
 
@@ -607,7 +607,7 @@ int fm_rms_norm_backward(const void* dy, int64_t dy_stride, const void* sum, int
  *   and the groups at x_outer (x_inner 0: none); loss [rows] float32; stats
  *   [rows, 4] float32 or NULL: what the backward needs (the largest x and the log
  *   of the sum of exp((x - largest) / T), both also over the tokens that are not
- *   named).  T in [2^-10, 2^10]; vocab <
+ *   named).  T in [2^-10, 2^10], the largest |x| / T within float32; vocab <
  *   2^31 - 65536, rows * (row segments) < 2^31.
  */
 int64_t fm_distill_workspace(int64_t rows, int64_t vocab, int dtype);
@@ -627,7 +627,7 @@ int fm_distill_backward(const void* x, int64_t x_stride, int64_t x_inner, int64_
 /*
  * fm_adjust_args -- logits before a token is chosen from them; per row and token
  *
- *   x = x > 0 ? x / repetition : x * repetition    if the token is in the history
+ *   x = x > 0 ? x * (1 / repetition) : x * repetition   if it is in the history
  *   x = x - frequency * count - presence * (count > 0)
  *   x = x + the sum of the token's biases, in their order
  *   x = -inf                                       if its bit of `allowed` is 0

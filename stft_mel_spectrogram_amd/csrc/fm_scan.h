@@ -18,6 +18,12 @@
 //
 // A group of channels that would cross the end is read four channels before the
 // end instead; its lane stores only the channels that are its own.
+//
+// 16 x 1501 x 2048 bf16 (ragged, with gates): forward 84 us, 328 MB, 3.9 TB/s, the
+// vector units busy 61% of the time; backward 170 us, 590 MB, 3.5 TB/s, 58%: memory,
+// with the exponentials and the joins of a tile between its loads and its stores.  8 x
+// 1501 x 1024: 26 and 54.  In time ranges x and forget cross memory twice: 1 x 100003 x
+// 256 f16 22 + 41 us.  1 x 101 x 128 f32: 4.9 and 6.3, one tile; 8 x 1 x 1024 bf16: 3.3.
 #pragma once
 
 #include <type_traits>
@@ -746,7 +752,11 @@ int scan_forward_t(ScanArgs a, void* stream) {
   }
   FM_SCAN_FWD(128, 2, false)
   FM_SCAN_FWD(128, 4, false)
-  FM_SCAN_FWD(64, 4, false)
+  if constexpr (sizeof(T) == 4) {
+    FM_SCAN_FWD(64, 2, false)
+  } else {
+    FM_SCAN_FWD(64, 4, false)
+  }
   FM_SCAN_FWD(64, 1, true)
 #undef FM_SCAN_FWD
   return set_error(FM_E_UNSUPPORTED, "gated recurrence: no kernel for this shape");

@@ -56,7 +56,8 @@ inline int64_t scan_blocks(int channels, int row, int size) {
 // bf16: forward 10, unsplit 21; backward 16 and 50; 1 x 100003 x 256 f16: 60 and 1230).
 // A first launch then reads x and forget (backward: forget, gate and grad_y) twice.
 // Four frames a lane forward (16 x 1501 x 2048: 83, 2 frames the same, 8 x 1501 x 1024: 26
-// and 28), two backward (four do not fit the registers), two for what one tile holds.
+// and 28; float32 in 64-byte rows two, so that two workgroups share a unit: 38, four 42),
+// two backward (four do not fit the registers), two for what one tile holds.
 // Fewer than four channels have kernels of their own, single frames.
 inline ScanSplit scan_split(int batch, int time, int channels, int size, bool backward) {
   ScanSplit p;
@@ -65,7 +66,7 @@ inline ScanSplit scan_split(int batch, int time, int channels, int size, bool ba
   const bool tiny = channels < 4;
   const bool brief = time <= scan_tile(128, 2, size);
   p.row = tiny || (!brief && wide < 256 && narrow >= 160 && (!backward || size == 4)) ? 64 : 128;
-  p.frames = tiny ? 1 : backward || brief ? 2 : 4;
+  p.frames = tiny ? 1 : backward || brief || (p.row == 64 && size == 4) ? 2 : 4;
   const int64_t units = p.row == 128 ? wide : narrow;
   const int tile = scan_tile(p.row, p.frames, size);
   const int64_t tiles = ((int64_t)time + tile - 1) / tile;

@@ -6,9 +6,9 @@ import math
 
 import pytest
 
-from stft_mel_spectrogram_amd import _native as N
+torch = pytest.importorskip("torch")  # before the library, which then takes torch's HIP runtime
+from stft_mel_spectrogram_amd import _native as N  # noqa: E402
 
-torch = pytest.importorskip("torch")
 P = 1 << 20  # an address that must not be touched
 
 
