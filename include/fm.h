@@ -511,8 +511,8 @@ int fm_attention_backward(const fm_attention_args* args, void* workspace, void* 
  *                grad_state NULL is not wanted;
  *   lengths      [batch] int32 (clamped to [0, time]) or NULL: time;
  *   saved        [batch, (time + 63) / 64, channels] float32, the state before
- *                every 64th frame: written by the forward (NULL: not wanted),
- *                read by the backward;
+ *                every 64th frame below the entry's length: written by the forward
+ *                (NULL: not wanted), read by the backward;
  * backward: grad_y and grad_last in; grad_x, grad_forget, grad_gate (with a
  *                gate) and grad_state out; y and last_state are not looked at.
  * batch, time < 2^30, channels <= 2^20, batch * (blocks of 16 channels) < 2^23;

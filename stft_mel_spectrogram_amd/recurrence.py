@@ -89,8 +89,8 @@ class _Call:
                              "last axis")
         T.contiguous_f32(saved, self.saved_shape(), "saved")
         T.contiguous_f32(grad_state, (b, c), "grad_state")
-        dx, df = x.new_empty(self.shape), x.new_empty(self.shape)
-        dg = None if self.gate is None else x.new_empty(self.shape)
+        dx, df = T.like(grad_y), T.like(grad_y)
+        dg = None if self.gate is None else T.like(grad_y)
         ds = None if self.state is None else torch.empty_like(self.state)
         a = N.RecurrenceArgs(*self.head, None, None, saved.data_ptr(), grad_y.data_ptr(), T.ptr(grad_state),
                              dx.data_ptr(), df.data_ptr(), T.ptr(dg), T.ptr(ds), *self.strides,
