@@ -18,7 +18,7 @@
 // others' formula everywhere and then the named tokens again, after a barrier.
 // 4096 x 32000 bf16, the best 20 and the rest: forward 78 us (3.4 TB/s, vector units
 // busy 67% of the time: an exponential and eight instructions per logit), backward 124
-// (4.2 TB/s); 24008 x 129 f32, the best 8: 8.1 and 12.6.
+// (4.2 TB/s); 24008 x 129 f32, the best 8: 6.7 and 9.6.
 #pragma once
 
 #include "fm_logit.h"
@@ -26,10 +26,9 @@
 
 namespace fm {
 
-// A row's entries in groups of L lanes: entry e * L + lane.  id -1: none.
-template <int L>
+// A row's entries in groups of L lanes, E of a lane: entry e * L + lane.  id -1: none.
+template <int L, int E>
 struct Teacher {
-  static constexpr int E = kDistillMaxTop / L;
   int id[E];
   float t[E];
   bool lost = false;  // an id past the vocabulary
@@ -69,16 +68,15 @@ __device__ __forceinline__ float lanes_max_nan(float v) {
 }
 
 // q of the lane's entries, r, whether the row has a target at all.
-template <int L>
+template <int L, int E>
 struct Target {
-  float q[Teacher<L>::E], logq[Teacher<L>::E];
+  float q[E], logq[E];
   float r = 0.f, sum = 1.f;
   bool none;
 };
-template <int L, bool REST>
-__device__ __forceinline__ Target<L> distill_target(const Teacher<L>& t, float inv_t) {
-  constexpr int E = Teacher<L>::E;
-  Target<L> o;
+template <int L, int E, bool REST>
+__device__ __forceinline__ Target<L, E> distill_target(const Teacher<L, E>& t, float inv_t) {
+  Target<L, E> o;
   bool any = false;
 #pragma unroll
   for (int e = 0; e < E; ++e) any |= t.id[e] >= 0;
@@ -160,11 +158,10 @@ __device__ __forceinline__ float2 distill_scale(float temperature) {
 
 // The row's loss and statistics from `all`, the sum over its tokens (REST: those
 // that are not named); m in units of x.
-template <class T, int L, bool REST>
-__device__ __forceinline__ void distill_finish(DistillSum all, const Teacher<L>& t, const T* xr, int64_t row, int top,
+template <class T, int L, int E, bool REST>
+__device__ __forceinline__ void distill_finish(DistillSum all, const Teacher<L, E>& t, const T* xr, int64_t row, int top,
                                                float temperature, float inv_t, float* loss, float* stats, int lane) {
-  constexpr int E = Teacher<L>::E;
-  const Target<L> q = distill_target<L, REST>(t, inv_t);
+  const Target<L, E> q = distill_target<L, E, REST>(t, inv_t);
   float xk[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) xk[e] = t.id[e] >= 0 ? (float)xr[t.id[e]] : -INFINITY;
@@ -217,7 +214,7 @@ __device__ __forceinline__ void distill_finish(DistillSum all, const Teacher<L>&
 }
 
 // Rows that L lanes hold, V groups each.
-template <class T, int L, int V, bool REST>
+template <class T, int L, int V, int E, bool REST>
 __global__ __launch_bounds__(256) void distill_row_kernel(const ScoreIn<T> x, const int64_t* __restrict__ ids,
                                                           const float* __restrict__ lps, float* __restrict__ loss,
                                                           float* __restrict__ stats, int64_t rows, int vocab, int top,
@@ -233,7 +230,7 @@ __global__ __launch_bounds__(256) void distill_row_kernel(const ScoreIn<T> x, co
     const int c = (i * L + lane) * VE;
     v[i] = load16_part(xr + c, end - c, (T)-INFINITY);
   }
-  const Teacher<L> t(ids, lps, row, top, vocab, lane, row < rows);
+  const Teacher<L, E> t(ids, lps, row, top, vocab, lane, row < rows);
   if constexpr (REST) {
     // a byte per group of the row, a bit per token
     __shared__ uint32_t named[64 * V];
@@ -242,7 +239,7 @@ __global__ __launch_bounds__(256) void distill_row_kernel(const ScoreIn<T> x, co
     for (int i = 0; i < V; ++i) ((uint8_t*)mine)[i * L + lane] = 0;
     wave_lds_fence();
 #pragma unroll
-    for (int e = 0; e < Teacher<L>::E; ++e)
+    for (int e = 0; e < E; ++e)
       if (t.id[e] >= 0) {
         const int group = t.id[e] / VE;
         atomicOr(mine + group / 4, 1u << (group % 4 * 8 + t.id[e] % VE));
@@ -259,7 +256,7 @@ __global__ __launch_bounds__(256) void distill_row_kernel(const ScoreIn<T> x, co
   r.m = lanes_max<L>(score_max(v));
   r.s = lanes_sum<L>(distill_add(v, r.m == -INFINITY ? 0.f : r.m, distill_scale(temperature)));
   if (row < rows)
-    distill_finish<T, L, REST>(r, t, xr, row, top, temperature, inv_t, loss, stats, lane);
+    distill_finish<T, L, E, REST>(r, t, xr, row, top, temperature, inv_t, loss, stats, lane);
 }
 
 // 4 waves per row segment; with several segments `part` gets (m, s) of each.
@@ -277,7 +274,7 @@ __global__ __launch_bounds__(256) void distill_forward_kernel(
   const T* __restrict__ xr = x.row(row);
   const int beg = seg * seg_len;
   const int end = score_segment_end(beg, seg_len, vocab);
-  const Teacher<64> t(ids, lps, row, top, vocab, lane, REST || wave == 0);
+  const Teacher<64, 1> t(ids, lps, row, top, vocab, lane, REST || wave == 0);
   const float2 scale = distill_scale(temperature);
   DistillSum acc = {-INFINITY, 0.f};
   for (int c0 = beg; c0 < end; c0 += CH) {
@@ -316,7 +313,7 @@ __global__ __launch_bounds__(256) void distill_forward_kernel(
 #pragma unroll
   for (int w = 1; w < 4; ++w) acc = unscaled(distill_join(scaled(acc), scaled(sums[w])), fmaxf(acc.m, sums[w].m));
   if (segs == 1) {
-    distill_finish<T, 64, REST>(acc, t, xr, row, top, temperature, inv_t, loss, stats, lane);
+    distill_finish<T, 64, 1, REST>(acc, t, xr, row, top, temperature, inv_t, loss, stats, lane);
   } else if (lane == 0) {
     part[unit * 2 + 0] = acc.m;
     part[unit * 2 + 1] = acc.s;
@@ -331,7 +328,7 @@ __global__ __launch_bounds__(64) void distill_join_kernel(
     int segs) {
   const int lane = threadIdx.x;
   const int64_t row = blockIdx.x;
-  const Teacher<64> t(ids, lps, row, top, vocab, lane, true);
+  const Teacher<64, 1> t(ids, lps, row, top, vocab, lane, true);
   DistillSum acc = {-INFINITY, 0.f};
   float most = -INFINITY;
   for (int s = lane; s < segs; s += 64) {
@@ -341,19 +338,18 @@ __global__ __launch_bounds__(64) void distill_join_kernel(
   }
   acc = distill_join_lanes<64>(acc);
   acc.m = lanes_max<64>(most);
-  distill_finish<T, 64, REST>(acc, t, x.row(row), row, top, temperature, inv_t, loss, stats, lane);
+  distill_finish<T, 64, 1, REST>(acc, t, x.row(row), row, top, temperature, inv_t, loss, stats, lane);
 }
 
 // dx of one row segment (L = 256), or of whole rows that L < 256 lanes hold with V
 // groups each.
-template <class T, int L, int V, bool REST>
+template <class T, int L, int V, int E, bool REST>
 __global__ __launch_bounds__(256) void distill_backward_kernel(
     const ScoreIn<T> x, const int64_t* __restrict__ ids, const float* __restrict__ lps,
     const float* __restrict__ stats, const float* __restrict__ grad, T* __restrict__ dx, int64_t rows, int vocab,
     int top, float temperature, float inv_t, int seg_len, int segs) {
   constexpr int VE = Vec16<T>::n;
   constexpr int LT = L < 64 ? L : 64;  // lanes that hold the teacher's entries
-  constexpr int E = Teacher<LT>::E;
   const int tid = threadIdx.x % L, lane = threadIdx.x % LT;
   const int64_t unit = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
   const int64_t row = L == 256 ? unit / segs : unit;
@@ -369,8 +365,8 @@ __global__ __launch_bounds__(256) void distill_backward_kernel(
     const int c = beg + (i * L + tid) * VE;
     v[i] = load16_part(xr + c, end - c, (T)0.f);
   }
-  const Teacher<LT> t(ids, lps, row, top, vocab, lane, real);
-  const Target<LT> q = distill_target<LT, REST>(t, inv_t);
+  const Teacher<LT, E> t(ids, lps, row, top, vocab, lane, real);
+  const Target<LT, E> q = distill_target<LT, E, REST>(t, inv_t);
   const float m = real ? stats[4 * row] : 0.f, log_s = real ? stats[4 * row + 1] : 0.f;
   const float g = real ? grad[row] * temperature : 0.f;
   const bool zero = q.none || m == -INFINITY;
@@ -439,17 +435,25 @@ int distill_forward_t(const DistillArgs& a) {
   const ScoreSplit p = score_split(a.rows, a.vocab, Vec16<T>::n, 0);
   const float inv_t = 1.f / a.temperature;
   const auto stats_at = [&](int64_t at) { return a.stats ? a.stats + 4 * at : nullptr; };
-#define FM_DISTILL_ROW(L, V)                                                                    \
-  if (p.lanes == L && p.vecs == V)                                                              \
+#define FM_DISTILL_ROW_E(L, V, E)                                                               \
+  if (p.lanes == L && p.vecs == V && a.top <= L * E)                                            \
     return by_rows(a.rows, kGridThreads / L, [&](int64_t at, int64_t rows) {                    \
       return launch("distillation",                                                             \
-                    a.rest ? distill_row_kernel<T, L, V, true> : distill_row_kernel<T, L, V, false>, \
+                    a.rest ? distill_row_kernel<T, L, V, E, true> : distill_row_kernel<T, L, V, E, false>, \
                     dim3((unsigned)((rows + 256 / L - 1) / (256 / L))), dim3(256), 0, a.stream, \
                     score_in<T>(a, at), a.ids + at * a.top, a.lps + at * a.top, a.loss + at,    \
                     stats_at(at), rows, a.vocab, a.top, a.temperature, inv_t);                  \
     });
+// one entry of a lane where that holds them (24008 x 129 f32, the best 8: 6.7 us, with
+// room for 64 of them 8.1; backward 9.6 and 12.6)
+#define FM_DISTILL_ROW(L, V)                                                                    \
+  FM_DISTILL_ROW_E(L, V, 1)                                                                     \
+  if constexpr (L < 64) {                                                                       \
+    FM_DISTILL_ROW_E(L, V, 64 / L)                                                              \
+  }
   FM_SCORE_SHAPES(FM_DISTILL_ROW)
 #undef FM_DISTILL_ROW
+#undef FM_DISTILL_ROW_E
   float* part = (float*)a.workspace;
   const auto go = [&](auto kernel) {
     return by_rows(a.rows, kGridThreads / 256 / p.segs, [&](int64_t at, int64_t rows) {
@@ -471,20 +475,26 @@ template <class T>
 int distill_backward_t(const DistillArgs& a) {
   const ScoreSplit p = score_split(a.rows, a.vocab, Vec16<T>::n, 0);
   const float inv_t = 1.f / a.temperature;
-#define FM_DISTILL_BWD(L, V)                                                                     \
-  if (p.lanes == L && (L < 256 ? p.vecs == V : true))                                            \
+#define FM_DISTILL_BWD_E(L, V, E)                                                                \
+  if (p.lanes == L && (L < 256 ? p.vecs == V : true) && a.top <= (L < 64 ? L : 64) * E)          \
     return by_rows(a.rows, kGridThreads / L / p.segs, [&](int64_t at, int64_t rows) {            \
       return launch("distillation backward",                                                     \
-                    a.rest ? distill_backward_kernel<T, L, V, true>                              \
-                           : distill_backward_kernel<T, L, V, false>,                            \
+                    a.rest ? distill_backward_kernel<T, L, V, E, true>                            \
+                           : distill_backward_kernel<T, L, V, E, false>,                            \
                     dim3((unsigned)((rows * p.segs + 256 / L - 1) / (256 / L))), dim3(256), 0,   \
                     a.stream, score_in<T>(a, at), a.ids + at * a.top, a.lps + at * a.top,        \
                     a.stats + 4 * at, a.grad + at, (T*)a.dx + at * a.vocab, rows, a.vocab, a.top, \
                     a.temperature, inv_t, p.seg_len, p.segs);                                    \
     });
+#define FM_DISTILL_BWD(L, V)                                                                     \
+  FM_DISTILL_BWD_E(L, V, 1)                                                                      \
+  if constexpr (L < 64) {                                                                        \
+    FM_DISTILL_BWD_E(L, V, 64 / L)                                                               \
+  }
   FM_SCORE_SHAPES(FM_DISTILL_BWD)
-  FM_DISTILL_BWD(256, 4)
+  FM_DISTILL_BWD_E(256, 4, 1)
 #undef FM_DISTILL_BWD
+#undef FM_DISTILL_BWD_E
   return set_error(FM_E_UNSUPPORTED, "distillation: no kernel for this shape");
 }
 
