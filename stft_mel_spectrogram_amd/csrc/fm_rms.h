@@ -5,7 +5,9 @@
 //   rstd = 1 / sqrt(mean(s^2) + eps), u = s rstd, y = u w
 //   g = dy w, dx = dr = rstd (g - u mean(g u)) + ds, dw = sum over rows of dy u
 //   8 bits: scale = max |y| / 448 (e4m3) or 127 (int8) per row, y / scale rounded
-//   to nearest from the unrounded y.  Sums and scales are float32.
+//   to nearest from the unrounded y, whose steps are single float32 operations:
+//   s / sqrt(..), its product with w, the quotient by the scale.  Sums and scales
+//   are float32.
 //
 // The lane layouts are layer norm's: a row stays in the registers of LPR lanes,
 // VPL groups of 16 bytes each, so that every tensor moves once; wider rows are
@@ -48,14 +50,25 @@ __device__ __forceinline__ float rms_scale(uint32_t most) {
   const float m = __uint_as_float(most) / (OUT == 1 ? 448.f : 127.f);
   return m < 0x1p-126f ? 0x1p-126f : m;
 }
+// v / d, rounded once: the product with 1 / d, then what it misses.  Short numbers
+// often have quotients right between two 8-bit values (one in 10^4 of bfloat16 rows),
+// which one rounding more would decide.  What v / inf gives is 0.
+struct RmsDivisor {
+  float inv, d;
+  __device__ __forceinline__ explicit RmsDivisor(float by) : inv(1.f / by), d(by == INFINITY ? 0.f : by) {}
+  __device__ __forceinline__ float operator()(float v) const {
+    const float q = v * inv;
+    return fmaf(fmaf(-q, d, v), inv, q);
+  }
+};
 template <int OUT, int N>
-__device__ __forceinline__ void rms_store8(uint8_t* p, const float (&y)[N], float inv, int have) {
+__device__ __forceinline__ void rms_store8(uint8_t* p, const float (&y)[N], RmsDivisor scale, int have) {
   uint32_t v[N / 4];
 #pragma unroll
   for (int i = 0; i < N / 4; ++i) {
     float z[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) z[e] = y[4 * i + e] * inv;
+    for (int e = 0; e < 4; ++e) z[e] = scale(y[4 * i + e]);
     if constexpr (OUT == 1) {
       const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(z[0], z[1], 0, false);
       v[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(z[2], z[3], lo, true);
@@ -134,9 +147,10 @@ __global__ __launch_bounds__(norm_threads(LPR)) void rms_forward_kernel(
     for (int i = 0; i < VPL; ++i)
 #pragma unroll
       for (int e = 0; e < VE; ++e) q = fmaf((float)s[i].v[e], (float)s[i].v[e], q);
-    const float rs = 1.f / sqrtf(row_sum<LPR>(q, red + (odd ? SLOTS : 0)) / n + eps);
-    if (rstd && lane == 0 && row < rows) rstd[row] = rs;
+    const float root = sqrtf(row_sum<LPR>(q, red + (odd ? SLOTS : 0)) / n + eps);
     if constexpr (OUT == 0) {
+      const float rs = 1.f / root;
+      if (rstd && lane == 0 && row < rows) rstd[row] = rs;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
         const int c = (i * LPR + lane) * VE;
@@ -148,27 +162,25 @@ __global__ __launch_bounds__(norm_threads(LPR)) void rms_forward_kernel(
         }
       }
     } else {
+      const RmsDivisor by(root);
       uint32_t most = 0;
+      float v[VPL][VE];
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
           // past the end s is 0 and w 1
-          const uint32_t b = __float_as_uint((float)s[i].v[e] * rs * (float)wv[i].v[e]) & 0x7fffffffu;
+          v[i][e] = by((float)s[i].v[e]) * (float)wv[i].v[e];
+          const uint32_t b = __float_as_uint(v[i][e]) & 0x7fffffffu;
           most = b > most ? b : most;
         }
       const float sc = rms_scale<OUT>(row_umax<LPR>(most, umax + (odd ? SLOTS : 0)));
       if (lane == 0 && row < rows) scale[row] = sc;
-      const float inv = 1.f / sc;
+      const RmsDivisor to(sc);
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
         const int c = (i * LPR + lane) * VE;
-        if (have_all - c > 0) {
-          float v[VE];
-#pragma unroll
-          for (int e = 0; e < VE; ++e) v[e] = (float)s[i].v[e] * rs * (float)wv[i].v[e];
-          rms_store8<OUT, VE>((uint8_t*)y + row * width + c, v, inv, have_all - c);
-        }
+        if (have_all - c > 0) rms_store8<OUT, VE>((uint8_t*)y + row * width + c, v[i], to, have_all - c);
       }
     }
     odd = !odd;
@@ -201,14 +213,17 @@ __global__ __launch_bounds__(kNormWide) void rms_forward_wide_kernel(
 #pragma unroll
     for (int e = 0; e < VE; ++e) q = fmaf((float)v.v[e], (float)v.v[e], q);
   }
-  const float rs = 1.f / sqrtf(row_sum<kNormWide>(q, red) / n + eps);
+  const float root = sqrtf(row_sum<kNormWide>(q, red) / n + eps);
+  const float rs = 1.f / root;
   if (rstd && threadIdx.x == 0) rstd[row] = rs;
   const T* from = rr ? sr : xr;
+  const RmsDivisor by(root);
   const auto value = [&](const Vec16<T>& v, int c, int e) {
     const int ce = c + e < width ? c + e : c;
-    return (float)v.v[e] * rs * (w ? (float)w[ce] : 1.f);
+    const float u = OUT == 0 ? (float)v.v[e] * rs : by((float)v.v[e]);
+    return u * (w ? (float)w[ce] : 1.f);
   };
-  float inv = 1.f;
+  float sc = 1.f;
   if constexpr (OUT != 0) {
     uint32_t most = 0;
 #pragma unroll 1
@@ -220,10 +235,10 @@ __global__ __launch_bounds__(kNormWide) void rms_forward_wide_kernel(
         most = b > most ? b : most;
       }
     }
-    const float sc = rms_scale<OUT>(row_umax<kNormWide>(most, umax));
+    sc = rms_scale<OUT>(row_umax<kNormWide>(most, umax));
     if (threadIdx.x == 0) scale[row] = sc;
-    inv = 1.f / sc;
   }
+  const RmsDivisor to(sc);
 #pragma unroll 1
   for (int c = threadIdx.x * VE; c < width; c += kNormWide * VE) {
     Vec16<T> v = load16_part(from + c, width - c, (T)0.f);
@@ -235,7 +250,7 @@ __global__ __launch_bounds__(kNormWide) void rms_forward_wide_kernel(
       float z[VE];
 #pragma unroll
       for (int e = 0; e < VE; ++e) z[e] = value(v, c, e);
-      rms_store8<OUT, VE>((uint8_t*)y + row * width + c, z, inv, width - c);
+      rms_store8<OUT, VE>((uint8_t*)y + row * width + c, z, to, width - c);
     }
   }
 }
