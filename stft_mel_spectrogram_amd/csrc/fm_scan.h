@@ -2,8 +2,9 @@
 //
 //   a = sigmoid(f), h_t = a_t h_{t-1} + (1 - a_t) x_t, y_t = h_t silu(g_t)
 //   e_t = dy_t silu(g_t), d_t = e_t + m_{t+1}, m_t = a_t d_t (m past the end: the
-//   last state's gradient), dx = (1 - a) d, df = dx (h - x), dg = dy h silu'(g),
-//   dstate = m_0.  (a (1 - a) (h_{t-1} - x) d = dx (h - x), since h - x = a (h_{t-1} - x).)
+//   last state's gradient), dx = (1 - a) d, df = dx a (h_{t-1} - x), dg = dy h silu'(g),
+//   dstate = m_0.  (a (h_{t-1} - x) is h - x too, but as a difference of two nearly equal
+//   numbers where a is small.)
 //
 // Both directions are the recurrence z = a z' + u, and two successive ranges of
 // frames join as (A1, U1), (A2, U2) -> (A1 A2, A2 U1 + U2).  A workgroup takes
@@ -683,14 +684,14 @@ __global__ __launch_bounds__(64 * kScanWaves, (sizeof(T) == 2 && ROW == 128 ? 4 
       // x is unpacked again rather than kept in registers since the first walk
 #pragma unroll
       for (int r = 0; r < R; ++r) xr[r].forget();
-      // hs: h - x from here on, and dg in place of dy silu'(g)
+      // hs: a (h - x) of the state before the frame, and dg in place of dy silu'(g)
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
           const float xe = xr[r].get(e);
+          hs[r][e] = av[r][e] * (h[e] - xe);
           h[e] = fmaf(av[r][e], h[e], rest[r][e] * xe);
-          hs[r][e] = h[e] - xe;
           if constexpr (GATE) gd[r][e] *= h[e];
         }
 #pragma unroll
