@@ -121,21 +121,28 @@ __device__ __forceinline__ Target<L, E> distill_target(const Teacher<L, E>& t, f
   return o;
 }
 
-// exp(z - m) added up; m finite or everything is -inf.
+// exp((x - m) / T) added up around a maximum m of x itself; m finite or everything is -inf.
 struct DistillSum {
   float m, s;
 };
-__device__ __forceinline__ DistillSum distill_join(DistillSum a, DistillSum b) {
+// exp((from - to) / T), scale as below: a difference of the maxima as they are, since
+// maxima over T would be off by a rounding of their size, not of their distance's.
+__device__ __forceinline__ float distill_shift(float from, float to, float2 scale) {
+  const float d = from - to;
+  // a set of -inf has s = 0
+  return from == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(fmaf(d, scale.x, d * scale.y));
+}
+__device__ __forceinline__ DistillSum distill_join(DistillSum a, DistillSum b, float2 scale) {
   const float m = fmaxf(a.m, b.m);
-  return {m, a.s * __builtin_amdgcn_exp2f(score_shift(a.m, m)) + b.s * __builtin_amdgcn_exp2f(score_shift(b.m, m))};
+  return {m, a.s * distill_shift(a.m, m, scale) + b.s * distill_shift(b.m, m, scale)};
 }
 template <int L>
-__device__ __forceinline__ DistillSum distill_join_lanes(DistillSum a) {
+__device__ __forceinline__ DistillSum distill_join_lanes(DistillSum a, float2 scale) {
   const float m = lanes_max<L>(a.m);
-  return {m, lanes_sum<L>(a.s * __builtin_amdgcn_exp2f(score_shift(a.m, m)))};
+  return {m, lanes_sum<L>(a.s * distill_shift(a.m, m, scale))};
 }
 // scale: log2 e / T in two parts (what one alone is off by goes the same way in
-// every term, and a loss is a small difference); m is a maximum of x itself.
+// every term, and a loss is a small difference).
 template <class T, int V>
 __device__ __forceinline__ float distill_add(const Vec16<T> (&v)[V], float m, float2 scale) {
   float s = 0.f;
@@ -296,22 +303,17 @@ __global__ __launch_bounds__(256) void distill_forward_kernel(
       }
     }
     const float m = fmaxf(acc.m, score_max(v));
-    const float d = acc.m == -INFINITY ? 0.f : (acc.m - m) * scale.x;
-    acc.s = acc.s * __builtin_amdgcn_exp2f(d) + distill_add(v, m == -INFINITY ? 0.f : m, scale);
+    acc.s = acc.s * distill_shift(acc.m, m, scale) + distill_add(v, m == -INFINITY ? 0.f : m, scale);
     acc.m = m;
   }
-  // sums around maxima of x: distances in units of 1 / T
-  const auto scaled = [&](DistillSum a) { return DistillSum{a.m * inv_t, a.s}; };
-  const auto unscaled = [&](DistillSum a, float m) { return DistillSum{m, a.s}; };
-  const float most = lanes_max<64>(acc.m);
-  acc = unscaled(distill_join_lanes<64>(scaled(acc)), most);
+  acc = distill_join_lanes<64>(acc, scale);
   __shared__ DistillSum sums[4];
   if (lane == 0) sums[wave] = acc;
   __syncthreads();
   if (wave != 0) return;
   acc = sums[0];
 #pragma unroll
-  for (int w = 1; w < 4; ++w) acc = unscaled(distill_join(scaled(acc), scaled(sums[w])), fmaxf(acc.m, sums[w].m));
+  for (int w = 1; w < 4; ++w) acc = distill_join(acc, sums[w], scale);
   if (segs == 1) {
     distill_finish<T, 64, 1, REST>(acc, t, xr, row, top, temperature, inv_t, loss, stats, lane);
   } else if (lane == 0) {
@@ -329,15 +331,13 @@ __global__ __launch_bounds__(64) void distill_join_kernel(
   const int lane = threadIdx.x;
   const int64_t row = blockIdx.x;
   const Teacher<64, 1> t(ids, lps, row, top, vocab, lane, true);
+  const float2 scale = distill_scale(temperature);
   DistillSum acc = {-INFINITY, 0.f};
-  float most = -INFINITY;
   for (int s = lane; s < segs; s += 64) {
     const float* p = part + (row * segs + s) * 2;
-    most = fmaxf(most, p[0]);
-    acc = distill_join(acc, DistillSum{p[0] * inv_t, p[1]});
+    acc = distill_join(acc, DistillSum{p[0], p[1]}, scale);
   }
-  acc = distill_join_lanes<64>(acc);
-  acc.m = lanes_max<64>(most);
+  acc = distill_join_lanes<64>(acc, scale);
   distill_finish<T, 64, 1, REST>(acc, t, x.row(row), row, top, temperature, inv_t, loss, stats, lane);
 }
 
