@@ -19,6 +19,11 @@ from . import _native as N
 from . import _tensors as T
 
 
+def _detached(lps):
+    if T.wants_grad(lps):
+        raise ValueError("teacher_logprobs has no gradient here: detach it")
+
+
 def _check(logits, ids, lps):
     code = T.dtype_code(logits, "logits")
     rows, vocab, *at = T.grouped_rows_of(logits, "logits")
@@ -32,8 +37,7 @@ def _check(logits, ids, lps):
         raise TypeError(f"teacher_logprobs must be float32, got {lps.dtype}")
     if lps.shape != ids.shape:
         raise ValueError(f"teacher_logprobs must have teacher_ids' shape {tuple(ids.shape)}, got {tuple(lps.shape)}")
-    if torch.is_grad_enabled() and lps.requires_grad:
-        raise ValueError("teacher_logprobs has no gradient here: detach it")
+    _detached(lps)
     at = (*at, 0, 0) if len(at) == 1 else at
     if not ids.is_contiguous():
         ids = ids.contiguous()
@@ -59,6 +63,7 @@ def topk_distillation(logits, teacher_ids, teacher_logprobs, *, temperature: flo
     temperature in 2^-10 .. 2^10; rest=True counts the mass outside the named
     tokens too (temperature 1 only, teacher_logprobs as they are).
     """
+    _detached(teacher_logprobs)  # (within the recorded function nothing wants a gradient)
     if T.wants_grad(logits):
         return _TopkDistillation.apply(logits, teacher_ids, teacher_logprobs, temperature, rest)
     return _forward(logits, teacher_ids, teacher_logprobs, temperature, rest, False)[0]
