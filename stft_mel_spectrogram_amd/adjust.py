@@ -48,8 +48,8 @@ def adjust_logits(logits, history=None, history_lengths=None, *, prompt_lengths=
     the logits themselves.  Not differentiable.
     """
     code = T.dtype_code(logits, "logits")
-    if logits.requires_grad and torch.is_grad_enabled():
-        raise ValueError("adjust_logits has no gradient: call it on detached logits or under no_grad")
+    if T.wants_grad(logits, repetition, frequency, presence, bias):
+        raise ValueError("adjust_logits has no gradient: call it on detached tensors or under no_grad")
     rows, vocab, stride = T.rows_of(logits, "logits")
     lead = logits.shape[:-1]
     T.same_device(logits, ("history", "history_lengths", "prompt_lengths", "bias_ids", "bias", "allowed", "out"),
