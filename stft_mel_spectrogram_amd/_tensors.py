@@ -147,5 +147,11 @@ def workspace(x: torch.Tensor, nbytes: int):
     return x.new_empty((nbytes,), dtype=torch.uint8) if nbytes else None
 
 
+def written(*given) -> None:
+    """Counts given results (those that are not None) as changed, as torch does for
+    its own: a backward that saved them before says so."""
+    torch.autograd.graph.increment_version([t for t in given if t is not None])
+
+
 def ptr(t):
     return None if t is None else t.data_ptr()

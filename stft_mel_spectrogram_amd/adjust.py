@@ -48,7 +48,7 @@ def adjust_logits(logits, history=None, history_lengths=None, *, prompt_lengths=
     the logits themselves.  Not differentiable.
     """
     code = T.dtype_code(logits, "logits")
-    if T.wants_grad(logits, repetition, frequency, presence, bias):
+    if T.wants_grad(logits, repetition, frequency, presence, bias, out):
         raise ValueError("adjust_logits has no gradient: call it on detached tensors or under no_grad")
     rows, vocab, stride = T.rows_of(logits, "logits")
     lead = logits.shape[:-1]
@@ -82,6 +82,7 @@ def adjust_logits(logits, history=None, history_lengths=None, *, prompt_lengths=
             raise ValueError(f"bias_ids must be a contiguous tensor of shape {tuple(lead)} and a number of biases")
         biases = bias_ids.shape[-1]
         T.contiguous_f32(bias, bias_ids.shape, "bias")
+    given = out is not None
     a_stride = 0
     if allowed is not None:
         words = (vocab + 31) // 32
@@ -102,4 +103,6 @@ def adjust_logits(logits, history=None, history_lengths=None, *, prompt_lengths=
                      T.ptr(prompt_lengths), T.ptr(rep), T.ptr(freq), T.ptr(pres), T.ptr(bias_ids), T.ptr(bias),
                      T.ptr(allowed))
     T.call(logits, N.lib.fm_adjust_logits, ctypes.byref(a))
+    if given:
+        T.written(out)
     return out

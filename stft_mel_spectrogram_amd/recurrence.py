@@ -62,6 +62,7 @@ class _Call:
 
     def forward(self, save: bool, out=None, out_state=None):
         x, (b, t, c) = self.x, self.shape
+        given = out is not None or out_state is not None
         if out is None:
             out = x.new_empty(self.shape)
         elif (not isinstance(out, torch.Tensor) or out.shape != self.shape or out.dtype != x.dtype
@@ -79,6 +80,8 @@ class _Call:
         # (one tile takes none)
         ws = T.workspace(x, N.lib.fm_gated_recurrence_workspace(ref, 0)) if t > SAVED_FRAMES else None
         T.call(x, N.lib.fm_gated_recurrence_forward, ref, T.ptr(ws))
+        if given:
+            T.written(out, out_state)
         return out, out_state, saved
 
     def backward(self, grad_y, saved, grad_state):
@@ -109,9 +112,9 @@ def gated_recurrence(x, forget, gate=None, state=None, *, lengths=None, out=None
     None; out and out_state take the results (out_state may be state itself, for
     a program that goes on frame by frame).
     """
-    if T.wants_grad(x, forget, gate, state):
+    if T.wants_grad(x, forget, gate, state, out, out_state):
         if out is not None or out_state is not None:
-            raise ValueError("out= and out_state= are not supported for inputs that require grad")
+            raise ValueError("out= and out_state= are not supported for tensors that require grad")
         return _GatedRecurrence.apply(x, forget, gate, state, lengths)
     return _Call(x, forget, gate, state, lengths).forward(False, out, out_state)[:2]
 

@@ -55,20 +55,23 @@ def _sum(x, residual, out_sum):
 
 def _forward(x, weight, residual, eps, stats: bool, out=None, out_sum=None):
     code, pcode, rows, width, stride, r_stride = _check(x, weight, residual)
+    given = out is not None or out_sum is not None
     out = _result(x, out, "out")
     total = _sum(x, residual, out_sum)
     rstd = x.new_empty(x.shape[:-1], dtype=torch.float32) if stats else None
     T.call(x, N.lib.fm_rms_norm_forward, x.data_ptr(), stride, T.ptr(residual), r_stride, T.ptr(weight),
            out.data_ptr(), T.ptr(total), T.ptr(rstd), rows, width, float(eps), code, pcode)
+    if given:
+        T.written(out, total)
     return out, total, rstd
 
 
 def rms_norm(x, weight=None, residual=None, eps: float = 1e-6, *, out=None, out_sum=None):
     """y, or (y, x + residual) with a residual; differentiable in all of them.
     out and out_sum take the results (out_sum may be the residual itself)."""
-    if T.wants_grad(x, weight, residual):
+    if T.wants_grad(x, weight, residual, out, out_sum):
         if out is not None or out_sum is not None:
-            raise ValueError("out= and out_sum= are not supported for inputs that require grad")
+            raise ValueError("out= and out_sum= are not supported for tensors that require grad")
         y, total = _RmsNorm.apply(x, weight, residual, eps)
     else:
         y, total, _ = _forward(x, weight, residual, eps, False, out, out_sum)
@@ -114,7 +117,7 @@ def rms_norm_quantized(x, weight=None, residual=None, eps: float = 1e-6, dtype=t
     largest |y| over 448 or 127.  Not differentiable."""
     if dtype not in _OUT8:
         raise TypeError(f"dtype must be torch.float8_e4m3fn or torch.int8, got {dtype}")
-    if T.wants_grad(x, weight, residual):
+    if T.wants_grad(x, weight, residual, out_sum):
         raise ValueError("rms_norm_quantized has no gradient: call it on detached tensors or under no_grad")
     code, pcode, rows, width, stride, r_stride = _check(x, weight, residual)
     total = _sum(x, residual, out_sum)
@@ -122,6 +125,8 @@ def rms_norm_quantized(x, weight=None, residual=None, eps: float = 1e-6, dtype=t
     scale = x.new_empty(x.shape[:-1], dtype=torch.float32)
     T.call(x, N.lib.fm_rms_norm_quantized, x.data_ptr(), stride, T.ptr(residual), r_stride, T.ptr(weight),
            q.data_ptr(), scale.data_ptr(), T.ptr(total), rows, width, float(eps), code, pcode, _OUT8[dtype])
+    if out_sum is not None:
+        T.written(out_sum)
     return (q, scale) if residual is None else (q, scale, total)
 
 
