@@ -516,7 +516,8 @@ int fm_attention_backward(const fm_attention_args* args, void* workspace, void* 
  * backward: grad_y and grad_last in; grad_x, grad_forget, grad_gate (with a
  *                gate) and grad_state out; y and last_state are not looked at.
  * batch, time < 2^30, channels <= 2^20, batch * (blocks of 16 channels) < 2^23;
- * frames of x, forget, gate and grad_y less than 8 MiB apart.
+ * frames of x, forget, gate and grad_y less than 8 MiB apart where there are more than
+ * one (more than two in a forward without saved).
  */
 typedef struct fm_recurrence_args {
   int dtype, reserved;

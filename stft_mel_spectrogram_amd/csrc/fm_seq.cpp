@@ -46,6 +46,8 @@ int recurrence_args(const fm_recurrence_args* p, ScanArgs& a) {
     a.gs[i] = p->gate_stride[i];
     a.dys[i] = p->grad_y_stride[i];
   }
+  // one frame has no next one, whatever its stride says
+  if (a.time <= 1) a.xs[1] = a.fs[1] = a.gs[1] = a.dys[1] = 0;
   // workgroups of 512 threads and single threads, below 2^32 threads
   const int size = elem_bytes(p->dtype);
   int64_t units = 0;
@@ -67,8 +69,11 @@ int recurrence_pointers(const ScanArgs& a, int dtype, bool backward) {
       (backward && !scan_strides_fit(a.dys)))
     return bad("gated recurrence: strides must be >= 0");
   const int es = elem_bytes(dtype);
-  if (a.xs[1] >= kScanMaxStride / es || a.fs[1] >= kScanMaxStride / es || (a.g && a.gs[1] >= kScanMaxStride / es) ||
-      (backward && a.dys[1] >= kScanMaxStride / es))
+  // (few frames are walked with addresses in 64 bits)
+  const bool tiles = backward || !scan_steps(a);
+  if (tiles &&
+      (a.xs[1] >= kScanMaxStride / es || a.fs[1] >= kScanMaxStride / es || (a.g && a.gs[1] >= kScanMaxStride / es) ||
+       (backward && a.dys[1] >= kScanMaxStride / es)))
     return set_error(FM_E_UNSUPPORTED, "gated recurrence: frames must be less than 8 MiB apart");
   if (!aligned_to(a.x, es) || !aligned_to(a.f, es) || !aligned_to(a.g, es) || !aligned_to(a.y, es) ||
       !aligned_to(a.dy, es) || !aligned_to(a.dx, es) || !aligned_to(a.df, es) || !aligned_to(a.dg, es) ||

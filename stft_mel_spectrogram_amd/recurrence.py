@@ -3,12 +3,12 @@
     a = sigmoid(forget[t]),  h[t] = a h[t - 1] + (1 - a) x[t],  y[t] = h[t] silu(gate[t])
 
 per channel, from h[-1] = state.  x, forget and gate are [batch, time,
-channels] in float32, float16 or bfloat16 on the GPU, with any strides of batch
-and time (slices of one projection are read as they lie); states are float32
-[batch, channels].  forget of +inf keeps the state, -inf replaces it; without a
-gate y = h.  Frames at or past an entry's length are not part of the sequence:
-what lies there (NaN) does no harm, and y and the gradients are 0 there.  The
-last state carries a sequence on: a whole recording in pieces, or frame by frame.
+channels] in float32, float16 or bfloat16 on the GPU, with any stride of batch and
+strides of time below 8 MiB (slices of one projection are read as they lie; a
+single frame's does not matter); states are float32 [batch, channels].  forget of
++inf keeps the state, -inf replaces it; without a gate y = h.  Frames at or past
+an entry's length are not part of the sequence: what lies there (NaN) does no
+harm, and y and the gradients are 0 there.  The last state carries a sequence on: a whole recording in pieces, or frame by frame.
 """
 from __future__ import annotations
 
