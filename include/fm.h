@@ -642,7 +642,7 @@ int fm_distill_backward(const void* x, int64_t x_stride, int64_t x_inner, int64_
  *   (clamped to [0, history_len]) or NULL: history_len, 0.  Tokens outside
  *   [0, vocab) are none;
  *   repetition, frequency, presence [rows] float32 or NULL: the *_value for all
- *   rows (repetition > 0);
+ *   rows (repetition > 0, finite in float32 like its reciprocal);
  *   bias_ids [rows, biases] int64, bias [rows, biases] float32, contiguous; ids
  *   outside [0, vocab) are none; the same one twice counts twice;
  *   allowed: rows of (vocab + 31) / 32 words of 32 bits, lowest first,

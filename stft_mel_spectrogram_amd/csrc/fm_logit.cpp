@@ -109,10 +109,13 @@ int fm_adjust_logits(const fm_adjust_args* p, void* stream) try {
   if (p->biases < 0) return bad("adjusted logits: biases must be >= 0");
   if (p->biases > fm::kAdjustMaxBiases)
     return fm::set_error(FM_E_UNSUPPORTED, "adjusted logits: at most 1024 biases per row");
-  if (!p->repetition && !(p->repetition_value > 0.0 && std::isfinite(p->repetition_value)))
-    return bad("adjusted logits: repetition must be finite and > 0");
-  if ((!p->frequency && !std::isfinite(p->frequency_value)) || (!p->presence && !std::isfinite(p->presence_value)))
-    return bad("adjusted logits: frequency and presence must be finite");
+  // as the kernels take them
+  const float rep = static_cast<float>(p->repetition_value);
+  if (!p->repetition && !(rep > 0.f && std::isfinite(rep) && std::isfinite(1.f / rep)))
+    return bad("adjusted logits: repetition must be > 0, and finite in float32 like its reciprocal");
+  if ((!p->frequency && !std::isfinite(static_cast<float>(p->frequency_value))) ||
+      (!p->presence && !std::isfinite(static_cast<float>(p->presence_value))))
+    return bad("adjusted logits: frequency and presence must be finite in float32");
   fm::AdjustArgs a = {};
   a.rows = p->rows;
   a.vocab = static_cast<int>(p->vocab);
@@ -144,7 +147,7 @@ int fm_adjust_logits(const fm_adjust_args* p, void* stream) try {
   a.repetition = p->repetition;
   a.frequency = p->frequency;
   a.presence = p->presence;
-  a.repetition_value = static_cast<float>(p->repetition_value);
+  a.repetition_value = rep;
   a.frequency_value = static_cast<float>(p->frequency_value);
   a.presence_value = static_cast<float>(p->presence_value);
   a.bias_ids = p->bias_ids;

@@ -8,7 +8,8 @@ strides of time below 8 MiB (slices of one projection are read as they lie; a
 single frame's does not matter); states are float32 [batch, channels].  forget of
 +inf keeps the state, -inf replaces it; without a gate y = h.  Frames at or past
 an entry's length are not part of the sequence: what lies there (NaN) does no
-harm, and y and the gradients are 0 there.  The last state carries a sequence on: a whole recording in pieces, or frame by frame.
+harm, and y and the gradients are 0 there.  The last state carries a sequence on:
+a whole recording in pieces, or frame by frame.
 """
 from __future__ import annotations
 
