@@ -557,7 +557,9 @@ int fm_gated_recurrence_backward(const fm_recurrence_args* args, void* workspace
  *   contiguous takes s where there is a residual (NULL otherwise) and may be the
  *   residual's own memory if that is contiguous; weight [width] of type
  *   param_dtype (dtype or FM_F32) or NULL; rstd [rows] float32 or NULL (the
- *   backward needs it).  0 <= rows < 2^31, 1 <= width <= 2^20, eps >= 0.
+ *   backward needs it).  0 <= rows < 2^31, 1 <= width <= 2^20, eps >= 0
+ *   and finite in float32.  A row's sum of squares is a float32: past its range
+ *   (|s| around 10^19) y is 0.
  */
 int fm_rms_norm_forward(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
                         const void* weight, void* y, void* sum, float* rstd, int64_t rows, int64_t width,

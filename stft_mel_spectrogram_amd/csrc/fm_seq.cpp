@@ -4,6 +4,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <limits>
 
 #include "fm_check.h"
 
@@ -99,10 +100,16 @@ int check_rms(int64_t rows, int64_t width, int dtype) {
   return FM_OK;
 }
 
+// In float32; what is above 0 stays so: a row of zeros is normed to zeros.
+float rms_eps(double eps) {
+  const float e = static_cast<float>(eps);
+  return eps > 0.0 && e == 0.f ? std::numeric_limits<float>::denorm_min() : e;
+}
+
 int rms_forward(const RmsForward& a, double eps, int dtype, int param_dtype) {
   if (param_dtype != dtype && param_dtype != FM_F32)
     return bad("rms norm: param_dtype must be the rows' dtype or FM_F32");
-  if (!(eps >= 0.0) || !std::isfinite(eps)) return bad("rms norm: eps must be finite and >= 0");
+  if (!(eps >= 0.0) || !std::isfinite(a.eps)) return bad("rms norm: eps must be >= 0 and finite in float32");
   if (a.rows == 0) return FM_OK;
   if (!a.x || !a.y) return bad("rms norm: x and the output must not be NULL");
   if ((a.residual != nullptr) != (a.sum != nullptr)) return bad("rms norm: residual and sum go together");
@@ -171,7 +178,7 @@ int fm_rms_norm_forward(const void* x, int64_t x_stride, const void* residual, i
                         double eps, int dtype, int param_dtype, void* stream) try {
   if (int st = fm::check_rms(rows, width, dtype)) return st;
   const fm::RmsForward a = {x,   x_stride, residual, residual_stride, weight, y, 0, nullptr, sum, rstd, rows,
-                            static_cast<int>(width), static_cast<float>(eps), stream};
+                            static_cast<int>(width), fm::rms_eps(eps), stream};
   return fm::rms_forward(a, eps, dtype, param_dtype);
 } catch (...) {
   return FM_E_NOMEM;
@@ -183,7 +190,7 @@ int fm_rms_norm_quantized(const void* x, int64_t x_stride, const void* residual,
   if (int st = fm::check_rms(rows, width, dtype)) return st;
   if (out_dtype != FM_E4M3 && out_dtype != FM_I8) return bad("rms norm: out_dtype must be FM_E4M3 or FM_I8");
   const fm::RmsForward a = {x, x_stride, residual, residual_stride, weight, q, out_dtype == FM_E4M3 ? 1 : 2,
-                            scale, sum, nullptr, rows, static_cast<int>(width), static_cast<float>(eps), stream};
+                            scale, sum, nullptr, rows, static_cast<int>(width), fm::rms_eps(eps), stream};
   return fm::rms_forward(a, eps, dtype, param_dtype);
 } catch (...) {
   return FM_E_NOMEM;
