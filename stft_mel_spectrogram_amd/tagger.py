@@ -94,6 +94,8 @@ def tag_bits(tags, count: int, device="cuda"):
     """The given tags of `count` as a mask of allowed ones (int32 words)."""
     words = [0] * ((count + 31) // 32)
     for t in tags:
+        if not 0 <= t < count:
+            raise ValueError(f"tags must be in [0, {count}), got {t}")
         words[t // 32] |= 1 << t % 32
     return torch.tensor([w - (1 << 32) if w >> 31 else w for w in words], dtype=torch.int32, device=device)
 
