@@ -85,7 +85,7 @@ class _Call:
             T.written(out, out_state)
         return out, out_state, saved
 
-    def backward(self, grad_y, saved, grad_state):
+    def backward(self, grad_y, saved, grad_state, with_state: bool):
         x, (b, t, c) = self.x, self.shape
         T.same_device(x, ("grad_state",), grad_y=grad_y, saved=saved, grad_state=grad_state)
         if grad_y.shape != self.shape or grad_y.dtype != x.dtype or (c > 1 and grad_y.stride(2) != 1):
@@ -95,7 +95,7 @@ class _Call:
         T.contiguous_f32(grad_state, (b, c), "grad_state")
         dx, df = T.like(grad_y), T.like(grad_y)
         dg = None if self.gate is None else T.like(grad_y)
-        ds = None if self.state is None else torch.empty_like(self.state)
+        ds = x.new_empty((b, c), dtype=torch.float32) if with_state else None
         a = N.RecurrenceArgs(*self.head, None, None, saved.data_ptr(), grad_y.data_ptr(), T.ptr(grad_state),
                              dx.data_ptr(), df.data_ptr(), T.ptr(dg), T.ptr(ds), *self.strides,
                              *grad_y.stride()[:2])
@@ -130,7 +130,7 @@ def gated_recurrence_backward(grad_y, x, forget, gate, state, saved, *, lengths=
     """(grad_x, grad_forget, grad_gate, grad_state) of sum(grad_y * y) +
     sum(grad_state * last state); the latter two are None without a gate or a
     state.  grad_state: float32 [batch, channels] or None."""
-    return _Call(x, forget, gate, state, lengths).backward(grad_y, saved, grad_state)
+    return _Call(x, forget, gate, state, lengths).backward(grad_y, saved, grad_state, state is not None)
 
 
 class _GatedRecurrence(torch.autograd.Function):
@@ -138,13 +138,15 @@ class _GatedRecurrence(torch.autograd.Function):
     def forward(ctx, x, forget, gate, state, lengths):
         y, last, saved = gated_recurrence_forward(x, forget, gate, state, lengths=lengths)
         ctx.set_materialize_grads(False)
-        ctx.save_for_backward(x, forget, gate, state, lengths, saved)
+        # not the state: `saved` has it, and a program may go on in its memory meanwhile
+        ctx.save_for_backward(x, forget, gate, lengths, saved)
+        ctx.with_state = state is not None
         return y, last
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_y, grad_state):
-        x, forget, gate, state, lengths, saved = ctx.saved_tensors
+        x, forget, gate, lengths, saved = ctx.saved_tensors
         if grad_y is None and grad_state is None:
             return None, None, None, None, None
         if grad_y is None:
@@ -153,6 +155,5 @@ class _GatedRecurrence(torch.autograd.Function):
             grad_y = grad_y.contiguous()
         if grad_state is not None:
             grad_state = grad_state.contiguous()
-        grads = gated_recurrence_backward(grad_y, x, forget, gate, state, saved, lengths=lengths,
-                                          grad_state=grad_state)
+        grads = _Call(x, forget, gate, None, lengths).backward(grad_y, saved, grad_state, ctx.with_state)
         return (*(g if need else None for g, need in zip(grads, ctx.needs_input_grad)), None)
