@@ -6,22 +6,17 @@
 #include <cstdint>
 #include <string>
 
+#include "fm_check.h"
+
 namespace fm {
 namespace {
 
 int bad(const char* what) { return set_error(FM_E_INVAL, what); }
 
-int elem_size(int dtype) {
-  return dtype == FM_F32 ? 4 : (dtype == FM_F16 || dtype == FM_BF16) ? 2 : 0;
-}
-int vec_elems(int dtype) { return 16 / elem_size(dtype); }
-
-bool aligned(const void* p, int bytes) {
-  return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(bytes - 1)) == 0;
-}
+int vec_elems(int dtype) { return 16 / elem_bytes(dtype); }
 
 int check_norm(int64_t rows, int64_t width, int dtype) {
-  if (!elem_size(dtype)) return bad("layer norm: dtype must be FM_F32, FM_F16 or FM_BF16");
+  if (!elem_bytes(dtype)) return bad("layer norm: dtype must be FM_F32, FM_F16 or FM_BF16");
   if (rows < 0 || rows >= (int64_t(1) << 31)) return bad("layer norm: rows must be in [0, 2^31)");
   if (width < 1) return bad("layer norm: width must be >= 1");
   if (width > kNormMaxWidth)
@@ -37,7 +32,7 @@ int check_params(int dtype, int param_dtype, const void* w, const void* b) {
 }
 
 int check_scores(int64_t rows, int64_t vocab, int top, int dtype) {
-  if (!elem_size(dtype)) return bad("token log probabilities: dtype must be FM_F32, FM_F16 or FM_BF16");
+  if (!elem_bytes(dtype)) return bad("token log probabilities: dtype must be FM_F32, FM_F16 or FM_BF16");
   if (rows < 0) return bad("token log probabilities: rows must be >= 0");
   if (vocab < 1 || vocab >= (int64_t(1) << 31) - 65536)
     return bad("token log probabilities: vocab must be in [1, 2^31 - 65536)");
@@ -66,7 +61,7 @@ bool strides_fit(const int64_t* s) {
 // translates the public struct.
 int attention_args(const fm_attention_args* p, AttnArgs& a) {
   if (!p) return bad("attention: args must not be NULL");
-  if (!elem_size(p->dtype)) return bad("attention: dtype must be FM_F32, FM_F16 or FM_BF16");
+  if (!elem_bytes(p->dtype)) return bad("attention: dtype must be FM_F32, FM_F16 or FM_BF16");
   if (p->table_dtype != p->dtype && p->table_dtype != FM_F32)
     return bad("attention: table_dtype must be dtype or FM_F32");
   const int64_t most = int64_t(1) << 30;
@@ -104,7 +99,7 @@ int attention_args(const fm_attention_args* p, AttnArgs& a) {
   a.q_len = static_cast<int>(p->q_len);
   a.k_len = static_cast<int>(p->k_len);
   a.dim = static_cast<int>(p->head_dim);
-  a.size = elem_size(p->dtype);
+  a.size = elem_bytes(p->dtype);
   a.scale = static_cast<float>(p->scale);
   for (int i = 0; i < 3; ++i) {
     a.qs[i] = p->q_stride[i];
@@ -135,14 +130,14 @@ int attention_pointers(const AttnArgs& a, int dtype, bool backward) {
       (backward && (!strides_fit(a.dos) || !strides_fit(a.dqs) || !strides_fit(a.dks) || !strides_fit(a.dvs))))
     return bad("attention: strides must be >= 0");
   if (!a.table || !a.map) return bad("attention: table and bucket_map must not be NULL");
-  const int es = elem_size(dtype);
+  const int es = elem_bytes(dtype);
   const bool q = attn_rows(a) > 0, k = q && a.k_len > 0;
   if (q && (!a.q || !a.o)) return bad("attention: q and o must not be NULL");
   if (k && (!a.k || !a.v)) return bad("attention: k and v must not be NULL");
-  if (!aligned(a.q, es) || !aligned(a.k, es) || !aligned(a.v, es) || !aligned(a.o, es) ||
-      !aligned(a.d_o, es) || !aligned(a.dq, es) || !aligned(a.dk, es) ||
-      !aligned(a.dv, es) || !aligned(a.map, 4) || !aligned(a.key_lengths, 4) ||
-      !aligned(a.query_offset, 4))
+  if (!aligned_to(a.q, es) || !aligned_to(a.k, es) || !aligned_to(a.v, es) || !aligned_to(a.o, es) ||
+      !aligned_to(a.d_o, es) || !aligned_to(a.dq, es) || !aligned_to(a.dk, es) ||
+      !aligned_to(a.dv, es) || !aligned_to(a.map, 4) || !aligned_to(a.key_lengths, 4) ||
+      !aligned_to(a.query_offset, 4))
     return bad("attention: misaligned pointer");
   return FM_OK;
 }
@@ -163,8 +158,8 @@ int fm_layer_norm_forward(const void* x, int64_t x_stride, const void* weight, c
   if (rows == 0) return FM_OK;
   if (!x || !y) return bad("layer norm: x and y must not be NULL");
   if (rows > 1 && x_stride < 0) return bad("layer norm: x_stride must be >= 0");
-  const int es = fm::elem_size(dtype);
-  if (!fm::aligned(x, es) || !fm::aligned(y, es)) return bad("layer norm: misaligned pointer");
+  const int es = fm::elem_bytes(dtype);
+  if (!fm::aligned_to(x, es) || !fm::aligned_to(y, es)) return bad("layer norm: misaligned pointer");
   const fm::NormForward a = {x, x_stride, weight, bias, y, mean, rstd, rows,
                              static_cast<int>(width), static_cast<float>(eps), stream};
   const bool w32 = param_dtype == FM_F32;
@@ -195,11 +190,11 @@ int fm_layer_norm_backward(const void* dy, int64_t dy_stride, const void* x, int
     if (!dy || !x || !dx || !mean || !rstd)
       return bad("layer norm: dy, x, mean, rstd and dx must not be NULL");
     if (dw && !fm::norm_single(rows, static_cast<int>(width), fm::vec_elems(dtype)) &&
-        (!workspace || !fm::aligned(workspace, 16)))
+        (!workspace || !fm::aligned_to(workspace, 16)))
       return bad("layer norm: the workspace must be 16-byte aligned device memory");
     if (rows > 1 && (x_stride < 0 || dy_stride < 0)) return bad("layer norm: strides must be >= 0");
-    const int es = fm::elem_size(dtype);
-    if (!fm::aligned(x, es) || !fm::aligned(dy, es) || !fm::aligned(dx, es))
+    const int es = fm::elem_bytes(dtype);
+    if (!fm::aligned_to(x, es) || !fm::aligned_to(dy, es) || !fm::aligned_to(dx, es))
       return bad("layer norm: misaligned pointer");
   }
   const fm::NormBackward a = {dy, dy_stride, x,  x_stride,  weight, mean,
@@ -231,10 +226,10 @@ int fm_token_logprobs_strided(const void* x, int64_t x_stride, int64_t x_inner, 
   if (top > 0 && (!top_ids || !top_lp))
     return bad("token log probabilities: top_ids and top_lp must not be NULL");
   if (int st = fm::check_score_strides(rows, x_stride, x_inner, x_outer)) return st;
-  if (!fm::aligned(x, fm::elem_size(dtype)) || !fm::aligned(tokens, token_bits / 8))
+  if (!fm::aligned_to(x, fm::elem_bytes(dtype)) || !fm::aligned_to(tokens, token_bits / 8))
     return bad("token log probabilities: misaligned pointer");
   if (fm::score_workspace(rows, static_cast<int>(vocab), top, fm::vec_elems(dtype)) > 0 &&
-      (!workspace || !fm::aligned(workspace, 16)))
+      (!workspace || !fm::aligned_to(workspace, 16)))
     return bad("token log probabilities: the workspace must be 16-byte aligned device memory");
   const fm::ScoreForward a = {x, x_stride, x_inner, x_outer, tokens, token_bits == 64, lp, ent, lse, top_ids,
                               top_lp, workspace, rows, static_cast<int>(vocab), top, stream};
@@ -259,8 +254,8 @@ int fm_token_logprobs_backward_strided(const void* x, int64_t x_stride, int64_t 
   if (g_ent && !ent) return bad("token log probabilities: g_ent needs ent");
   if (g_top && (!top_ids || top < 1)) return bad("token log probabilities: g_top needs top_ids");
   if (int st = fm::check_score_strides(rows, x_stride, x_inner, x_outer)) return st;
-  const int es = fm::elem_size(dtype);
-  if (!fm::aligned(x, es) || !fm::aligned(dx, es) || !fm::aligned(tokens, token_bits / 8))
+  const int es = fm::elem_bytes(dtype);
+  if (!fm::aligned_to(x, es) || !fm::aligned_to(dx, es) || !fm::aligned_to(tokens, token_bits / 8))
     return bad("token log probabilities: misaligned pointer");
   const fm::ScoreBackward a = {x,   x_stride, x_inner, x_outer, tokens, token_bits == 64,
                                lse, ent,      g_lp,    g_ent,   top_ids, g_top,
@@ -303,7 +298,7 @@ int fm_attention_forward(const fm_attention_args* args, void* workspace, void* s
   if (int st = fm::attention_pointers(a, args->dtype, false)) return st;
   if (fm::attn_rows(a) == 0) return FM_OK;
   if (a.splits > 1) {
-    if (!workspace || !fm::aligned(workspace, 16))
+    if (!workspace || !fm::aligned_to(workspace, 16))
       return bad("attention: the workspace must be 16-byte aligned device memory");
     a.part_o = static_cast<float*>(workspace);
     a.part_lse = a.part_o + fm::attn_round16(4 * a.splits * fm::attn_rows(a) * a.dim) / 4;
@@ -323,7 +318,7 @@ int fm_attention_backward(const fm_attention_args* args, void* workspace, void* 
   if (a.batch > 0 && a.k_len > 0 && (!a.k || !a.v || !a.dk || !a.dv))
     return bad("attention: k, v, grad_k and grad_v must not be NULL");
   const fm::AttnBackwardSpace w = fm::attn_backward_space(a, args->dtype == FM_F16);
-  if (w.total > 0 && (!workspace || !fm::aligned(workspace, 16)))
+  if (w.total > 0 && (!workspace || !fm::aligned_to(workspace, 16)))
     return bad("attention: the workspace must be 16-byte aligned device memory");
   char* base = static_cast<char*>(workspace);
   a.delta = reinterpret_cast<float*>(base);
