@@ -1,7 +1,7 @@
 """Logits before a token is chosen from them: penalties for repeated tokens,
 biases, and masks of allowed tokens, in one pass.
 
-    x = x > 0 ? x / repetition : x * repetition       for tokens of the history
+    x = x > 0 ? x (1 / repetition) : x repetition     for tokens of the history
     x = x - frequency * count - presence * (count > 0)
     x = x + the token's biases
     x = -inf                                          where a token is not allowed
@@ -45,7 +45,8 @@ def adjust_logits(logits, history=None, history_lengths=None, *, prompt_lengths=
     outside the vocabulary are none, the same id twice counts twice.  allowed:
     int32 words of 32 tokens' bits, the lowest bit first, [(vocab + 31) // 32]
     for all rows or [..., (vocab + 31) // 32].  out takes the result and may be
-    the logits themselves.  Not differentiable.
+    the logits themselves.  Up to 2^22 rows times segments of 2048 tokens.  Not
+    differentiable: tensors that require grad are refused.
     """
     code = T.dtype_code(logits, "logits")
     if T.wants_grad(logits, repetition, frequency, presence, bias, out):

@@ -11,9 +11,10 @@
 // token's first entry in its slot; where a token has several, that entry adds them up
 // in order.  Then each lane works on its own elements: one read, one write, in place
 // too.  Every segment reads the row's history and biases again, from the cache.
-// Without a history bound by memory; with a long one by the vector units (256 x 131072
-// f16, a history of 4000, 300 biases: 46 us, the units busy 79% of the time; without
-// biases 38, without either 23; a copy of the logits 20).  8 x 50001 bf16: 5.
+// Without a history bound by memory; with a long one by the vector units, 34 instructions
+// per token (256 x 131072 f16, a history of 4000, 300 biases: 52 us from memory, 46 where
+// the last-level cache still holds the operands, the units then busy 79% of the time;
+// there without biases 38; with a mask alone 29 from memory, 4.7 TB/s).  8 x 50001 bf16: 5.
 #pragma once
 
 #include "fm_logit.h"
@@ -52,7 +53,7 @@ __global__ __launch_bounds__(kAdjustThreads) void adjust_kernel(const AdjustArgs
   }
   const int prompt = a.prompt_lengths && len > 0 ? a.prompt_lengths[row] : 0;
   const float rep = a.repetition ? a.repetition[row] : a.repetition_value;
-  const float over = 1.f / rep;  // one rounding more than a division, for a tenth of its instructions
+  const float over = 1.f / rep;  // one rounding of 2^-24 more than a division, for a tenth of its instructions
   const float freq = a.frequency ? a.frequency[row] : a.frequency_value;
   const float pres = a.presence ? a.presence[row] : a.presence_value;
   // tokens as slots of this segment, or -1

@@ -17,7 +17,7 @@
 // whether one of the entries (one per lane) lies there.  The backward writes the
 // others' formula everywhere and then the named tokens again, after a barrier.
 // 4096 x 32000 bf16, the best 20 and the rest: forward 78 us (3.4 TB/s, vector units
-// busy 67% of the time: an exponential and eight instructions per logit), backward 124
+// busy 67% of the time: twelve instructions per logit, one an exponential), backward 124
 // (4.2 TB/s); 24008 x 129 f32, the best 8: 6.7 and 9.6.
 #pragma once
 

@@ -61,8 +61,9 @@ constexpr int kAdjustThreads = 512;
 
 // 16-byte groups of a lane: a workgroup takes a segment of a row, of 8192 tokens
 // while there are 512 of them, two per compute unit, since each reads the row's
-// history again (256 x 131072 f16, history 4000, 300 biases, with an earlier counting
-// loop: 52 us, 4096 tokens 66, 16384 66; 64 x 131072 f32: 24, 4096 tokens 26, 2048 30).
+// history again (history 4000, 300 biases, us: 256 x 131072 f16 52, segments of 4096 tokens
+// 69; f32 72, 4096 tokens 78, 2048 106; 64 x 131072 f32 24, 24, 26).  Fewer tokens where
+// there are fewer workgroups (8 x 50001 bf16: 4096 tokens 5.2, 8192 6.2).
 inline int adjust_vecs(int64_t rows, int vocab, int ve) {
   int v = 16 / ve;
   for (; v > 1; v /= 2) {

@@ -38,7 +38,8 @@ __device__ __forceinline__ float from_lane(int byte_lane, float v) {
   return __int_as_float(__builtin_amdgcn_ds_bpermute(byte_lane, __float_as_int(v)));
 }
 
-// exp(-v).  The product's rounding is made good for results in 32 bits.
+// exp(-v), off by 2^-24 (1.25 |v| + 2) of itself; the product's rounding (the |v|) is made
+// good for inputs in 32 bits, not for gates that have 8 or 11 bits themselves.
 template <class T>
 __device__ __forceinline__ float exp_minus(float v) {
   const float y = v * -kLog2e;
@@ -50,7 +51,7 @@ __device__ __forceinline__ float exp_minus(float v) {
   }
   return e;
 }
-// sigmoid and one minus it, each to its own precision.
+// sigmoid and one minus it, each to its own precision (the reciprocal's 2^-23 included).
 template <class T>
 __device__ __forceinline__ void sigmoids(float v, float& s, float& rest) {
   const float e = exp_minus<T>(v);

@@ -9,7 +9,9 @@ token_logprobs(..., top_k) of a larger model gives them:
 over the given tokens, T the temperature.  With rest=True (T = 1) q = exp(lps),
 and the mass that the teacher leaves for all others stands against the
 student's: one more term, r log(r / R).  A negative id is no entry; a row without
-entries has loss 0 and no gradient.
+entries has loss 0 and no gradient.  A student that leaves no other token any
+probability (all of them -inf, or none there) has no such term, since r may be
+rounding alone; a named token of -inf gives an infinite loss.
 """
 from __future__ import annotations
 
